@@ -101,6 +101,27 @@ typedef enum mx_format {
   MX_FMT_RESERVED_MAX_ = 2147483647
 } mx_format;
 
+/* Element type of the activations the operators around the experts take
+ * (mx_moe_*, mx_block_norm*, mx_lora_add). */
+typedef enum mx_dtype {
+  MX_DT_BF16 = 0,
+  MX_DT_F16 = 1,
+  MX_DT_F32 = 2,
+  /* not types: they make every int32 value a valid mx_dtype (an unknown one is MX_ERR_FORMAT) */
+  MX_DT_RESERVED_MIN_ = -2147483647 - 1,
+  MX_DT_RESERVED_MAX_ = 2147483647
+} mx_dtype;
+
+/* What one value of the gate of mx_block_norm covers. */
+typedef enum mx_gate {
+  MX_GATE_NONE = 0,      /* no gate: gate is NULL */
+  MX_GATE_CHANNEL = 1,   /* gate [H]: a column */
+  MX_GATE_TOKEN = 2,     /* gate [T]: a row */
+  MX_GATE_FULL = 3,      /* gate [T, H]: an element */
+  MX_GATE_RESERVED_MIN_ = -2147483647 - 1,
+  MX_GATE_RESERVED_MAX_ = 2147483647
+} mx_gate;
+
 /*
  * mx_dequant -- dequantise a block-scaled matrix to bf16. The operation is the
  * pages' offline dequant script: the FP8 weights times their 128 x 128 block
@@ -510,6 +531,124 @@ typedef struct mx_phase_stat {
 
 MX_API mx_status mx_profile_start(void);
 MX_API mx_status mx_profile_stop(mx_phase_stat* stats, int32_t max_stats, int32_t* n_stats);
+
+/*
+ * Rows to the experts and back. mx_grouped_expert_mlp sorts, gathers and
+ * combines inside one call; these give a caller the same steps around experts of
+ * its own (experts dequantised by mx_dequant for fine-tuning, a dense
+ * adapter per expert), with the gradient.
+ *
+ * mx_moe_sort -- the slots p = t*k + j of topk_ids [T, k] in the order of
+ * (expert, p), the order of mx_grouped_expert_mlp, as two inverse maps:
+ *   expert_off [E+1]  int32: expert e's rows are expert_off[e] .. expert_off[e+1] - 1
+ *   row_slot   [T*k]  int32: the slot of each row (its token is row_slot / k);
+ *                     -1 for the rows past expert_off[E]
+ *   slot_row   [T, k] int32: the row of each slot; -1 where its id is outside
+ *                     [0, E) (the expert is on another rank, or there is none)
+ * A token may name an expert more than once. With k = 1 this sorts tokens by any
+ * small id: mx_lora_add takes expert_off and row_slot of the adapter ids.
+ * k >= 1, 1 <= E <= 512, T*k <= 2^30; T == 0 writes E + 1 zeros. workspace:
+ * mx_moe_sort_workspace_size(T, k, E) bytes, 256-byte aligned (0 bytes for few
+ * slots: workspace may then be NULL). Alignment: 4 bytes. The outputs must not
+ * overlap each other or topk_ids.
+ */
+MX_API mx_status mx_moe_sort(const int32_t* topk_ids, int64_t T, int32_t k, int32_t E, int32_t* expert_off,
+                             int32_t* row_slot, int32_t* slot_row, void* workspace, size_t ws_bytes, void* stream);
+MX_API size_t mx_moe_sort_workspace_size(int64_t T, int32_t k, int32_t E);
+
+/*
+ * mx_moe_permute -- xs[slot_row[t, j]] = x[t] for every slot that has a row.
+ *   x [T, hidden] and xs [rows, hidden] of type dt; slot_row [T, k] as written
+ *   by mx_moe_sort. Rows of xs that no slot names are left as they are; a slot
+ *   whose row is outside [0, rows) is skipped (rows is normally T*k).
+ * mx_moe_unpermute -- y[t] = sum_j w[t, j] * ys[slot_row[t, j]] over the slots
+ * that have a row, in slot order in fp32, rounded once; 0 for a token without
+ * any. topk_w [T, k] fp32, or NULL for weights of 1: then it is the gradient of
+ * mx_moe_permute for x, given that of xs. The weight of a slot without a row is
+ * not read.
+ * mx_moe_unpermute_grad -- the gradient of mx_moe_unpermute, given d_y [T, hidden]:
+ *   d_ys[slot_row[t, j]] = w[t, j] * d_y[t]      (rows that no slot names left as they are)
+ *   d_w[t, j] = sum_c d_y[t, c] * ys[slot_row[t, j], c], fp32; 0 for a slot without a row
+ * No two slots may share a row. hidden is 1 to 2^20; T, rows >= 0, T*k <= 2^30.
+ * Alignment: one element (16-byte aligned rows, hidden times the element's size
+ * a multiple of 16, are faster). Outputs must not overlap inputs.
+ */
+MX_API mx_status mx_moe_permute(mx_dtype dt, const void* x, int64_t T, int64_t hidden, const int32_t* slot_row,
+                                int32_t k, int64_t rows, void* xs, void* stream);
+MX_API mx_status mx_moe_unpermute(mx_dtype dt, const void* ys, int64_t rows, int64_t hidden, const int32_t* slot_row,
+                                  const float* topk_w, int64_t T, int32_t k, void* y, void* stream);
+MX_API mx_status mx_moe_unpermute_grad(mx_dtype dt, const void* d_y, const void* ys, int64_t rows, int64_t hidden,
+                                       const int32_t* slot_row, const float* topk_w, int64_t T, int32_t k,
+                                       void* d_ys, float* d_w, void* stream);
+
+/*
+ * mx_block_norm -- the norms before and after a block (an expert MLP, an
+ * attention) with the block's gate and the residual scale, in one pass. Over
+ * rows of H elements, with rms(v) = sqrt(mean(v^2) + eps):
+ *   u            = y / rms(y) * w_post     (u = y where w_post is NULL)
+ *   residual_out = residual + res_scale * gate * u
+ *   normed       = r / rms(r) * w_pre      (r = residual_out before its rounding)
+ * y == NULL: normed of the residual itself (the first norm of a stack); w_post,
+ * gate and residual_out must then be NULL. w_pre == NULL: no normed output
+ * (normed must be NULL; the last block). Not both.
+ *   y, normed [T, H], w_post, w_pre [H] and gate of type dt; gate_kind says the
+ *   gate's shape (mx_gate; gate is NULL exactly for MX_GATE_NONE).
+ *   residual, residual_out [T, H] of type res_dt: dt, or MX_DT_F32.
+ * residual_out may be residual, and normed may be y (in place); no other
+ * overlap. 1 <= H <= 16384, eps >= 0, res_scale finite. Sums of squares are fp32:
+ * |values| up to about 10^17. Alignment: one element (H a multiple of 8 with all
+ * pointers 16-byte aligned is faster).
+ */
+MX_API mx_status mx_block_norm(mx_dtype dt, mx_dtype res_dt, const void* y, const void* residual, const void* w_post,
+                               mx_gate gate_kind, const void* gate, float res_scale, const void* w_pre, float eps,
+                               int64_t T, int64_t H, void* residual_out, void* normed, void* stream);
+
+/*
+ * mx_block_norm_grad -- the gradient of mx_block_norm at the stored residual_out
+ * (without y: at the residual), given d_normed [T, H] of type dt (with w_pre,
+ * else NULL) and d_residual_out [T, H] of type res_dt, the gradient that
+ * residual_out receives from the stack behind it (NULL: none):
+ *   d_residual [T, H] of type res_dt: the whole gradient of residual_out, which
+ *              is also that of residual
+ *   d_y        [T, H] of type dt (with y, else NULL)
+ *   d_gate     MX_GATE_FULL: [T, H] of type dt; MX_GATE_CHANNEL: [H] fp32;
+ *              MX_GATE_TOKEN: [T] fp32
+ *   dw_pre     [H] fp32 (with w_pre), dw_post [H] fp32 (with w_post)
+ * Sums over rows run in a fixed order for given sizes (no atomics). T == 0 writes
+ * zeros to dw_pre, dw_post and a channel gate's d_gate.
+ * d_residual may be d_residual_out, and d_y may be d_normed or y; no other
+ * overlap. workspace: mx_block_norm_grad_workspace_size(T, H) bytes, 256-byte
+ * aligned. Limits and alignment as for mx_block_norm.
+ */
+MX_API mx_status mx_block_norm_grad(mx_dtype dt, mx_dtype res_dt, const void* y, const void* residual_out,
+                                    const void* w_post, mx_gate gate_kind, const void* gate, float res_scale,
+                                    const void* w_pre, float eps, int64_t T, int64_t H, const void* d_normed,
+                                    const void* d_residual_out, void* d_residual, void* d_y, void* d_gate,
+                                    float* dw_post, float* dw_pre, void* workspace, size_t ws_bytes, void* stream);
+MX_API size_t mx_block_norm_grad_workspace_size(int64_t T, int64_t H);
+
+/*
+ * mx_lora_add -- the low-rank adapters of many requests on top of a shared
+ * projection (mx_nvfp4_linear, mx_fp8_block_linear, or any other), in place:
+ *   y[t] += scale[a] * (x[t] . A[a]^T) . B[a]^T,   a the adapter of token t
+ *   x [M, K], rows ldx elements apart; y [M, N], rows ldy elements apart
+ *   a [n, R, K], b [n, N, R], all of type dt (MX_DT_BF16 or MX_DT_F16)
+ *   scale [n] fp32, or NULL for 1
+ *   adapter_off [n+1], row_token [M]: expert_off and row_slot of mx_moe_sort over
+ *     the tokens' adapter ids (k = 1, E = n), made once and used for every
+ *     projection of a step; tokens with an id outside [0, n) keep their y.
+ * x . A^T is held in fp32 accuracy between the two products; y is rounded once.
+ * R a multiple of 8 up to 128 (adapters of smaller rank are padded with zero
+ * rows of A and zero columns of B), K and N multiples of 8 up to 2^20,
+ * M <= 2^24, 1 <= n <= 512, ldx >= K and ldy >= N multiples of 8.
+ * workspace: mx_lora_add_workspace_size(M, K, R, n) bytes, 256-byte aligned; x, a
+ * and b must not overlap y. Alignment: x, a, b, y 16 bytes; the others 4.
+ */
+MX_API mx_status mx_lora_add(mx_dtype dt, const void* x, int64_t ldx, int64_t M, int64_t K, const void* a,
+                             const void* b, const float* scale, int32_t n, int64_t R, const int32_t* adapter_off,
+                             const int32_t* row_token, void* y, int64_t ldy, int64_t N, void* workspace,
+                             size_t ws_bytes, void* stream);
+MX_API size_t mx_lora_add_workspace_size(int64_t M, int64_t K, int64_t R, int32_t n);
 
 /*
  * Measurement probes (not steps of the pages' pipeline): kernels whose measured

@@ -19,6 +19,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 # the CPU tests load); by default the in-tree libmxfp4.so.
 LIB_PATH = os.environ.get("MXFP4_LIB") or os.path.join(HERE, "libmxfp4.so")
 
+MX_DT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+MX_GATE = {"none": 0, "channel": 1, "token": 2, "full": 3}
 MX_FMT = {"mxfp4": 0, "fp8_b128": 1, "nvfp4": 2, "mxfp8": 3}
 STATUS = {0: "MX_OK", 1: "MX_ERR_NULL", 2: "MX_ERR_SHAPE", 3: "MX_ERR_ALIGN", 4: "MX_ERR_FORMAT",
           5: "MX_ERR_WORKSPACE", 6: "MX_ERR_HIP", 7: "MX_ERR_VALUE"}
@@ -69,6 +71,17 @@ SIGNATURES = {
     "mx_last_error": (ctypes.c_char_p, []),
     "mx_profile_start": (_I32, []),
     "mx_profile_stop": (_I32, [ctypes.POINTER(PhaseStat), _I32, ctypes.POINTER(_I32)]),
+    "mx_moe_sort": (_I32, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
+    "mx_moe_sort_workspace_size": (_SZ, [_I64, _I32, _I32]),
+    "mx_moe_permute": (_I32, [_I32, _P, _I64, _I64, _P, _I32, _I64, _P, _P]),
+    "mx_moe_unpermute": (_I32, [_I32, _P, _I64, _I64, _P, _P, _I64, _I32, _P, _P]),
+    "mx_moe_unpermute_grad": (_I32, [_I32, _P, _P, _I64, _I64, _P, _P, _I64, _I32, _P, _P, _P]),
+    "mx_block_norm": (_I32, [_I32, _I32, _P, _P, _P, _I32, _P, _F, _P, _F, _I64, _I64, _P, _P, _P]),
+    "mx_block_norm_grad": (_I32, [_I32, _I32, _P, _P, _P, _I32, _P, _F, _P, _F, _I64, _I64, _P, _P, _P, _P, _P, _P,
+                                  _P, _P, _SZ, _P]),
+    "mx_block_norm_grad_workspace_size": (_SZ, [_I64, _I64]),
+    "mx_lora_add": (_I32, [_I32, _P, _I64, _I64, _I64, _P, _P, _P, _I32, _I64, _P, _P, _P, _I64, _I64, _P, _SZ, _P]),
+    "mx_lora_add_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
     "mx_probe_mfma_fp4": (_I32, [_P, _I64, _I32, _P, _P]),
     "mx_probe_read": (_I32, [_I32, _I32, _I32, _P, _I64, _P, _P]),
     "mx_probe_copy": (_I32, [_P, _P, _I64, _P]),
@@ -420,6 +433,254 @@ def fp8_expert_mlp(x, w1, w1s, w3, w3s, w2, w2s, out=None, workspace=None, strea
     _check(lib().mx_fp8_expert_mlp(_ptr(x), M, hidden, inter, _ptr(w1), _ptr(w1s), _ptr(w3), _ptr(w3s), _ptr(w2),
                                    _ptr(w2s), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# The operators around the experts. Their tensors are checked here against each
+# other (type, shape, device), since the library sees pointers only; a call runs
+# on the tensors' device, on its current stream unless one is given.
+
+def _need(cond, what):
+    if not cond:
+        raise ValueError(what)
+
+
+def _tensor(t, name, dtype, shape, device):
+    """t as a device pointer, once its type, shape, device and layout are as said."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}: got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def _dtype(t, name):
+    if t.device.type != "cuda":
+        raise ValueError("libmxfp4 takes device tensors")
+    dt = MX_DT.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} is {t.dtype}: bf16, fp16 or fp32 is taken")
+    return dt
+
+
+def _run(fn, device, stream, scratch, *args):
+    """fn(*args, stream) on `device`; `scratch` is memory of this call's own that the stream goes on using."""
+    if stream is None:
+        s = torch.cuda.current_stream(device)
+    else:
+        s = stream
+        if scratch is not None:
+            scratch.record_stream(s)
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, s.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, s.cuda_stream))
+
+
+def _own(out, shape, dtype, device, stream):
+    """`out`, or a new tensor, known to `stream` where it is not the current one."""
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+        if stream is not None:
+            out.record_stream(stream)
+    return out
+
+
+def _scratch(workspace, nbytes, device):
+    """(tensor to keep if it is the call's own, pointer, bytes)"""
+    if workspace is not None:
+        _need(workspace.device == device and workspace.is_contiguous(), f"workspace must be contiguous and on {device}")
+        return None, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if nbytes == 0:
+        return None, None, 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), nbytes
+
+
+def moe_sort_workspace_size(T, k, E) -> int:
+    return int(lib().mx_moe_sort_workspace_size(T, k, E))
+
+
+def moe_sort(topk_ids, E: int, expert_off=None, row_slot=None, slot_row=None, workspace=None, stream=None):
+    """mx_moe_sort: int32 topk_ids [T, k] -> (expert_off [E+1], row_slot [T*k], slot_row [T, k]), all int32."""
+    T, k = topk_ids.shape
+    dev, i32 = topk_ids.device, torch.int32
+    _need(dev.type == "cuda", "libmxfp4 takes device tensors")
+    _need(1 <= E <= 512, f"E {E} not in [1, 512]")
+    ids = _tensor(topk_ids, "topk_ids", i32, (T, k), dev)
+    expert_off = _own(expert_off, (E + 1,), i32, dev, stream)
+    row_slot = _own(row_slot, (T * k,), i32, dev, stream)
+    slot_row = _own(slot_row, (T, k), i32, dev, stream)
+    L = lib()
+    ws, wp, wn = _scratch(workspace, int(L.mx_moe_sort_workspace_size(T, k, E)), dev)
+    _run(L.mx_moe_sort, dev, stream, ws, ids, T, k, E, _tensor(expert_off, "expert_off", i32, (E + 1,), dev),
+         _tensor(row_slot, "row_slot", i32, (T * k,), dev), _tensor(slot_row, "slot_row", i32, (T, k), dev), wp, wn)
+    return expert_off, row_slot, slot_row
+
+
+def moe_permute(x, slot_row, out=None, stream=None):
+    """mx_moe_permute: x [T, H] to its rows of out [rows, H] (default: a new [T*k, H], whose other rows are
+    whatever they are)."""
+    T, H = x.shape
+    k = slot_row.shape[1]
+    dev = x.device
+    dt = _dtype(x, "x")
+    out = _own(out, (T * k, H), x.dtype, dev, stream)
+    rows = out.shape[0]
+    _run(lib().mx_moe_permute, dev, stream, None, dt, _tensor(x, "x", x.dtype, (T, H), dev), T, H,
+         _tensor(slot_row, "slot_row", torch.int32, (T, k), dev), k, rows,
+         _tensor(out, "out", x.dtype, (rows, H), dev))
+    return out
+
+
+def moe_unpermute(ys, slot_row, topk_w=None, out=None, stream=None):
+    """mx_moe_unpermute: ys [rows, H] -> y [T, H], weighted by fp32 topk_w [T, k] (None: 1)."""
+    rows, H = ys.shape
+    T, k = slot_row.shape
+    dev = ys.device
+    dt = _dtype(ys, "ys")
+    out = _own(out, (T, H), ys.dtype, dev, stream)
+    _run(lib().mx_moe_unpermute, dev, stream, None, dt, _tensor(ys, "ys", ys.dtype, (rows, H), dev), rows, H,
+         _tensor(slot_row, "slot_row", torch.int32, (T, k), dev),
+         None if topk_w is None else _tensor(topk_w, "topk_w", torch.float32, (T, k), dev), T, k,
+         _tensor(out, "out", ys.dtype, (T, H), dev))
+    return out
+
+
+def moe_unpermute_grad(d_y, ys, slot_row, topk_w, d_ys=None, d_w=None, stream=None):
+    """mx_moe_unpermute_grad -> (d_ys [rows, H], d_w [T, k] fp32). Without d_ys, rows that no slot names come
+    back as zeros; a given d_ys keeps them."""
+    rows, H = ys.shape
+    T, k = slot_row.shape
+    dev = ys.device
+    dt = _dtype(ys, "ys")
+    if d_ys is None:
+        with torch.cuda.stream(stream):
+            d_ys = torch.zeros_like(ys)
+    d_w = _own(d_w, (T, k), torch.float32, dev, stream)
+    _run(lib().mx_moe_unpermute_grad, dev, stream, None, dt, _tensor(d_y, "d_y", ys.dtype, (T, H), dev),
+         _tensor(ys, "ys", ys.dtype, (rows, H), dev), rows, H,
+         _tensor(slot_row, "slot_row", torch.int32, (T, k), dev),
+         _tensor(topk_w, "topk_w", torch.float32, (T, k), dev), T, k,
+         _tensor(d_ys, "d_ys", ys.dtype, (rows, H), dev), _tensor(d_w, "d_w", torch.float32, (T, k), dev))
+    return d_ys, d_w
+
+
+def _gate(gate, T, H):
+    """(mx_gate, shape of the gate) from the gate's shape: None, [H], [T, 1] or [T, H]."""
+    if gate is None:
+        return 0, None
+    if gate.shape == (H,):
+        return 1, (H,)
+    if gate.shape == (T, H) and H > 1:
+        return 3, (T, H)
+    if gate.shape == (T, 1):
+        return 2, (T, 1)
+    raise ValueError(f"gate of shape {tuple(gate.shape)}: [H], [T, 1] or [T, H] is taken, T {T}, H {H}")
+
+
+def block_norm(residual, w_pre=None, y=None, w_post=None, gate=None, res_scale: float = 1.0, eps: float = 1e-6,
+               residual_out=None, normed=None, stream=None):
+    """mx_block_norm -> (normed [T, H] or None without w_pre, residual_out [T, H] or, without y, the residual).
+    gate: None, [H] (per channel), [T, 1] (per token) or [T, H]."""
+    T, H = residual.shape
+    dev = residual.device
+    rdt = _dtype(residual, "residual")
+    _need(y is not None or w_pre is not None, "y and w_pre are both None: nothing to do")
+    like = y if y is not None else w_pre
+    dt, adt = _dtype(like, "y or w_pre"), like.dtype
+    kind, gshape = _gate(gate, T, H)
+    res = _tensor(residual, "residual", residual.dtype, (T, H), dev)
+    ro = no = None
+    if y is not None:
+        residual_out = _own(residual_out, (T, H), residual.dtype, dev, stream)
+        ro = _tensor(residual_out, "residual_out", residual.dtype, (T, H), dev)
+    else:
+        _need(w_post is None and gate is None and residual_out is None, "w_post, gate and residual_out need y")
+    if w_pre is not None:
+        normed = _own(normed, (T, H), adt, dev, stream)
+        no = _tensor(normed, "normed", adt, (T, H), dev)
+    else:
+        _need(normed is None, "normed needs w_pre")
+    _run(lib().mx_block_norm, dev, stream, None, dt, rdt,
+         None if y is None else _tensor(y, "y", adt, (T, H), dev), res,
+         None if w_post is None else _tensor(w_post, "w_post", adt, (H,), dev), kind,
+         None if gate is None else _tensor(gate, "gate", adt, gshape, dev), res_scale,
+         None if w_pre is None else _tensor(w_pre, "w_pre", adt, (H,), dev), eps, T, H, ro, no)
+    return normed, (residual if y is None else residual_out)
+
+
+def block_norm_grad_workspace_size(T, H) -> int:
+    return int(lib().mx_block_norm_grad_workspace_size(T, H))
+
+
+def block_norm_grad(residual_out, w_pre=None, d_normed=None, d_residual_out=None, y=None, w_post=None, gate=None,
+                    res_scale: float = 1.0, eps: float = 1e-6, d_residual=None, d_y=None, workspace=None, stream=None):
+    """mx_block_norm_grad at the stored residual_out (without y: the residual) -> (d_residual, dw_pre, d_y, dw_post,
+    d_gate); None for what there is none of. dw_pre, dw_post and the d_gate of a [H] or [T, 1] gate are fp32."""
+    T, H = residual_out.shape
+    dev, f32 = residual_out.device, torch.float32
+    rdt = _dtype(residual_out, "residual_out")
+    _need(y is not None or w_pre is not None, "y and w_pre are both None: nothing to do")
+    _need((w_pre is None) == (d_normed is None), "w_pre and d_normed go together")
+    _need(w_pre is not None or d_residual_out is not None, "d_residual_out is needed without w_pre")
+    _need(y is not None or (w_post is None and gate is None and d_y is None), "w_post, gate and d_y need y")
+    like = y if y is not None else w_pre
+    dt, adt = _dtype(like, "y or w_pre"), like.dtype
+    kind, gshape = _gate(gate, T, H)
+    dw_pre = None if w_pre is None else _own(None, (H,), f32, dev, stream)
+    dw_post = None if w_post is None else _own(None, (H,), f32, dev, stream)
+    d_gate = None if gate is None else _own(None, gshape, adt if kind == 3 else f32, dev, stream)
+    d_residual = _own(d_residual, (T, H), residual_out.dtype, dev, stream)
+    if y is not None:
+        d_y = _own(d_y, (T, H), adt, dev, stream)
+    L = lib()
+    ws, wp, wn = _scratch(workspace, int(L.mx_block_norm_grad_workspace_size(T, H)), dev)
+
+    def act(t, name, shape):
+        return None if t is None else _tensor(t, name, adt, shape, dev)
+    _run(L.mx_block_norm_grad, dev, stream, ws, dt, rdt, act(y, "y", (T, H)),
+         _tensor(residual_out, "residual_out", residual_out.dtype, (T, H), dev), act(w_post, "w_post", (H,)), kind,
+         act(gate, "gate", gshape), res_scale, act(w_pre, "w_pre", (H,)), eps, T, H, act(d_normed, "d_normed", (T, H)),
+         None if d_residual_out is None else _tensor(d_residual_out, "d_residual_out", residual_out.dtype, (T, H), dev),
+         _tensor(d_residual, "d_residual", residual_out.dtype, (T, H), dev), act(d_y, "d_y", (T, H)),
+         None if d_gate is None else d_gate.data_ptr(), None if dw_post is None else dw_post.data_ptr(),
+         None if dw_pre is None else dw_pre.data_ptr(), wp, wn)
+    return d_residual, dw_pre, d_y, dw_post, d_gate
+
+
+def lora_add_workspace_size(M, K, R, n) -> int:
+    return int(lib().mx_lora_add_workspace_size(M, K, R, n))
+
+
+def _rows(t, name, dtype, rows, device):
+    """(pointer, width, row stride) of a matrix whose rows are contiguous."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.device != device or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a {dtype} matrix of {rows} rows with contiguous columns on {device}: got "
+                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    return t.data_ptr(), t.shape[1], t.stride(0) if rows > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+def lora_add(y, x, a, b, adapter_off, row_token, scale=None, workspace=None, stream=None):
+    """mx_lora_add: y [M, N] += scale[a] * (x [M, K] . a[a]^T) . b[a]^T in place, a [n, R, K], b [n, N, R], for the
+    tokens sorted by adapter (expert_off and row_slot of moe_sort over adapter ids [M, 1]). x and y may be column
+    ranges of wider matrices. Returns y."""
+    M = x.shape[0]
+    dev = x.device
+    dt = _dtype(x, "x")
+    n, R, K = a.shape
+    xp, kx, ldx = _rows(x, "x", x.dtype, M, dev)
+    yp, N, ldy = _rows(y, "y", x.dtype, M, dev)
+    _need(kx == K, f"x has {kx} columns, a takes {K}")
+    L = lib()
+    ws, wp, wn = _scratch(workspace, int(L.mx_lora_add_workspace_size(M, K, R, n)), dev)
+    _run(L.mx_lora_add, dev, stream, ws, dt, xp, ldx, M, K, _tensor(a, "a", x.dtype, (n, R, K), dev),
+         _tensor(b, "b", x.dtype, (n, N, R), dev),
+         None if scale is None else _tensor(scale, "scale", torch.float32, (n,), dev), n, R,
+         _tensor(adapter_off, "adapter_off", torch.int32, (n + 1,), dev),
+         _tensor(row_token, "row_token", torch.int32, (M,), dev), yp, ldy, N, wp, wn)
+    return y
 
 
 class MoeRunner:

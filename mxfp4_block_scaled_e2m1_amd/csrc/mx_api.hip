@@ -8,6 +8,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -1422,5 +1423,387 @@ mx_status mx_probe_copy(const void* src, void* dst, int64_t bytes, void* stream)
   return ok();
 }
 
-}  // extern "C"
+// ---------------------------------------------------------------- operators around the experts
+namespace {
 
+mx_status check_dtype(mx_dtype dt) {
+  if (dt == MX_DT_BF16 || dt == MX_DT_F16 || dt == MX_DT_F32) return MX_OK;
+  return fail(MX_ERR_FORMAT, "unknown element type %d", (int)dt);
+}
+
+// A buffer of a call, for the overlap checks.
+struct Span {
+  const char* name;
+  const void* p;
+  int64_t bytes;
+};
+bool overlaps(const Span& a, const Span& b) {
+  if (a.p == nullptr || b.p == nullptr || a.bytes <= 0 || b.bytes <= 0) return false;
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+// `out` may be exactly one of the buffers in `same`, and overlaps nothing else of `all`.
+mx_status check_apart(const Span& out, std::initializer_list<Span> all, std::initializer_list<const void*> same = {}) {
+  for (const Span& o : all) {
+    if (!overlaps(out, o)) continue;
+    if (out.p == o.p && std::find(same.begin(), same.end(), o.p) != same.end()) continue;
+    return fail(MX_ERR_VALUE, "%s overlaps %s", out.name, o.name);
+  }
+  return MX_OK;
+}
+
+mx_status check_slots(int64_t T, int32_t k) {
+  if (T < 0) return fail(MX_ERR_SHAPE, "token count %lld is negative", (long long)T);
+  if (k < 1) return fail(MX_ERR_SHAPE, "k %d must be at least 1", k);
+  if (T > ((int64_t)1 << 30) / k) return fail(MX_ERR_SHAPE, "%lld x %d slots are above 2^30", (long long)T, k);
+  return MX_OK;
+}
+
+mx_status check_rows(mx_dtype dt, int64_t T, int32_t k, int64_t rows, int64_t hidden) {
+  MX_TRY(check_dtype(dt));
+  MX_TRY(check_slots(T, k));
+  if (hidden < 1 || hidden > (1 << 20)) return fail(MX_ERR_SHAPE, "hidden %lld not in [1, 2^20]", (long long)hidden);
+  if (rows < 0 || rows > ((int64_t)1 << 30)) return fail(MX_ERR_SHAPE, "rows %lld not in [0, 2^30]", (long long)rows);
+  return MX_OK;
+}
+
+}  // namespace
+
+size_t mx_moe_sort_workspace_size(int64_t T, int32_t k, int32_t E) {
+  if (T < 0 || k < 1 || E < 1 || E > ROUTE_MAX_EXPERTS || T > ((int64_t)1 << 30) / k) return 0;
+  const int64_t P = T * k;
+  if (sort_in_one_block(P, E)) return 0;
+  Carve c(nullptr);
+  c.take((size_t)((P + ROUTE_CHUNK - 1) / ROUTE_CHUNK * E * 4));
+  c.take((size_t)(E + 1) * 4);
+  return c.off;
+}
+
+mx_status mx_moe_sort(const int32_t* topk_ids, int64_t T, int32_t k, int32_t E, int32_t* expert_off,
+                      int32_t* row_slot, int32_t* slot_row, void* workspace, size_t ws_bytes, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_slots(T, k));
+  if (E < 1 || E > ROUTE_MAX_EXPERTS) return fail(MX_ERR_SHAPE, "E %d not in [1, %d]", E, ROUTE_MAX_EXPERTS);
+  const int64_t P = T * k;
+  MX_REQUIRE_PTR(expert_off);
+  MX_REQUIRE_ALIGN(expert_off, 4);
+  if (P > 0) {
+    MX_REQUIRE_PTR(topk_ids);
+    MX_REQUIRE_PTR(row_slot);
+    MX_REQUIRE_PTR(slot_row);
+    MX_REQUIRE_ALIGN(topk_ids, 4);
+    MX_REQUIRE_ALIGN(row_slot, 4);
+    MX_REQUIRE_ALIGN(slot_row, 4);
+  }
+  const size_t need = mx_moe_sort_workspace_size(T, k, E);
+  if (need > 0) {
+    MX_REQUIRE_PTR(workspace);
+    MX_REQUIRE_ALIGN(workspace, 256);
+  }
+  if (ws_bytes < need) return fail(MX_ERR_WORKSPACE, "workspace %zu bytes < required %zu", ws_bytes, need);
+  const Span ids{"topk_ids", topk_ids, P * 4}, off{"expert_off", expert_off, ((int64_t)E + 1) * 4},
+      rs{"row_slot", row_slot, P * 4}, sr{"slot_row", slot_row, P * 4}, ws{"workspace", workspace, (int64_t)need};
+  MX_TRY(check_apart(off, {ids, rs, sr, ws}));
+  MX_TRY(check_apart(rs, {ids, sr, ws}));
+  MX_TRY(check_apart(sr, {ids, ws}));
+  MX_TRY(check_apart(ws, {ids}));
+  int32_t *counts = nullptr, *tiles = nullptr;
+  if (need > 0) {
+    Carve c(workspace);
+    counts = (int32_t*)c.take((size_t)((P + ROUTE_CHUNK - 1) / ROUTE_CHUNK * E * 4));
+    tiles = (int32_t*)c.take((size_t)(E + 1) * 4);
+  }
+  MX_HIP(phase("moe_sort", s, [&] { return launch_sort(topk_ids, P, E, expert_off, row_slot, slot_row, counts, tiles, s); }),
+         "moe_sort");
+  return ok();
+}
+
+mx_status mx_moe_permute(mx_dtype dt, const void* x, int64_t T, int64_t hidden, const int32_t* slot_row, int32_t k,
+                         int64_t rows, void* xs, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_rows(dt, T, k, rows, hidden));
+  if (T == 0 || rows == 0) return ok();
+  const int es = dt_bytes((DType)dt);
+  MX_REQUIRE_PTR(x);
+  MX_REQUIRE_PTR(slot_row);
+  MX_REQUIRE_PTR(xs);
+  MX_REQUIRE_ALIGN(x, es);
+  MX_REQUIRE_ALIGN(xs, es);
+  MX_REQUIRE_ALIGN(slot_row, 4);
+  MX_TRY(check_apart({"xs", xs, rows * hidden * es}, {{"x", x, T * hidden * es}, {"slot_row", slot_row, T * k * 4}}));
+  MX_HIP(phase("moe_permute", s, [&] { return launch_permute(x, es, T, k, (int)hidden, slot_row, rows, xs, s); }),
+         "moe_permute");
+  return ok();
+}
+
+mx_status mx_moe_unpermute(mx_dtype dt, const void* ys, int64_t rows, int64_t hidden, const int32_t* slot_row,
+                           const float* topk_w, int64_t T, int32_t k, void* y, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_rows(dt, T, k, rows, hidden));
+  if (T == 0) return ok();
+  const int es = dt_bytes((DType)dt);
+  if (rows > 0) MX_REQUIRE_PTR(ys);
+  MX_REQUIRE_PTR(slot_row);
+  MX_REQUIRE_PTR(y);
+  MX_REQUIRE_ALIGN(ys, es);
+  MX_REQUIRE_ALIGN(y, es);
+  MX_REQUIRE_ALIGN(slot_row, 4);
+  MX_REQUIRE_ALIGN(topk_w, 4);
+  MX_TRY(check_apart({"y", y, T * hidden * es}, {{"ys", ys, rows * hidden * es},
+                                                 {"slot_row", slot_row, T * k * 4},
+                                                 {"topk_w", topk_w, T * k * 4}}));
+  MX_HIP(phase("moe_unpermute", s,
+               [&] { return launch_unpermute(ys, (DType)dt, rows, slot_row, topk_w, T, k, (int)hidden, y, s); }),
+         "moe_unpermute");
+  return ok();
+}
+
+mx_status mx_moe_unpermute_grad(mx_dtype dt, const void* d_y, const void* ys, int64_t rows, int64_t hidden,
+                                const int32_t* slot_row, const float* topk_w, int64_t T, int32_t k, void* d_ys,
+                                float* d_w, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_rows(dt, T, k, rows, hidden));
+  if (T == 0) return ok();
+  const int es = dt_bytes((DType)dt);
+  MX_REQUIRE_PTR(d_y);
+  if (rows > 0) {
+    MX_REQUIRE_PTR(ys);
+    MX_REQUIRE_PTR(d_ys);
+  }
+  MX_REQUIRE_PTR(slot_row);
+  MX_REQUIRE_PTR(topk_w);
+  MX_REQUIRE_PTR(d_w);
+  MX_REQUIRE_ALIGN(d_y, es);
+  MX_REQUIRE_ALIGN(ys, es);
+  MX_REQUIRE_ALIGN(d_ys, es);
+  MX_REQUIRE_ALIGN(slot_row, 4);
+  MX_REQUIRE_ALIGN(topk_w, 4);
+  MX_REQUIRE_ALIGN(d_w, 4);
+  const Span dy{"d_y", d_y, T * hidden * es}, y{"ys", ys, rows * hidden * es}, sr{"slot_row", slot_row, T * k * 4},
+      w{"topk_w", topk_w, T * k * 4}, dys{"d_ys", d_ys, rows * hidden * es}, dw{"d_w", d_w, T * k * 4};
+  MX_TRY(check_apart(dys, {dy, y, sr, w, dw}));
+  MX_TRY(check_apart(dw, {dy, y, sr, w}));
+  MX_HIP(phase("moe_unpermute_grad", s,
+               [&] {
+                 return launch_unpermute_grad(d_y, ys, (DType)dt, rows, slot_row, topk_w, T, k, (int)hidden, d_ys, d_w,
+                                              s);
+               }),
+         "moe_unpermute_grad");
+  return ok();
+}
+
+namespace {
+
+mx_status check_norm(mx_dtype dt, mx_dtype res_dt, const void* y, const void* w_post, mx_gate kind, const void* gate,
+                     float res_scale, const void* w_pre, float eps, int64_t T, int64_t H) {
+  MX_TRY(check_dtype(dt));
+  if (res_dt != dt && res_dt != MX_DT_F32)
+    return fail(MX_ERR_FORMAT, "residual type %d is neither the activations' nor fp32", (int)res_dt);
+  if (kind < MX_GATE_NONE || kind > MX_GATE_FULL) return fail(MX_ERR_FORMAT, "unknown gate kind %d", (int)kind);
+  if (T < 0 || T > ((int64_t)1 << 30)) return fail(MX_ERR_SHAPE, "T %lld not in [0, 2^30]", (long long)T);
+  if (H < 1 || H > BLOCK_NORM_MAX_H) return fail(MX_ERR_SHAPE, "H %lld not in [1, %d]", (long long)H, BLOCK_NORM_MAX_H);
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(MX_ERR_VALUE, "eps %g must be finite and >= 0", (double)eps);
+  if (!std::isfinite(res_scale)) return fail(MX_ERR_VALUE, "res_scale %g must be finite", (double)res_scale);
+  if (kind == MX_GATE_NONE && gate != nullptr) return fail(MX_ERR_VALUE, "gate given with MX_GATE_NONE");
+  if (kind != MX_GATE_NONE && (T > 0 || kind == MX_GATE_CHANNEL)) MX_REQUIRE_PTR(gate);
+  if (T == 0) return MX_OK;
+  if (y == nullptr && (w_post != nullptr || kind != MX_GATE_NONE))
+    return fail(MX_ERR_VALUE, "w_post and gate need y");
+  if (y == nullptr && w_pre == nullptr) return fail(MX_ERR_NULL, "y and w_pre are both NULL: nothing to do");
+  return MX_OK;
+}
+
+int64_t gate_values(mx_gate kind, int64_t T, int64_t H) {
+  return kind == MX_GATE_CHANNEL ? H : kind == MX_GATE_TOKEN ? T : kind == MX_GATE_FULL ? T * H : 0;
+}
+
+}  // namespace
+
+mx_status mx_block_norm(mx_dtype dt, mx_dtype res_dt, const void* y, const void* residual, const void* w_post,
+                        mx_gate gate_kind, const void* gate, float res_scale, const void* w_pre, float eps, int64_t T,
+                        int64_t H, void* residual_out, void* normed, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_norm(dt, res_dt, y, w_post, gate_kind, gate, res_scale, w_pre, eps, T, H));
+  if (T == 0) return ok();
+  const int es = dt_bytes((DType)dt), rs = dt_bytes((DType)res_dt);
+  MX_REQUIRE_PTR(residual);
+  if (y != nullptr) MX_REQUIRE_PTR(residual_out);
+  else if (residual_out != nullptr) return fail(MX_ERR_VALUE, "residual_out given without y");
+  if (w_pre != nullptr) MX_REQUIRE_PTR(normed);
+  else if (normed != nullptr) return fail(MX_ERR_VALUE, "normed given without w_pre");
+  MX_REQUIRE_ALIGN(y, es);
+  MX_REQUIRE_ALIGN(w_post, es);
+  MX_REQUIRE_ALIGN(gate, es);
+  MX_REQUIRE_ALIGN(w_pre, es);
+  MX_REQUIRE_ALIGN(normed, es);
+  MX_REQUIRE_ALIGN(residual, rs);
+  MX_REQUIRE_ALIGN(residual_out, rs);
+  const Span sy{"y", y, T * H * es}, sr{"residual", residual, T * H * rs}, sp{"w_post", w_post, H * es},
+      sg{"gate", gate, gate_values(gate_kind, T, H) * es}, sw{"w_pre", w_pre, H * es},
+      so{"residual_out", residual_out, T * H * rs}, sn{"normed", normed, T * H * es};
+  MX_TRY(check_apart(so, {sy, sr, sp, sg, sw, sn}, {residual}));
+  MX_TRY(check_apart(sn, {sy, sr, sp, sg, sw}, {y}));
+  BlockNormArgs a;
+  a.dt = (DType)dt; a.rdt = (DType)res_dt;
+  a.T = T; a.H = (int)H;
+  a.y = y; a.residual = residual; a.w_post = w_post; a.gate = gate; a.w_pre = w_pre;
+  a.gate_kind = (GateKind)gate_kind;
+  a.res_scale = res_scale; a.eps = eps;
+  a.residual_out = residual_out; a.normed = normed;
+  const uintptr_t all = (uintptr_t)y | (uintptr_t)residual | (uintptr_t)w_post | (uintptr_t)w_pre |
+                        (uintptr_t)residual_out | (uintptr_t)normed |
+                        (gate_kind == MX_GATE_TOKEN ? (uintptr_t)0 : (uintptr_t)gate);
+  MX_HIP(phase("block_norm", s, [&] { return launch_block_norm(a, block_norm_vec((int)H, all), s); }), "block_norm");
+  return ok();
+}
+
+size_t mx_block_norm_grad_workspace_size(int64_t T, int64_t H) {
+  if (T < 0 || H < 1 || H > BLOCK_NORM_MAX_H || T > ((int64_t)1 << 30)) return 0;
+  Carve c(nullptr);
+  c.take((size_t)block_norm_grad_grid(T, (int)H) * 2 * (size_t)H * 4);
+  return c.off;
+}
+
+mx_status mx_block_norm_grad(mx_dtype dt, mx_dtype res_dt, const void* y, const void* residual_out, const void* w_post,
+                             mx_gate gate_kind, const void* gate, float res_scale, const void* w_pre, float eps,
+                             int64_t T, int64_t H, const void* d_normed, const void* d_residual_out, void* d_residual,
+                             void* d_y, void* d_gate, float* dw_post, float* dw_pre, void* workspace, size_t ws_bytes,
+                             void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_norm(dt, res_dt, y, w_post, gate_kind, gate, res_scale, w_pre, eps, T, H));
+  const int es = dt_bytes((DType)dt), rs = dt_bytes((DType)res_dt);
+  const int gs = gate_kind == MX_GATE_FULL ? es : 4;
+  if (w_pre != nullptr) MX_REQUIRE_PTR(dw_pre);
+  else if (dw_pre != nullptr) return fail(MX_ERR_VALUE, "dw_pre given without w_pre");
+  if (w_post != nullptr) MX_REQUIRE_PTR(dw_post);
+  else if (dw_post != nullptr) return fail(MX_ERR_VALUE, "dw_post given without w_post");
+  if (gate_kind == MX_GATE_NONE && d_gate != nullptr) return fail(MX_ERR_VALUE, "d_gate given with MX_GATE_NONE");
+  if (gate_kind != MX_GATE_NONE && (T > 0 || gate_kind == MX_GATE_CHANNEL)) MX_REQUIRE_PTR(d_gate);
+  if (T > 0) {
+    if (w_pre != nullptr) {
+      MX_REQUIRE_PTR(residual_out);
+      MX_REQUIRE_PTR(d_normed);
+    } else if (d_normed != nullptr) {
+      return fail(MX_ERR_VALUE, "d_normed given without w_pre");
+    }
+    if (w_pre == nullptr) MX_REQUIRE_PTR(d_residual_out);
+    MX_REQUIRE_PTR(d_residual);
+    if (y != nullptr) MX_REQUIRE_PTR(d_y);
+    else if (d_y != nullptr) return fail(MX_ERR_VALUE, "d_y given without y");
+    const size_t need = mx_block_norm_grad_workspace_size(T, H);
+    MX_REQUIRE_PTR(workspace);
+    MX_REQUIRE_ALIGN(workspace, 256);
+    if (ws_bytes < need) return fail(MX_ERR_WORKSPACE, "workspace %zu bytes < required %zu", ws_bytes, need);
+  }
+  MX_REQUIRE_ALIGN(y, es);
+  MX_REQUIRE_ALIGN(w_post, es);
+  MX_REQUIRE_ALIGN(gate, es);
+  MX_REQUIRE_ALIGN(w_pre, es);
+  MX_REQUIRE_ALIGN(d_normed, es);
+  MX_REQUIRE_ALIGN(d_y, es);
+  MX_REQUIRE_ALIGN(residual_out, rs);
+  MX_REQUIRE_ALIGN(d_residual_out, rs);
+  MX_REQUIRE_ALIGN(d_residual, rs);
+  MX_REQUIRE_ALIGN(d_gate, gs);
+  MX_REQUIRE_ALIGN(dw_post, 4);
+  MX_REQUIRE_ALIGN(dw_pre, 4);
+  const int64_t gv = gate_values(gate_kind, T, H);
+  const Span sy{"y", y, T * H * es}, sr{"residual_out", residual_out, T * H * rs}, sp{"w_post", w_post, H * es},
+      sg{"gate", gate, gv * es}, sw{"w_pre", w_pre, H * es}, sdn{"d_normed", d_normed, T * H * es},
+      sdo{"d_residual_out", d_residual_out, T * H * rs}, sdr{"d_residual", d_residual, T * H * rs},
+      sdy{"d_y", d_y, T * H * es}, sdg{"d_gate", d_gate, gv * gs}, sdp{"dw_post", dw_post, H * 4},
+      sdw{"dw_pre", dw_pre, H * 4}, sws{"workspace", workspace, T > 0 ? (int64_t)ws_bytes : 0};
+  MX_TRY(check_apart(sdr, {sy, sr, sp, sg, sw, sdn, sdo, sdy, sdg, sdp, sdw, sws}, {d_residual_out}));
+  MX_TRY(check_apart(sdy, {sy, sr, sp, sg, sw, sdn, sdo, sdg, sdp, sdw, sws}, {y, d_normed}));
+  MX_TRY(check_apart(sdg, {sy, sr, sp, sg, sw, sdn, sdo, sdp, sdw, sws}));
+  MX_TRY(check_apart(sdp, {sy, sr, sp, sg, sw, sdn, sdo, sdw, sws}));
+  MX_TRY(check_apart(sdw, {sy, sr, sp, sg, sw, sdn, sdo, sws}));
+  MX_TRY(check_apart(sws, {sy, sr, sp, sg, sw, sdn, sdo}));
+  BlockNormGradArgs a;
+  a.dt = (DType)dt; a.rdt = (DType)res_dt;
+  a.T = T; a.H = (int)H;
+  a.y = y; a.residual_out = residual_out; a.w_post = w_post; a.gate = gate; a.w_pre = w_pre;
+  a.gate_kind = (GateKind)gate_kind;
+  a.res_scale = res_scale; a.eps = eps;
+  a.d_normed = d_normed; a.d_residual_out = d_residual_out;
+  a.d_residual = d_residual; a.dy = d_y; a.dgate = d_gate;
+  a.dw_pre = dw_pre; a.dw_post = dw_post;
+  a.part = (float*)workspace;
+  const uintptr_t all = (uintptr_t)y | (uintptr_t)residual_out | (uintptr_t)w_post | (uintptr_t)w_pre |
+                        (uintptr_t)d_normed | (uintptr_t)d_residual_out | (uintptr_t)d_residual | (uintptr_t)d_y |
+                        (gate_kind == MX_GATE_TOKEN ? (uintptr_t)0 : (uintptr_t)gate) |
+                        (gate_kind == MX_GATE_FULL ? (uintptr_t)d_gate : (uintptr_t)0);
+  MX_HIP(phase("block_norm_grad", s, [&] { return launch_block_norm_grad(a, block_norm_vec((int)H, all), s); }),
+         "block_norm_grad");
+  return ok();
+}
+
+size_t mx_lora_add_workspace_size(int64_t M, int64_t K, int64_t R, int32_t n) {
+  if (M < 0 || K < 8 || R < 8 || n < 1 || M > (1 << 24) || K > (1 << 20) || R > LORA_MAX_RANK || n > ROUTE_MAX_EXPERTS)
+    return 0;
+  Carve c(nullptr);
+  c.take((size_t)lora_splits(M, K, (int)R, n) * (size_t)M * (size_t)R * 4);
+  return c.off;
+}
+
+mx_status mx_lora_add(mx_dtype dt, const void* x, int64_t ldx, int64_t M, int64_t K, const void* a, const void* b,
+                      const float* scale, int32_t n, int64_t R, const int32_t* adapter_off, const int32_t* row_token,
+                      void* y, int64_t ldy, int64_t N, void* workspace, size_t ws_bytes, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_dtype(dt));
+  if (dt == MX_DT_F32) return fail(MX_ERR_FORMAT, "lora_add takes bf16 or fp16, not fp32");
+  if (M < 0 || M > (1 << 24)) return fail(MX_ERR_SHAPE, "M %lld not in [0, 2^24]", (long long)M);
+  if (K < 8 || K % 8 != 0 || K > (1 << 20)) return fail(MX_ERR_SHAPE, "K %lld must be a multiple of 8 in [8, 2^20]", (long long)K);
+  if (N < 8 || N % 8 != 0 || N > (1 << 20)) return fail(MX_ERR_SHAPE, "N %lld must be a multiple of 8 in [8, 2^20]", (long long)N);
+  if (R < 8 || R % 8 != 0 || R > LORA_MAX_RANK)
+    return fail(MX_ERR_SHAPE, "rank %lld must be a multiple of 8 in [8, %d]", (long long)R, LORA_MAX_RANK);
+  if (n < 1 || n > ROUTE_MAX_EXPERTS) return fail(MX_ERR_SHAPE, "%d adapters not in [1, %d]", n, ROUTE_MAX_EXPERTS);
+  if (ldx < K || ldx % 8 != 0 || ldx > ((int64_t)1 << 30))
+    return fail(MX_ERR_SHAPE, "ldx %lld must be a multiple of 8 of at least K", (long long)ldx);
+  if (ldy < N || ldy % 8 != 0 || ldy > ((int64_t)1 << 30))
+    return fail(MX_ERR_SHAPE, "ldy %lld must be a multiple of 8 of at least N", (long long)ldy);
+  if (M == 0) return ok();
+  MX_REQUIRE_PTR(x);
+  MX_REQUIRE_PTR(a);
+  MX_REQUIRE_PTR(b);
+  MX_REQUIRE_PTR(adapter_off);
+  MX_REQUIRE_PTR(row_token);
+  MX_REQUIRE_PTR(y);
+  MX_REQUIRE_ALIGN(x, 16);
+  MX_REQUIRE_ALIGN(a, 16);
+  MX_REQUIRE_ALIGN(b, 16);
+  MX_REQUIRE_ALIGN(y, 16);
+  MX_REQUIRE_ALIGN(scale, 4);
+  MX_REQUIRE_ALIGN(adapter_off, 4);
+  MX_REQUIRE_ALIGN(row_token, 4);
+  MX_REQUIRE_PTR(workspace);
+  MX_REQUIRE_ALIGN(workspace, 256);
+  const size_t need = mx_lora_add_workspace_size(M, K, R, n);
+  if (ws_bytes < need) return fail(MX_ERR_WORKSPACE, "workspace %zu bytes < required %zu", ws_bytes, need);
+  // x and y may be interleaved column ranges of one matrix: only equal or
+  // row-overlapping ranges are refused
+  const Span sa{"a", a, n * R * K * 2}, sb{"b", b, n * R * N * 2}, sc{"scale", scale, (int64_t)n * 4},
+      so{"adapter_off", adapter_off, ((int64_t)n + 1) * 4}, st{"row_token", row_token, M * 4},
+      sx{"x", x, ((M - 1) * ldx + K) * 2}, sy{"y", y, ((M - 1) * ldy + N) * 2}, sw{"workspace", workspace, (int64_t)need};
+  MX_TRY(check_apart(sw, {sa, sb, sc, so, st, sx, sy}));
+  MX_TRY(check_apart(sy, {sa, sb, sc, so, st}));
+  if (overlaps(sx, sy)) {
+    const int64_t d = ((const char*)y - (const char*)x) / 2;
+    const int64_t col = ldx == ldy ? ((d % ldx) + ldx) % ldx : 0;
+    if (ldx != ldy || ((const char*)y - (const char*)x) % 2 != 0 || col < K || col + N > ldx)
+      return fail(MX_ERR_VALUE, "y overlaps x");
+  }
+  LoraArgs p;
+  p.dt = (DType)dt;
+  p.x = x; p.ldx = ldx; p.M = (int)M; p.K = (int)K; p.N = (int)N; p.R = (int)R; p.n = n;
+  p.a = a; p.b = b; p.scale = scale;
+  p.adapter_off = adapter_off; p.row_token = row_token;
+  p.y = y; p.ldy = ldy;
+  p.part = (float*)workspace;
+  p.splits = lora_splits(M, K, (int)R, n);
+  MX_HIP(phase("lora_shrink", s, [&] { return launch_lora_shrink(p, s); }), "lora_shrink");
+  MX_HIP(phase("lora_expand", s, [&] { return launch_lora_expand(p, s); }), "lora_expand");
+  return ok();
+}
+
+}  // extern "C"

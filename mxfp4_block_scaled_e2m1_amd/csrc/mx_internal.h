@@ -237,6 +237,91 @@ bool fp8_linear_fits(int64_t K);
 // h = bf16(silu(g) * u) elementwise over n values (n % 8 == 0, 16-byte aligned).
 hipError_t launch_silu_mul_bf16(const uint16_t* g, const uint16_t* u, int64_t n, uint16_t* h, hipStream_t s);
 
+// ---- Activation types of the operators around the experts ------------------
+// (mx_dtype of the C ABI)
+enum DType : int { DT_BF16 = 0, DT_F16 = 1, DT_F32 = 2 };
+inline int dt_bytes(DType dt) { return dt == DT_F32 ? 4 : 2; }
+template <int D> struct DtC { static constexpr int value = D; };
+template <class F>
+void dispatch_dt(DType dt, F&& f) {
+  if (dt == DT_BF16) f(DtC<DT_BF16>());
+  else if (dt == DT_F16) f(DtC<DT_F16>());
+  else f(DtC<DT_F32>());
+}
+
+// ---- Sort by expert as a plan (route.hip) -----------------------------------
+// expert_off [E+1], row_slot [P] (-1 past the last routed pair), slot_row [P]
+// (-1: id outside [0, E)). tile_base [E+1] and block_counts [chunks, E] are
+// scratch, not used when sort_in_one_block().
+constexpr int64_t SORT_ONE_BLOCK = 4096;
+// One workgroup sorts all pairs: its counts, one per expert and 64 pairs, fit LDS.
+inline bool sort_in_one_block(int64_t P, int n_experts) {
+  return P <= SORT_ONE_BLOCK && (P + 63) / 64 * n_experts * 4 <= 60 * 1024;
+}
+hipError_t launch_sort(const int32_t* ids, int64_t P, int n_experts, int32_t* expert_off, int32_t* row_slot,
+                       int32_t* slot_row, int32_t* block_counts, int32_t* tile_base, hipStream_t s);
+
+// ---- Rows to the experts and back (moe_rows.hip) -----------------------------
+// rows: row capacity of xs / ys; slots whose row is outside [0, rows) are skipped.
+hipError_t launch_permute(const void* x, int esize, int64_t T, int k, int H, const int32_t* slot_row, int64_t rows,
+                          void* xs, hipStream_t s);
+hipError_t launch_unpermute(const void* ys, DType dt, int64_t rows, const int32_t* slot_row, const float* w,
+                            int64_t T, int k, int H, void* y, hipStream_t s);
+hipError_t launch_unpermute_grad(const void* dy, const void* ys, DType dt, int64_t rows, const int32_t* slot_row,
+                                 const float* w, int64_t T, int k, int H, void* dys, float* dw, hipStream_t s);
+
+// ---- Norms around a block (block_norm.hip) ------------------------------------
+// mx_gate of the C ABI: what one gate value covers.
+enum GateKind : int { GATE_NONE = 0, GATE_CHANNEL = 1, GATE_TOKEN = 2, GATE_FULL = 3 };
+constexpr int BLOCK_NORM_MAX_H = 16384;
+struct BlockNormArgs {
+  DType dt, rdt;               // y, gate, weights, normed; residual and residual_out
+  int64_t T;
+  int H;
+  const void *y, *residual, *w_post, *gate, *w_pre;   // y, w_post, gate, w_pre may be null
+  GateKind gate_kind;
+  float res_scale, eps;
+  void *residual_out, *normed; // written with y / with w_pre
+};
+struct BlockNormGradArgs {
+  DType dt, rdt;
+  int64_t T;
+  int H;
+  const void *y, *residual_out, *w_post, *gate, *w_pre;
+  GateKind gate_kind;
+  float res_scale, eps;
+  const void *d_normed, *d_residual_out;              // with w_pre; may be null
+  void *d_residual, *dy, *dgate;
+  float *dw_pre, *dw_post;
+  float* part;                 // [block_norm_grad_grid][2][H]
+};
+// Whether rows can be taken eight elements at a time: all_pointers is the
+// bitwise or of every row and weight pointer in use.
+bool block_norm_vec(int H, uintptr_t all_pointers);
+int block_norm_grad_grid(int64_t T, int H);
+hipError_t launch_block_norm(const BlockNormArgs& a, bool vec, hipStream_t s);
+hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, bool vec, hipStream_t s);
+
+// ---- Low-rank adapters (lora.hip) -----------------------------------------------
+constexpr int LORA_MAX_RANK = 128;
+struct LoraArgs {
+  DType dt;                     // DT_BF16 or DT_F16
+  const void* x;                // [M, K], rows ldx elements apart
+  int64_t ldx;
+  int M, K, N, R, n;            // n adapters
+  const void *a, *b;            // [n, R, K], [n, N, R]
+  const float* scale;           // [n] or null (1)
+  const int32_t* adapter_off;   // [n+1] first sorted row of each adapter
+  const int32_t* row_token;     // [M] token of each sorted row
+  void* y;                      // [M, N], rows ldy elements apart
+  int64_t ldy;
+  float* part;                  // [splits][M][R]
+  int splits;
+};
+int lora_splits(int64_t M, int64_t K, int R, int n);
+hipError_t launch_lora_shrink(const LoraArgs& p, hipStream_t s);
+hipError_t launch_lora_expand(const LoraArgs& p, hipStream_t s);
+
 // Measurement probes (probe.hip). mode 0: reads into registers, 1: into LDS;
 // loads_per_wave 8 or 32; bytes a multiple of loads_per_wave KiB; out holds
 // workgroups * 4 words. operands: 512 x 16 words; out: workgroups * 512 floats.

@@ -13,6 +13,8 @@
 //      and the expert offsets and m-tile bases,
 //   3. scatter: every pair's place is its chunk's base plus its rank in the chunk.
 // Ids outside [0, E) belong to experts on other ranks and are skipped.
+#include <algorithm>
+
 #include "mx_device.h"
 #include "mx_internal.h"
 
@@ -177,6 +179,128 @@ __global__ __launch_bounds__(ROUTE_CHUNK) void k_route_scatter(
   }
 }
 
+// The 64 lanes whose valid id equals this lane's: one ballot per id bit, so the
+// cost does not grow with the number of distinct ids in the wave.
+__device__ __forceinline__ uint64_t same_id(int e, bool valid, int bits) {
+  uint64_t m = __ballot(valid);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (e >> b) & 1;
+    const uint64_t v = __ballot(one);
+    m &= one ? v : ~v;
+  }
+  return m;
+}
+
+// The scatter of the sort as a plan: places as in k_route_scatter, written as
+// the two inverse maps, -1 where there is no row or no slot.
+__global__ __launch_bounds__(ROUTE_CHUNK) void k_sort_scatter(const int32_t* __restrict__ ids, int64_t P, int E,
+                                                              int bits, const int32_t* __restrict__ chunk_base,
+                                                              const int32_t* __restrict__ expert_off,
+                                                              int32_t* __restrict__ row_slot,
+                                                              int32_t* __restrict__ slot_row) {
+  extern __shared__ int wc[];   // [NW][E] pairs per expert in each wave of this chunk
+  constexpr int NW = ROUTE_CHUNK / 64;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int64_t b = blockIdx.x;
+  for (int i = tid; i < NW * E; i += ROUTE_CHUNK) wc[i] = 0;
+  __syncthreads();
+  const int64_t p = b * ROUTE_CHUNK + tid;
+  const int e = (p < P) ? ids[p] : -1;
+  const bool valid = (unsigned)e < (unsigned)E;
+  const uint64_t m = same_id(e, valid, bits);
+  const int rank = __popcll(m & ((1ull << lane) - 1));
+  if (valid && rank == 0) wc[w * E + e] = __popcll(m);
+  __syncthreads();
+  int pos = -1;
+  if (valid) {
+    pos = expert_off[e] + chunk_base[b * E + e] + rank;
+    for (int x = 0; x < w; ++x) pos += wc[x * E + e];
+    row_slot[pos] = (int)p;
+  }
+  if (p < P) {
+    slot_row[p] = pos;
+    if (p >= expert_off[E]) row_slot[p] = -1;   // rows behind the last routed pair: written by no slot
+  }
+}
+
+// The whole sort in one workgroup, for few pairs: every wave counts its pairs
+// of each chunk, the counts are scanned expert by expert in (chunk, wave) order,
+// and the places follow. wc [chunks * NW][E]: LDS counts, then exclusive bases.
+__global__ __launch_bounds__(ROUTE_CHUNK) void k_sort_one(const int32_t* __restrict__ ids, int P, int E, int bits,
+                                                          int32_t* __restrict__ expert_off,
+                                                          int32_t* __restrict__ row_slot,
+                                                          int32_t* __restrict__ slot_row) {
+  constexpr int NW = ROUTE_CHUNK / 64;
+  constexpr int CH = (int)(SORT_ONE_BLOCK / ROUTE_CHUNK);
+  __shared__ int tot[ROUTE_MAX_EXPERTS];   // pairs per expert, then first rows
+  __shared__ int all;
+  extern __shared__ int wc[];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int parts = (P + 63) / 64;         // waves of pairs: part q holds pairs [64 q, 64 q + 64)
+  for (int i = tid; i < parts * E; i += blockDim.x) wc[i] = 0;
+  int id[CH], rank[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int p = c * ROUTE_CHUNK + tid;
+    id[c] = p < P ? ids[p] : -1;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    if (c * ROUTE_CHUNK >= P) break;
+    const bool valid = (unsigned)id[c] < (unsigned)E;
+    const uint64_t m = same_id(id[c], valid, bits);
+    rank[c] = __popcll(m & ((1ull << lane) - 1));
+    if (valid && rank[c] == 0) wc[(c * NW + w) * E + id[c]] = __popcll(m);
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += blockDim.x) {
+    int acc = 0;
+    for (int q = 0; q < parts; ++q) {
+      const int v = wc[q * E + e];
+      wc[q * E + e] = acc;
+      acc += v;
+    }
+    tot[e] = acc;
+  }
+  __syncthreads();
+  if (tid < 64) {   // lane l scans experts [l * per, (l + 1) * per)
+    const int per = (E + 63) / 64;
+    const int x0 = min(tid * per, E), x1 = min(x0 + per, E);
+    int ps = 0;
+    for (int x = x0; x < x1; ++x) ps += tot[x];
+    int pi = ps;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int pu = __shfl_up(pi, d);
+      if (tid >= d) pi += pu;
+    }
+    int o = pi - ps;
+    for (int x = x0; x < x1; ++x) {
+      const int n = tot[x];
+      tot[x] = o;
+      expert_off[x] = o;
+      o += n;
+    }
+    if (tid == 63) {
+      expert_off[E] = pi;
+      all = pi;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int p = c * ROUTE_CHUNK + tid;
+    if (p >= P) break;
+    int pos = -1;
+    if ((unsigned)id[c] < (unsigned)E) {
+      pos = tot[id[c]] + wc[(c * NW + w) * E + id[c]] + rank[c];
+      row_slot[pos] = p;
+    }
+    slot_row[p] = pos;
+    if (p >= all) row_slot[p] = -1;
+  }
+}
+
 constexpr int COMBINE_BATCH = 8;   // slots whose rows are loaded together
 
 // Sorted row r of the routed pairs gets token row_token[r] of a row-major
@@ -253,6 +377,26 @@ hipError_t launch_route(const int32_t* topk_ids, const float* topk_w, int64_t to
   const size_t lds = (size_t)(ROUTE_CHUNK / 64) * n_experts * sizeof(int);
   k_route_scatter<<<nblocks, ROUTE_CHUNK, lds, s>>>(topk_ids, topk_w, P, k, n_experts, rb.block_counts,
                                                     rb.expert_off, rb.row_token, rb.row_slot, rb.row_weight);
+  return hipGetLastError();
+}
+
+hipError_t launch_sort(const int32_t* ids, int64_t P, int n_experts, int32_t* expert_off, int32_t* row_slot,
+                       int32_t* slot_row, int32_t* block_counts, int32_t* tile_base, hipStream_t s) {
+  int bits = 0;
+  while ((1 << bits) < n_experts) ++bits;
+  const int64_t parts = (P + 63) / 64;
+  if (sort_in_one_block(P, n_experts)) {
+    const int threads = P >= ROUTE_CHUNK ? ROUTE_CHUNK : std::max(64, (int)parts * 64);
+    k_sort_one<<<1, threads, (size_t)(parts * n_experts) * sizeof(int), s>>>(ids, (int)P, n_experts, bits, expert_off,
+                                                                            row_slot, slot_row);
+    return hipGetLastError();
+  }
+  const int nblocks = (int)((P + ROUTE_CHUNK - 1) / ROUTE_CHUNK);
+  k_route_count<<<nblocks, 256, 0, s>>>(ids, P, n_experts, block_counts);
+  k_route_scan<<<1, ROUTE_SCAN_THREADS, 0, s>>>(block_counts, nblocks, n_experts, expert_off, tile_base);
+  const size_t lds = (size_t)(ROUTE_CHUNK / 64) * n_experts * sizeof(int);
+  k_sort_scatter<<<nblocks, ROUTE_CHUNK, lds, s>>>(ids, P, n_experts, bits, block_counts, expert_off, row_slot,
+                                                   slot_row);
   return hipGetLastError();
 }
 

@@ -1,0 +1,139 @@
+"""mx_lora_add against the fp64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+from around_util import U, f64, half_step, pair, rounded, within
+from oracle import around
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mx():
+    import mxfp4_block_scaled_e2m1_amd as m
+    return m
+
+
+def _plan(mx, adapter, n):
+    off, row_token, _ = mx.moe_sort(torch.from_numpy(adapter.astype(np.int32).reshape(-1, 1)).cuda(), n)
+    return off, row_token
+
+
+def _bound(y, x, a, b, adapter, scale, name):
+    """v = A x: K products and additions in fp32; its two 16-bit halves keep 2^-17 of it (2^-21 in fp16, where
+    the halves of the row's smallest values may be subnormal: 2^-23 of the row's largest). Then 2 R more."""
+    tol = np.zeros_like(y)
+    K, R = a.shape[2], a.shape[1]
+    keep = 2.0 ** -17 if name == "bf16" else 2.0 ** -21
+    for t, i in enumerate(adapter):
+        if 0 <= i < a.shape[0]:
+            s = 1.0 if scale is None else abs(scale[i])
+            v = np.abs(a[i] @ x[t])
+            ev = (K + 8) * U * (np.abs(a[i]) @ np.abs(x[t]))
+            ev = ev + keep * (v + ev) + (2.0 ** -23 * (v + ev).max() if name == "fp16" else 0.0)
+            tol[t] = s * (np.abs(b[i]) @ (ev + (2 * R + 8) * U * v)) + 4 * U * np.abs(y[t])
+    return tol
+
+
+def _case(mx, M, K, N, R, n, adapter, name, seed, scaled=True, keep_scale=1.0):
+    rng = np.random.default_rng(seed)
+    x, x64 = pair(rng.standard_normal((M, K)), name)
+    y, y64 = pair(rng.standard_normal((M, N)), name)
+    a, a64 = pair(rng.standard_normal((n, R, K)) * K ** -0.5, name)
+    b, b64 = pair(rng.standard_normal((n, N, R)) * R ** -0.5, name)
+    s, s64 = pair(rng.uniform(-2, 2, n), "fp32") if scaled else (None, None)
+    got = mx.lora_add(y, x, a, b, *_plan(mx, adapter, n), scale=s)
+    assert got is y
+    ref = around.lora_add(y64, x64, a64, b64, adapter, s64)
+    tol = _bound(y64, x64, a64, b64, adapter, s64, name)
+    within(got, ref, 1.01 * (tol * (1 + half_step(name)) + rounded(ref, name)))
+    bare = (adapter < 0) | (adapter >= n)
+    assert np.array_equal(f64(got)[bare], y64[bare])
+
+
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,K,N,R,n", [(1, 8, 8, 8, 1), (1, 256, 128, 64, 4), (3, 40, 72, 24, 2), (16, 128, 64, 16, 16),
+                                       (17, 136, 200, 32, 3), (33, 512, 264, 128, 5), (64, 264, 128, 40, 64),
+                                       (130, 104, 520, 72, 2), (200, 256, 136, 8, 1), (257, 64, 64, 96, 7)])
+def test_lora(mx, M, K, N, R, n, name):
+    rng = np.random.default_rng(M)
+    _case(mx, M, K, N, R, n, rng.integers(-1, n + 1, size=M), name, M + K)
+
+
+def test_without_scale_and_without_tokens(mx):
+    _case(mx, 20, 64, 64, 16, 3, np.arange(20) % 4, "bf16", 1, scaled=False)
+    _case(mx, 20, 64, 64, 16, 3, np.full(20, -1), "bf16", 2)            # no token has an adapter
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    a = torch.empty((2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    y = mx.lora_add(x.clone(), x, a, torch.empty((2, 64, 8), dtype=torch.bfloat16, device="cuda"),
+                    *_plan(mx, np.empty(0), 2))
+    assert y.shape == (0, 64)
+
+
+@pytest.mark.parametrize("M,K,N,R,n", [(1, 7168, 1536, 64, 4), (64, 7168, 7168, 16, 32), (700, 7168, 1536, 128, 3),
+                                       (300, 1536, 7168, 40, 100), (2100, 520, 1000, 24, 6)])
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+def test_whole_numbers_come_out_exactly(mx, M, K, N, R, n, name):
+    """Small whole numbers keep every sum exact in fp32 and every v exact in its halves, so that the output is
+    the exact sum, rounded once; real sizes, many requests."""
+    rng = np.random.default_rng(R)
+    x, x64 = pair(rng.integers(-2, 3, size=(M, K)), name)
+    y, y64 = pair(rng.integers(-8, 9, size=(M, N)), name)
+    a, a64 = pair(rng.integers(-1, 2, size=(n, R, K)), name)
+    b, b64 = pair(rng.integers(-1, 2, size=(n, N, R)) * 0.5, name)
+    s, s64 = pair(2.0 ** rng.integers(-3, 1, size=n), "fp32")
+    adapter = np.sort(rng.integers(-1, n, size=M))
+    rng.shuffle(adapter[:M // 2])
+    mx.lora_add(y, x, a, b, *_plan(mx, adapter, n), scale=s)
+    ref = y64.copy()
+    for i in range(n):
+        t = np.nonzero(adapter == i)[0]
+        ref[t] += s64[i] * ((x64[t] @ a64[i].T) @ b64[i].T)
+    expect = torch.from_numpy(ref).to(y.dtype)
+    assert torch.equal(y.cpu(), expect)
+
+
+def test_column_ranges_of_wider_matrices(mx):
+    """x a slice of columns; y one half of a stacked gate-and-up output, also inside the matrix that holds x."""
+    rng = np.random.default_rng(9)
+    M, K, N, R, n = 37, 72, 96, 16, 3
+    adapter = rng.integers(-1, n, size=M)
+    a, a64 = pair(rng.integers(-1, 2, size=(n, R, K)), "bf16")
+    b, b64 = pair(rng.integers(-1, 2, size=(n, N, R)), "bf16")
+    wide, w64 = pair(rng.integers(-2, 3, size=(M, K + 2 * N + 16)), "bf16")
+    x, y = wide[:, 8:8 + K], wide[:, K + 8 + N:K + 8 + 2 * N]
+    ref = w64.copy()
+    ref[:, K + 8 + N:K + 8 + 2 * N] = around.lora_add(w64[:, K + 8 + N:K + 8 + 2 * N], w64[:, 8:8 + K], a64, b64, adapter)
+    mx.lora_add(y, x, a, b, *_plan(mx, adapter, n))
+    assert torch.equal(wide.cpu(), torch.from_numpy(ref).to(torch.bfloat16))
+    with pytest.raises(mx.MxError, match="overlaps x"):
+        mx.lora_add(wide[:, 16:16 + N], x, a, b, *_plan(mx, adapter, n))
+
+
+@pytest.mark.parametrize("name,big", [("bf16", 1e30), ("fp16", 60000.0)])
+def test_large_and_non_finite_values_stay_in_their_rows(mx, name, big):
+    """v beyond fp16's range, and NaN and infinities of one token, leave the other tokens alone."""
+    rng = np.random.default_rng(2)
+    M, K, N, R, n = 24, 64, 64, 16, 2
+    adapter = np.arange(M) % n
+    xv = rng.integers(-2, 3, size=(M, K)).astype(np.float64)
+    xv[5] = big
+    x, x64 = pair(xv, name)
+    xn = x.clone()
+    xn[6, 3], xn[7, 9] = float("nan"), float("inf")
+    # |A| <= 2^-14: the product of a large x with it stays in range of y
+    a, a64 = pair(rng.integers(0, 2, size=(n, R, K)), name)
+    b, b64 = pair(rng.integers(0, 2, size=(n, N, R)) * 2.0 ** -14, name)
+    y0, y64 = pair(np.zeros((M, N)), name)
+    plan = _plan(mx, adapter, n)
+    clean = mx.lora_add(y0.clone(), x, a, b, *plan)
+    dirty = mx.lora_add(y0.clone(), xn, a, b, *plan)
+    ref = around.lora_add(y64, x64, a64, b64, adapter)
+    tol = _bound(y64, x64, a64, b64, adapter, None, name)
+    within(clean, ref, 1.01 * (tol * (1 + half_step(name)) + rounded(ref, name)))
+    others = [t for t in range(M) if t not in (6, 7)]
+    assert torch.equal(clean[others], dirty[others])
+    assert not torch.isfinite(dirty[6]).all() and not torch.isfinite(dirty[7]).all()
+    assert torch.isnan(dirty[6][b[0].sum(1) > 0]).any()
