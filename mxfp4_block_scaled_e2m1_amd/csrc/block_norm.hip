@@ -25,115 +25,122 @@ namespace mx {
 
 namespace {
 
-// Element c of the row held by thread tid, piece v: (v * threads + tid) * N.
-template <int DT, int RDT, int N, int V>
+// A workgroup's waves share a row; element c of it held by thread tid, piece v:
+// (v * threads + tid) * N. GATE: the gate kind.
+template <int DT, int RDT, int N, int V, int GATE>
 __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a) {
   __shared__ float red[2 * 16];
-  const int threads = blockDim.x, waves = threads >> 6, tid = threadIdx.x;
+  const int threads = blockDim.x, waves = threads >> 6, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int H = a.H;
   const float inv_h = 1.0f / (float)H;
+  const bool has_y = a.y != nullptr, has_post = a.w_post != nullptr, has_pre = a.w_pre != nullptr;
   Raw<DT, N> wpost[V], wpre[V], gch[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = (v * threads + tid) * N;
     wpost[v].zero(); wpre[v].zero(); gch[v].zero();
     if (c < H) {
-      if (a.w_post) wpost[v].load(a.w_post, c);
-      if (a.w_pre) wpre[v].load(a.w_pre, c);
-      if (a.gate_kind == GATE_CHANNEL) gch[v].load(a.gate, c);
+      if (has_post) wpost[v].load(a.w_post, c);
+      else wpost[v].fill(1.0f);
+      if (has_pre) wpre[v].load(a.w_pre, c);
+      if (GATE == GATE_CHANNEL) gch[v].load(a.gate, c);
     }
   }
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     const int64_t base = t * H;
-    Raw<DT, N> yr[V], gr[V];
-    Raw<RDT, N> rr[V];
+    Raw<DT, N> y[V], g[V];
+    Raw<RDT, N> res[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (v * threads + tid) * N;
-      yr[v].zero(); rr[v].zero(); gr[v].zero();
+      y[v].zero(); res[v].zero(); g[v].zero();
       if (c < H) {
-        if (a.y) yr[v].load(a.y, base + c);
-        rr[v].load(a.residual, base + c);
-        if (a.gate_kind == GATE_FULL) gr[v].load(a.gate, base + c);
+        if (has_y) y[v].load(at<DT>(a.y, base), c);
+        res[v].load(at<RDT>(a.residual, base), c);
+        if (GATE == GATE_FULL) g[v].load(at<DT>(a.gate, base), c);
+      }
+      if (dt_size<DT> == 2) {
+        wpre[v].pin(); wpost[v].pin();
+        if (GATE == GATE_CHANNEL) gch[v].pin();
       }
     }
-    float r[V][N];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int i = 0; i < N; ++i) r[v][i] = rr[v].get(i);
-    if (a.y) {
-      float f = a.res_scale;
-      if (a.gate_kind == GATE_TOKEN) {
-        Raw<DT, 1> g;
-        g.load(a.gate, t);
-        f *= g.get(0);
-      }
-      if (a.w_post) {
-        float ss[1] = {0.0f};
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-          for (int i = 0; i < N; ++i) ss[0] = fmaf(yr[v].get(i), yr[v].get(i), ss[0]);
-        group_sum<1>(ss, red, waves);
-        f *= rsqrtf(ss[0] * inv_h + a.eps);
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          float u = yr[v].get(i) * f;
-          if (a.w_post) u *= wpost[v].get(i);
-          if (a.gate_kind == GATE_CHANNEL) u *= gch[v].get(i);
-          if (a.gate_kind == GATE_FULL) u *= gr[v].get(i);
-          r[v][i] += u;
-        }
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = (v * threads + tid) * N;
-        if (c < H) {
-          Raw<RDT, N> o;
-          o.set(r[v]);
-          o.store(a.residual_out, base + c);
-        }
-      }
+    float f = a.res_scale;
+    if (GATE == GATE_TOKEN) {
+      Raw<DT, 1> gt;
+      gt.load(at<DT>(a.gate, t), 0);
+      f *= gt.get(0);
     }
-    if (a.w_pre) {
+    if (has_post) {
       float ss[1] = {0.0f};
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int i = 0; i < N; ++i) ss[0] = fmaf(r[v][i], r[v][i], ss[0]);
-      group_sum<1>(ss, red + 16, waves);
-      const float f = rsqrtf(ss[0] * inv_h + a.eps);
+        for (int i = 0; i < N; ++i) ss[0] = fmaf(y[v].get(i), y[v].get(i), ss[0]);
+      group_sum<1>(ss, red, waves, lane, wave);
+      f *= rsqrtf(ss[0] * inv_h + a.eps);
+    }
+    float r[V][N], ss[1] = {0.0f};
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * threads + tid) * N;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        r[v][i] = res[v].get(i);
+        if (has_y) {
+          float u = y[v].get(i) * f * wpost[v].get(i);
+          if (GATE == GATE_CHANNEL) u *= gch[v].get(i);
+          if (GATE == GATE_FULL) u *= g[v].get(i);
+          r[v][i] += u;
+        }
+        ss[0] = fmaf(r[v][i], r[v][i], ss[0]);
+      }
+      if (has_y && c < H) {
+        Raw<RDT, N> o;
+        o.set(r[v]);
+        o.store(at<RDT>(a.residual_out, base), c);
+      }
+    }
+    if (has_pre) {
+      group_sum<1>(ss, red + 16, waves, lane, wave);
+      const float fn = rsqrtf(ss[0] * inv_h + a.eps);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = (v * threads + tid) * N;
         if (c < H) {
           float n[N];
 #pragma unroll
-          for (int i = 0; i < N; ++i) n[i] = r[v][i] * f * wpre[v].get(i);
+          for (int i = 0; i < N; ++i) n[i] = r[v][i] * fn * wpre[v].get(i);
           Raw<DT, N> o;
           o.set(n);
-          o.store(a.normed, base + c);
+          o.store(at<DT>(a.normed, base), c);
         }
       }
     }
     // the two sums of a row use the two halves of red, and a barrier of one
     // keeps the other's next use apart; with a single sum per row it takes one
-    if (!(a.y && a.w_post && a.w_pre)) __syncthreads();
+    if (!(has_post && has_pre)) __syncthreads();
   }
 }
 
-// A workgroup strides over rows and keeps the column sums of its rows in
-// registers: part [grid][2][H] fp32 (w_pre's, then the shared sum of w_post and
-// a channel gate, see k_block_norm_cols).
-template <int DT, int RDT, int N, int V>
-__global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a) {
-  __shared__ float red[4 * 16];
-  const int threads = blockDim.x, waves = threads >> 6, tid = threadIdx.x;
+// The rows of a group of `gw` waves, one at a time; a workgroup holds `groups`
+// such groups, which take rows side by side, and strides over the rows. Each
+// thread keeps the column sums of its columns in registers; at the end the
+// groups' sums are joined in LDS and the workgroup writes part [2][H] fp32
+// (w_pre's, then the shared sum of w_post and a channel gate, see
+// k_block_norm_cols). GATE: the gate kind. PF: the next row's pieces are loaded
+// before this row's sums are waited for, since one workgroup fills a CU and its
+// two row sums would otherwise leave HBM idle.
+template <int DT, int RDT, int N, int V, int GATE, bool PF>
+__global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a, int gw) {
+  __shared__ float red_all[16 * 4 * 16];                 // per group 4 * 16
+  extern __shared__ float cols[];                        // [groups][H], when groups > 1
+  const int threads = gw * 64, groups = blockDim.x / threads;
+  const int group = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) / gw), tid = threadIdx.x - group * threads;
+  float* red = red_all + group * 64;
   const int H = a.H;
   const float inv_h = 1.0f / (float)H;
+  const bool has_post = a.w_post != nullptr, has_pre = a.w_pre != nullptr, has_y = a.y != nullptr,
+             has_dro = a.d_residual_out != nullptr;
   Raw<DT, N> wpost[V], wpre[V], gch[V];
   float cpre[V][N], cpost[V][N];
 #pragma unroll
@@ -141,29 +148,43 @@ __global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a) {
     const int c = (v * threads + tid) * N;
     wpost[v].zero(); wpre[v].zero(); gch[v].zero();
     if (c < H) {
-      if (a.w_post) wpost[v].load(a.w_post, c);
-      if (a.w_pre) wpre[v].load(a.w_pre, c);
-      if (a.gate_kind == GATE_CHANNEL) gch[v].load(a.gate, c);
+      if (has_post) wpost[v].load(a.w_post, c);
+      else wpost[v].fill(1.0f);
+      if (has_pre) wpre[v].load(a.w_pre, c);
+      if (GATE == GATE_CHANNEL) gch[v].load(a.gate, c);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) cpre[v][i] = cpost[v][i] = 0.0f;
   }
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+  struct Row {
+    Raw<DT, N> y[V], dn[V], g[V];
+    Raw<RDT, N> r[V], dro[V];
+  };
+  auto fetch = [&](Row& f, int64_t t) {
     const int64_t base = t * H;
-    Raw<DT, N> yr[V], dn[V], gr[V];
-    Raw<RDT, N> rr[V], dro[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (v * threads + tid) * N;
-      yr[v].zero(); dn[v].zero(); gr[v].zero(); rr[v].zero(); dro[v].zero();
-      if (c < H) {
-        if (a.w_pre) {
-          rr[v].load(a.residual_out, base + c);
-          dn[v].load(a.d_normed, base + c);
+      f.y[v].zero(); f.dn[v].zero(); f.g[v].zero(); f.r[v].zero(); f.dro[v].zero();
+      if (c < H && t < a.T) {
+        if (has_pre) {
+          f.r[v].load(at<RDT>(a.residual_out, base), c);
+          f.dn[v].load(at<DT>(a.d_normed, base), c);
         }
-        if (a.y) yr[v].load(a.y, base + c);
-        if (a.d_residual_out) dro[v].load(a.d_residual_out, base + c);
-        if (a.gate_kind == GATE_FULL) gr[v].load(a.gate, base + c);
+        if (has_y) f.y[v].load(at<DT>(a.y, base), c);
+        if (has_dro) f.dro[v].load(at<RDT>(a.d_residual_out, base), c);
+        if (GATE == GATE_FULL) f.g[v].load(at<DT>(a.gate, base), c);
+      }
+    }
+  };
+  auto turn = [&](Row& f, int64_t t) {
+    const bool live = t < a.T;
+    const int64_t base = t * H;
+    if (dt_size<DT> == 2) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        wpre[v].pin(); wpost[v].pin();
+        if (GATE == GATE_CHANNEL) gch[v].pin();
       }
     }
     // sums of r'^2, dn w_pre r' and y^2
@@ -172,140 +193,189 @@ __global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a) {
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float x = rr[v].get(i), y = yr[v].get(i);
+        const float x = f.r[v].get(i), y = f.y[v].get(i);
         s1[0] = fmaf(x, x, s1[0]);
-        s1[1] = fmaf(dn[v].get(i) * wpre[v].get(i), x, s1[1]);
+        s1[1] = fmaf(f.dn[v].get(i) * wpre[v].get(i), x, s1[1]);
         s1[2] = fmaf(y, y, s1[2]);
       }
-    group_sum<3>(s1, red, waves);
-    const float fr = rsqrtf(s1[0] * inv_h + a.eps);
+    float gt = a.res_scale;
+    if (GATE == GATE_TOKEN && live) {
+      Raw<DT, 1> g;
+      g.load(at<DT>(a.gate, t), 0);
+      gt *= g.get(0);
+    }
+    group_sum<3>(s1, red, gw, threadIdx.x & 63, tid >> 6);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (dt_size<DT> == 2) { f.y[v].pin(); f.dn[v].pin(); f.g[v].pin(); }
+      if (dt_size<RDT> == 2) { f.r[v].pin(); f.dro[v].pin(); }
+    }
+    // what a call leaves out drops out of the formulas: without w_pre fr = 0,
+    // without w_post fy = 1, my = 0 (and the weights loaded as ones); a row
+    // past the last has 0 for both
+    const float fr = has_pre && live ? rsqrtf(s1[0] * inv_h + a.eps) : 0.0f;
     const float mr = s1[1] * fr * inv_h * fr;      // mean(dn w_pre rh) / rms(r')
-    const float fy = a.w_post ? rsqrtf(s1[2] * inv_h + a.eps) : 1.0f;
+    const float fy = !live ? 0.0f : has_post ? rsqrtf(s1[2] * inv_h + a.eps) : 1.0f;
     float dr[V][N];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (v * threads + tid) * N;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        dr[v][i] = dro[v].get(i);
-        if (a.w_pre) {
-          const float rh = rr[v].get(i) * fr, d = dn[v].get(i);
-          cpre[v][i] = fmaf(d, rh, cpre[v][i]);
-          dr[v][i] += d * wpre[v].get(i) * fr - rh * mr;
-        }
+        const float rh = f.r[v].get(i) * fr, d = f.dn[v].get(i);
+        cpre[v][i] = fmaf(d, rh, cpre[v][i]);
+        dr[v][i] = fmaf(-rh, mr, fmaf(d * wpre[v].get(i), fr, f.dro[v].get(i)));
       }
-      if (c < H) {
+      if (c < H && live) {
         Raw<RDT, N> o;
         o.set(dr[v]);
-        o.store(a.d_residual, base + c);
+        o.store(at<RDT>(a.d_residual, base), c);
       }
     }
-    if (a.y) {
-      float gt = a.res_scale;
-      if (a.gate_kind == GATE_TOKEN) {
-        Raw<DT, 1> g;
-        g.load(a.gate, t);
-        gt *= g.get(0);
-      }
-      // the sum of dr u (times gate values inside the row): dgate of a token
-      // gate, and the mean that dy needs
-      float s2[1] = {0.0f};
-      if (a.w_post || a.gate_kind == GATE_TOKEN) {
+    if (has_y) {
+      // e = dr * gate values inside the row * w_post; the sum of e y is dgate of
+      // a token gate and the mean that dy needs
+      float s2[1] = {0.0f}, e[V][N];
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v)
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            float d = dr[v][i] * yr[v].get(i);
-            if (a.w_post) d *= wpost[v].get(i);
-            if (a.gate_kind == GATE_CHANNEL) d *= gch[v].get(i);
-            if (a.gate_kind == GATE_FULL) d *= gr[v].get(i);
-            s2[0] += d;
-          }
-        group_sum<1>(s2, red + 48, waves);
-        s2[0] *= fy;
-      }
-      if (a.gate_kind == GATE_TOKEN && tid == 0) ((float*)a.dgate)[t] = a.res_scale * s2[0];
-      const float my = gt * s2[0] * inv_h;         // mean(du w_post yh)
+        for (int i = 0; i < N; ++i) {
+          float g = dr[v][i];
+          if (GATE == GATE_FULL) g *= f.g[v].get(i);
+          // columns: du yh; a channel gate's value is left to the last step,
+          // since its own gradient is the same sum times w_post
+          cpost[v][i] = fmaf(gt * g, f.y[v].get(i) * fy, cpost[v][i]);
+          if (GATE == GATE_CHANNEL) g *= gch[v].get(i);
+          e[v][i] = g * wpost[v].get(i);
+          s2[0] = fmaf(e[v][i], f.y[v].get(i), s2[0]);
+        }
+      if (has_post || GATE == GATE_TOKEN) group_sum<1>(s2, red + 48, gw, threadIdx.x & 63, tid >> 6);
+      s2[0] *= fy;
+      if (GATE == GATE_TOKEN && tid == 0 && live) ((float*)a.dgate)[t] = a.res_scale * s2[0];
+      const float gf = gt * fy, my = has_post ? gf * s2[0] * inv_h * fy : 0.0f;   // mean(du w_post yh) / rms(y)^2
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = (v * threads + tid) * N;
-        float dy[N], dg[N];
+        float dy[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float yh = yr[v].get(i) * fy;
-          const float w = a.w_post ? wpost[v].get(i) : 1.0f;
-          float g = gt;
-          if (a.gate_kind == GATE_CHANNEL) g *= gch[v].get(i);
-          if (a.gate_kind == GATE_FULL) g *= gr[v].get(i);
-          // columns: du yh; a channel gate's value is left to the last step,
-          // since its own gradient is the same sum times w_post
-          cpost[v][i] = fmaf(dr[v][i] * (a.gate_kind == GATE_CHANNEL ? gt : g), yh, cpost[v][i]);
-          const float d = g * dr[v][i] * w;
-          dy[i] = a.w_post ? fy * (d - yh * my) : d;
-          dg[i] = a.res_scale * dr[v][i] * yh * w;
-        }
-        if (c < H) {
+        for (int i = 0; i < N; ++i) dy[i] = fmaf(gf, e[v][i], -f.y[v].get(i) * my);
+        if (c < H && live) {
           Raw<DT, N> o;
           o.set(dy);
-          o.store(a.dy, base + c);
-          if (a.gate_kind == GATE_FULL) {
+          o.store(at<DT>(a.dy, base), c);
+          if (GATE == GATE_FULL) {
+            float dg[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) dg[i] = a.res_scale * dr[v][i] * (f.y[v].get(i) * fy) * wpost[v].get(i);
             o.set(dg);
-            o.store(a.dgate, base + c);
+            o.store(at<DT>(a.dgate, base), c);
           }
         }
       }
     }
-    __syncthreads();   // red is free again
+    // red's two areas are used in turn: with both sums in a row their barriers
+    // already keep this row's reads and the next row's writes apart
+    if (!(has_y && (has_post || GATE == GATE_TOKEN))) __syncthreads();
+  };
+  // every group makes the same number of turns, so that all meet at the barriers;
+  // a group past the last row works on zeros and stores nothing
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t t0 = (int64_t)blockIdx.x * groups;
+  Row f0;
+  fetch(f0, t0 + group);
+  if (PF) {
+    Row f1;
+    while (true) {
+      fetch(f1, t0 + step + group);
+      turn(f0, t0 + group);
+      t0 += step;
+      if (t0 >= a.T) break;
+      fetch(f0, t0 + step + group);
+      turn(f1, t0 + group);
+      t0 += step;
+      if (t0 >= a.T) break;
+    }
+  } else {
+    for (; t0 < a.T; t0 += step) {
+      if (t0 != (int64_t)blockIdx.x * groups) fetch(f0, t0 + group);
+      turn(f0, t0 + group);
+    }
   }
   float* part = a.part + (int64_t)blockIdx.x * 2 * H;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = (v * threads + tid) * N;
-    if (c < H) {
+  for (int which = 0; which < 2; ++which) {
+    if (!(which == 0 ? has_pre : has_y)) continue;
+    if (groups > 1) __syncthreads();
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (a.w_pre) part[c + i] = cpre[v][i];
-        if (a.y) part[H + c + i] = cpost[v][i];
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * threads + tid) * N;
+      if (c < H) {
+        Raw<DT_F32, N> o;
+        o.set(which == 0 ? cpre[v] : cpost[v]);
+        if (groups > 1) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) cols[group * H + c + i] = o.get(i);
+        } else if constexpr (N == 1) {
+          part[which * H + c] = o.get(0);
+        } else {
+          o.store(part + which * H, c);
+        }
+      }
+    }
+    if (groups > 1) {
+      __syncthreads();
+      for (int c = threadIdx.x; c < H; c += blockDim.x) {
+        float sum = cols[c];
+        for (int g = 1; g < groups; ++g) sum += cols[g * H + c];
+        part[which * H + c] = sum;
       }
     }
   }
 }
 
 // Column sums over the workgroups' partial sums, in workgroup order: 64 columns
-// by 16 runs of parts per workgroup, then the runs in order.
+// by 16 runs of parts per workgroup, then the runs in order. blockIdx.y: 0 the
+// w_pre sums, 1 the shared sums of w_post and a channel gate.
 template <int DT>
 __global__ __launch_bounds__(1024) void k_block_norm_cols(BlockNormGradArgs a, int parts) {
-  __shared__ float sh[2][16][64];
-  const int lane = threadIdx.x & 63, run = threadIdx.x >> 6;
+  constexpr int B = 8;
+  __shared__ float sh[16][64];
+  const int lane = threadIdx.x & 63, run = threadIdx.x >> 6, which = blockIdx.y;
   const int c = blockIdx.x * 64 + lane;
+  const bool channel = a.gate_kind == GATE_CHANNEL;
+  if (!(which == 0 ? a.dw_pre != nullptr : a.dw_post != nullptr || channel)) return;
   const int lo = parts * run / 16, hi = parts * (run + 1) / 16;
-  const bool pre = a.dw_pre != nullptr, channel = a.gate_kind == GATE_CHANNEL, post = a.dw_post != nullptr || channel;
-  float s[2] = {0.0f, 0.0f};
+  float s = 0.0f;
   if (c < a.H) {
-    for (int p = lo; p < hi; ++p) {
-      const float* q = a.part + (int64_t)p * 2 * a.H + c;
-      if (pre) s[0] += q[0];
-      if (post) s[1] += q[a.H];
+    const float* q = a.part + which * a.H + c;
+    int p = lo;
+    for (; p + B <= hi; p += B) {      // B loads in flight
+      float v[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) v[i] = q[(int64_t)(p + i) * 2 * a.H];
+#pragma unroll
+      for (int i = 0; i < B; ++i) s += v[i];
     }
+    for (; p < hi; ++p) s += q[(int64_t)p * 2 * a.H];
   }
-  sh[0][run][lane] = s[0];
-  sh[1][run][lane] = s[1];
+  sh[run][lane] = s;
   __syncthreads();
   if (run != 0 || c >= a.H) return;
-  for (int r = 1; r < 16; ++r) {
-    s[0] += sh[0][r][lane];
-    s[1] += sh[1][r][lane];
+#pragma unroll
+  for (int r = 1; r < 16; ++r) s += sh[r][lane];
+  if (which == 0) {
+    a.dw_pre[c] = s;
+    return;
   }
-  if (pre) a.dw_pre[c] = s[0];
   if (channel) {
     Raw<DT, 1> g, w;
     g.load(a.gate, c);
     if (a.w_post) w.load(a.w_post, c);
     const bool rows = parts > 0;          // an empty sum is 0 whatever the factor
-    ((float*)a.dgate)[c] = a.w_post && rows ? s[1] * w.get(0) : s[1];
-    if (rows) s[1] *= g.get(0);
+    ((float*)a.dgate)[c] = a.w_post && rows ? s * w.get(0) : s;
+    if (rows) s *= g.get(0);
   }
-  if (a.dw_post) a.dw_post[c] = s[1];
+  if (a.dw_post) a.dw_post[c] = s;
 }
 
 // Pieces of N elements per thread (V) and waves of a row.
@@ -319,13 +389,20 @@ RowShape row_shape(int H, int N, int most_waves) {
   return {v, (pieces + 64 * v - 1) / (64 * v)};
 }
 
+// Rows that do not start on 16 bytes, element by element: V rounded up.
 template <class F>
 void dispatch_v(int V, F&& f) {
   if (V == 1) f(std::integral_constant<int, 1>());
-  else if (V == 2) f(std::integral_constant<int, 2>());
-  else if (V == 4) f(std::integral_constant<int, 4>());
-  else if (V == 8) f(std::integral_constant<int, 8>());
+  else if (V <= 4) f(std::integral_constant<int, 4>());
   else f(std::integral_constant<int, 16>());
+}
+
+template <class F>
+void dispatch_gate(GateKind kind, F&& f) {
+  if (kind == GATE_NONE) f(std::integral_constant<int, GATE_NONE>());
+  else if (kind == GATE_CHANNEL) f(std::integral_constant<int, GATE_CHANNEL>());
+  else if (kind == GATE_TOKEN) f(std::integral_constant<int, GATE_TOKEN>());
+  else f(std::integral_constant<int, GATE_FULL>());
 }
 
 // (activation type, residual type): the same, or an fp32 residual
@@ -340,51 +417,70 @@ void dispatch_pair(DType dt, DType rdt, F&& f) {
 
 }  // namespace
 
-// Eight elements per piece where every row starts on 16 bytes.
-bool block_norm_vec(int H, uintptr_t all_pointers) { return H % 8 == 0 && all_pointers % 16 == 0; }
+// Eight elements per piece, four of fp32, where every row starts on 16 bytes.
+static int piece(DType dt) { return dt == DT_F32 ? 4 : 8; }
+bool block_norm_vec(DType dt, int H, uintptr_t all_pointers) { return H % piece(dt) == 0 && all_pointers % 16 == 0; }
 
-int block_norm_grad_grid(int64_t T, int H) {
-  const RowShape s = row_shape(H, 8, 16);
-  return (int)std::min<int64_t>(T, (int64_t)cu_count() * std::max(1, 16 / s.waves));
-}
+// One workgroup of up to 16 waves per CU; partial sums of that many workgroups
+// (256 on any device, so that the workspace does not depend on it).
+int block_norm_grad_grid(int64_t T) { return (int)std::min<int64_t>(T, 256); }
 
 hipError_t launch_block_norm(const BlockNormArgs& a, bool vec, hipStream_t s) {
-  const int N = vec ? 8 : 1;
+  const int N = vec ? piece(a.dt) : 1;
   const RowShape sh = row_shape(a.H, N, vec ? 8 : 16);
   const int grid = (int)std::min<int64_t>(a.T, (int64_t)cu_count() * std::max(1, 32 / sh.waves));
   dispatch_pair(a.dt, a.rdt, [&](auto d, auto r) {
     constexpr int D = decltype(d)::value, R = decltype(r)::value;
-    if (vec) {
-      if (sh.V == 1) k_block_norm<D, R, 8, 1><<<grid, 64 * sh.waves, 0, s>>>(a);
-      else if (sh.V == 2) k_block_norm<D, R, 8, 2><<<grid, 64 * sh.waves, 0, s>>>(a);
-      else k_block_norm<D, R, 8, 4><<<grid, 64 * sh.waves, 0, s>>>(a);
-    } else {
-      dispatch_v(sh.V, [&](auto v) {
-        k_block_norm<D, R, 1, decltype(v)::value><<<grid, 64 * sh.waves, 0, s>>>(a);
+    auto go = [&](auto n, auto v) {
+      constexpr int NN = decltype(n)::value, VV = decltype(v)::value;
+      dispatch_gate(a.gate_kind, [&](auto g) {
+        k_block_norm<D, R, NN, VV, decltype(g)::value><<<grid, 64 * sh.waves, 0, s>>>(a);
       });
+    };
+    if (vec) {
+      std::integral_constant<int, D == DT_F32 ? 4 : 8> n;
+      if (sh.V == 1) go(n, std::integral_constant<int, 1>());
+      else if (sh.V == 2) go(n, std::integral_constant<int, 2>());
+      else if (sh.V == 4) go(n, std::integral_constant<int, 4>());
+      else if constexpr (D == DT_F32) go(n, std::integral_constant<int, 8>());
+    } else {
+      dispatch_v(sh.V, [&](auto v) { go(std::integral_constant<int, 1>(), v); });
     }
   });
   return hipGetLastError();
 }
 
 hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, bool vec, hipStream_t s) {
-  const int N = vec ? 8 : 1;
+  const int N = vec ? piece(a.dt) : 1;
   const RowShape sh = row_shape(a.H, N, 16);
-  const int grid = block_norm_grad_grid(a.T, a.H);
+  const int groups = 16 / sh.waves;
+  const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, block_norm_grad_grid(a.T));
+  const size_t lds = groups > 1 ? (size_t)groups * a.H * 4 : 0;
+  const int threads = 64 * sh.waves * groups;
   dispatch_pair(a.dt, a.rdt, [&](auto d, auto r) {
     constexpr int D = decltype(d)::value, R = decltype(r)::value;
+    auto go = [&](auto n, auto v, auto pf) {
+      constexpr int NN = decltype(n)::value, VV = decltype(v)::value;
+      constexpr bool PF = decltype(pf)::value;
+      auto with = [&](auto g) {
+        // a full gate beside an fp32 residual: the next row would not fit the registers
+        constexpr bool P = PF && !(decltype(g)::value == GATE_FULL && D != DT_F32 && R == DT_F32);
+        k_block_norm_grad<D, R, NN, VV, decltype(g)::value, P><<<grid, threads, lds, s>>>(a, sh.waves);
+      };
+      dispatch_gate(a.gate_kind, with);
+    };
     if (grid == 0) {
       // no rows: the column sums are zeros
     } else if (vec) {
-      if (sh.V == 1) k_block_norm_grad<D, R, 8, 1><<<grid, 64 * sh.waves, 0, s>>>(a);
-      else k_block_norm_grad<D, R, 8, 2><<<grid, 64 * sh.waves, 0, s>>>(a);
+      std::integral_constant<int, D == DT_F32 ? 4 : 8> n;
+      if (sh.V == 1) go(n, std::integral_constant<int, 1>(), std::true_type());
+      else if (sh.V == 2) go(n, std::integral_constant<int, 2>(), std::false_type());
+      else if constexpr (D == DT_F32) go(n, std::integral_constant<int, 4>(), std::false_type());
     } else {
-      dispatch_v(sh.V, [&](auto v) {
-        k_block_norm_grad<D, R, 1, decltype(v)::value><<<grid, 64 * sh.waves, 0, s>>>(a);
-      });
+      dispatch_v(sh.V, [&](auto v) { go(std::integral_constant<int, 1>(), v, std::false_type()); });
     }
     if (a.dw_pre || a.dw_post || a.gate_kind == GATE_CHANNEL)
-      k_block_norm_cols<D><<<(a.H + 63) / 64, 1024, 0, s>>>(a, grid);
+      k_block_norm_cols<D><<<dim3((a.H + 63) / 64, 2), 1024, 0, s>>>(a, grid);
   });
   return hipGetLastError();
 }

@@ -230,12 +230,12 @@ __global__ __launch_bounds__(64 * LORA_WAVES) void k_lora_expand(LoraArgs p) {
         const int n = n0 + 16 * q + 8 * half;
         if (n >= p.N) continue;        // N % 8 == 0
         Raw<DT, 8> y;
-        y.load(p.y, yrow[m] + n);
+        y.load(at<DT>(p.y, yrow[m]), n);
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = fmaf(f[m], acc[m][2 * half + (i >> 2)][i & 3], y.get(i));
         y.set(o);
-        y.store(p.y, yrow[m] + n);
+        y.store(at<DT>(p.y, yrow[m]), n);
       }
     }
   }

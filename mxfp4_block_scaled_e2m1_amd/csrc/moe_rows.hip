@@ -44,10 +44,10 @@ __global__ __launch_bounds__(64 * MR_WAVES) void k_permute(const char* __restric
     const int c = (int)(unit - t * segs) * 64 + (threadIdx.x & 63);
     if (c >= pieces) continue;
     Raw<W == 2 ? DT_BF16 : DT_F32, EL> v;
-    v.load(x + t * width, (int64_t)c * EL);
+    v.load(x + t * width, c * EL);
     for (int j = 0; j < k; ++j) {
       const int r = slot_row[t * k + j];
-      if ((unsigned)r < (unsigned)rows) v.store(xs + (int64_t)r * width, (int64_t)c * EL);
+      if ((unsigned)r < (unsigned)rows) v.store(xs + (int64_t)r * width, c * EL);
     }
   }
 }
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(64 * MR_WAVES) void k_unpermute(const void* __restr
         v[q].zero();
         if ((unsigned)r < (unsigned)rows) {
           wt[q] = w != nullptr ? w[t * k + j0 + q] : 1.0f;
-          v[q].load(ys, (int64_t)r * H + c);
+          v[q].load(at<DT>(ys, (int64_t)r * H), c);
         }
       }
 #pragma unroll
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(64 * MR_WAVES) void k_unpermute(const void* __restr
     }
     Raw<DT, N> o;
     o.set(acc);
-    o.store(y, t * H + c);
+    o.store(at<DT>(y, t * H), c);
   }
 }
 
@@ -112,10 +112,10 @@ __global__ __launch_bounds__(1024) void k_unpermute_grad(const void* __restrict_
       }
       for (int c = threadIdx.x * N; c < H; c += blockDim.x * N) {
         Raw<DT, N> d, v[SLOT_BATCH];
-        d.load(dy, t * H + c);
+        d.load(at<DT>(dy, t * H), c);
 #pragma unroll
         for (int q = 0; q < SLOT_BATCH; ++q)
-          if (row[q] >= 0) v[q].load(ys, (int64_t)row[q] * H + c);
+          if (row[q] >= 0) v[q].load(at<DT>(ys, (int64_t)row[q] * H), c);
 #pragma unroll
         for (int q = 0; q < SLOT_BATCH; ++q) {
           if (row[q] < 0) continue;
@@ -128,10 +128,10 @@ __global__ __launch_bounds__(1024) void k_unpermute_grad(const void* __restrict_
           }
           Raw<DT, N> r;
           r.set(o);
-          r.store(dys, (int64_t)row[q] * H + c);
+          r.store(at<DT>(dys, (int64_t)row[q] * H), c);
         }
       }
-      group_sum<SLOT_BATCH>(dot, red, waves);
+      group_sum<SLOT_BATCH>(dot, red, waves, threadIdx.x & 63, threadIdx.x >> 6);
       if (threadIdx.x == 0) {
 #pragma unroll
         for (int q = 0; q < SLOT_BATCH; ++q)

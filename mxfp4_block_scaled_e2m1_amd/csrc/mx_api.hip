@@ -1653,14 +1653,14 @@ mx_status mx_block_norm(mx_dtype dt, mx_dtype res_dt, const void* y, const void*
   const uintptr_t all = (uintptr_t)y | (uintptr_t)residual | (uintptr_t)w_post | (uintptr_t)w_pre |
                         (uintptr_t)residual_out | (uintptr_t)normed |
                         (gate_kind == MX_GATE_TOKEN ? (uintptr_t)0 : (uintptr_t)gate);
-  MX_HIP(phase("block_norm", s, [&] { return launch_block_norm(a, block_norm_vec((int)H, all), s); }), "block_norm");
+  MX_HIP(phase("block_norm", s, [&] { return launch_block_norm(a, block_norm_vec(a.dt, (int)H, all), s); }), "block_norm");
   return ok();
 }
 
 size_t mx_block_norm_grad_workspace_size(int64_t T, int64_t H) {
   if (T < 0 || H < 1 || H > BLOCK_NORM_MAX_H || T > ((int64_t)1 << 30)) return 0;
   Carve c(nullptr);
-  c.take((size_t)block_norm_grad_grid(T, (int)H) * 2 * (size_t)H * 4);
+  c.take((size_t)block_norm_grad_grid(T) * 2 * (size_t)H * 4);
   return c.off;
 }
 
@@ -1733,7 +1733,7 @@ mx_status mx_block_norm_grad(mx_dtype dt, mx_dtype res_dt, const void* y, const 
                         (uintptr_t)d_normed | (uintptr_t)d_residual_out | (uintptr_t)d_residual | (uintptr_t)d_y |
                         (gate_kind == MX_GATE_TOKEN ? (uintptr_t)0 : (uintptr_t)gate) |
                         (gate_kind == MX_GATE_FULL ? (uintptr_t)d_gate : (uintptr_t)0);
-  MX_HIP(phase("block_norm_grad", s, [&] { return launch_block_norm_grad(a, block_norm_vec((int)H, all), s); }),
+  MX_HIP(phase("block_norm_grad", s, [&] { return launch_block_norm_grad(a, block_norm_vec(a.dt, (int)H, all), s); }),
          "block_norm_grad");
   return ok();
 }

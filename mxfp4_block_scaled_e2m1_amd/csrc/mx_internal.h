@@ -295,10 +295,10 @@ struct BlockNormGradArgs {
   float *dw_pre, *dw_post;
   float* part;                 // [block_norm_grad_grid][2][H]
 };
-// Whether rows can be taken eight elements at a time: all_pointers is the
+// Whether rows can be taken in 16-byte pieces: all_pointers is the
 // bitwise or of every row and weight pointer in use.
-bool block_norm_vec(int H, uintptr_t all_pointers);
-int block_norm_grad_grid(int64_t T, int H);
+bool block_norm_vec(DType dt, int H, uintptr_t all_pointers);
+int block_norm_grad_grid(int64_t T);   // an upper bound
 hipError_t launch_block_norm(const BlockNormArgs& a, bool vec, hipStream_t s);
 hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, bool vec, hipStream_t s);
 

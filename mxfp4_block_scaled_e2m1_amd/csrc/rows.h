@@ -31,7 +31,14 @@ __device__ __forceinline__ float hi_f32(uint32_t w) {
   else return (float)__builtin_bit_cast(f16x2, w)[1];
 }
 
-// N consecutive elements as they lie in memory. N is 1 (any element address)
+// The element at 64-bit index i: the start of a row, uniform over a wave where i
+// is, so that a lane's own 32-bit offset into the row is all it has to hold.
+template <int DT>
+__device__ __forceinline__ const char* at(const void* p, int64_t i) { return (const char*)p + i * dt_size<DT>; }
+template <int DT>
+__device__ __forceinline__ char* at(void* p, int64_t i) { return (char*)p + i * dt_size<DT>; }
+
+// N consecutive elements as they lie in memory, at element i of a row. N is 1 (any element address)
 // or fills whole 16-byte pieces (16-byte aligned address), except N = 4 of a
 // 16-bit type: one 8-byte piece.
 template <int DT, int N>
@@ -44,10 +51,16 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < WORDS; ++i) w[i] = 0u;
   }
+  // Keeps the packed words where they are: without this the compiler unpacks a
+  // loop-invariant row of weights to fp32 ahead of the loop, in twice the registers.
+  __device__ __forceinline__ void pin() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(w[i]));
+  }
   // NT: a streaming access, for data that nothing reads again soon.
   template <bool NT = false>
-  __device__ __forceinline__ void load(const void* base, int64_t i) {
-    const char* p = (const char*)base + i * dt_size<DT>;
+  __device__ __forceinline__ void load(const void* row, uint32_t i) {
+    const char* p = (const char*)row + i * (uint32_t)dt_size<DT>;
     if constexpr (BYTES == 2) {
       w[0] = NT ? __builtin_nontemporal_load((const uint16_t*)p) : *(const uint16_t*)p;
     } else if constexpr (BYTES == 4) {
@@ -65,8 +78,8 @@ struct Raw {
     }
   }
   template <bool NT = false>
-  __device__ __forceinline__ void store(void* base, int64_t i) const {
-    char* p = (char*)base + i * dt_size<DT>;
+  __device__ __forceinline__ void store(void* row, uint32_t i) const {
+    char* p = (char*)row + i * (uint32_t)dt_size<DT>;
     if constexpr (BYTES == 2) {
       if (NT) __builtin_nontemporal_store((uint16_t)w[0], (uint16_t*)p);
       else *(uint16_t*)p = (uint16_t)w[0];
@@ -86,6 +99,12 @@ struct Raw {
       }
     }
   }
+  __device__ __forceinline__ void fill(float x) {
+    float f[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = x;
+    set(f);
+  }
   __device__ __forceinline__ float get(int i) const {   // i a compile-time constant after unrolling
     if constexpr (DT == DT_F32) return __uint_as_float(w[i]);
     else return (i & 1) ? hi_f32<DT>(w[i >> 1]) : lo_f32<DT>(w[i >> 1]);
@@ -103,32 +122,51 @@ struct Raw {
   }
 };
 
-// Sum over the 64 lanes, in every lane (xor butterfly: the same order always).
+// v plus v of the lanes that a DPP control names (0 where there is none).
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, ROWS, 0xF, false));
+}
+// Sum over each row of 16 lanes, in the row's last lane.
+__device__ __forceinline__ float row_sum(float v) {
+  v = dpp_add<0x111>(v);   // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112>(v);
+  v = dpp_add<0x114>(v);
+  return dpp_add<0x118>(v);
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+// Sum over the 64 lanes, uniform over the wave, by DPP adds (lane shuffles go
+// through LDS and cost a norm row several times as much).
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  v = row_sum(v);
+  v = dpp_add<0x142, 0xA>(v);   // row_bcast 15: rows 1 and 3 add the row before
+  v = dpp_add<0x143, 0xC>(v);   // row_bcast 31: rows 2 and 3 add the first half
+  return lane_value(v, 63);
 }
 
-// Sums of N values over the `waves` waves of the workgroup, in every thread.
-// red: LDS, N * 16 floats, used alternately by the caller (two areas) so that
-// one barrier per sum is enough.
+// Sums of N values over a group of `waves` (at most 16) waves of the workgroup,
+// uniform over the group; `wave` is the thread's wave in its group. All groups
+// of the workgroup call this together. red: the group's LDS, N * 16 floats, used
+// alternately by the caller (two areas) so that one barrier per sum is enough.
 template <int N>
-__device__ __forceinline__ void group_sum(float (&v)[N], float* red, int waves) {
+__device__ __forceinline__ void group_sum(float (&v)[N], float* red, int waves, int lane, int wave) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if (waves == 1) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (lane == 0) {
 #pragma unroll
     for (int i = 0; i < N; ++i) red[i * 16 + wave] = v[i];
   }
   __syncthreads();
+  // a row of 16 lanes per value, a lane per wave
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float s = 0.0f;
-    for (int w = 0; w < waves; ++w) s += red[i * 16 + w];
-    v[i] = s;
+  for (int i = 0; i < N; i += 4) {
+    const bool has = (lane & 15) < waves && (lane >> 4) < N - i;
+    const float s = row_sum(has ? red[i * 16 + lane] : 0.0f);
+#pragma unroll
+    for (int j = 0; j < 4 && i + j < N; ++j) v[i + j] = lane_value(s, 16 * j + 15);
   }
 }
 
