@@ -25,12 +25,51 @@ namespace mx {
 
 namespace {
 
-// A workgroup's waves share a row; element c of it held by thread tid, piece v:
-// (v * threads + tid) * N. GATE: the gate kind.
-template <int DT, int RDT, int N, int V, int GATE>
-__global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a) {
-  __shared__ float red[2 * 16];
-  const int threads = blockDim.x, waves = threads >> 6, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// The rows of a group: the workgroup's groups take rows side by side and stride
+// over them by the grid. Every group makes the same number of turns, so that all
+// meet at the barriers; one past the last row works on zeros and stores nothing.
+// PF: two row buffers, the next row fetched before the turn on this one.
+template <bool PF, class Row, class Fetch, class Turn>
+__device__ __forceinline__ void walk_rows(int64_t T, int groups, int group, Fetch&& fetch, Turn&& turn) {
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t t0 = (int64_t)blockIdx.x * groups;
+  Row f0;
+  fetch(f0, t0 + group);
+  if constexpr (PF) {
+    Row f1;
+    while (true) {
+      fetch(f1, t0 + step + group);
+      turn(f0, t0 + group);
+      t0 += step;
+      if (t0 >= T) break;
+      fetch(f0, t0 + step + group);
+      turn(f1, t0 + group);
+      t0 += step;
+      if (t0 >= T) break;
+    }
+  } else {
+    while (true) {
+      turn(f0, t0 + group);
+      t0 += step;
+      if (t0 >= T) break;
+      fetch(f0, t0 + group);
+    }
+  }
+}
+
+// A group of `gw` waves holds a row, element c in thread tid, piece v:
+// (v * threads + tid) * N. A workgroup holds blockDim / (64 gw) such groups, which
+// take rows side by side, and strides over the rows. GATE: the gate kind. PF: the
+// next row's pieces are loaded before this row's sums are waited for: with
+// one workgroup on a CU the sums would otherwise leave HBM idle, and more
+// workgroups are slower (the streams they make spread over HBM).
+template <int DT, int RDT, int N, int V, int GATE, bool PF>
+__global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a, int gw) {
+  __shared__ float red_all[16 * 2 * 16];                 // per group 2 * 16
+  const int threads = gw * 64, groups = blockDim.x / threads, lane = threadIdx.x & 63;
+  const int group = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) / gw), tid = threadIdx.x - group * threads;
+  const int wave = tid >> 6;
+  float* red = red_all + group * 32;
   const int H = a.H;
   const float inv_h = 1.0f / (float)H;
   const bool has_y = a.y != nullptr, has_post = a.w_post != nullptr, has_pre = a.w_pre != nullptr;
@@ -46,38 +85,46 @@ __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a) {
       if (GATE == GATE_CHANNEL) gch[v].load(a.gate, c);
     }
   }
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const int64_t base = t * H;
+  struct Row {
     Raw<DT, N> y[V], g[V];
     Raw<RDT, N> res[V];
+    Raw<DT, 1> gt;      // of a token gate
+  };
+  auto fetch = [&](Row& f, int64_t t) {
+    const int64_t base = t * H;
+    f.gt.zero();
+    if (GATE == GATE_TOKEN && t < a.T) f.gt.load(at<DT>(a.gate, t), 0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (v * threads + tid) * N;
-      y[v].zero(); res[v].zero(); g[v].zero();
-      if (c < H) {
-        if (has_y) y[v].load(at<DT>(a.y, base), c);
-        res[v].load(at<RDT>(a.residual, base), c);
-        if (GATE == GATE_FULL) g[v].load(at<DT>(a.gate, base), c);
+      f.y[v].zero(); f.res[v].zero(); f.g[v].zero();
+      if (c < H && t < a.T) {
+        if (has_y) f.y[v].template load<true>(at<DT>(a.y, base), c);
+        f.res[v].template load<true>(at<RDT>(a.residual, base), c);
+        if (GATE == GATE_FULL) f.g[v].template load<true>(at<DT>(a.gate, base), c);
       }
-      if (dt_size<DT> == 2) {
+    }
+  };
+  auto turn = [&](Row& f, int64_t t) {
+    const bool live = t < a.T;
+    const int64_t base = t * H;
+    if (dt_size<DT> == 2) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
         wpre[v].pin(); wpost[v].pin();
         if (GATE == GATE_CHANNEL) gch[v].pin();
       }
     }
-    float f = a.res_scale;
-    if (GATE == GATE_TOKEN) {
-      Raw<DT, 1> gt;
-      gt.load(at<DT>(a.gate, t), 0);
-      f *= gt.get(0);
-    }
+    float s = a.res_scale;
+    if (GATE == GATE_TOKEN) s *= f.gt.get(0);
     if (has_post) {
       float ss[1] = {0.0f};
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int i = 0; i < N; ++i) ss[0] = fmaf(y[v].get(i), y[v].get(i), ss[0]);
-      group_sum<1>(ss, red, waves, lane, wave);
-      f *= rsqrtf(ss[0] * inv_h + a.eps);
+        for (int i = 0; i < N; ++i) ss[0] = fmaf(f.y[v].get(i), f.y[v].get(i), ss[0]);
+      group_sum<1>(ss, red, gw, lane, wave);
+      s *= rsqrtf(ss[0] * inv_h + a.eps);
     }
     float r[V][N], ss[1] = {0.0f};
 #pragma unroll
@@ -85,28 +132,28 @@ __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a) {
       const int c = (v * threads + tid) * N;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        r[v][i] = res[v].get(i);
+        r[v][i] = f.res[v].get(i);
         if (has_y) {
-          float u = y[v].get(i) * f * wpost[v].get(i);
+          float u = f.y[v].get(i) * s * wpost[v].get(i);
           if (GATE == GATE_CHANNEL) u *= gch[v].get(i);
-          if (GATE == GATE_FULL) u *= g[v].get(i);
+          if (GATE == GATE_FULL) u *= f.g[v].get(i);
           r[v][i] += u;
         }
         ss[0] = fmaf(r[v][i], r[v][i], ss[0]);
       }
-      if (has_y && c < H) {
+      if (has_y && live && c < H) {
         Raw<RDT, N> o;
         o.set(r[v]);
         o.store(at<RDT>(a.residual_out, base), c);
       }
     }
     if (has_pre) {
-      group_sum<1>(ss, red + 16, waves, lane, wave);
+      group_sum<1>(ss, red + 16, gw, lane, wave);
       const float fn = rsqrtf(ss[0] * inv_h + a.eps);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = (v * threads + tid) * N;
-        if (c < H) {
+        if (live && c < H) {
           float n[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) n[i] = r[v][i] * fn * wpre[v].get(i);
@@ -119,7 +166,8 @@ __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a) {
     // the two sums of a row use the two halves of red, and a barrier of one
     // keeps the other's next use apart; with a single sum per row it takes one
     if (!(has_post && has_pre)) __syncthreads();
-  }
+  };
+  walk_rows<PF, Row>(a.T, groups, group, fetch, turn);
 }
 
 // The rows of a group of `gw` waves, one at a time; a workgroup holds `groups`
@@ -159,21 +207,24 @@ __global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a, i
   struct Row {
     Raw<DT, N> y[V], dn[V], g[V];
     Raw<RDT, N> r[V], dro[V];
+    Raw<DT, 1> gt;      // of a token gate; with the rest, for a load in between would wait for the next row's
   };
   auto fetch = [&](Row& f, int64_t t) {
     const int64_t base = t * H;
+    f.gt.zero();
+    if (GATE == GATE_TOKEN && t < a.T) f.gt.load(at<DT>(a.gate, t), 0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (v * threads + tid) * N;
       f.y[v].zero(); f.dn[v].zero(); f.g[v].zero(); f.r[v].zero(); f.dro[v].zero();
       if (c < H && t < a.T) {
         if (has_pre) {
-          f.r[v].load(at<RDT>(a.residual_out, base), c);
-          f.dn[v].load(at<DT>(a.d_normed, base), c);
+          f.r[v].template load<true>(at<RDT>(a.residual_out, base), c);
+          f.dn[v].template load<true>(at<DT>(a.d_normed, base), c);
         }
-        if (has_y) f.y[v].load(at<DT>(a.y, base), c);
-        if (has_dro) f.dro[v].load(at<RDT>(a.d_residual_out, base), c);
-        if (GATE == GATE_FULL) f.g[v].load(at<DT>(a.gate, base), c);
+        if (has_y) f.y[v].template load<true>(at<DT>(a.y, base), c);
+        if (has_dro) f.dro[v].template load<true>(at<RDT>(a.d_residual_out, base), c);
+        if (GATE == GATE_FULL) f.g[v].template load<true>(at<DT>(a.gate, base), c);
       }
     }
   };
@@ -199,11 +250,7 @@ __global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a, i
         s1[2] = fmaf(y, y, s1[2]);
       }
     float gt = a.res_scale;
-    if (GATE == GATE_TOKEN && live) {
-      Raw<DT, 1> g;
-      g.load(at<DT>(a.gate, t), 0);
-      gt *= g.get(0);
-    }
+    if (GATE == GATE_TOKEN) gt *= f.gt.get(0);
     group_sum<3>(s1, red, gw, threadIdx.x & 63, tid >> 6);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -277,30 +324,7 @@ __global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a, i
     // already keep this row's reads and the next row's writes apart
     if (!(has_y && (has_post || GATE == GATE_TOKEN))) __syncthreads();
   };
-  // every group makes the same number of turns, so that all meet at the barriers;
-  // a group past the last row works on zeros and stores nothing
-  const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t t0 = (int64_t)blockIdx.x * groups;
-  Row f0;
-  fetch(f0, t0 + group);
-  if (PF) {
-    Row f1;
-    while (true) {
-      fetch(f1, t0 + step + group);
-      turn(f0, t0 + group);
-      t0 += step;
-      if (t0 >= a.T) break;
-      fetch(f0, t0 + step + group);
-      turn(f1, t0 + group);
-      t0 += step;
-      if (t0 >= a.T) break;
-    }
-  } else {
-    for (; t0 < a.T; t0 += step) {
-      if (t0 != (int64_t)blockIdx.x * groups) fetch(f0, t0 + group);
-      turn(f0, t0 + group);
-    }
-  }
+  walk_rows<PF, Row>(a.T, groups, group, fetch, turn);
   float* part = a.part + (int64_t)blockIdx.x * 2 * H;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
@@ -421,20 +445,29 @@ void dispatch_pair(DType dt, DType rdt, F&& f) {
 static int piece(DType dt) { return dt == DT_F32 ? 4 : 8; }
 bool block_norm_vec(DType dt, int H, uintptr_t all_pointers) { return H % piece(dt) == 0 && all_pointers % 16 == 0; }
 
-// One workgroup of up to 16 waves per CU; partial sums of that many workgroups
-// (256 on any device, so that the workspace does not depend on it).
-int block_norm_grad_grid(int64_t T) { return (int)std::min<int64_t>(T, 256); }
+// One workgroup of up to 16 waves per CU of an MI355X. Measured on 4096 x 7168,
+// bf16 beside an fp32 residual, before the prefetch: 14 waves on every CU 65.9 us,
+// twice as many workgroups 68.8, four times 72.6; 7 waves, V = 2: 67.6 to 76.1.
+constexpr int ROW_GRID = 256;
+// Groups per workgroup: as many as there are rows for on every CU.
+int row_groups(int64_t T, int waves) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(16 / waves, (T + ROW_GRID - 1) / ROW_GRID));
+}
+
+// An upper bound of the workgroups of the way back, each with a partial sum.
+int block_norm_grad_grid(int64_t T) { return (int)std::min<int64_t>(T, ROW_GRID); }
 
 hipError_t launch_block_norm(const BlockNormArgs& a, bool vec, hipStream_t s) {
-  const int N = vec ? piece(a.dt) : 1;
-  const RowShape sh = row_shape(a.H, N, vec ? 8 : 16);
-  const int grid = (int)std::min<int64_t>(a.T, (int64_t)cu_count() * std::max(1, 32 / sh.waves));
+  const RowShape sh = row_shape(a.H, vec ? piece(a.dt) : 1, 16);
+  const int groups = row_groups(a.T, sh.waves);
+  const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, ROW_GRID);
+  const int threads = 64 * sh.waves * groups;
   dispatch_pair(a.dt, a.rdt, [&](auto d, auto r) {
     constexpr int D = decltype(d)::value, R = decltype(r)::value;
     auto go = [&](auto n, auto v) {
       constexpr int NN = decltype(n)::value, VV = decltype(v)::value;
       dispatch_gate(a.gate_kind, [&](auto g) {
-        k_block_norm<D, R, NN, VV, decltype(g)::value><<<grid, 64 * sh.waves, 0, s>>>(a);
+        k_block_norm<D, R, NN, VV, decltype(g)::value, NN != 1 && VV == 1><<<grid, threads, 0, s>>>(a, sh.waves);
       });
     };
     if (vec) {
@@ -453,8 +486,8 @@ hipError_t launch_block_norm(const BlockNormArgs& a, bool vec, hipStream_t s) {
 hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, bool vec, hipStream_t s) {
   const int N = vec ? piece(a.dt) : 1;
   const RowShape sh = row_shape(a.H, N, 16);
-  const int groups = 16 / sh.waves;
-  const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, block_norm_grad_grid(a.T));
+  const int groups = row_groups(a.T, sh.waves);
+  const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, ROW_GRID);
   const size_t lds = groups > 1 ? (size_t)groups * a.H * 4 : 0;
   const int threads = 64 * sh.waves * groups;
   dispatch_pair(a.dt, a.rdt, [&](auto d, auto r) {
