@@ -26,7 +26,8 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int LORA_WAVES = 4;
+constexpr int SHRINK_WAVES = 8;   // waves of a shrink workgroup, which split its K range
+constexpr int EXPAND_WAVES = 4;   // waves of an expand workgroup, which split its columns
 
 template <int DT>
 __device__ __forceinline__ f32x4 mma(u32v4 a, u32v4 b, f32x4 c) {
@@ -39,234 +40,348 @@ __device__ __forceinline__ f32x4 mma(u32v4 a, u32v4 b, f32x4 c) {
 }
 
 struct Tile {
-  int adapter, row0, rows;   // sorted rows [row0, row0 + rows) of one adapter; adapter < 0: no such tile
+  int adapter, row0, rows;   // sorted rows [row0, row0 + rows) of one adapter; adapter < 0: none
+  int piece;                 // which of the tile's `pieces` workgroups this is
 };
 
-// The tile-th tile of up to TM sorted rows, adapters in order: 64 adapters at a
-// time, a prefix sum of their tile counts over the lanes.
+// The tile of workgroup `id`, of `pieces` workgroups per tile. A tile is up to TM
+// sorted rows of one adapter, adapters in order; how many there are is only known
+// here, so workgroups past the last one get none. Neighbouring tiles mostly share
+// an adapter, and workgroups go to the 8 XCDs in turn, so each XCD is given a
+// contiguous run of the work: its L2 then holds a few adapters instead of all
+// (8 adapters of 64 x 7168 beside 4096 tokens: 7.3 MB, more than its 4 MB).
 template <int TM>
-__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ off, int n, int M, int tile) {
+__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ off, int n, int M, int id, int pieces) {
   const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int a0 = 0; a0 < n; a0 += 64) {
+  // 64 adapters at a time: a prefix sum of their tile counts over the lanes
+  auto chunk = [&](int a0, int& lo, int& hi, int& cnt) {
     const int a = a0 + lane;
-    int lo = 0, hi = 0;
+    lo = hi = 0;
     if (a < n) {
       lo = min(max(off[a], 0), M);
       hi = min(max(off[a + 1], lo), M);
     }
-    const int cnt = (hi - lo + TM - 1) / TM;
+    cnt = (hi - lo + TM - 1) / TM;
     int inc = cnt;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int u = __shfl_up(inc, d);
       if (lane >= d) inc += u;
     }
+    return inc;
+  };
+  int lo, hi, cnt, total = 0;
+  for (int a0 = 0; a0 < n; a0 += 64) total += __builtin_amdgcn_readlane(chunk(a0, lo, hi, cnt), 63);
+  const int work = total * pieces;
+  if (id >= work) return {-1, 0, 0, 0};
+  const int xcd = id & 7, mine = (work >> 3) * xcd + min(xcd, work & 7) + (id >> 3);
+  const int tile = mine / pieces;
+  int before = 0;
+  for (int a0 = 0; a0 < n; a0 += 64) {
+    const int inc = chunk(a0, lo, hi, cnt);
     const uint64_t hit = __ballot(before + inc > tile);
     if (hit) {
       const int l = __ffsll((long long)hit) - 1;
       const int first = before + __builtin_amdgcn_readlane(inc, l) - __builtin_amdgcn_readlane(cnt, l);
       const int row0 = __builtin_amdgcn_readlane(lo, l) + (tile - first) * TM;
-      return {a0 + l, row0, min(TM, __builtin_amdgcn_readlane(hi, l) - row0)};
+      return {a0 + l, row0, min(TM, __builtin_amdgcn_readlane(hi, l) - row0), mine - tile * pieces};
     }
     before += __builtin_amdgcn_readlane(inc, 63);
   }
-  return {-1, 0, 0};
+  return {-1, 0, 0, 0};
+}
+
+// Between the lanes of one wave: LDS writes before, reads after.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // v [split][sorted row][R] of one tile: MT x RT blocks of 16 tokens x 16 ranks.
-// Grid: tile, K split, group of 16 RT ranks.
+// A matrix operand wants 16 rows side by side in the lanes, but a load whose
+// neighbouring lanes are in different rows takes the address path one row at a time
+// (4096 x 7168, rank 64: 39 us that way even with x in L2). So a wave loads whole
+// 128-byte lines, eight lanes each, the rows of a 64-wide step of K, turns them
+// in an LDS area of its own (pitch 144: conflict-free) and has the next
+// step's loads in flight meanwhile. The waves take the steps of a split in turn,
+// 1 KB of a row together, and join their sums in LDS.
+// Workgroups of a tile: K splits by groups of 16 RT ranks.
+constexpr int SHRINK_PITCH = 128 + 16;
 template <int DT, int MT, int RT>
-__global__ __launch_bounds__(64 * LORA_WAVES) void k_lora_shrink(LoraArgs p) {
-  constexpr int TM = 16 * MT;
-  __shared__ f32x4 sh[LORA_WAVES][MT * RT][64];
-  const Tile tile = find_tile<TM>(p.adapter_off, p.n, p.M, blockIdx.x);
+__global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(LoraArgs p) {
+  constexpr int TM = 16 * MT, XI = 2 * MT, AI = 2 * RT;      // loads of eight rows: of x, of A
+  constexpr int AREA = 16 * (MT + RT) * SHRINK_PITCH;
+  constexpr int JOIN = MT * RT * 1024;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[SHRINK_WAVES * (AREA > JOIN ? AREA : JOIN)];
+  const int rgroups = (p.R + 16 * RT - 1) / (16 * RT);
+  const Tile tile = find_tile<TM>(p.adapter_off, p.n, p.M, blockIdx.x, p.splits * rgroups);
   if (tile.adapter < 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.y, r0 = blockIdx.z * 16 * RT;
-  const int c = lane & 15, q8 = (lane >> 4) * 8;
+  const int split = tile.piece / rgroups, r0 = (tile.piece - split * rgroups) * 16 * RT;
+  const int lrow = lane >> 3, lcol = (lane & 7) * 8;          // of a load
   // rows past the tile or the rank repeat the last one; their results are not kept
-  const uint16_t* xr[MT];
+  const uint16_t* xr[XI];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = tile.row0 + min(m * 16 + c, tile.rows - 1);
-    const int tok = min(max(p.row_token[row], 0), p.M - 1);
-    xr[m] = (const uint16_t*)p.x + (int64_t)tok * p.ldx + q8;
+  for (int i = 0; i < XI; ++i) {
+    const int tok = p.row_token[tile.row0 + min(8 * i + lrow, tile.rows - 1)];
+    xr[i] = (const uint16_t*)p.x + (int64_t)min(max(tok, 0), p.M - 1) * p.ldx + lcol;
   }
-  const uint16_t* ar[RT];
+  const uint16_t* am = (const uint16_t*)p.a + (int64_t)tile.adapter * p.R * p.K;
+  uint32_t ao[AI];
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-    ar[r] = (const uint16_t*)p.a + ((int64_t)tile.adapter * p.R + min(r0 + r * 16 + c, p.R - 1)) * p.K + q8;
+  for (int i = 0; i < AI; ++i) ao[i] = (uint32_t)min(r0 + 8 * i + lrow, p.R - 1) * (uint32_t)p.K + lcol;
   f32x4 acc[MT][RT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[m][r] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // the 32-wide K steps, split evenly over (split, wave)
-  const int steps = (p.K + 31) / 32, parts = p.splits * LORA_WAVES, part = split * LORA_WAVES + wave;
-  const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
-  for (int s = s0; s < s1; ++s) {
-    const int k = s * 32;
-    const bool in = k + q8 < p.K;      // K % 8 == 0: a lane's eight elements are in or out
-    u32v4 xv[MT], av[RT];
+  u32v4 v[XI + AI];
+  auto fetch = [&](int k) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) xv[m] = in ? *(const u32v4*)(xr[m] + k) : u32v4{0, 0, 0, 0};
+    for (int i = 0; i < XI; ++i) v[i] = *(const u32v4*)(xr[i] + k);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) av[r] = in ? *(const u32v4*)(ar[r] + k) : u32v4{0, 0, 0, 0};
+    for (int i = 0; i < AI; ++i) v[XI + i] = *(const u32v4*)(am + k + ao[i]);
+  };
+  uint8_t* area = lds + wave * AREA;
+  uint8_t* put = area + lrow * SHRINK_PITCH + lcol * 2;
+  const uint8_t* get = area + (lane & 15) * SHRINK_PITCH + (lane >> 4) * 16;
+  auto stage = [&]() {
+    wave_sync();
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int i = 0; i < XI + AI; ++i) *(u32v4*)(put + 8 * i * SHRINK_PITCH) = v[i];
+    wave_sync();
+  };
+  auto multiply = [&]() {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) acc[m][r] = mma<DT>(av[r], xv[m], acc[m][r]);
+    for (int h = 0; h < 2; ++h) {
+      u32v4 af[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) af[r] = *(const u32v4*)(get + 16 * (MT + r) * SHRINK_PITCH + 64 * h);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const u32v4 xf = *(const u32v4*)(get + 16 * m * SHRINK_PITCH + 64 * h);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[m][r] = mma<DT>(af[r], xf, acc[m][r]);
+      }
+    }
+  };
+  const int steps = p.K / 64;
+  const int s1 = (int)((int64_t)steps * (split + 1) / p.splits);
+  int s = (int)((int64_t)steps * split / p.splits) + wave;
+  if (s < s1) {
+    fetch(s * 64);
+    for (; s < s1; s += SHRINK_WAVES) {
+      stage();
+      if (s + SHRINK_WAVES < s1) fetch((s + SHRINK_WAVES) * 64);
+      multiply();
+    }
   }
+  if (split == p.splits - 1 && wave == SHRINK_WAVES - 1 && steps * 64 < p.K) {
+    // the rest of K, a multiple of 8: a lane's eight elements are in or out
+    const int k = steps * 64;
+#pragma unroll
+    for (int i = 0; i < XI + AI; ++i) v[i] = u32v4{0, 0, 0, 0};
+    if (k + lcol < p.K) fetch(k);
+    stage();
+    multiply();
+  }
+  __syncthreads();                 // the areas become the sums to join
+  f32x4* sh = (f32x4*)lds;         // [wave][block][lane]
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) sh[wave][m * RT + r][lane] = acc[m][r];
+    for (int r = 0; r < RT; ++r) sh[(wave * MT * RT + m * RT + r) * 64 + lane] = acc[m][r];
   __syncthreads();
   // block b of the tile: lane l holds ranks 4 (l / 16) .. + 3 of token l % 16
   float* out = p.part + (int64_t)split * p.M * p.R;
-  for (int i = threadIdx.x; i < MT * RT * 64; i += 64 * LORA_WAVES) {
+  for (int i = threadIdx.x; i < MT * RT * 64; i += 64 * SHRINK_WAVES) {
     const int b = i >> 6, l = i & 63;
-    f32x4 v = sh[0][b][l];
+    f32x4 u = sh[i];
 #pragma unroll
-    for (int w = 1; w < LORA_WAVES; ++w) v += sh[w][b][l];
+    for (int w = 1; w < SHRINK_WAVES; ++w) u += sh[w * MT * RT * 64 + i];
     const int row = (b / RT) * 16 + (l & 15), r = r0 + (b % RT) * 16 + (l >> 4) * 4;
-    if (row < tile.rows && r < p.R) *(f32x4*)(out + (int64_t)(tile.row0 + row) * p.R + r) = v;
+    if (row < tile.rows && r < p.R) *(f32x4*)(out + (int64_t)(tile.row0 + row) * p.R + r) = u;
   }
 }
 
-// y += scale B v of one tile. A wave takes 64 columns at a time as four
-// matrix products of 16 columns each, column 16 (i / 4) + 4 f + i % 4 as row i
-// of product f, so that a lane ends up with 16 consecutive columns of a token.
-// Grid: tile, run of column groups.
-template <int DT, int MT>
-__global__ __launch_bounds__(64 * LORA_WAVES) void k_lora_expand(LoraArgs p) {
-  constexpr int TM = 16 * MT;
-  extern __shared__ uint32_t lds[];
-  const Tile tile = find_tile<TM>(p.adapter_off, p.n, p.M, blockIdx.x);
+// y += scale B v of one tile, RP the rank rounded up to 32, 64 or 128. A wave
+// takes 64 columns at a time: their rows of B, one piece of memory, come in
+// whole lines and are turned into matrix operands in the wave's own LDS area, and
+// so are the products on their way to y, which is read and written 128 bytes a
+// token (with the operands' own lanes, 16 tokens side by side, the address
+// path took most of 53 us for 4096 x 7168, rank 64).
+// Workgroups of a tile: runs of `run` column groups.
+template <int DT, int MT, int RP>
+__global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, int run) {
+  constexpr int TM = 16 * MT, VP = RP + 8;                   // pitch of v in 16-bit elements
+  constexpr int BP = RP * 2 + 16, CP = 64 * 4 + 16;          // pitches in bytes: of B, of the products
+  constexpr int AREA = 64 * BP > 16 * CP ? 64 * BP : 16 * CP;
+  __shared__ __attribute__((aligned(16))) uint16_t vh[TM * VP], vl[TM * VP];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[EXPAND_WAVES * AREA];
+  __shared__ float fac[TM];                                  // scale * 2^e
+  const int groups = (p.N + 63) / 64;                        // of 64 columns
+  const Tile tile = find_tile<TM>(p.adapter_off, p.n, p.M, blockIdx.x, (groups + run - 1) / run);
   if (tile.adapter < 0) return;
-  const int Rp = (p.R + 31) / 32 * 32, pitch = Rp + 8;     // 16-bit elements; the pad spreads the banks
-  uint16_t* vh = (uint16_t*)lds;                            // [TM][pitch] hi
-  uint16_t* vl = vh + TM * pitch;                           // [TM][pitch] lo
-  float* fac = (float*)(vl + TM * pitch);                   // [TM] scale * 2^e
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float scale = p.scale != nullptr ? p.scale[tile.adapter] : 1.0f;
-  for (int row = wave; row < TM; row += LORA_WAVES) {
-    float v[LORA_MAX_RANK / 64];
-    float amax = 0.0f;
+  // v of the tile: RP / 4 lanes per row, four ranks each; the splits' partial
+  // sums, eight loads at a time, in split order
+  constexpr int PER = RP / 4, ROWS = 64 / PER;
+  const int r = (lane & (PER - 1)) * 4;
+  for (int row = wave * ROWS + lane / PER; row < TM; row += EXPAND_WAVES * ROWS) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (r < p.R && row < tile.rows) {
+      const float* src = p.part + (int64_t)(tile.row0 + row) * p.R + r;
+      const int64_t next = (int64_t)p.M * p.R;
+      for (int s = 0; s < p.splits; s += 8) {
+        f32x4 u[8];
 #pragma unroll
-    for (int j = 0; j < LORA_MAX_RANK / 64; ++j) {
-      const int r = j * 64 + lane;
-      v[j] = 0.0f;
-      if (r < p.R && row < tile.rows)
-        for (int s = 0; s < p.splits; ++s) v[j] += p.part[((int64_t)s * p.M + tile.row0 + row) * p.R + r];
-      amax = fmaxf(amax, fabsf(v[j]));
-    }
+        for (int i = 0; i < 8; ++i) u[i] = *(const f32x4*)(src + (int64_t)min(s + i, p.splits - 1) * next);
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
-    // 2^-e with 2^e the exponent of the row's largest value, where that is an ordinary number
-    const uint32_t ex = __float_as_uint(amax) >> 23;
-    const bool plain = ex >= 2 && ex <= 252;
-    const float down = plain ? __uint_as_float((254u - ex) << 23) : 1.0f;
-    const float up = plain ? __uint_as_float(ex << 23) : 1.0f;
-#pragma unroll
-    for (int j = 0; j < LORA_MAX_RANK / 64; ++j) {
-      const int r = j * 64 + lane;
-      if (r < Rp) {
-        const float u = v[j] * down;
-        const uint32_t h = pack2<DT>(u, 0.0f);
-        const float hf = lo_f32<DT>(h);
-        const float rest = fabsf(hf) < INFINITY ? u - hf : 0.0f;   // an inf or NaN travels in hi alone
-        vh[row * pitch + r] = (uint16_t)h;
-        vl[row * pitch + r] = (uint16_t)pack2<DT>(rest, 0.0f);
+        for (int i = 0; i < 8; ++i)
+          if (s + i < p.splits) v += u[i];
       }
     }
-    if (lane == 0) fac[row] = scale * up;
+    float down = 1.0f, up = 1.0f;
+    if constexpr (DT == DT_F16) {
+      // 2^-e with 2^e the exponent of the row's largest value, where that is an
+      // ordinary number; bf16 has fp32's range and needs none
+      float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+      for (int d = PER / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
+      const uint32_t ex = __float_as_uint(amax) >> 23;
+      if (ex >= 2 && ex <= 252) {
+        down = __uint_as_float((254u - ex) << 23);
+        up = __uint_as_float(ex << 23);
+      }
+    }
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float u0 = v[2 * i] * down, u1 = v[2 * i + 1] * down;
+      h[i] = pack2<DT>(u0, u1);
+      const float h0 = lo_f32<DT>(h[i]), h1 = hi_f32<DT>(h[i]);
+      // an inf or NaN travels in hi alone
+      l[i] = pack2<DT>(fabsf(h0) < INFINITY ? u0 - h0 : 0.0f, fabsf(h1) < INFINITY ? u1 - h1 : 0.0f);
+    }
+    *(u32v2*)(vh + row * VP + r) = u32v2{h[0], h[1]};
+    *(u32v2*)(vl + row * VP + r) = u32v2{l[0], l[1]};
+    if (r == 0) fac[row] = scale * up;
+  }
+  const int c = lane & 15, q = lane >> 4, lrow = lane >> 3, lcol = (lane & 7) * 8;
+  // y pieces: token 8 i + lane / 8 of the tile, columns 8 (lane % 8) of the group;
+  // rows past the tile repeat the last one and are not written
+  const char* yr[2 * MT];
+  bool mine[2 * MT];
+#pragma unroll
+  for (int i = 0; i < 2 * MT; ++i) {
+    const int row = 8 * i + lrow, tok = p.row_token[tile.row0 + min(row, tile.rows - 1)];
+    mine[i] = row < tile.rows && (unsigned)tok < (unsigned)p.M;
+    yr[i] = at<DT>((const void*)p.y, (int64_t)min(max(tok, 0), p.M - 1) * p.ldy);
+  }
+  // B pieces of 16 bytes: number i * 64 + lane of the group's rows
+  const int per_row = p.R / 8;
+  uint8_t* area = lds + wave * AREA;
+  uint32_t bput[RP / 8];
+#pragma unroll
+  for (int i = 0; i < RP / 8; ++i) {
+    const int at = i * 64 + lane, row = at / per_row;
+    bput[i] = row * BP + (at - row * per_row) * 16;
   }
   __syncthreads();
-  const int c = lane & 15, q = lane >> 4;
   const uint16_t* bm = (const uint16_t*)p.b + (int64_t)tile.adapter * p.N * p.R;
-  const int groups = (p.N + 63) / 64;                       // of 64 columns
-  const int g0 = (int)((int64_t)groups * blockIdx.y / gridDim.y), g1 = (int)((int64_t)groups * (blockIdx.y + 1) / gridDim.y);
-  int64_t yrow[MT];
-  float f[MT];
+  const int g0 = tile.piece * run, g1 = min(groups, g0 + run);
+  for (int g = g0 + wave; g < g1; g += EXPAND_WAVES) {
+    const int n0 = g * 64, last = min(64, p.N - n0) * per_row - 1;
+    u32v4 bv[RP / 8];
+    const uint16_t* bg = bm + (int64_t)n0 * p.R;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = m * 16 + c;
-    const int tok = row < tile.rows ? p.row_token[tile.row0 + row] : -1;
-    yrow[m] = (unsigned)tok < (unsigned)p.M ? (int64_t)tok * p.ldy : -1;
-    f[m] = fac[row];
-  }
-  for (int g = g0 + wave; g < g1; g += LORA_WAVES) {
-    const int n0 = g * 64;
+    for (int i = 0; i < RP / 8; ++i)
+      if (i < per_row) bv[i] = *(const u32v4*)(bg + min(i * 64 + lane, last) * 8);
+    const int n = min(n0 + lcol, p.N - 8);                  // N % 8 == 0
+    Raw<DT, 8> y[2 * MT];
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) y[i].load(yr[i], n);
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < RP / 8; ++i)
+      if (i < per_row) *(u32v4*)(area + bput[i]) = bv[i];
+    wave_sync();
     f32x4 acc[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < Rp; k += 32) {
-      u32v4 bv[4];
+#pragma unroll
+    for (int k = 0; k < RP; k += 32) {
+      u32v4 bf[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int n = min(n0 + 16 * (c >> 2) + 4 * j + (c & 3), p.N - 1);
-        bv[j] = k + q * 8 < p.R ? *(const u32v4*)(bm + (int64_t)n * p.R + k + q * 8) : u32v4{0, 0, 0, 0};
+        bf[j] = *(const u32v4*)(area + (16 * j + c) * BP + k * 2 + q * 16);
+        if (k + q * 8 >= p.R) bf[j] = u32v4{0, 0, 0, 0};    // past the rank: whatever LDS held
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const int at = (m * 16 + c) * pitch + k + q * 8;
-        const u32v4 h = *(const u32v4*)(vh + at), l = *(const u32v4*)(vl + at);
+        const int w = (m * 16 + c) * VP + k + q * 8;
+        const u32v4 h = *(const u32v4*)(vh + w), l = *(const u32v4*)(vl + w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          acc[m][j] = mma<DT>(bv[j], l, acc[m][j]);
-          acc[m][j] = mma<DT>(bv[j], h, acc[m][j]);
+          acc[m][j] = mma<DT>(bf[j], l, acc[m][j]);
+          acc[m][j] = mma<DT>(bf[j], h, acc[m][j]);
         }
       }
     }
+    // product j: columns 16 j + 4 q .. + 3 of token c
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if (yrow[m] < 0) continue;
+      wave_sync();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *(f32x4*)(area + c * CP + (16 * j + 4 * q) * 4) = acc[m][j];
+      wave_sync();
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int n = n0 + 16 * q + 8 * half;
-        if (n >= p.N) continue;        // N % 8 == 0
-        Raw<DT, 8> y;
-        y.load(at<DT>(p.y, yrow[m]), n);
+        const int i = 2 * m + half;
+        const f32x4* d = (const f32x4*)(area + (8 * half + lrow) * CP + lcol * 4);
+        const f32x4 d0 = d[0], d1 = d[1];
+        const float f = fac[8 * i + lrow];
         float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = fmaf(f[m], acc[m][2 * half + (i >> 2)][i & 3], y.get(i));
-        y.set(o);
-        y.store(at<DT>(p.y, yrow[m]), n);
+        for (int e = 0; e < 4; ++e) {
+          o[e] = fmaf(f, d0[e], y[i].get(e));
+          o[4 + e] = fmaf(f, d1[e], y[i].get(4 + e));
+        }
+        y[i].set(o);
+        if (mine[i] && n0 + lcol < p.N) y[i].store((char*)yr[i], n);
       }
     }
   }
 }
 
-// Sorted rows per tile: 64 where adapters have many rows each, else 16 (a tile
-// holds one adapter's rows, so more would mostly be padding).
-int lora_mt(int64_t M, int n) { return M >= 32 * (int64_t)std::min<int64_t>(n, M) && M >= 64 ? 4 : 1; }
-int lora_tiles(int64_t M, int n, int mt) {
-  return (int)(M / (16 * mt) + std::min<int64_t>(n, M));
-}
+// Whether adapters have many rows each: tiles of several 16-row blocks then, else
+// of one (a tile holds one adapter's rows, so more would mostly be padding).
+bool many_rows(int64_t M, int n) { return M >= 32 * (int64_t)std::min<int64_t>(n, M) && M >= 64; }
+constexpr int SHRINK_MT = 4, EXPAND_MT = 4;
+// Upper bound of the tiles of mt 16-row blocks: every adapter adds one partly filled at most.
+int64_t lora_tiles(int64_t M, int n, int mt) { return M / (16 * mt) + std::min<int64_t>(n, M); }
 
 }  // namespace
 
-// K splits of the shrink: about two workgroups per compute unit of an MI355X,
-// each wave at least two 32-wide steps.
+// K splits of the shrink: one workgroup, which takes most of a CU's LDS, on every
+// CU of an MI355X, each wave at least one 64-wide step.
 int lora_splits(int64_t M, int64_t K, int R, int n) {
-  const int mt = lora_mt(M, n);
-  const int64_t tiles = (M + 16 * mt - 1) / (16 * mt);
-  const int64_t groups = (R + 63) / 64;
-  int64_t s = 512 / std::max<int64_t>(1, tiles * groups);
-  s = std::min<int64_t>(s, (K + 31) / 32 / (2 * LORA_WAVES));
+  const int mt = many_rows(M, n) ? SHRINK_MT : 1;
+  const int64_t tiles = (M + 16 * mt - 1) / (16 * mt), groups = (R + 63) / 64;
+  int64_t s = 256 / std::max<int64_t>(1, tiles * groups);
+  s = std::min<int64_t>(s, (K + 63) / 64 / SHRINK_WAVES);
   return (int)std::max<int64_t>(1, std::min<int64_t>(s, 16));
 }
 
 hipError_t launch_lora_shrink(const LoraArgs& p, hipStream_t s) {
-  const int mt = lora_mt(p.M, p.n);
+  const int mt = many_rows(p.M, p.n) ? SHRINK_MT : 1;
   const int rt = p.R <= 16 ? 1 : p.R <= 32 ? 2 : 4;
-  const dim3 grid((unsigned)lora_tiles(p.M, p.n, mt), (unsigned)p.splits, (unsigned)((p.R + 16 * rt - 1) / (16 * rt)));
+  const unsigned grid = (unsigned)(lora_tiles(p.M, p.n, mt) * p.splits * ((p.R + 16 * rt - 1) / (16 * rt)));
   auto go = [&](auto d, auto m, auto r) {
-    k_lora_shrink<decltype(d)::value, decltype(m)::value, decltype(r)::value><<<grid, 64 * LORA_WAVES, 0, s>>>(p);
+    k_lora_shrink<decltype(d)::value, decltype(m)::value, decltype(r)::value><<<grid, 64 * SHRINK_WAVES, 0, s>>>(p);
   };
   auto by_rt = [&](auto d, auto m) {
     if (rt == 1) go(d, m, std::integral_constant<int, 1>());
@@ -275,7 +390,7 @@ hipError_t launch_lora_shrink(const LoraArgs& p, hipStream_t s) {
   };
   auto by_mt = [&](auto d) {
     if (mt == 1) by_rt(d, std::integral_constant<int, 1>());
-    else by_rt(d, std::integral_constant<int, 4>());
+    else by_rt(d, std::integral_constant<int, SHRINK_MT>());
   };
   if (p.dt == DT_BF16) by_mt(DtC<DT_BF16>());
   else by_mt(DtC<DT_F16>());
@@ -283,19 +398,27 @@ hipError_t launch_lora_shrink(const LoraArgs& p, hipStream_t s) {
 }
 
 hipError_t launch_lora_expand(const LoraArgs& p, hipStream_t s) {
-  const int mt = lora_mt(p.M, p.n), tm = 16 * mt;
-  const int tiles = lora_tiles(p.M, p.n, mt);
+  const int mt = many_rows(p.M, p.n) ? EXPAND_MT : 1, tm = 16 * mt;
+  const int64_t tiles = (p.M + tm - 1) / tm;
   const int groups = (p.N + 63) / 64;
-  const int runs = std::max(1, std::min((groups + LORA_WAVES - 1) / LORA_WAVES, 1024 / std::max(1, (int)(p.M + tm - 1) / tm)));
-  const int Rp = (p.R + 31) / 32 * 32;
-  const size_t lds = (size_t)tm * (Rp + 8) * 4 + tm * 4;
-  const dim3 grid((unsigned)tiles, (unsigned)runs);
-  auto go = [&](auto d) {
-    if (mt == 1) k_lora_expand<decltype(d)::value, 1><<<grid, 64 * LORA_WAVES, lds, s>>>(p);
-    else k_lora_expand<decltype(d)::value, 4><<<grid, 64 * LORA_WAVES, lds, s>>>(p);
+  // column groups per wave: so many that about 12 waves per compute unit remain
+  const int each = (int)std::max<int64_t>(1, groups * tiles / (12 * 256));
+  const int run = std::min(groups, each * EXPAND_WAVES);
+  const unsigned grid = (unsigned)(lora_tiles(p.M, p.n, mt) * ((groups + run - 1) / run));
+  auto go = [&](auto d, auto m, auto r) {
+    k_lora_expand<decltype(d)::value, decltype(m)::value, decltype(r)::value><<<grid, 64 * EXPAND_WAVES, 0, s>>>(p, run);
   };
-  if (p.dt == DT_BF16) go(DtC<DT_BF16>());
-  else go(DtC<DT_F16>());
+  auto by_r = [&](auto d, auto m) {
+    if (p.R <= 32) go(d, m, std::integral_constant<int, 32>());
+    else if (p.R <= 64) go(d, m, std::integral_constant<int, 64>());
+    else go(d, m, std::integral_constant<int, 128>());
+  };
+  auto by_mt = [&](auto d) {
+    if (mt == 1) by_r(d, std::integral_constant<int, 1>());
+    else by_r(d, std::integral_constant<int, EXPAND_MT>());
+  };
+  if (p.dt == DT_BF16) by_mt(DtC<DT_BF16>());
+  else by_mt(DtC<DT_F16>());
   return hipGetLastError();
 }
 
