@@ -466,25 +466,39 @@ def _dtype(t, name):
 def _run(fn, device, stream, scratch, *args):
     """fn(*args, stream) on `device`; `scratch` is memory of this call's own that the stream goes on using."""
     if stream is None:
-        s = torch.cuda.current_stream(device)
+        # torch.cuda.current_stream(device).cuda_stream without the Stream object, which costs
+        # as much as the library call
+        s = torch._C._cuda_getCurrentRawStream(device.index)
     else:
-        s = stream
+        s = stream.cuda_stream
         if scratch is not None:
-            scratch.record_stream(s)
+            scratch.record_stream(stream)
     if torch.cuda.current_device() == device.index:
-        _check(fn(*args, s.cuda_stream))
+        _check(fn(*args, s))
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, s.cuda_stream))
+            _check(fn(*args, s))
 
 
-def _own(out, shape, dtype, device, stream):
-    """`out`, or a new tensor, known to `stream` where it is not the current one."""
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
-        if stream is not None:
-            out.record_stream(stream)
-    return out
+def _out(out, name, like, stream):
+    """(`out` or a new tensor, its pointer): of the type, shape and device of the contiguous `like`. A new one
+    is made known to `stream` where that is not the current one."""
+    if out is not None:
+        return out, _tensor(out, name, like.dtype, like.shape, like.device)
+    out = torch.empty_like(like)
+    if stream is not None:
+        out.record_stream(stream)
+    return out, out.data_ptr()
+
+
+def _new(out, name, shape, dtype, device, stream):
+    """_out for a tensor that is like no other."""
+    if out is not None:
+        return out, _tensor(out, name, dtype, shape, device)
+    out = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        out.record_stream(stream)
+    return out, out.data_ptr()
 
 
 def _scratch(workspace, nbytes, device):
@@ -509,13 +523,12 @@ def moe_sort(topk_ids, E: int, expert_off=None, row_slot=None, slot_row=None, wo
     _need(dev.type == "cuda", "libmxfp4 takes device tensors")
     _need(1 <= E <= 512, f"E {E} not in [1, 512]")
     ids = _tensor(topk_ids, "topk_ids", i32, (T, k), dev)
-    expert_off = _own(expert_off, (E + 1,), i32, dev, stream)
-    row_slot = _own(row_slot, (T * k,), i32, dev, stream)
-    slot_row = _own(slot_row, (T, k), i32, dev, stream)
+    expert_off, op = _new(expert_off, "expert_off", (E + 1,), i32, dev, stream)
+    row_slot, rp = _new(row_slot, "row_slot", (T * k,), i32, dev, stream)
+    slot_row, sp = _out(slot_row, "slot_row", topk_ids, stream)
     L = lib()
     ws, wp, wn = _scratch(workspace, int(L.mx_moe_sort_workspace_size(T, k, E)), dev)
-    _run(L.mx_moe_sort, dev, stream, ws, ids, T, k, E, _tensor(expert_off, "expert_off", i32, (E + 1,), dev),
-         _tensor(row_slot, "row_slot", i32, (T * k,), dev), _tensor(slot_row, "slot_row", i32, (T, k), dev), wp, wn)
+    _run(L.mx_moe_sort, dev, stream, ws, ids, T, k, E, op, rp, sp, wp, wn)
     return expert_off, row_slot, slot_row
 
 
@@ -526,11 +539,9 @@ def moe_permute(x, slot_row, out=None, stream=None):
     k = slot_row.shape[1]
     dev = x.device
     dt = _dtype(x, "x")
-    out = _own(out, (T * k, H), x.dtype, dev, stream)
-    rows = out.shape[0]
+    out, op = _new(out, "out", (T * k if out is None else out.shape[0], H), x.dtype, dev, stream)
     _run(lib().mx_moe_permute, dev, stream, None, dt, _tensor(x, "x", x.dtype, (T, H), dev), T, H,
-         _tensor(slot_row, "slot_row", torch.int32, (T, k), dev), k, rows,
-         _tensor(out, "out", x.dtype, (rows, H), dev))
+         _tensor(slot_row, "slot_row", torch.int32, (T, k), dev), k, out.shape[0], op)
     return out
 
 
@@ -540,11 +551,10 @@ def moe_unpermute(ys, slot_row, topk_w=None, out=None, stream=None):
     T, k = slot_row.shape
     dev = ys.device
     dt = _dtype(ys, "ys")
-    out = _own(out, (T, H), ys.dtype, dev, stream)
+    out, op = _new(out, "out", (T, H), ys.dtype, dev, stream)
     _run(lib().mx_moe_unpermute, dev, stream, None, dt, _tensor(ys, "ys", ys.dtype, (rows, H), dev), rows, H,
          _tensor(slot_row, "slot_row", torch.int32, (T, k), dev),
-         None if topk_w is None else _tensor(topk_w, "topk_w", torch.float32, (T, k), dev), T, k,
-         _tensor(out, "out", ys.dtype, (T, H), dev))
+         None if topk_w is None else _tensor(topk_w, "topk_w", torch.float32, (T, k), dev), T, k, op)
     return out
 
 
@@ -555,15 +565,15 @@ def moe_unpermute_grad(d_y, ys, slot_row, topk_w, d_ys=None, d_w=None, stream=No
     T, k = slot_row.shape
     dev = ys.device
     dt = _dtype(ys, "ys")
+    yp = _tensor(ys, "ys", ys.dtype, (rows, H), dev)
     if d_ys is None:
         with torch.cuda.stream(stream):
             d_ys = torch.zeros_like(ys)
-    d_w = _own(d_w, (T, k), torch.float32, dev, stream)
-    _run(lib().mx_moe_unpermute_grad, dev, stream, None, dt, _tensor(d_y, "d_y", ys.dtype, (T, H), dev),
-         _tensor(ys, "ys", ys.dtype, (rows, H), dev), rows, H,
-         _tensor(slot_row, "slot_row", torch.int32, (T, k), dev),
-         _tensor(topk_w, "topk_w", torch.float32, (T, k), dev), T, k,
-         _tensor(d_ys, "d_ys", ys.dtype, (rows, H), dev), _tensor(d_w, "d_w", torch.float32, (T, k), dev))
+    wp = _tensor(topk_w, "topk_w", torch.float32, (T, k), dev)
+    d_w, dwp = _out(d_w, "d_w", topk_w, stream)
+    _run(lib().mx_moe_unpermute_grad, dev, stream, None, dt, _tensor(d_y, "d_y", ys.dtype, (T, H), dev), yp, rows, H,
+         _tensor(slot_row, "slot_row", torch.int32, (T, k), dev), wp, T, k,
+         _tensor(d_ys, "d_ys", ys.dtype, (rows, H), dev), dwp)
     return d_ys, d_w
 
 
@@ -592,19 +602,18 @@ def block_norm(residual, w_pre=None, y=None, w_post=None, gate=None, res_scale: 
     dt, adt = _dtype(like, "y or w_pre"), like.dtype
     kind, gshape = _gate(gate, T, H)
     res = _tensor(residual, "residual", residual.dtype, (T, H), dev)
-    ro = no = None
+    yp = ro = no = None
     if y is not None:
-        residual_out = _own(residual_out, (T, H), residual.dtype, dev, stream)
-        ro = _tensor(residual_out, "residual_out", residual.dtype, (T, H), dev)
+        yp = _tensor(y, "y", adt, (T, H), dev)
+        residual_out, ro = _out(residual_out, "residual_out", residual, stream)
     else:
         _need(w_post is None and gate is None and residual_out is None, "w_post, gate and residual_out need y")
     if w_pre is not None:
-        normed = _own(normed, (T, H), adt, dev, stream)
-        no = _tensor(normed, "normed", adt, (T, H), dev)
+        normed, no = _out(normed, "normed", y, stream) if y is not None else \
+            _new(normed, "normed", (T, H), adt, dev, stream)
     else:
         _need(normed is None, "normed needs w_pre")
-    _run(lib().mx_block_norm, dev, stream, None, dt, rdt,
-         None if y is None else _tensor(y, "y", adt, (T, H), dev), res,
+    _run(lib().mx_block_norm, dev, stream, None, dt, rdt, yp, res,
          None if w_post is None else _tensor(w_post, "w_post", adt, (H,), dev), kind,
          None if gate is None else _tensor(gate, "gate", adt, gshape, dev), res_scale,
          None if w_pre is None else _tensor(w_pre, "w_pre", adt, (H,), dev), eps, T, H, ro, no)
@@ -629,24 +638,22 @@ def block_norm_grad(residual_out, w_pre=None, d_normed=None, d_residual_out=None
     like = y if y is not None else w_pre
     dt, adt = _dtype(like, "y or w_pre"), like.dtype
     kind, gshape = _gate(gate, T, H)
-    dw_pre = None if w_pre is None else _own(None, (H,), f32, dev, stream)
-    dw_post = None if w_post is None else _own(None, (H,), f32, dev, stream)
-    d_gate = None if gate is None else _own(None, gshape, adt if kind == 3 else f32, dev, stream)
-    d_residual = _own(d_residual, (T, H), residual_out.dtype, dev, stream)
-    if y is not None:
-        d_y = _own(d_y, (T, H), adt, dev, stream)
-    L = lib()
-    ws, wp, wn = _scratch(workspace, int(L.mx_block_norm_grad_workspace_size(T, H)), dev)
 
     def act(t, name, shape):
         return None if t is None else _tensor(t, name, adt, shape, dev)
-    _run(L.mx_block_norm_grad, dev, stream, ws, dt, rdt, act(y, "y", (T, H)),
-         _tensor(residual_out, "residual_out", residual_out.dtype, (T, H), dev), act(w_post, "w_post", (H,)), kind,
+    yp, rp = act(y, "y", (T, H)), _tensor(residual_out, "residual_out", residual_out.dtype, (T, H), dev)
+    none = (None, None)
+    dw_pre, wpre_p = none if w_pre is None else _new(None, "dw_pre", (H,), f32, dev, stream)
+    dw_post, wpost_p = none if w_post is None else _new(None, "dw_post", (H,), f32, dev, stream)
+    d_gate, gate_p = none if gate is None else _new(None, "d_gate", gshape, adt if kind == 3 else f32, dev, stream)
+    d_residual, dr_p = _out(d_residual, "d_residual", residual_out, stream)
+    d_y, dy_p = none if y is None else _out(d_y, "d_y", y, stream)
+    L = lib()
+    ws, wp, wn = _scratch(workspace, int(L.mx_block_norm_grad_workspace_size(T, H)), dev)
+    _run(L.mx_block_norm_grad, dev, stream, ws, dt, rdt, yp, rp, act(w_post, "w_post", (H,)), kind,
          act(gate, "gate", gshape), res_scale, act(w_pre, "w_pre", (H,)), eps, T, H, act(d_normed, "d_normed", (T, H)),
          None if d_residual_out is None else _tensor(d_residual_out, "d_residual_out", residual_out.dtype, (T, H), dev),
-         _tensor(d_residual, "d_residual", residual_out.dtype, (T, H), dev), act(d_y, "d_y", (T, H)),
-         None if d_gate is None else d_gate.data_ptr(), None if dw_post is None else dw_post.data_ptr(),
-         None if dw_pre is None else dw_pre.data_ptr(), wp, wn)
+         dr_p, dy_p, gate_p, wpost_p, wpre_p, wp, wn)
     return d_residual, dw_pre, d_y, dw_post, d_gate
 
 

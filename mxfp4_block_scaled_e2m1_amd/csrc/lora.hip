@@ -398,12 +398,14 @@ hipError_t launch_lora_shrink(const LoraArgs& p, hipStream_t s) {
 }
 
 hipError_t launch_lora_expand(const LoraArgs& p, hipStream_t s) {
-  const int mt = many_rows(p.M, p.n) ? EXPAND_MT : 1, tm = 16 * mt;
-  const int64_t tiles = (p.M + tm - 1) / tm;
+  const int mt = many_rows(p.M, p.n) ? EXPAND_MT : 1;
   const int groups = (p.N + 63) / 64;
-  // column groups per wave: so many that about 12 waves per compute unit remain
-  const int each = (int)std::max<int64_t>(1, groups * tiles / (12 * 256));
-  const int run = std::min(groups, each * EXPAND_WAVES);
+  // runs of column groups: as many workgroups as fit the CUs of an MI355X at once,
+  // since each joins the tile's splits anew. 4096 x 7168, rank 64: 31.2 us at two
+  // per CU, 41.3 at three (two rounds, the second half empty), 36.8 at four
+  const int64_t runs = std::max<int64_t>(1, (mt == 1 ? 4 : 2) * 256 / lora_tiles(p.M, p.n, mt));
+  const int each = (int)((groups + runs * EXPAND_WAVES - 1) / (runs * EXPAND_WAVES));
+  const int run = each * EXPAND_WAVES;
   const unsigned grid = (unsigned)(lora_tiles(p.M, p.n, mt) * ((groups + run - 1) / run));
   auto go = [&](auto d, auto m, auto r) {
     k_lora_expand<decltype(d)::value, decltype(m)::value, decltype(r)::value><<<grid, 64 * EXPAND_WAVES, 0, s>>>(p, run);
