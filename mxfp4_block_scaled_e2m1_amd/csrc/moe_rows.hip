@@ -14,7 +14,11 @@
 // 16 bytes of one token, which makes the slot's row and weight uniform over the
 // wave (scalar loads, and a skipped slot costs no vector load). Rows that no
 // slot names are neither read nor written. No atomics: the sums run in slot
-// order, so results do not vary between runs.
+// order, so results do not vary between runs. The k-fold side is read and
+// written with streaming accesses. 4096 tokens x 8 slots x 7168 bf16: permute
+// 104.8 -> 93 us with them (529 MB, 5.7 TB/s), unpermute 103.6 -> 89.7 us
+// (5.9 TB/s), gradient 202 -> 182 us (999 MB, 5.5 TB/s); a copy reaches
+// 5.4 to 5.7 TB/s on this card.
 #include <algorithm>
 #include <type_traits>
 
@@ -47,7 +51,7 @@ __global__ __launch_bounds__(64 * MR_WAVES) void k_permute(const char* __restric
     v.load(x + t * width, c * EL);
     for (int j = 0; j < k; ++j) {
       const int r = slot_row[t * k + j];
-      if ((unsigned)r < (unsigned)rows) v.store(xs + (int64_t)r * width, c * EL);
+      if ((unsigned)r < (unsigned)rows) v.template store<true>(xs + (int64_t)r * width, c * EL);
     }
   }
 }
@@ -74,7 +78,7 @@ __global__ __launch_bounds__(64 * MR_WAVES) void k_unpermute(const void* __restr
         v[q].zero();
         if ((unsigned)r < (unsigned)rows) {
           wt[q] = w != nullptr ? w[t * k + j0 + q] : 1.0f;
-          v[q].load(at<DT>(ys, (int64_t)r * H), c);
+          v[q].template load<true>(at<DT>(ys, (int64_t)r * H), c);
         }
       }
 #pragma unroll
@@ -85,7 +89,7 @@ __global__ __launch_bounds__(64 * MR_WAVES) void k_unpermute(const void* __restr
     }
     Raw<DT, N> o;
     o.set(acc);
-    o.store(at<DT>(y, t * H), c);
+    o.template store<true>(at<DT>(y, t * H), c);
   }
 }
 
@@ -115,7 +119,7 @@ __global__ __launch_bounds__(1024) void k_unpermute_grad(const void* __restrict_
         d.load(at<DT>(dy, t * H), c);
 #pragma unroll
         for (int q = 0; q < SLOT_BATCH; ++q)
-          if (row[q] >= 0) v[q].load(at<DT>(ys, (int64_t)row[q] * H), c);
+          if (row[q] >= 0) v[q].template load<true>(at<DT>(ys, (int64_t)row[q] * H), c);
 #pragma unroll
         for (int q = 0; q < SLOT_BATCH; ++q) {
           if (row[q] < 0) continue;
@@ -128,7 +132,7 @@ __global__ __launch_bounds__(1024) void k_unpermute_grad(const void* __restrict_
           }
           Raw<DT, N> r;
           r.set(o);
-          r.store(at<DT>(dys, (int64_t)row[q] * H), c);
+          r.template store<true>(at<DT>(dys, (int64_t)row[q] * H), c);
         }
       }
       group_sum<SLOT_BATCH>(dot, red, waves, threadIdx.x & 63, threadIdx.x >> 6);

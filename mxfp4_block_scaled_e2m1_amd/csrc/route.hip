@@ -179,6 +179,8 @@ __global__ __launch_bounds__(ROUTE_CHUNK) void k_route_scatter(
   }
 }
 
+constexpr int SORT_SELF_SCAN = 128;   // chunks up to which the scatter sums the histograms itself
+
 // The 64 lanes whose valid id equals this lane's: one ballot per id bit, so the
 // cost does not grow with the number of distinct ids in the wave.
 __device__ __forceinline__ uint64_t same_id(int e, bool valid, int bits) {
@@ -191,35 +193,95 @@ __device__ __forceinline__ uint64_t same_id(int e, bool valid, int bits) {
   return m;
 }
 
+// Wave 0 turns the expert totals in LDS into first rows (in place) and returns
+// their sum: lane l scans experts [l * per, (l + 1) * per) after the lanes below it.
+__device__ __forceinline__ int scan_totals(int* tot, int E, int lane) {
+  const int per = (E + 63) / 64;
+  const int x0 = min(lane * per, E), x1 = min(x0 + per, E);
+  int ps = 0;
+  for (int x = x0; x < x1; ++x) ps += tot[x];
+  int pi = ps;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int pu = __shfl_up(pi, d);
+    if (lane >= d) pi += pu;
+  }
+  int o = pi - ps;
+  for (int x = x0; x < x1; ++x) {
+    const int n = tot[x];
+    tot[x] = o;
+    o += n;
+  }
+  return __shfl(pi, 63);
+}
+
 // The scatter of the sort as a plan: places as in k_route_scatter, written as
-// the two inverse maps, -1 where there is no row or no slot.
+// the two inverse maps, -1 where there is no row or no slot. SCAN: every
+// workgroup sums the chunk histograms itself (counts [chunks, E] as k_route_count
+// leaves them), in G = threads / E runs of chunks per expert; a kernel of its own
+// for that costs a launch more than the few reads of a short list of chunks.
+// Otherwise counts and expert_off come scanned from k_route_scan.
+template <bool SCAN>
 __global__ __launch_bounds__(ROUTE_CHUNK) void k_sort_scatter(const int32_t* __restrict__ ids, int64_t P, int E,
-                                                              int bits, const int32_t* __restrict__ chunk_base,
-                                                              const int32_t* __restrict__ expert_off,
+                                                              int bits, const int32_t* __restrict__ counts,
+                                                              int32_t* __restrict__ expert_off,
                                                               int32_t* __restrict__ row_slot,
                                                               int32_t* __restrict__ slot_row) {
   extern __shared__ int wc[];   // [NW][E] pairs per expert in each wave of this chunk
+  __shared__ int run_before[SCAN ? ROUTE_CHUNK : 1], run_all[SCAN ? ROUTE_CHUNK : 1];   // [G][E]
+  __shared__ int before[SCAN ? ROUTE_MAX_EXPERTS : 1], first[SCAN ? ROUTE_MAX_EXPERTS : 1], all;
   constexpr int NW = ROUTE_CHUNK / 64;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int64_t b = blockIdx.x;
+  const int b = blockIdx.x, chunks = gridDim.x;
   for (int i = tid; i < NW * E; i += ROUTE_CHUNK) wc[i] = 0;
-  __syncthreads();
-  const int64_t p = b * ROUTE_CHUNK + tid;
+  const int64_t p = (int64_t)b * ROUTE_CHUNK + tid;
   const int e = (p < P) ? ids[p] : -1;
   const bool valid = (unsigned)e < (unsigned)E;
   const uint64_t m = same_id(e, valid, bits);
   const int rank = __popcll(m & ((1ull << lane) - 1));
-  if (valid && rank == 0) wc[w * E + e] = __popcll(m);
+  const int G = ROUTE_CHUNK / E, g = tid / E, ge = tid - g * E;
+  if (SCAN && g < G) {
+    int sum = 0, pre = 0;
+#pragma unroll 4
+    for (int c = chunks * g / G; c < chunks * (g + 1) / G; ++c) {
+      const int v = counts[(int64_t)c * E + ge];
+      sum += v;
+      pre += c < b ? v : 0;
+    }
+    run_before[tid] = pre;
+    run_all[tid] = sum;
+  }
   __syncthreads();
+  if (valid && rank == 0) wc[w * E + e] = __popcll(m);
+  if (SCAN && tid < E) {
+    int sum = 0, pre = 0;
+    for (int x = 0; x < G; ++x) {
+      pre += run_before[x * E + tid];
+      sum += run_all[x * E + tid];
+    }
+    before[tid] = pre;
+    first[tid] = sum;
+  }
+  __syncthreads();
+  if (SCAN) {
+    if (w == 0) {
+      const int n = scan_totals(first, E, lane);
+      if (lane == 0) all = n;
+    }
+    __syncthreads();
+    if (b == 0 && tid < E) expert_off[tid] = first[tid];
+    if (b == 0 && tid == 0) expert_off[E] = all;
+  }
   int pos = -1;
   if (valid) {
-    pos = expert_off[e] + chunk_base[b * E + e] + rank;
+    pos = SCAN ? first[e] + before[e] : expert_off[e] + counts[(int64_t)b * E + e];
+    pos += rank;
     for (int x = 0; x < w; ++x) pos += wc[x * E + e];
     row_slot[pos] = (int)p;
   }
   if (p < P) {
     slot_row[p] = pos;
-    if (p >= expert_off[E]) row_slot[p] = -1;   // rows behind the last routed pair: written by no slot
+    // rows behind the last routed pair: written by no slot
+    if (p >= (SCAN ? all : expert_off[E])) row_slot[p] = -1;
   }
 }
 
@@ -264,29 +326,12 @@ __global__ __launch_bounds__(ROUTE_CHUNK) void k_sort_one(const int32_t* __restr
     tot[e] = acc;
   }
   __syncthreads();
-  if (tid < 64) {   // lane l scans experts [l * per, (l + 1) * per)
-    const int per = (E + 63) / 64;
-    const int x0 = min(tid * per, E), x1 = min(x0 + per, E);
-    int ps = 0;
-    for (int x = x0; x < x1; ++x) ps += tot[x];
-    int pi = ps;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int pu = __shfl_up(pi, d);
-      if (tid >= d) pi += pu;
-    }
-    int o = pi - ps;
-    for (int x = x0; x < x1; ++x) {
-      const int n = tot[x];
-      tot[x] = o;
-      expert_off[x] = o;
-      o += n;
-    }
-    if (tid == 63) {
-      expert_off[E] = pi;
-      all = pi;
-    }
+  if (tid < 64) {
+    const int n = scan_totals(tot, E, tid);
+    if (tid == 0) all = n;
   }
   __syncthreads();
+  for (int e = tid; e <= E; e += blockDim.x) expert_off[e] = e < E ? tot[e] : all;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int p = c * ROUTE_CHUNK + tid;
@@ -392,11 +437,16 @@ hipError_t launch_sort(const int32_t* ids, int64_t P, int n_experts, int32_t* ex
     return hipGetLastError();
   }
   const int nblocks = (int)((P + ROUTE_CHUNK - 1) / ROUTE_CHUNK);
-  k_route_count<<<nblocks, 256, 0, s>>>(ids, P, n_experts, block_counts);
-  k_route_scan<<<1, ROUTE_SCAN_THREADS, 0, s>>>(block_counts, nblocks, n_experts, expert_off, tile_base);
   const size_t lds = (size_t)(ROUTE_CHUNK / 64) * n_experts * sizeof(int);
-  k_sort_scatter<<<nblocks, ROUTE_CHUNK, lds, s>>>(ids, P, n_experts, bits, block_counts, expert_off, row_slot,
-                                                   slot_row);
+  k_route_count<<<nblocks, 256, 0, s>>>(ids, P, n_experts, block_counts);
+  if (nblocks <= SORT_SELF_SCAN) {
+    k_sort_scatter<true><<<nblocks, ROUTE_CHUNK, lds, s>>>(ids, P, n_experts, bits, block_counts, expert_off, row_slot,
+                                                           slot_row);
+  } else {
+    k_route_scan<<<1, ROUTE_SCAN_THREADS, 0, s>>>(block_counts, nblocks, n_experts, expert_off, tile_base);
+    k_sort_scatter<false><<<nblocks, ROUTE_CHUNK, lds, s>>>(ids, P, n_experts, bits, block_counts, expert_off,
+                                                            row_slot, slot_row);
+  }
   return hipGetLastError();
 }
 
