@@ -26,7 +26,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int SHRINK_WAVES = 8;   // waves of a shrink workgroup, which split its K range
+constexpr int SHRINK_WAVES = 4;   // waves of a shrink workgroup, which split its K range
 constexpr int EXPAND_WAVES = 4;   // waves of an expand workgroup, which split its columns
 
 template <int DT>
@@ -70,15 +70,16 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ off, int n
     }
     return inc;
   };
-  int lo, hi, cnt, total = 0;
-  for (int a0 = 0; a0 < n; a0 += 64) total += __builtin_amdgcn_readlane(chunk(a0, lo, hi, cnt), 63);
+  int lo, hi, cnt, inc = chunk(0, lo, hi, cnt);
+  int total = __builtin_amdgcn_readlane(inc, 63);
+  for (int a0 = 64; a0 < n; a0 += 64) total += __builtin_amdgcn_readlane(chunk(a0, lo, hi, cnt), 63);
   const int work = total * pieces;
   if (id >= work) return {-1, 0, 0, 0};
   const int xcd = id & 7, mine = (work >> 3) * xcd + min(xcd, work & 7) + (id >> 3);
   const int tile = mine / pieces;
   int before = 0;
   for (int a0 = 0; a0 < n; a0 += 64) {
-    const int inc = chunk(a0, lo, hi, cnt);
+    if (n > 64) inc = chunk(a0, lo, hi, cnt);
     const uint64_t hit = __ballot(before + inc > tile);
     if (hit) {
       const int l = __ffsll((long long)hit) - 1;
@@ -103,7 +104,7 @@ __device__ __forceinline__ void wave_sync() {
 // (4096 x 7168, rank 64: 39 us that way even with x in L2). So a wave loads whole
 // 128-byte lines, eight lanes each, the rows of a 64-wide step of K, turns them
 // in an LDS area of its own (pitch 144: conflict-free) and has the next
-// step's loads in flight meanwhile. The waves take the steps of a split in turn,
+// two steps' loads in flight meanwhile. The waves take the steps of a split in turn,
 // 1 KB of a row together, and join their sums in LDS.
 // Workgroups of a tile: K splits by groups of 16 RT ranks.
 constexpr int SHRINK_PITCH = 128 + 16;
@@ -120,12 +121,9 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(LoraArgs p) {
   const int split = tile.piece / rgroups, r0 = (tile.piece - split * rgroups) * 16 * RT;
   const int lrow = lane >> 3, lcol = (lane & 7) * 8;          // of a load
   // rows past the tile or the rank repeat the last one; their results are not kept
-  const uint16_t* xr[XI];
+  int tok[XI];
 #pragma unroll
-  for (int i = 0; i < XI; ++i) {
-    const int tok = p.row_token[tile.row0 + min(8 * i + lrow, tile.rows - 1)];
-    xr[i] = (const uint16_t*)p.x + (int64_t)min(max(tok, 0), p.M - 1) * p.ldx + lcol;
-  }
+  for (int i = 0; i < XI; ++i) tok[i] = p.row_token[tile.row0 + min(8 * i + lrow, tile.rows - 1)];
   const uint16_t* am = (const uint16_t*)p.a + (int64_t)tile.adapter * p.R * p.K;
   uint32_t ao[AI];
 #pragma unroll
@@ -135,20 +133,27 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(LoraArgs p) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[m][r] = f32x4{0.f, 0.f, 0.f, 0.f};
-  u32v4 v[XI + AI];
-  auto fetch = [&](int k) {
+  struct Step {
+    u32v4 a[AI], x[XI];
+  };
+  const uint16_t* xr[XI];
+  auto fetch_a = [&](Step& f, int k) {
 #pragma unroll
-    for (int i = 0; i < XI; ++i) v[i] = *(const u32v4*)(xr[i] + k);
+    for (int i = 0; i < AI; ++i) f.a[i] = *(const u32v4*)(am + k + ao[i]);
+  };
+  auto fetch_x = [&](Step& f, int k) {
 #pragma unroll
-    for (int i = 0; i < AI; ++i) v[XI + i] = *(const u32v4*)(am + k + ao[i]);
+    for (int i = 0; i < XI; ++i) f.x[i] = *(const u32v4*)(xr[i] + k);
   };
   uint8_t* area = lds + wave * AREA;
   uint8_t* put = area + lrow * SHRINK_PITCH + lcol * 2;
   const uint8_t* get = area + (lane & 15) * SHRINK_PITCH + (lane >> 4) * 16;
-  auto stage = [&]() {
+  auto stage = [&](const Step& f) {
     wave_sync();
 #pragma unroll
-    for (int i = 0; i < XI + AI; ++i) *(u32v4*)(put + 8 * i * SHRINK_PITCH) = v[i];
+    for (int i = 0; i < XI; ++i) *(u32v4*)(put + 8 * i * SHRINK_PITCH) = f.x[i];
+#pragma unroll
+    for (int i = 0; i < AI; ++i) *(u32v4*)(put + 8 * (XI + i) * SHRINK_PITCH) = f.a[i];
     wave_sync();
   };
   auto multiply = [&]() {
@@ -165,14 +170,43 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(LoraArgs p) {
       }
     }
   };
-  const int steps = p.K / 64;
-  const int s1 = (int)((int64_t)steps * (split + 1) / p.splits);
-  int s = (int)((int64_t)steps * split / p.splits) + wave;
-  if (s < s1) {
-    fetch(s * 64);
-    for (; s < s1; s += SHRINK_WAVES) {
-      stage();
-      if (s + SHRINK_WAVES < s1) fetch((s + SHRINK_WAVES) * 64);
+  // this wave's steps: of the split's, every SHRINK_WAVES-th
+  const int steps = p.K / 64, s0 = (int)((int64_t)steps * split / p.splits) + wave;
+  const int n = ((int)((int64_t)steps * (split + 1) / p.splits) - s0 + SHRINK_WAVES - 1) / SHRINK_WAVES;
+  auto k_of = [&](int i) { return (s0 + i * SHRINK_WAVES) * 64; };
+  Step fa, fb;
+  if (n > 0) fetch_a(fa, k_of(0));       // does not wait for the tokens
+#pragma unroll
+  for (int i = 0; i < XI; ++i) xr[i] = (const uint16_t*)p.x + (int64_t)min(max(tok[i], 0), p.M - 1) * p.ldx + lcol;
+  if (n > 0) {
+    // two steps in flight; no condition on a load inside the loop, or its wait
+    // would be for everything
+    fetch_x(fa, k_of(0));
+    fetch_a(fb, k_of(min(1, n - 1)));
+    fetch_x(fb, k_of(min(1, n - 1)));
+    int i = 0;
+    for (; i + 3 < n; i += 2) {
+      stage(fa);
+      fetch_a(fa, k_of(i + 2));
+      fetch_x(fa, k_of(i + 2));
+      multiply();
+      stage(fb);
+      fetch_a(fb, k_of(i + 3));
+      fetch_x(fb, k_of(i + 3));
+      multiply();
+    }
+    stage(fa);
+    if (i + 2 < n) {
+      fetch_a(fa, k_of(i + 2));
+      fetch_x(fa, k_of(i + 2));
+    }
+    multiply();
+    if (i + 1 < n) {
+      stage(fb);
+      multiply();
+    }
+    if (i + 2 < n) {
+      stage(fa);
       multiply();
     }
   }
@@ -180,9 +214,14 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(LoraArgs p) {
     // the rest of K, a multiple of 8: a lane's eight elements are in or out
     const int k = steps * 64;
 #pragma unroll
-    for (int i = 0; i < XI + AI; ++i) v[i] = u32v4{0, 0, 0, 0};
-    if (k + lcol < p.K) fetch(k);
-    stage();
+    for (int i = 0; i < AI; ++i) fa.a[i] = u32v4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < XI; ++i) fa.x[i] = u32v4{0, 0, 0, 0};
+    if (k + lcol < p.K) {
+      fetch_a(fa, k);
+      fetch_x(fa, k);
+    }
+    stage(fa);
     multiply();
   }
   __syncthreads();                 // the areas become the sums to join
@@ -205,16 +244,17 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(LoraArgs p) {
 }
 
 // y += scale B v of one tile, RP the rank rounded up to 32, 64 or 128. A wave
-// takes 64 columns at a time: their rows of B, one piece of memory, come in
-// whole lines and are turned into matrix operands in the wave's own LDS area, and
-// so are the products on their way to y, which is read and written 128 bytes a
-// token (with the operands' own lanes, 16 tokens side by side, the address
-// path took most of 53 us for 4096 x 7168, rank 64).
+// takes 64 columns at a time, their ranks up to 64 at a time: these rows of B come
+// in whole lines, one piece ahead, and are turned into matrix operands in the
+// wave's own LDS area, and so are the products on their way to y, which is read
+// and written 128 bytes a token (with the operands' own lanes, 16 tokens side
+// by side, the address path took most of 53 us for 4096 x 7168, rank 64).
 // Workgroups of a tile: runs of `run` column groups.
 template <int DT, int MT, int RP>
 __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, int run) {
   constexpr int TM = 16 * MT, VP = RP + 8;                   // pitch of v in 16-bit elements
-  constexpr int BP = RP * 2 + 16, CP = 64 * 4 + 16;          // pitches in bytes: of B, of the products
+  constexpr int RH = RP < 64 ? RP : 64, HALVES = RP / RH;    // ranks at a time
+  constexpr int BP = RH * 2 + 16, CP = 64 * 4 + 16;          // pitches in bytes: of B, of the products
   constexpr int AREA = 64 * BP > 16 * CP ? 64 * BP : 16 * CP;
   __shared__ __attribute__((aligned(16))) uint16_t vh[TM * VP], vl[TM * VP];
   __shared__ __attribute__((aligned(16))) uint8_t lds[EXPAND_WAVES * AREA];
@@ -224,6 +264,38 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
   if (tile.adapter < 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float scale = p.scale != nullptr ? p.scale[tile.adapter] : 1.0f;
+  const int c = lane & 15, q = lane >> 4, lrow = lane >> 3, lcol = (lane & 7) * 8;
+  int ytok[2 * MT];
+#pragma unroll
+  for (int i = 0; i < 2 * MT; ++i) ytok[i] = p.row_token[tile.row0 + min(8 * i + lrow, tile.rows - 1)];
+  // B pieces of 16 bytes. Ranks up to 32: the group's rows are one run of
+  // 64 R / 8 pieces, 64 at a time. Above: eight lanes per row, those past the rank
+  // repeat its last piece (what they bring is masked below).
+  constexpr int BI = RH / 8;
+  const int per_row = p.R / 8;
+  uint32_t bsrc[BI], bput[BI];
+#pragma unroll
+  for (int i = 0; i < BI; ++i) {
+    const int flat = i * 64 + lane;
+    const int row = RP == 32 ? flat / per_row : flat >> 3, piece = RP == 32 ? flat - row * per_row : flat & 7;
+    bsrc[i] = RP == 32 ? flat * 8 : row * p.R;
+    bput[i] = row * BP + piece * 16;
+  }
+  const uint16_t* bm = (const uint16_t*)p.b + (int64_t)tile.adapter * p.N * p.R;
+  u32v4 bv[BI];
+  auto fetch = [&](int g, int h) {
+    const int n0 = g * 64, rows = min(64, p.N - n0);
+    const uint16_t* bg = bm + (int64_t)n0 * p.R;
+#pragma unroll
+    for (int i = 0; i < BI; ++i) {
+      uint32_t at;
+      if constexpr (RP == 32) at = min(bsrc[i], (uint32_t)(rows * p.R - 8));
+      else at = min(bsrc[i], (uint32_t)((rows - 1) * p.R)) + min(h * 64 + (lane & 7) * 8, p.R - 8);
+      if (RP != 32 || i < per_row) bv[i] = *(const u32v4*)(bg + at);
+    }
+  };
+  const int g0 = tile.piece * run, g1 = min(groups, g0 + run);
+  if (g0 + wave < g1) fetch(g0 + wave, 0);                   // on its way while v is formed
   // v of the tile: RP / 4 lanes per row, four ranks each; the splits' partial
   // sums, eight loads at a time, in split order
   constexpr int PER = RP / 4, ROWS = 64 / PER;
@@ -268,66 +340,55 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
     *(u32v2*)(vl + row * VP + r) = u32v2{l[0], l[1]};
     if (r == 0) fac[row] = scale * up;
   }
-  const int c = lane & 15, q = lane >> 4, lrow = lane >> 3, lcol = (lane & 7) * 8;
   // y pieces: token 8 i + lane / 8 of the tile, columns 8 (lane % 8) of the group;
   // rows past the tile repeat the last one and are not written
   const char* yr[2 * MT];
   bool mine[2 * MT];
 #pragma unroll
   for (int i = 0; i < 2 * MT; ++i) {
-    const int row = 8 * i + lrow, tok = p.row_token[tile.row0 + min(row, tile.rows - 1)];
-    mine[i] = row < tile.rows && (unsigned)tok < (unsigned)p.M;
-    yr[i] = at<DT>((const void*)p.y, (int64_t)min(max(tok, 0), p.M - 1) * p.ldy);
+    mine[i] = 8 * i + lrow < tile.rows && (unsigned)ytok[i] < (unsigned)p.M;
+    yr[i] = at<DT>((const void*)p.y, (int64_t)min(max(ytok[i], 0), p.M - 1) * p.ldy);
   }
-  // B pieces of 16 bytes: number i * 64 + lane of the group's rows
-  const int per_row = p.R / 8;
   uint8_t* area = lds + wave * AREA;
-  uint32_t bput[RP / 8];
-#pragma unroll
-  for (int i = 0; i < RP / 8; ++i) {
-    const int at = i * 64 + lane, row = at / per_row;
-    bput[i] = row * BP + (at - row * per_row) * 16;
-  }
   __syncthreads();
-  const uint16_t* bm = (const uint16_t*)p.b + (int64_t)tile.adapter * p.N * p.R;
-  const int g0 = tile.piece * run, g1 = min(groups, g0 + run);
   for (int g = g0 + wave; g < g1; g += EXPAND_WAVES) {
-    const int n0 = g * 64, last = min(64, p.N - n0) * per_row - 1;
-    u32v4 bv[RP / 8];
-    const uint16_t* bg = bm + (int64_t)n0 * p.R;
-#pragma unroll
-    for (int i = 0; i < RP / 8; ++i)
-      if (i < per_row) bv[i] = *(const u32v4*)(bg + min(i * 64 + lane, last) * 8);
-    const int n = min(n0 + lcol, p.N - 8);                  // N % 8 == 0
+    const int n0 = g * 64, n = min(n0 + lcol, p.N - 8);     // N % 8 == 0
     Raw<DT, 8> y[2 * MT];
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i) y[i].load(yr[i], n);
-    wave_sync();
-#pragma unroll
-    for (int i = 0; i < RP / 8; ++i)
-      if (i < per_row) *(u32v4*)(area + bput[i]) = bv[i];
-    wave_sync();
     f32x4 acc[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < RP; k += 32) {
-      u32v4 bf[4];
+    for (int h = 0; h < HALVES; ++h) {
+      wave_sync();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf[j] = *(const u32v4*)(area + (16 * j + c) * BP + k * 2 + q * 16);
-        if (k + q * 8 >= p.R) bf[j] = u32v4{0, 0, 0, 0};    // past the rank: whatever LDS held
-      }
+      for (int i = 0; i < BI; ++i)
+        if (RP != 32 || i < per_row) *(u32v4*)(area + bput[i]) = bv[i];
+      wave_sync();
+      // the next piece, or at the end this one again: no condition on the loads
+      if (h + 1 < HALVES) fetch(g, h + 1);
+      else fetch(min(g + EXPAND_WAVES, groups - 1), 0);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int w = (m * 16 + c) * VP + k + q * 8;
-        const u32v4 h = *(const u32v4*)(vh + w), l = *(const u32v4*)(vl + w);
+      for (int k = 0; k < RH; k += 32) {
+        const int r0 = h * RH + k + q * 8;
+        u32v4 bf[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          acc[m][j] = mma<DT>(bf[j], l, acc[m][j]);
-          acc[m][j] = mma<DT>(bf[j], h, acc[m][j]);
+          bf[j] = *(const u32v4*)(area + (16 * j + c) * BP + k * 2 + q * 16);
+          if (r0 >= p.R) bf[j] = u32v4{0, 0, 0, 0};          // past the rank: whatever LDS held
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int w = (m * 16 + c) * VP + r0;
+          const u32v4 hi = *(const u32v4*)(vh + w), lo = *(const u32v4*)(vl + w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[m][j] = mma<DT>(bf[j], lo, acc[m][j]);
+            acc[m][j] = mma<DT>(bf[j], hi, acc[m][j]);
+          }
         }
       }
     }
@@ -357,27 +418,43 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
   }
 }
 
-// Whether adapters have many rows each: tiles of several 16-row blocks then, else
-// of one (a tile holds one adapter's rows, so more would mostly be padding).
-bool many_rows(int64_t M, int n) { return M >= 32 * (int64_t)std::min<int64_t>(n, M) && M >= 64; }
-constexpr int SHRINK_MT = 4, EXPAND_MT = 4;
+// 16-row blocks per tile. A tile holds one adapter's rows, so it is no larger than
+// an adapter's share; and a larger one reads A and B less often but leaves fewer
+// workgroups, so it takes many rows to pay.
+int row_blocks(int64_t M, int n, int most, int64_t from) {
+  const int64_t share = M / std::min<int64_t>(n, std::max<int64_t>(M, 1));
+  return M >= from && share >= 16 * most ? most : 1;
+}
+constexpr int SHRINK_MT = 2, EXPAND_MT = 4;
+int shrink_mt(int64_t M, int n) { return row_blocks(M, n, SHRINK_MT, 1024); }
+int expand_mt(int64_t M, int n) { return row_blocks(M, n, EXPAND_MT, 2048); }
 // Upper bound of the tiles of mt 16-row blocks: every adapter adds one partly filled at most.
 int64_t lora_tiles(int64_t M, int n, int mt) { return M / (16 * mt) + std::min<int64_t>(n, M); }
 
 }  // namespace
 
-// K splits of the shrink: one workgroup, which takes most of a CU's LDS, on every
-// CU of an MI355X, each wave at least one 64-wide step.
+// K splits of the shrink: the number that a workgroup's steps and the rounds of
+// workgroups, two on each CU of an MI355X, make fastest; a workgroup costs about
+// three steps beside its own. 1 to 16, each wave at least one step.
 int lora_splits(int64_t M, int64_t K, int R, int n) {
-  const int mt = many_rows(M, n) ? SHRINK_MT : 1;
-  const int64_t tiles = (M + 16 * mt - 1) / (16 * mt), groups = (R + 63) / 64;
-  int64_t s = 256 / std::max<int64_t>(1, tiles * groups);
-  s = std::min<int64_t>(s, (K + 63) / 64 / SHRINK_WAVES);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(s, 16));
+  const int mt = shrink_mt(M, n);
+  const int64_t tiles = (M + 16 * mt - 1) / (16 * mt) + std::min<int64_t>(n, M) / 2, groups = (R + 63) / 64;
+  const int64_t steps = K / 64, most = std::min<int64_t>(16, std::max<int64_t>(1, steps / SHRINK_WAVES));
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= most; ++s) {
+    const int64_t rounds = (tiles * groups * s + 511) / 512;
+    const double cost = (double)rounds * ((double)steps / (s * SHRINK_WAVES) + 3.0);
+    if (s == 1 || cost < least) {
+      best = s;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 hipError_t launch_lora_shrink(const LoraArgs& p, hipStream_t s) {
-  const int mt = many_rows(p.M, p.n) ? SHRINK_MT : 1;
+  const int mt = shrink_mt(p.M, p.n);
   const int rt = p.R <= 16 ? 1 : p.R <= 32 ? 2 : 4;
   const unsigned grid = (unsigned)(lora_tiles(p.M, p.n, mt) * p.splits * ((p.R + 16 * rt - 1) / (16 * rt)));
   auto go = [&](auto d, auto m, auto r) {
@@ -398,7 +475,7 @@ hipError_t launch_lora_shrink(const LoraArgs& p, hipStream_t s) {
 }
 
 hipError_t launch_lora_expand(const LoraArgs& p, hipStream_t s) {
-  const int mt = many_rows(p.M, p.n) ? EXPAND_MT : 1;
+  const int mt = expand_mt(p.M, p.n);
   const int groups = (p.N + 63) / 64;
   // runs of column groups: as many workgroups as fit the CUs of an MI355X at once,
   // since each joins the tile's splits anew. 4096 x 7168, rank 64: 31.2 us at two
