@@ -63,7 +63,7 @@ __device__ __forceinline__ void walk_rows(int64_t T, int groups, int group, Fetc
 // next row's pieces are loaded before this row's sums are waited for: with
 // one workgroup on a CU the sums would otherwise leave HBM idle, and more
 // workgroups are slower (the streams they make spread over HBM).
-template <int DT, int RDT, int N, int V, int GATE, bool PF>
+template <int DT, int RDT, int N, int V, int GATE, bool PF, bool AL>
 __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a, int gw) {
   __shared__ float red_all[16 * 2 * 16];                 // per group 2 * 16
   const int threads = gw * 64, groups = blockDim.x / threads, lane = threadIdx.x & 63;
@@ -79,16 +79,24 @@ __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a, int gw) {
     const int c = (v * threads + tid) * N;
     wpost[v].zero(); wpre[v].zero(); gch[v].zero();
     if (c < H) {
-      if (has_post) wpost[v].load(a.w_post, c);
+      if (has_post) wpost[v].template load_row<false, AL>(a.w_post, c, H);
       else wpost[v].fill(1.0f);
-      if (has_pre) wpre[v].load(a.w_pre, c);
-      if (GATE == GATE_CHANNEL) gch[v].load(a.gate, c);
+      if (has_pre) wpre[v].template load_row<false, AL>(a.w_pre, c, H);
+      if (GATE == GATE_CHANNEL) gch[v].template load_row<false, AL>(a.gate, c, H);
+      wpost[v].template settle<AL>(c, H);
+      wpre[v].template settle<AL>(c, H);
+      gch[v].template settle<AL>(c, H);
     }
   }
   struct Row {
     Raw<DT, N> y[V], g[V];
     Raw<RDT, N> res[V];
     Raw<DT, 1> gt;      // of a token gate
+    __device__ __forceinline__ void settle(int v, int c, int H) {
+      y[v].template settle<AL>(c, H);
+      if (GATE == GATE_FULL) g[v].template settle<AL>(c, H);
+      res[v].template settle<AL>(c, H);
+    }
   };
   auto fetch = [&](Row& f, int64_t t) {
     const int64_t base = t * H;
@@ -99,15 +107,22 @@ __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a, int gw) {
       const int c = (v * threads + tid) * N;
       f.y[v].zero(); f.res[v].zero(); f.g[v].zero();
       if (c < H && t < a.T) {
-        if (has_y) f.y[v].template load<true>(at<DT>(a.y, base), c);
-        f.res[v].template load<true>(at<RDT>(a.residual, base), c);
-        if (GATE == GATE_FULL) f.g[v].template load<true>(at<DT>(a.gate, base), c);
+        if (has_y) f.y[v].template load_row<true, AL>(at<DT>(a.y, base), c, H);
+        f.res[v].template load_row<true, AL>(at<RDT>(a.residual, base), c, H);
+        if (GATE == GATE_FULL) f.g[v].template load_row<true, AL>(at<DT>(a.gate, base), c, H);
       }
     }
   };
   auto turn = [&](Row& f, int64_t t) {
     const bool live = t < a.T;
     const int64_t base = t * H;
+    if (!AL) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * threads + tid) * N;
+        if (c < H) f.settle(v, c, H);
+      }
+    }
     if (dt_size<DT> == 2) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -144,7 +159,7 @@ __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a, int gw) {
       if (has_y && live && c < H) {
         Raw<RDT, N> o;
         o.set(r[v]);
-        o.store(at<RDT>(a.residual_out, base), c);
+        o.template store_row<false, AL>(at<RDT>(a.residual_out, base), c, H);
       }
     }
     if (has_pre) {
@@ -159,7 +174,7 @@ __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a, int gw) {
           for (int i = 0; i < N; ++i) n[i] = r[v][i] * fn * wpre[v].get(i);
           Raw<DT, N> o;
           o.set(n);
-          o.store(at<DT>(a.normed, base), c);
+          o.template store_row<false, AL>(at<DT>(a.normed, base), c, H);
         }
       }
     }
@@ -178,7 +193,7 @@ __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a, int gw) {
 // k_block_norm_cols). GATE: the gate kind. PF: the next row's pieces are loaded
 // before this row's sums are waited for, since one workgroup fills a CU and its
 // two row sums would otherwise leave HBM idle.
-template <int DT, int RDT, int N, int V, int GATE, bool PF>
+template <int DT, int RDT, int N, int V, int GATE, bool PF, bool AL>
 __global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a, int gw) {
   __shared__ float red_all[16 * 4 * 16];                 // per group 4 * 16
   extern __shared__ float cols[];                        // [groups][H], when groups > 1
@@ -196,10 +211,13 @@ __global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a, i
     const int c = (v * threads + tid) * N;
     wpost[v].zero(); wpre[v].zero(); gch[v].zero();
     if (c < H) {
-      if (has_post) wpost[v].load(a.w_post, c);
+      if (has_post) wpost[v].template load_row<false, AL>(a.w_post, c, H);
       else wpost[v].fill(1.0f);
-      if (has_pre) wpre[v].load(a.w_pre, c);
-      if (GATE == GATE_CHANNEL) gch[v].load(a.gate, c);
+      if (has_pre) wpre[v].template load_row<false, AL>(a.w_pre, c, H);
+      if (GATE == GATE_CHANNEL) gch[v].template load_row<false, AL>(a.gate, c, H);
+      wpost[v].template settle<AL>(c, H);
+      wpre[v].template settle<AL>(c, H);
+      gch[v].template settle<AL>(c, H);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) cpre[v][i] = cpost[v][i] = 0.0f;
@@ -208,6 +226,13 @@ __global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a, i
     Raw<DT, N> y[V], dn[V], g[V];
     Raw<RDT, N> r[V], dro[V];
     Raw<DT, 1> gt;      // of a token gate; with the rest, for a load in between would wait for the next row's
+    __device__ __forceinline__ void settle(int v, int c, int H) {
+      y[v].template settle<AL>(c, H);
+      dn[v].template settle<AL>(c, H);
+      if (GATE == GATE_FULL) g[v].template settle<AL>(c, H);
+      r[v].template settle<AL>(c, H);
+      dro[v].template settle<AL>(c, H);
+    }
   };
   auto fetch = [&](Row& f, int64_t t) {
     const int64_t base = t * H;
@@ -219,18 +244,25 @@ __global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a, i
       f.y[v].zero(); f.dn[v].zero(); f.g[v].zero(); f.r[v].zero(); f.dro[v].zero();
       if (c < H && t < a.T) {
         if (has_pre) {
-          f.r[v].template load<true>(at<RDT>(a.residual_out, base), c);
-          f.dn[v].template load<true>(at<DT>(a.d_normed, base), c);
+          f.r[v].template load_row<true, AL>(at<RDT>(a.residual_out, base), c, H);
+          f.dn[v].template load_row<true, AL>(at<DT>(a.d_normed, base), c, H);
         }
-        if (has_y) f.y[v].template load<true>(at<DT>(a.y, base), c);
-        if (has_dro) f.dro[v].template load<true>(at<RDT>(a.d_residual_out, base), c);
-        if (GATE == GATE_FULL) f.g[v].template load<true>(at<DT>(a.gate, base), c);
+        if (has_y) f.y[v].template load_row<true, AL>(at<DT>(a.y, base), c, H);
+        if (has_dro) f.dro[v].template load_row<true, AL>(at<RDT>(a.d_residual_out, base), c, H);
+        if (GATE == GATE_FULL) f.g[v].template load_row<true, AL>(at<DT>(a.gate, base), c, H);
       }
     }
   };
   auto turn = [&](Row& f, int64_t t) {
     const bool live = t < a.T;
     const int64_t base = t * H;
+    if (!AL) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * threads + tid) * N;
+        if (c < H) f.settle(v, c, H);
+      }
+    }
     if (dt_size<DT> == 2) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -276,7 +308,7 @@ __global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a, i
       if (c < H && live) {
         Raw<RDT, N> o;
         o.set(dr[v]);
-        o.store(at<RDT>(a.d_residual, base), c);
+        o.template store_row<false, AL>(at<RDT>(a.d_residual, base), c, H);
       }
     }
     if (has_y) {
@@ -309,13 +341,13 @@ __global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a, i
         if (c < H && live) {
           Raw<DT, N> o;
           o.set(dy);
-          o.store(at<DT>(a.dy, base), c);
+          o.template store_row<false, AL>(at<DT>(a.dy, base), c, H);
           if (GATE == GATE_FULL) {
             float dg[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) dg[i] = a.res_scale * dr[v][i] * (f.y[v].get(i) * fy) * wpost[v].get(i);
             o.set(dg);
-            o.store(at<DT>(a.dgate, base), c);
+            o.template store_row<false, AL>(at<DT>(a.dgate, base), c, H);
           }
         }
       }
@@ -338,11 +370,10 @@ __global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradArgs a, i
         o.set(which == 0 ? cpre[v] : cpost[v]);
         if (groups > 1) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) cols[group * H + c + i] = o.get(i);
-        } else if constexpr (N == 1) {
-          part[which * H + c] = o.get(0);
+          for (int i = 0; i < N; ++i)
+            if (AL || c + i < H) cols[group * H + c + i] = o.get(i);
         } else {
-          o.store(part + which * H, c);
+          o.template store_row<false, AL>(part + which * H, c, H);
         }
       }
     }
@@ -402,23 +433,15 @@ __global__ __launch_bounds__(1024) void k_block_norm_cols(BlockNormGradArgs a, i
   if (a.dw_post) a.dw_post[c] = s;
 }
 
-// Pieces of N elements per thread (V) and waves of a row.
+// Pieces of N elements per thread (V) and waves of a row of up to 16384 elements.
 struct RowShape {
   int V, waves;
 };
 RowShape row_shape(int H, int N, int most_waves) {
   const int pieces = (H + N - 1) / N;
   const int V = (pieces + 64 * most_waves - 1) / (64 * most_waves);
-  const int v = V <= 1 ? 1 : V <= 2 ? 2 : V <= 4 ? 4 : V <= 8 ? 8 : 16;
+  const int v = V <= 1 ? 1 : V <= 2 ? 2 : 4;
   return {v, (pieces + 64 * v - 1) / (64 * v)};
-}
-
-// Rows that do not start on 16 bytes, element by element: V rounded up.
-template <class F>
-void dispatch_v(int V, F&& f) {
-  if (V == 1) f(std::integral_constant<int, 1>());
-  else if (V <= 4) f(std::integral_constant<int, 4>());
-  else f(std::integral_constant<int, 16>());
 }
 
 template <class F>
@@ -441,9 +464,9 @@ void dispatch_pair(DType dt, DType rdt, F&& f) {
 
 }  // namespace
 
-// Eight elements per piece, four of fp32, where every row starts on 16 bytes.
+// Elements per piece: 16 bytes of the activations.
 static int piece(DType dt) { return dt == DT_F32 ? 4 : 8; }
-bool block_norm_vec(DType dt, int H, uintptr_t all_pointers) { return H % piece(dt) == 0 && all_pointers % 16 == 0; }
+bool block_norm_aligned(DType dt, int H, uintptr_t all_pointers) { return H % piece(dt) == 0 && all_pointers % 16 == 0; }
 
 // One workgroup of up to 16 waves per CU of an MI355X. Measured on 4096 x 7168,
 // bf16 beside an fp32 residual, before the prefetch: 14 waves on every CU 65.9 us,
@@ -457,61 +480,59 @@ int row_groups(int64_t T, int waves) {
 // An upper bound of the workgroups of the way back, each with a partial sum.
 int block_norm_grad_grid(int64_t T) { return (int)std::min<int64_t>(T, ROW_GRID); }
 
-hipError_t launch_block_norm(const BlockNormArgs& a, bool vec, hipStream_t s) {
-  const RowShape sh = row_shape(a.H, vec ? piece(a.dt) : 1, 16);
+// f(elements per piece, pieces per thread, aligned)
+template <int D, class F>
+void dispatch_shape(int H, int V, bool aligned, F&& f) {
+  constexpr int P = D == DT_F32 ? 4 : 8;
+  std::integral_constant<int, P> n;
+  auto v = [&](auto vc) {
+    if (aligned) f(n, vc, std::true_type());
+    else f(n, vc, std::false_type());
+  };
+  if (H < P) f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>(), std::true_type());   // no whole piece
+  else if (V == 1) v(std::integral_constant<int, 1>());
+  else if (V == 2) v(std::integral_constant<int, 2>());
+  else if constexpr (D == DT_F32) v(std::integral_constant<int, 4>());
+}
+
+hipError_t launch_block_norm(const BlockNormArgs& a, bool aligned, hipStream_t s) {
+  const RowShape sh = row_shape(a.H, piece(a.dt), 16);
   const int groups = row_groups(a.T, sh.waves);
   const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, ROW_GRID);
   const int threads = 64 * sh.waves * groups;
   dispatch_pair(a.dt, a.rdt, [&](auto d, auto r) {
     constexpr int D = decltype(d)::value, R = decltype(r)::value;
-    auto go = [&](auto n, auto v) {
-      constexpr int NN = decltype(n)::value, VV = decltype(v)::value;
+    dispatch_shape<D>(a.H, sh.V, aligned, [&](auto n, auto v, auto al) {
       dispatch_gate(a.gate_kind, [&](auto g) {
-        k_block_norm<D, R, NN, VV, decltype(g)::value, NN != 1 && VV == 1><<<grid, threads, 0, s>>>(a, sh.waves);
+        constexpr int V = decltype(v)::value;
+        k_block_norm<D, R, decltype(n)::value, V, decltype(g)::value, V == 1, decltype(al)::value>
+            <<<grid, threads, 0, s>>>(a, sh.waves);
       });
-    };
-    if (vec) {
-      std::integral_constant<int, D == DT_F32 ? 4 : 8> n;
-      if (sh.V == 1) go(n, std::integral_constant<int, 1>());
-      else if (sh.V == 2) go(n, std::integral_constant<int, 2>());
-      else if (sh.V == 4) go(n, std::integral_constant<int, 4>());
-      else if constexpr (D == DT_F32) go(n, std::integral_constant<int, 8>());
-    } else {
-      dispatch_v(sh.V, [&](auto v) { go(std::integral_constant<int, 1>(), v); });
-    }
+    });
   });
   return hipGetLastError();
 }
 
-hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, bool vec, hipStream_t s) {
-  const int N = vec ? piece(a.dt) : 1;
-  const RowShape sh = row_shape(a.H, N, 16);
+hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, bool aligned, hipStream_t s) {
+  const RowShape sh = row_shape(a.H, piece(a.dt), 16);
   const int groups = row_groups(a.T, sh.waves);
   const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, ROW_GRID);
   const size_t lds = groups > 1 ? (size_t)groups * a.H * 4 : 0;
   const int threads = 64 * sh.waves * groups;
   dispatch_pair(a.dt, a.rdt, [&](auto d, auto r) {
     constexpr int D = decltype(d)::value, R = decltype(r)::value;
-    auto go = [&](auto n, auto v, auto pf) {
-      constexpr int NN = decltype(n)::value, VV = decltype(v)::value;
-      constexpr bool PF = decltype(pf)::value;
-      auto with = [&](auto g) {
-        // a full gate beside an fp32 residual: the next row would not fit the registers
-        constexpr bool P = PF && !(decltype(g)::value == GATE_FULL && D != DT_F32 && R == DT_F32);
-        k_block_norm_grad<D, R, NN, VV, decltype(g)::value, P><<<grid, threads, lds, s>>>(a, sh.waves);
-      };
-      dispatch_gate(a.gate_kind, with);
-    };
-    if (grid == 0) {
-      // no rows: the column sums are zeros
-    } else if (vec) {
-      std::integral_constant<int, D == DT_F32 ? 4 : 8> n;
-      if (sh.V == 1) go(n, std::integral_constant<int, 1>(), std::true_type());
-      else if (sh.V == 2) go(n, std::integral_constant<int, 2>(), std::false_type());
-      else if constexpr (D == DT_F32) go(n, std::integral_constant<int, 4>(), std::false_type());
-    } else {
-      dispatch_v(sh.V, [&](auto v) { go(std::integral_constant<int, 1>(), v, std::false_type()); });
-    }
+    // no rows: the column sums are zeros
+    if (grid > 0) dispatch_shape<D>(a.H, sh.V, aligned, [&](auto n, auto v, auto al) {
+      dispatch_gate(a.gate_kind, [&](auto g) {
+        constexpr int V = decltype(v)::value, G = decltype(g)::value;
+        // a full gate beside an fp32 residual, or unaligned rows: the next row would not
+        // fit the registers
+        constexpr bool AL = decltype(al)::value;
+        constexpr bool PF = V == 1 && AL && !(G == GATE_FULL && D != DT_F32 && R == DT_F32);
+        k_block_norm_grad<D, R, decltype(n)::value, V, G, PF, AL>
+            <<<grid, threads, lds, s>>>(a, sh.waves);
+      });
+    });
     if (a.dw_pre || a.dw_post || a.gate_kind == GATE_CHANNEL)
       k_block_norm_cols<D><<<dim3((a.H + 63) / 64, 2), 1024, 0, s>>>(a, grid);
   });

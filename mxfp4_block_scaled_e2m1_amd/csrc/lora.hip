@@ -143,7 +143,7 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(LoraArgs p) {
   };
   auto fetch_x = [&](Step& f, int k) {
 #pragma unroll
-    for (int i = 0; i < XI; ++i) f.x[i] = *(const u32v4*)(xr[i] + k);
+    for (int i = 0; i < XI; ++i) f.x[i] = __builtin_nontemporal_load((const u32v4*)(xr[i] + k));
   };
   uint8_t* area = lds + wave * AREA;
   uint8_t* put = area + lrow * SHRINK_PITCH + lcol * 2;

@@ -36,27 +36,26 @@ __device__ __forceinline__ int64_t first_unit() {
   return (int64_t)blockIdx.x * MR_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 }
 
-// One wave per (token, segment of 64 pieces of W bytes).
-template <int W>
-__global__ __launch_bounds__(64 * MR_WAVES) void k_permute(const char* __restrict__ x, int64_t T, int k, int pieces,
+// One wave per (token, segment of 64 pieces). DT: a type of the elements' size.
+template <int DT, int N, bool AL>
+__global__ __launch_bounds__(64 * MR_WAVES) void k_permute(const void* __restrict__ x, int64_t T, int k, int H,
                                                            int segs, const int32_t* __restrict__ slot_row,
-                                                           int64_t rows, char* __restrict__ xs) {
-  constexpr int EL = W == 2 ? 1 : W / 4;
-  const int64_t width = (int64_t)pieces * W;
+                                                           int64_t rows, void* __restrict__ xs) {
   for (int64_t unit = first_unit(); unit < T * segs; unit += (int64_t)gridDim.x * MR_WAVES) {
     const int64_t t = unit / segs;
-    const int c = (int)(unit - t * segs) * 64 + (threadIdx.x & 63);
-    if (c >= pieces) continue;
-    Raw<W == 2 ? DT_BF16 : DT_F32, EL> v;
-    v.load(x + t * width, c * EL);
+    const int c = ((int)(unit - t * segs) * 64 + (threadIdx.x & 63)) * N;
+    if (c >= H) continue;
+    Raw<DT, N> v;
+    v.template load_row<false, AL>(at<DT>(x, t * H), c, H);
+    v.template settle<AL>(c, H);
     for (int j = 0; j < k; ++j) {
       const int r = slot_row[t * k + j];
-      if ((unsigned)r < (unsigned)rows) v.template store<true>(xs + (int64_t)r * width, c * EL);
+      if ((unsigned)r < (unsigned)rows) v.template store_row<true, AL>(at<DT>(xs, (int64_t)r * H), c, H);
     }
   }
 }
 
-template <int DT, int N>
+template <int DT, int N, bool AL>
 __global__ __launch_bounds__(64 * MR_WAVES) void k_unpermute(const void* __restrict__ ys, int64_t rows,
                                                              const int32_t* __restrict__ slot_row,
                                                              const float* __restrict__ w, int64_t T, int k, int H,
@@ -78,25 +77,26 @@ __global__ __launch_bounds__(64 * MR_WAVES) void k_unpermute(const void* __restr
         v[q].zero();
         if ((unsigned)r < (unsigned)rows) {
           wt[q] = w != nullptr ? w[t * k + j0 + q] : 1.0f;
-          v[q].template load<true>(at<DT>(ys, (int64_t)r * H), c);
+          v[q].template load_row<true, AL>(at<DT>(ys, (int64_t)r * H), c, H);
         }
       }
 #pragma unroll
       for (int q = 0; q < SLOT_BATCH; ++q) {
+        v[q].template settle<AL>(c, H);
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] = fmaf(wt[q], v[q].get(i), acc[i]);
       }
     }
     Raw<DT, N> o;
     o.set(acc);
-    o.template store<true>(at<DT>(y, t * H), c);
+    o.template store_row<true, AL>(at<DT>(y, t * H), c, H);
   }
 }
 
 // One workgroup per token: its dy pieces stay in registers while the rows of
 // up to SLOT_BATCH slots stream by; the dot products are summed over the lanes
 // and waves at the end.
-template <int DT, int N>
+template <int DT, int N, bool AL>
 __global__ __launch_bounds__(1024) void k_unpermute_grad(const void* __restrict__ dy, const void* __restrict__ ys,
                                                          int64_t rows, const int32_t* __restrict__ slot_row,
                                                          const float* __restrict__ w, int64_t T, int k, int H,
@@ -116,13 +116,15 @@ __global__ __launch_bounds__(1024) void k_unpermute_grad(const void* __restrict_
       }
       for (int c = threadIdx.x * N; c < H; c += blockDim.x * N) {
         Raw<DT, N> d, v[SLOT_BATCH];
-        d.load(at<DT>(dy, t * H), c);
+        d.template load_row<false, AL>(at<DT>(dy, t * H), c, H);
 #pragma unroll
         for (int q = 0; q < SLOT_BATCH; ++q)
-          if (row[q] >= 0) v[q].template load<true>(at<DT>(ys, (int64_t)row[q] * H), c);
+          if (row[q] >= 0) v[q].template load_row<true, AL>(at<DT>(ys, (int64_t)row[q] * H), c, H);
+        d.template settle<AL>(c, H);
 #pragma unroll
         for (int q = 0; q < SLOT_BATCH; ++q) {
           if (row[q] < 0) continue;
+          v[q].template settle<AL>(c, H);
           float o[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
@@ -132,7 +134,7 @@ __global__ __launch_bounds__(1024) void k_unpermute_grad(const void* __restrict_
           }
           Raw<DT, N> r;
           r.set(o);
-          r.template store<true>(at<DT>(dys, (int64_t)row[q] * H), c);
+          r.template store_row<true, AL>(at<DT>(dys, (int64_t)row[q] * H), c, H);
         }
       }
       group_sum<SLOT_BATCH>(dot, red, waves, threadIdx.x & 63, threadIdx.x >> 6);
@@ -146,7 +148,7 @@ __global__ __launch_bounds__(1024) void k_unpermute_grad(const void* __restrict_
   }
 }
 
-bool vec16(int64_t row_bytes, const void* a, const void* b, const void* c = nullptr) {
+bool rows_aligned(int64_t row_bytes, const void* a, const void* b, const void* c = nullptr) {
   return row_bytes % 16 == 0 && (((uintptr_t)a | (uintptr_t)b | (uintptr_t)c) & 15) == 0;
 }
 
@@ -154,52 +156,55 @@ bool vec16(int64_t row_bytes, const void* a, const void* b, const void* c = null
 constexpr int64_t MAX_GRID = (int64_t)1 << 20;
 unsigned wave_grid(int64_t units) { return (unsigned)std::min((units + MR_WAVES - 1) / MR_WAVES, MAX_GRID); }
 
+
+// f(type, elements of a 16-byte piece, aligned)
+template <class F>
+void dispatch_piece(DType dt, int H, bool aligned, F&& f) {
+  dispatch_dt(dt, [&](auto d) {
+    std::integral_constant<int, 16 / dt_size<decltype(d)::value>> n;
+    if (H < n) f(d, std::integral_constant<int, 1>(), std::true_type());   // no whole piece
+    else if (aligned) f(d, n, std::true_type());
+    else f(d, n, std::false_type());
+  });
+}
+
+int segments(int H, int N) { return (H + 64 * N - 1) / (64 * N); }
+
 }  // namespace
 
-hipError_t launch_permute(const void* x, int esize, int64_t T, int k, int H, const int32_t* slot_row, int64_t rows,
+hipError_t launch_permute(const void* x, DType dt, int64_t T, int k, int H, const int32_t* slot_row, int64_t rows,
                           void* xs, hipStream_t s) {
-  const int64_t bytes = (int64_t)H * esize;
-  auto go = [&](auto w) {
-    constexpr int W = decltype(w)::value;
-    const int pieces = (int)(bytes / W), segs = (pieces + 63) / 64;
-    k_permute<W><<<wave_grid(T * segs), 64 * MR_WAVES, 0, s>>>((const char*)x, T, k, pieces, segs, slot_row,
-                                                                         rows, (char*)xs);
-  };
-  const uintptr_t any = (uintptr_t)x | (uintptr_t)xs | (uintptr_t)bytes;
-  if (any % 16 == 0) go(std::integral_constant<int, 16>());
-  else if (any % 8 == 0) go(std::integral_constant<int, 8>());
-  else if (any % 4 == 0) go(std::integral_constant<int, 4>());
-  else go(std::integral_constant<int, 2>());
+  if (dt == DT_F16) dt = DT_BF16;          // elements are moved as they are
+  dispatch_piece(dt, H, rows_aligned((int64_t)H * dt_bytes(dt), x, xs), [&](auto d, auto n, auto al) {
+    constexpr int D = decltype(d)::value, N = decltype(n)::value;
+    const int segs = segments(H, N);
+    if constexpr (D != DT_F16)
+      k_permute<D, N, decltype(al)::value><<<wave_grid(T * segs), 64 * MR_WAVES, 0, s>>>(x, T, k, H, segs, slot_row,
+                                                                                        rows, xs);
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_unpermute(const void* ys, DType dt, int64_t rows, const int32_t* slot_row, const float* w,
                             int64_t T, int k, int H, void* y, hipStream_t s) {
-  auto go = [&](auto dtc, auto nc) {
-    constexpr int DT = decltype(dtc)::value, N = decltype(nc)::value;
-    const int segs = (H + 64 * N - 1) / (64 * N);
-    k_unpermute<DT, N><<<wave_grid(T * segs), 64 * MR_WAVES, 0, s>>>(ys, rows, slot_row, w, T, k, H, segs,
-                                                                               y);
-  };
-  const bool vec = vec16((int64_t)H * dt_bytes(dt), ys, y);
-  dispatch_dt(dt, [&](auto dtc) {
-    if (vec) go(dtc, std::integral_constant<int, 16 / dt_size<decltype(dtc)::value>>());
-    else go(dtc, std::integral_constant<int, 1>());
+  dispatch_piece(dt, H, rows_aligned((int64_t)H * dt_bytes(dt), ys, y), [&](auto d, auto n, auto al) {
+    constexpr int D = decltype(d)::value, N = decltype(n)::value;
+    const int segs = segments(H, N);
+    k_unpermute<D, N, decltype(al)::value><<<wave_grid(T * segs), 64 * MR_WAVES, 0, s>>>(ys, rows, slot_row, w, T, k,
+                                                                                        H, segs, y);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_unpermute_grad(const void* dy, const void* ys, DType dt, int64_t rows, const int32_t* slot_row,
                                  const float* w, int64_t T, int k, int H, void* dys, float* dw, hipStream_t s) {
-  auto go = [&](auto dtc, auto nc) {
-    constexpr int DT = decltype(dtc)::value, N = decltype(nc)::value;
-    const int waves = std::min(16, (H + 64 * N - 1) / (64 * N));
-    k_unpermute_grad<DT, N><<<(unsigned)std::min<int64_t>(T, MAX_GRID), 64 * waves, 0, s>>>(dy, ys, rows, slot_row, w, T, k, H, dys, dw);
-  };
-  const bool vec = vec16((int64_t)H * dt_bytes(dt), ys, dy, dys);
-  dispatch_dt(dt, [&](auto dtc) {
-    if (vec) go(dtc, std::integral_constant<int, 16 / dt_size<decltype(dtc)::value>>());
-    else go(dtc, std::integral_constant<int, 1>());
+  dispatch_piece(dt, H, rows_aligned((int64_t)H * dt_bytes(dt), ys, dy, dys), [&](auto d, auto n, auto al) {
+    constexpr int D = decltype(d)::value, N = decltype(n)::value;
+    // a wave for every 64 pieces of the row: fewer waves with more pieces each were slower (14, 7, 4
+    // and 2 waves, 7168 bf16: 182, 186, 187 and 192 us)
+    const int waves = std::min(16, segments(H, N));
+    k_unpermute_grad<D, N, decltype(al)::value><<<(unsigned)std::min<int64_t>(T, MAX_GRID), 64 * waves, 0, s>>>(
+        dy, ys, rows, slot_row, w, T, k, H, dys, dw);
   });
   return hipGetLastError();
 }

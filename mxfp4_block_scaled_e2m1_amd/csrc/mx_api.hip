@@ -1531,7 +1531,7 @@ mx_status mx_moe_permute(mx_dtype dt, const void* x, int64_t T, int64_t hidden, 
   MX_REQUIRE_ALIGN(xs, es);
   MX_REQUIRE_ALIGN(slot_row, 4);
   MX_TRY(check_apart({"xs", xs, rows * hidden * es}, {{"x", x, T * hidden * es}, {"slot_row", slot_row, T * k * 4}}));
-  MX_HIP(phase("moe_permute", s, [&] { return launch_permute(x, es, T, k, (int)hidden, slot_row, rows, xs, s); }),
+  MX_HIP(phase("moe_permute", s, [&] { return launch_permute(x, (DType)dt, T, k, (int)hidden, slot_row, rows, xs, s); }),
          "moe_permute");
   return ok();
 }
@@ -1653,7 +1653,7 @@ mx_status mx_block_norm(mx_dtype dt, mx_dtype res_dt, const void* y, const void*
   const uintptr_t all = (uintptr_t)y | (uintptr_t)residual | (uintptr_t)w_post | (uintptr_t)w_pre |
                         (uintptr_t)residual_out | (uintptr_t)normed |
                         (gate_kind == MX_GATE_TOKEN ? (uintptr_t)0 : (uintptr_t)gate);
-  MX_HIP(phase("block_norm", s, [&] { return launch_block_norm(a, block_norm_vec(a.dt, (int)H, all), s); }), "block_norm");
+  MX_HIP(phase("block_norm", s, [&] { return launch_block_norm(a, block_norm_aligned(a.dt, (int)H, all), s); }), "block_norm");
   return ok();
 }
 
@@ -1733,7 +1733,7 @@ mx_status mx_block_norm_grad(mx_dtype dt, mx_dtype res_dt, const void* y, const 
                         (uintptr_t)d_normed | (uintptr_t)d_residual_out | (uintptr_t)d_residual | (uintptr_t)d_y |
                         (gate_kind == MX_GATE_TOKEN ? (uintptr_t)0 : (uintptr_t)gate) |
                         (gate_kind == MX_GATE_FULL ? (uintptr_t)d_gate : (uintptr_t)0);
-  MX_HIP(phase("block_norm_grad", s, [&] { return launch_block_norm_grad(a, block_norm_vec(a.dt, (int)H, all), s); }),
+  MX_HIP(phase("block_norm_grad", s, [&] { return launch_block_norm_grad(a, block_norm_aligned(a.dt, (int)H, all), s); }),
          "block_norm_grad");
   return ok();
 }

@@ -263,7 +263,7 @@ hipError_t launch_sort(const int32_t* ids, int64_t P, int n_experts, int32_t* ex
 
 // ---- Rows to the experts and back (moe_rows.hip) -----------------------------
 // rows: row capacity of xs / ys; slots whose row is outside [0, rows) are skipped.
-hipError_t launch_permute(const void* x, int esize, int64_t T, int k, int H, const int32_t* slot_row, int64_t rows,
+hipError_t launch_permute(const void* x, DType dt, int64_t T, int k, int H, const int32_t* slot_row, int64_t rows,
                           void* xs, hipStream_t s);
 hipError_t launch_unpermute(const void* ys, DType dt, int64_t rows, const int32_t* slot_row, const float* w,
                             int64_t T, int k, int H, void* y, hipStream_t s);
@@ -295,12 +295,12 @@ struct BlockNormGradArgs {
   float *dw_pre, *dw_post;
   float* part;                 // [block_norm_grad_grid][2][H]
 };
-// Whether rows can be taken in 16-byte pieces: all_pointers is the
-// bitwise or of every row and weight pointer in use.
-bool block_norm_vec(DType dt, int H, uintptr_t all_pointers);
+// Whether every piece of a row is 16-byte aligned: all_pointers is the bitwise
+// or of every row and weight pointer in use.
+bool block_norm_aligned(DType dt, int H, uintptr_t all_pointers);
 int block_norm_grad_grid(int64_t T);   // an upper bound
-hipError_t launch_block_norm(const BlockNormArgs& a, bool vec, hipStream_t s);
-hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, bool vec, hipStream_t s);
+hipError_t launch_block_norm(const BlockNormArgs& a, bool aligned, hipStream_t s);
+hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, bool aligned, hipStream_t s);
 
 // ---- Low-rank adapters (lora.hip) -----------------------------------------------
 constexpr int LORA_MAX_RANK = 128;

@@ -3,6 +3,8 @@
 // a few at a time, and sums over the lanes of a workgroup.
 #pragma once
 
+#include <type_traits>
+
 #include "mx_device.h"
 #include "mx_internal.h"
 
@@ -38,13 +40,20 @@ __device__ __forceinline__ const char* at(const void* p, int64_t i) { return (co
 template <int DT>
 __device__ __forceinline__ char* at(void* p, int64_t i) { return (char*)p + i * dt_size<DT>; }
 
-// N consecutive elements as they lie in memory, at element i of a row. N is 1 (any element address)
-// or fills whole 16-byte pieces (16-byte aligned address), except N = 4 of a
-// 16-bit type: one 8-byte piece.
+// The same vector at any element's address: the hardware and its ABI take
+// unaligned global accesses, so a row that does not start on 16 bytes still moves 16
+// bytes a lane (element by element, norms of 4096 x 4097 bf16 took 194 us
+// instead of 28, their gradient 680 instead of 48).
+typedef uint32_t u32v4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// N consecutive elements as they lie in memory, at element i of a row: one
+// element, or whole 16-byte pieces. AL: the address is a multiple of 16.
+// NT: a streaming access, for data that nothing reads again soon.
 template <int DT, int N>
 struct Raw {
   static constexpr int BYTES = N * dt_size<DT>;
   static constexpr int WORDS = BYTES < 4 ? 1 : BYTES / 4;
+  static_assert(N == 1 || BYTES % 16 == 0, "one element or whole pieces");
   uint32_t w[WORDS];
 
   __device__ __forceinline__ void zero() {
@@ -57,28 +66,26 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(w[i]));
   }
-  // NT: a streaming access, for data that nothing reads again soon.
-  template <bool NT = false>
+  template <bool NT = false, bool AL = true>
   __device__ __forceinline__ void load(const void* row, uint32_t i) {
+    typedef std::conditional_t<AL, u32v4, u32v4_any> vec;
     const char* p = (const char*)row + i * (uint32_t)dt_size<DT>;
     if constexpr (BYTES == 2) {
       w[0] = NT ? __builtin_nontemporal_load((const uint16_t*)p) : *(const uint16_t*)p;
     } else if constexpr (BYTES == 4) {
       w[0] = NT ? __builtin_nontemporal_load((const uint32_t*)p) : *(const uint32_t*)p;
-    } else if constexpr (BYTES == 8) {
-      const u32v2 v = NT ? __builtin_nontemporal_load((const u32v2*)p) : *(const u32v2*)p;
-      w[0] = v[0]; w[1] = v[1];
     } else {
 #pragma unroll
       for (int j = 0; j < BYTES / 16; ++j) {
-        const u32v4 v = NT ? __builtin_nontemporal_load((const u32v4*)p + j) : ((const u32v4*)p)[j];
+        const u32v4 v = NT ? __builtin_nontemporal_load((const vec*)p + j) : ((const vec*)p)[j];
 #pragma unroll
         for (int q = 0; q < 4; ++q) w[4 * j + q] = v[q];
       }
     }
   }
-  template <bool NT = false>
+  template <bool NT = false, bool AL = true>
   __device__ __forceinline__ void store(void* row, uint32_t i) const {
+    typedef std::conditional_t<AL, u32v4, u32v4_any> vec;
     char* p = (char*)row + i * (uint32_t)dt_size<DT>;
     if constexpr (BYTES == 2) {
       if (NT) __builtin_nontemporal_store((uint16_t)w[0], (uint16_t*)p);
@@ -86,18 +93,56 @@ struct Raw {
     } else if constexpr (BYTES == 4) {
       if (NT) __builtin_nontemporal_store(w[0], (uint32_t*)p);
       else *(uint32_t*)p = w[0];
-    } else if constexpr (BYTES == 8) {
-      const u32v2 v = {w[0], w[1]};
-      if (NT) __builtin_nontemporal_store(v, (u32v2*)p);
-      else *(u32v2*)p = v;
     } else {
 #pragma unroll
       for (int j = 0; j < BYTES / 16; ++j) {
         const u32v4 v = {w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
-        if (NT) __builtin_nontemporal_store(v, (u32v4*)p + j);
-        else ((u32v4*)p)[j] = v;
+        if (NT) __builtin_nontemporal_store((vec)v, (vec*)p + j);
+        else ((vec*)p)[j] = v;
       }
     }
+  }
+  // The piece at column c < H of a row of H >= N elements. A row's last piece may
+  // reach past its end (!AL): then the row's last N elements are loaded, and
+  // settle(), which has to wait for them, turns them into what the piece has
+  // (zeros behind); a store writes these one by one.
+  template <bool NT = false, bool AL = true>
+  __device__ __forceinline__ void load_row(const void* row, uint32_t c, uint32_t H) {
+    load<NT, AL>(row, AL ? c : min(c, H - N));
+  }
+  template <bool AL>
+  __device__ __forceinline__ void settle(uint32_t c, uint32_t H) {
+    if constexpr (!AL) {
+      if (c + N > H) drop(c + N - H);
+    }
+  }
+  // The first n < N elements leave, zeros come in behind.
+  __device__ __forceinline__ void drop(uint32_t n) {
+    const uint32_t words = dt_size<DT> == 2 ? n >> 1 : n;
+#pragma unroll
+    for (int b = 1; b < WORDS; b *= 2)
+      if (words & b) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = i + b < WORDS ? w[i + b] : 0u;
+      }
+    if (dt_size<DT> == 2 && (n & 1)) {
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) w[i] = (w[i] >> 16) | (i + 1 < WORDS ? w[i + 1] << 16 : 0u);
+    }
+  }
+  template <bool NT = false, bool AL = true>
+  __device__ __forceinline__ void store_row(void* row, uint32_t c, uint32_t H) const {
+    if (AL || c + N <= H) {
+      store<NT, AL>(row, c);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < N - 1; ++j)
+      if (c + j < H) {
+        Raw<DT, 1> e;
+        e.w[0] = w[j * dt_size<DT> / 4] >> (j * dt_size<DT> % 4 * 8);
+        e.store(row, c + j);
+      }
   }
   __device__ __forceinline__ void fill(float x) {
     float f[N];
