@@ -37,6 +37,7 @@ __device__ __forceinline__ int64_t first_unit() {
 }
 
 // One wave per (token, segment of 64 pieces). DT: a type of the elements' size.
+// Streaming stores only of whole lines (2048 x 8 x 4097 bf16: 46 us with, 40 without).
 template <int DT, int N, bool AL>
 __global__ __launch_bounds__(64 * MR_WAVES) void k_permute(const void* __restrict__ x, int64_t T, int k, int H,
                                                            int segs, const int32_t* __restrict__ slot_row,
@@ -50,7 +51,7 @@ __global__ __launch_bounds__(64 * MR_WAVES) void k_permute(const void* __restric
     v.template settle<AL>(c, H);
     for (int j = 0; j < k; ++j) {
       const int r = slot_row[t * k + j];
-      if ((unsigned)r < (unsigned)rows) v.template store_row<true, AL>(at<DT>(xs, (int64_t)r * H), c, H);
+      if ((unsigned)r < (unsigned)rows) v.template store_row<AL, AL>(at<DT>(xs, (int64_t)r * H), c, H);
     }
   }
 }

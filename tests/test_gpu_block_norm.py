@@ -247,3 +247,39 @@ def test_grad_is_the_same_every_time(mx):
     for _ in range(3):
         again = _grad(mx, t, h, "bf16", "bf16")
         assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+@pytest.mark.parametrize("H", [9, 12, 15, 70, 1001, 4099, 8189, 8200, 12347])
+@pytest.mark.parametrize("name,res_name", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("gate", ["channel", "full"])
+def test_rows_that_start_anywhere(mx, H, name, res_name, gate):
+    """Widths that are no whole number of 16-byte pieces, more rows than workgroups hold at once."""
+    T = 300 if H < 2000 else 5
+    _forward(mx, T, H, name, res_name, gate, True)
+    t, h = _inputs(T, H, name, res_name, gate, True)
+    _grad(mx, t, h, name, res_name)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 5])
+def test_views_at_any_alignment(mx, shift):
+    """Buffers off 16 bytes give the bits of aligned ones, and nothing around them is written."""
+    t, _ = _inputs(37, 520, "bf16", "fp32", "full", True)
+
+    def off(v):
+        buf = torch.full((v.numel() + 16,), 7.0, dtype=v.dtype, device="cuda")
+        view = buf[shift:shift + v.numel()].view(v.shape)
+        view.copy_(v)
+        return buf, view
+    want = mx.block_norm(t["residual"], t["w_pre"], y=t["y"], w_post=t["w_post"], gate=t["gate"], eps=EPS)
+    grad = mx.block_norm_grad(want[1], t["w_pre"], t["dn"], d_residual_out=t["dro"], y=t["y"], w_post=t["w_post"],
+                              gate=t["gate"], eps=EPS)
+    u = {k: off(v)[1] for k, v in t.items()}
+    outs = [off(torch.zeros_like(v)) for v in (want[0], want[1], grad[0], grad[2])]
+    mx.block_norm(u["residual"], u["w_pre"], y=u["y"], w_post=u["w_post"], gate=u["gate"], eps=EPS,
+                  normed=outs[0][1], residual_out=outs[1][1])
+    g = mx.block_norm_grad(outs[1][1], u["w_pre"], u["dn"], d_residual_out=u["dro"], y=u["y"], w_post=u["w_post"],
+                           gate=u["gate"], eps=EPS, d_residual=outs[2][1], d_y=outs[3][1])
+    for (buf, view), ref in zip(outs, (want[0], want[1], grad[0], grad[2])):
+        assert torch.equal(view, ref)
+        assert (buf[:shift] == 7).all() and (buf[shift + view.numel():] == 7).all()
+    assert all(torch.equal(g[i], grad[i]) for i in (1, 3, 4))

@@ -68,7 +68,8 @@ def _maps(mx, rng, T, k, E, total):
 
 
 SHAPES = [(1, 1, 1, 1, 8), (1, 8, 48, 48, 7168), (5, 3, 4, 4, 1), (7, 2, 6, 6, 33), (9, 9, 16, 16, 100),
-          (33, 6, 8, 64, 1000), (64, 4, 8, 8, 2049), (130, 17, 32, 32, 264)]
+          (33, 6, 8, 64, 1000), (64, 4, 8, 8, 2049), (130, 17, 32, 32, 264),
+          (20, 3, 5, 9, 5), (20, 3, 5, 9, 9), (20, 3, 5, 9, 14), (6, 2, 4, 4, 4099)]
 
 
 @pytest.mark.parametrize("name", ["bf16", "fp16", "fp32"])
