@@ -283,3 +283,30 @@ def test_views_at_any_alignment(mx, shift):
         assert torch.equal(view, ref)
         assert (buf[:shift] == 7).all() and (buf[shift + view.numel():] == 7).all()
     assert all(torch.equal(g[i], grad[i]) for i in (1, 3, 4))
+
+
+def test_more_than_2_to_the_31_elements(mx):
+    """Offsets past 32 bits: the last rows of 300,001 x 7168 as the same rows alone give them."""
+    T, H, n = 300001, 7168, 5
+    t, _ = _inputs(n, H, "bf16", "bf16", "token", True)
+    big = {}
+    for k in ("y", "residual", "dn", "dro"):
+        big[k] = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+        big[k][-n:] = t[k]
+    gate = torch.zeros((T, 1), dtype=torch.bfloat16, device="cuda")
+    gate[-n:] = t["gate"]
+    a = mx.block_norm(big["residual"], t["w_pre"], y=big["y"], w_post=t["w_post"], gate=gate, eps=EPS)
+    b = mx.block_norm(t["residual"], t["w_pre"], y=t["y"], w_post=t["w_post"], gate=t["gate"], eps=EPS)
+    assert all(torch.equal(x[-n:], y) and not x[:-n].any() for x, y in zip(a, b))
+    g = mx.block_norm_grad(a[1], t["w_pre"], big["dn"], d_residual_out=big["dro"], y=big["y"], w_post=t["w_post"],
+                           gate=gate, eps=EPS)
+    r = mx.block_norm_grad(b[1], t["w_pre"], t["dn"], d_residual_out=t["dro"], y=t["y"], w_post=t["w_post"],
+                           gate=t["gate"], eps=EPS)
+    assert all(torch.equal(g[i][-n:], r[i]) and not g[i][:-n].any() for i in (0, 2, 4))
+    # the column sums: the same five terms among zeros, joined in another order: two sums of five, each off by at
+    # most four halves of a step of the sum of the terms' sizes
+    rh = np.abs(f64(b[1])) / _rms(f64(b[1]))
+    yh = np.abs(f64(t["y"])) / _rms(f64(t["y"]))
+    du = np.abs(f64(t["gate"]) * f64(r[0]))
+    for i, mass in ((1, np.abs(f64(t["dn"])) * rh), (3, du * yh)):
+        within(g[i], f64(r[i]), 1.02 * 8 * U * mass.sum(0))

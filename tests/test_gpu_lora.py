@@ -137,3 +137,20 @@ def test_large_and_non_finite_values_stay_in_their_rows(mx, name, big):
     assert torch.equal(clean[others], dirty[others])
     assert not torch.isfinite(dirty[6]).all() and not torch.isfinite(dirty[7]).all()
     assert torch.isnan(dirty[6][b[0].sum(1) > 0]).any()
+
+
+def test_more_than_2_to_the_31_elements(mx):
+    """Offsets past 32 bits in x and y, whole numbers, only the last tokens with adapters."""
+    M, K, N, R, n = 300001, 7168, 7200, 16, 2
+    rng = np.random.default_rng(4)
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    xt, x64 = pair(rng.integers(-2, 3, size=(40, K)), "bf16")
+    a, a64 = pair(rng.integers(-1, 2, size=(n, R, K)), "bf16")
+    b, b64 = pair(rng.integers(-1, 2, size=(n, N, R)), "bf16")
+    x[-40:] = xt
+    adapter = np.full(M, -1)
+    adapter[-40:] = np.arange(40) % 3 - 1
+    mx.lora_add(y, x, a, b, *_plan(mx, adapter, n))
+    ref = around.lora_add(np.zeros((40, N)), x64, a64, b64, adapter[-40:])
+    assert torch.equal(y[-40:].cpu(), torch.from_numpy(ref).to(torch.bfloat16)) and not y[:-40].any()
