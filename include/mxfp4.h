@@ -640,7 +640,7 @@ MX_API size_t mx_block_norm_grad_workspace_size(int64_t T, int64_t H);
  * x . A^T is held in fp32 accuracy between the two products; y is rounded once.
  * R a multiple of 8 up to 128 (adapters of smaller rank are padded with zero
  * rows of A and zero columns of B), K and N multiples of 8 up to 2^20,
- * M <= 2^24, 1 <= n <= 512, ldx >= K and ldy >= N multiples of 8.
+ * M <= 2^24, M * K <= 2^38, 1 <= n <= 512, ldx >= K and ldy >= N multiples of 8.
  * workspace: mx_lora_add_workspace_size(M, K, R, n) bytes, 256-byte aligned; x, a
  * and b must not overlap y. Alignment: x, a, b, y 16 bytes; the others 4.
  */

@@ -39,58 +39,83 @@ __device__ __forceinline__ f32x4 mma(u32v4 a, u32v4 b, f32x4 c) {
                                                   0);
 }
 
+// A tile is up to TM sorted rows of one adapter, adapters in order. How many there
+// are, and where each lies, is only known on the device: every wave looks at
+// the adapters' offsets itself, 64 at a time.
 struct Tile {
-  int adapter, row0, rows;   // sorted rows [row0, row0 + rows) of one adapter; adapter < 0: none
-  int piece;                 // which of the tile's `pieces` workgroups this is
+  int adapter, row0, rows;   // sorted rows [row0, row0 + rows)
 };
-
-// The tile of workgroup `id`, of `pieces` workgroups per tile. A tile is up to TM
-// sorted rows of one adapter, adapters in order; how many there are is only known
-// here, so workgroups past the last one get none. Neighbouring tiles mostly share
-// an adapter, and workgroups go to the 8 XCDs in turn, so each XCD is given a
-// contiguous run of the work: its L2 then holds a few adapters instead of all
-// (8 adapters of 64 x 7168 beside 4096 tokens: 7.3 MB, more than its 4 MB).
 template <int TM>
-__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ off, int n, int M, int id, int pieces) {
-  const int lane = threadIdx.x & 63;
-  // 64 adapters at a time: a prefix sum of their tile counts over the lanes
-  auto chunk = [&](int a0, int& lo, int& hi, int& cnt) {
-    const int a = a0 + lane;
+struct Tiles {
+  const int32_t* off;
+  int n, M, total;
+  int lo, hi, cnt, inc;      // of the lane's adapter among the first 64: rows, tiles, tiles up to it
+
+  __device__ __forceinline__ void look(int a0) {
+    const int lane = threadIdx.x & 63, a = a0 + lane;
     lo = hi = 0;
     if (a < n) {
       lo = min(max(off[a], 0), M);
       hi = min(max(off[a + 1], lo), M);
     }
     cnt = (hi - lo + TM - 1) / TM;
-    int inc = cnt;
+    inc = cnt;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int u = __shfl_up(inc, d);
       if (lane >= d) inc += u;
     }
-    return inc;
-  };
-  int lo, hi, cnt, inc = chunk(0, lo, hi, cnt);
-  int total = __builtin_amdgcn_readlane(inc, 63);
-  for (int a0 = 64; a0 < n; a0 += 64) total += __builtin_amdgcn_readlane(chunk(a0, lo, hi, cnt), 63);
-  const int work = total * pieces;
-  if (id >= work) return {-1, 0, 0, 0};
-  const int xcd = id & 7, mine = (work >> 3) * xcd + min(xcd, work & 7) + (id >> 3);
-  const int tile = mine / pieces;
-  int before = 0;
-  for (int a0 = 0; a0 < n; a0 += 64) {
-    if (n > 64) inc = chunk(a0, lo, hi, cnt);
-    const uint64_t hit = __ballot(before + inc > tile);
-    if (hit) {
-      const int l = __ffsll((long long)hit) - 1;
-      const int first = before + __builtin_amdgcn_readlane(inc, l) - __builtin_amdgcn_readlane(cnt, l);
-      const int row0 = __builtin_amdgcn_readlane(lo, l) + (tile - first) * TM;
-      return {a0 + l, row0, min(TM, __builtin_amdgcn_readlane(hi, l) - row0), mine - tile * pieces};
-    }
-    before += __builtin_amdgcn_readlane(inc, 63);
   }
-  return {-1, 0, 0, 0};
+  __device__ __forceinline__ Tiles(const int32_t* off_, int n_, int M_) : off(off_), n(n_), M(M_) {
+    total = 0;
+    for (int a0 = (n - 1) / 64 * 64; a0 >= 0; a0 -= 64) {    // ends on the first 64
+      look(a0);
+      total += __builtin_amdgcn_readlane(inc, 63);
+    }
+  }
+  __device__ __forceinline__ Tile find(int tile) {
+    int before = 0;
+    for (int a0 = 0; a0 < n; a0 += 64) {
+      if (n > 64) look(a0);
+      const uint64_t hit = __ballot(before + inc > tile);
+      if (hit) {
+        const int l = __ffsll((long long)hit) - 1;
+        const int first = before + __builtin_amdgcn_readlane(inc, l) - __builtin_amdgcn_readlane(cnt, l);
+        const int row0 = __builtin_amdgcn_readlane(lo, l) + (tile - first) * TM;
+        return {a0 + l, row0, min(TM, __builtin_amdgcn_readlane(hi, l) - row0)};
+      }
+      before += __builtin_amdgcn_readlane(inc, 63);
+    }
+    return {0, 0, 0};
+  }
+};
+
+// Workgroups go to the 8 XCDs in turn, and neighbouring tiles mostly share an
+// adapter: each XCD gets a contiguous run of the `work` pieces, so that its L2
+// holds a few adapters (8 adapters of 64 x 7168: 7.3 MB, more than its 4 MB).
+__device__ __forceinline__ int xcd_run(int id, int work) {
+  const int xcd = id & 7;
+  return (work >> 3) * xcd + min(xcd, work & 7) + (id >> 3);
 }
+
+// How the shrink's work is shared out. A unit is a tile and a group of ranks, its
+// work the 64-wide steps of K (a shorter rest of K goes with the last); units
+// one after another make one row of steps, cut into equal runs of q, one per
+// workgroup, so that all finish together however many tiles there are. A unit's
+// v is then the sum of what the workgroups from first() to last() left of it.
+// (Divisions cost a few calls of this their latency: what the host knows of q comes
+// with the arguments.)
+struct Share {
+  uint32_t steps, q, total;
+  __device__ __forceinline__ Share(const LoraArgs& p, int units) {
+    steps = max(p.K / 64, 1);
+    total = (uint32_t)units * steps;
+    q = max((total + (1u << p.slots_log2) - 1) >> p.slots_log2, (uint32_t)p.least);
+  }
+  __device__ __forceinline__ int groups() const { return (total + q - 1) / q; }
+  __device__ __forceinline__ int first(int unit) const { return (uint32_t)unit * steps / q; }
+  __device__ __forceinline__ int last(int unit) const { return ((uint32_t)(unit + 1) * steps - 1) / q; }
+};
 
 // Between the lanes of one wave: LDS writes before, reads after.
 __device__ __forceinline__ void wave_sync() {
@@ -98,15 +123,14 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// v [split][sorted row][R] of one tile: MT x RT blocks of 16 tokens x 16 ranks.
+// Parts of v, [part][sorted row][R]: per unit MT x RT blocks of 16 tokens x 16 ranks.
 // A matrix operand wants 16 rows side by side in the lanes, but a load whose
 // neighbouring lanes are in different rows takes the address path one row at a time
 // (4096 x 7168, rank 64: 39 us that way even with x in L2). So a wave loads whole
 // 128-byte lines, eight lanes each, the rows of a 64-wide step of K, turns them
 // in an LDS area of its own (pitch 144: conflict-free) and has the next
-// two steps' loads in flight meanwhile. The waves take the steps of a split in turn,
-// 1 KB of a row together, and join their sums in LDS.
-// Workgroups of a tile: K splits by groups of 16 RT ranks.
+// two steps' loads in flight meanwhile. The waves take a workgroup's steps in turn,
+// 512 bytes of a row together, and join their sums in LDS.
 constexpr int SHRINK_PITCH = 128 + 16;
 template <int DT, int MT, int RT>
 __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(LoraArgs p) {
@@ -114,132 +138,142 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(LoraArgs p) {
   constexpr int AREA = 16 * (MT + RT) * SHRINK_PITCH;
   constexpr int JOIN = MT * RT * 1024;
   __shared__ __attribute__((aligned(16))) uint8_t lds[SHRINK_WAVES * (AREA > JOIN ? AREA : JOIN)];
-  const int rgroups = (p.R + 16 * RT - 1) / (16 * RT);
-  const Tile tile = find_tile<TM>(p.adapter_off, p.n, p.M, blockIdx.x, p.splits * rgroups);
-  if (tile.adapter < 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = tile.piece / rgroups, r0 = (tile.piece - split * rgroups) * 16 * RT;
-  const int lrow = lane >> 3, lcol = (lane & 7) * 8;          // of a load
-  // rows past the tile or the rank repeat the last one; their results are not kept
-  int tok[XI];
+  const int rlog = p.R > 16 * RT;       // groups of 16 RT ranks: 1 or, above 64 ranks, 2
+  Tiles<TM> tiles(p.adapter_off, p.n, p.M);
+  const Share share(p, tiles.total << rlog);
+  const int all = share.groups();
+  if ((int)blockIdx.x >= all) return;
+  const int group = xcd_run(blockIdx.x, all);
+  uint32_t at = group * share.q;
+  const uint32_t end = min(at + share.q, share.total);
+  while (at < end) {
+    const int unit = at / share.steps, k0 = at - unit * share.steps, k1 = min(share.steps, k0 + end - at);
+    at += k1 - k0;
+    const Tile tile = tiles.find(unit >> rlog);
+    const int r0 = (unit & rlog) * 16 * RT;
+    const int lrow = lane >> 3, lcol = (lane & 7) * 8;          // of a load
+    // rows past the tile or the rank repeat the last one; their results are not kept
+    int tok[XI];
 #pragma unroll
-  for (int i = 0; i < XI; ++i) tok[i] = p.row_token[tile.row0 + min(8 * i + lrow, tile.rows - 1)];
-  const uint16_t* am = (const uint16_t*)p.a + (int64_t)tile.adapter * p.R * p.K;
-  uint32_t ao[AI];
+    for (int i = 0; i < XI; ++i) tok[i] = p.row_token[tile.row0 + min(8 * i + lrow, tile.rows - 1)];
+    const uint16_t* am = (const uint16_t*)p.a + (int64_t)tile.adapter * p.R * p.K;
+    uint32_t ao[AI];
 #pragma unroll
-  for (int i = 0; i < AI; ++i) ao[i] = (uint32_t)min(r0 + 8 * i + lrow, p.R - 1) * (uint32_t)p.K + lcol;
-  f32x4 acc[MT][RT];
+    for (int i = 0; i < AI; ++i) ao[i] = (uint32_t)min(r0 + 8 * i + lrow, p.R - 1) * (uint32_t)p.K + lcol;
+    f32x4 acc[MT][RT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[m][r] = f32x4{0.f, 0.f, 0.f, 0.f};
-  struct Step {
-    u32v4 a[AI], x[XI];
-  };
-  const uint16_t* xr[XI];
-  auto fetch_a = [&](Step& f, int k) {
+      for (int r = 0; r < RT; ++r) acc[m][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+    struct Step {
+      u32v4 a[AI], x[XI];
+    };
+    const uint16_t* xr[XI];
+    auto fetch_a = [&](Step& f, int k) {
 #pragma unroll
-    for (int i = 0; i < AI; ++i) f.a[i] = *(const u32v4*)(am + k + ao[i]);
-  };
-  auto fetch_x = [&](Step& f, int k) {
+      for (int i = 0; i < AI; ++i) f.a[i] = *(const u32v4*)(am + k + ao[i]);
+    };
+    auto fetch_x = [&](Step& f, int k) {
 #pragma unroll
-    for (int i = 0; i < XI; ++i) f.x[i] = __builtin_nontemporal_load((const u32v4*)(xr[i] + k));
-  };
-  uint8_t* area = lds + wave * AREA;
-  uint8_t* put = area + lrow * SHRINK_PITCH + lcol * 2;
-  const uint8_t* get = area + (lane & 15) * SHRINK_PITCH + (lane >> 4) * 16;
-  auto stage = [&](const Step& f) {
-    wave_sync();
+      for (int i = 0; i < XI; ++i) f.x[i] = __builtin_nontemporal_load((const u32v4*)(xr[i] + k));
+    };
+    uint8_t* area = lds + wave * AREA;
+    uint8_t* put = area + lrow * SHRINK_PITCH + lcol * 2;
+    const uint8_t* get = area + (lane & 15) * SHRINK_PITCH + (lane >> 4) * 16;
+    auto stage = [&](const Step& f) {
+      wave_sync();
 #pragma unroll
-    for (int i = 0; i < XI; ++i) *(u32v4*)(put + 8 * i * SHRINK_PITCH) = f.x[i];
+      for (int i = 0; i < XI; ++i) *(u32v4*)(put + 8 * i * SHRINK_PITCH) = f.x[i];
 #pragma unroll
-    for (int i = 0; i < AI; ++i) *(u32v4*)(put + 8 * (XI + i) * SHRINK_PITCH) = f.a[i];
-    wave_sync();
-  };
-  auto multiply = [&]() {
+      for (int i = 0; i < AI; ++i) *(u32v4*)(put + 8 * (XI + i) * SHRINK_PITCH) = f.a[i];
+      wave_sync();
+    };
+    auto multiply = [&]() {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u32v4 af[RT];
+      for (int h = 0; h < 2; ++h) {
+        u32v4 af[RT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) af[r] = *(const u32v4*)(get + 16 * (MT + r) * SHRINK_PITCH + 64 * h);
+        for (int r = 0; r < RT; ++r) af[r] = *(const u32v4*)(get + 16 * (MT + r) * SHRINK_PITCH + 64 * h);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const u32v4 xf = *(const u32v4*)(get + 16 * m * SHRINK_PITCH + 64 * h);
+        for (int m = 0; m < MT; ++m) {
+          const u32v4 xf = *(const u32v4*)(get + 16 * m * SHRINK_PITCH + 64 * h);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) acc[m][r] = mma<DT>(af[r], xf, acc[m][r]);
+          for (int r = 0; r < RT; ++r) acc[m][r] = mma<DT>(af[r], xf, acc[m][r]);
+        }
+      }
+    };
+    // this wave's whole steps: of the workgroup's, every SHRINK_WAVES-th
+    const int s0 = k0 + wave, n = (min(k1, p.K / 64) - s0 + SHRINK_WAVES - 1) / SHRINK_WAVES;
+    auto k_of = [&](int i) { return (s0 + i * SHRINK_WAVES) * 64; };
+    Step fa, fb;
+    if (n > 0) fetch_a(fa, k_of(0));       // does not wait for the tokens
+#pragma unroll
+    for (int i = 0; i < XI; ++i) xr[i] = (const uint16_t*)p.x + (int64_t)min(max(tok[i], 0), p.M - 1) * p.ldx + lcol;
+    if (n > 0) {
+      // two steps in flight; no condition on a load inside the loop, or its wait
+      // would be for everything
+      fetch_x(fa, k_of(0));
+      fetch_a(fb, k_of(min(1, n - 1)));
+      fetch_x(fb, k_of(min(1, n - 1)));
+      int i = 0;
+      for (; i + 3 < n; i += 2) {
+        stage(fa);
+        fetch_a(fa, k_of(i + 2));
+        fetch_x(fa, k_of(i + 2));
+        multiply();
+        stage(fb);
+        fetch_a(fb, k_of(i + 3));
+        fetch_x(fb, k_of(i + 3));
+        multiply();
+      }
+      stage(fa);
+      if (i + 2 < n) {
+        fetch_a(fa, k_of(i + 2));
+        fetch_x(fa, k_of(i + 2));
+      }
+      multiply();
+      if (i + 1 < n) {
+        stage(fb);
+        multiply();
+      }
+      if (i + 2 < n) {
+        stage(fa);
+        multiply();
       }
     }
-  };
-  // this wave's steps: of the split's, every SHRINK_WAVES-th
-  const int steps = p.K / 64, s0 = (int)((int64_t)steps * split / p.splits) + wave;
-  const int n = ((int)((int64_t)steps * (split + 1) / p.splits) - s0 + SHRINK_WAVES - 1) / SHRINK_WAVES;
-  auto k_of = [&](int i) { return (s0 + i * SHRINK_WAVES) * 64; };
-  Step fa, fb;
-  if (n > 0) fetch_a(fa, k_of(0));       // does not wait for the tokens
+    if (k1 == (int)share.steps && wave == SHRINK_WAVES - 1 && p.K % 64 != 0) {
+      // the rest of K, a multiple of 8: a lane's eight elements are in or out
+      const int k = p.K / 64 * 64;
 #pragma unroll
-  for (int i = 0; i < XI; ++i) xr[i] = (const uint16_t*)p.x + (int64_t)min(max(tok[i], 0), p.M - 1) * p.ldx + lcol;
-  if (n > 0) {
-    // two steps in flight; no condition on a load inside the loop, or its wait
-    // would be for everything
-    fetch_x(fa, k_of(0));
-    fetch_a(fb, k_of(min(1, n - 1)));
-    fetch_x(fb, k_of(min(1, n - 1)));
-    int i = 0;
-    for (; i + 3 < n; i += 2) {
-      stage(fa);
-      fetch_a(fa, k_of(i + 2));
-      fetch_x(fa, k_of(i + 2));
-      multiply();
-      stage(fb);
-      fetch_a(fb, k_of(i + 3));
-      fetch_x(fb, k_of(i + 3));
-      multiply();
-    }
-    stage(fa);
-    if (i + 2 < n) {
-      fetch_a(fa, k_of(i + 2));
-      fetch_x(fa, k_of(i + 2));
-    }
-    multiply();
-    if (i + 1 < n) {
-      stage(fb);
-      multiply();
-    }
-    if (i + 2 < n) {
+      for (int i = 0; i < AI; ++i) fa.a[i] = u32v4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < XI; ++i) fa.x[i] = u32v4{0, 0, 0, 0};
+      if (k + lcol < p.K) {
+        fetch_a(fa, k);
+        fetch_x(fa, k);
+      }
       stage(fa);
       multiply();
     }
-  }
-  if (split == p.splits - 1 && wave == SHRINK_WAVES - 1 && steps * 64 < p.K) {
-    // the rest of K, a multiple of 8: a lane's eight elements are in or out
-    const int k = steps * 64;
+    __syncthreads();                 // the areas become the sums to join
+    f32x4* sh = (f32x4*)lds;         // [wave][block][lane]
 #pragma unroll
-    for (int i = 0; i < AI; ++i) fa.a[i] = u32v4{0, 0, 0, 0};
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int i = 0; i < XI; ++i) fa.x[i] = u32v4{0, 0, 0, 0};
-    if (k + lcol < p.K) {
-      fetch_a(fa, k);
-      fetch_x(fa, k);
+      for (int r = 0; r < RT; ++r) sh[(wave * MT * RT + m * RT + r) * 64 + lane] = acc[m][r];
+    __syncthreads();
+    // block b of the tile: lane l holds ranks 4 (l / 16) .. + 3 of token l % 16
+    float* out = p.part + (int64_t)(group - share.first(unit)) * p.M * p.R;
+    for (int i = threadIdx.x; i < MT * RT * 64; i += 64 * SHRINK_WAVES) {
+      const int b = i >> 6, l = i & 63;
+      f32x4 u = sh[i];
+#pragma unroll
+      for (int w = 1; w < SHRINK_WAVES; ++w) u += sh[w * MT * RT * 64 + i];
+      const int row = (b / RT) * 16 + (l & 15), r = r0 + (b % RT) * 16 + (l >> 4) * 4;
+      if (row < tile.rows && r < p.R) *(f32x4*)(out + (int64_t)(tile.row0 + row) * p.R + r) = u;
     }
-    stage(fa);
-    multiply();
-  }
-  __syncthreads();                 // the areas become the sums to join
-  f32x4* sh = (f32x4*)lds;         // [wave][block][lane]
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) sh[(wave * MT * RT + m * RT + r) * 64 + lane] = acc[m][r];
-  __syncthreads();
-  // block b of the tile: lane l holds ranks 4 (l / 16) .. + 3 of token l % 16
-  float* out = p.part + (int64_t)split * p.M * p.R;
-  for (int i = threadIdx.x; i < MT * RT * 64; i += 64 * SHRINK_WAVES) {
-    const int b = i >> 6, l = i & 63;
-    f32x4 u = sh[i];
-#pragma unroll
-    for (int w = 1; w < SHRINK_WAVES; ++w) u += sh[w * MT * RT * 64 + i];
-    const int row = (b / RT) * 16 + (l & 15), r = r0 + (b % RT) * 16 + (l >> 4) * 4;
-    if (row < tile.rows && r < p.R) *(f32x4*)(out + (int64_t)(tile.row0 + row) * p.R + r) = u;
+    __syncthreads();                 // and areas again
   }
 }
 
@@ -251,7 +285,7 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(LoraArgs p) {
 // by side, the address path took most of 53 us for 4096 x 7168, rank 64).
 // Workgroups of a tile: runs of `run` column groups.
 template <int DT, int MT, int RP>
-__global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, int run) {
+__global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, int run, int runs) {
   constexpr int TM = 16 * MT, VP = RP + 8;                   // pitch of v in 16-bit elements
   constexpr int RH = RP < 64 ? RP : 64, HALVES = RP / RH;    // ranks at a time
   constexpr int BP = RH * 2 + 16, CP = 64 * 4 + 16;          // pitches in bytes: of B, of the products
@@ -260,9 +294,14 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
   __shared__ __attribute__((aligned(16))) uint8_t lds[EXPAND_WAVES * AREA];
   __shared__ float fac[TM];                                  // scale * 2^e
   const int groups = (p.N + 63) / 64;                        // of 64 columns
-  const Tile tile = find_tile<TM>(p.adapter_off, p.n, p.M, blockIdx.x, (groups + run - 1) / run);
-  if (tile.adapter < 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Tiles<TM> tiles(p.adapter_off, p.n, p.M);
+  const int work = tiles.total * runs;
+  if ((int)blockIdx.x >= work) return;
+  const int mine_at = xcd_run(blockIdx.x, work), index = mine_at / runs;
+  const Tile tile = tiles.find(index);
+  const int rlog = RP > 64;                                  // as in the shrink
+  const Share share(p, tiles.total << rlog);
   const float scale = p.scale != nullptr ? p.scale[tile.adapter] : 1.0f;
   const int c = lane & 15, q = lane >> 4, lrow = lane >> 3, lcol = (lane & 7) * 8;
   int ytok[2 * MT];
@@ -294,10 +333,10 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
       if (RP != 32 || i < per_row) bv[i] = *(const u32v4*)(bg + at);
     }
   };
-  const int g0 = tile.piece * run, g1 = min(groups, g0 + run);
+  const int g0 = (mine_at - index * runs) * run, g1 = min(groups, g0 + run);
   if (g0 + wave < g1) fetch(g0 + wave, 0);                   // on its way while v is formed
-  // v of the tile: RP / 4 lanes per row, four ranks each; the splits' partial
-  // sums, eight loads at a time, in split order
+  // v of the tile: RP / 4 lanes per row, four ranks each; the sum of the parts,
+  // eight loads at a time, in their order
   constexpr int PER = RP / 4, ROWS = 64 / PER;
   const int r = (lane & (PER - 1)) * 4;
   for (int row = wave * ROWS + lane / PER; row < TM; row += EXPAND_WAVES * ROWS) {
@@ -305,13 +344,14 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
     if (r < p.R && row < tile.rows) {
       const float* src = p.part + (int64_t)(tile.row0 + row) * p.R + r;
       const int64_t next = (int64_t)p.M * p.R;
-      for (int s = 0; s < p.splits; s += 8) {
+      const int unit = (index << rlog) + (r >> 6), parts = share.last(unit) - share.first(unit) + 1;
+      for (int s = 0; s < parts; s += 8) {
         f32x4 u[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = *(const f32x4*)(src + (int64_t)min(s + i, p.splits - 1) * next);
+        for (int i = 0; i < 8; ++i) u[i] = *(const f32x4*)(src + (int64_t)min(s + i, parts - 1) * next);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (s + i < p.splits) v += u[i];
+          if (s + i < parts) v += u[i];
       }
     }
     float down = 1.0f, up = 1.0f;
@@ -420,43 +460,66 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
 
 // 16-row blocks per tile. A tile holds one adapter's rows, so it is no larger than
 // an adapter's share; and a larger one reads A and B less often but leaves fewer
-// workgroups, so it takes many rows to pay.
-int row_blocks(int64_t M, int n, int most, int64_t from) {
+// workgroups to the expand, so it takes many rows to pay: 7168 x 7168, rank 64, 8
+// adapters, one block against four: 1024 tokens 24.1 and 26.1 us, 4096 tokens 63.8 and 51.9.
+constexpr int BIG_MT = 4;
+int row_blocks(int64_t M, int n) {
   const int64_t share = M / std::min<int64_t>(n, std::max<int64_t>(M, 1));
-  return M >= from && share >= 16 * most ? most : 1;
+  return M >= 2048 && share >= 16 * BIG_MT ? BIG_MT : 1;
 }
-constexpr int SHRINK_MT = 2, EXPAND_MT = 4;
-int shrink_mt(int64_t M, int n) { return row_blocks(M, n, SHRINK_MT, 1024); }
-int expand_mt(int64_t M, int n) { return row_blocks(M, n, EXPAND_MT, 2048); }
 // Upper bound of the tiles of mt 16-row blocks: every adapter adds one partly filled at most.
 int64_t lora_tiles(int64_t M, int n, int mt) { return M / (16 * mt) + std::min<int64_t>(n, M); }
 
-}  // namespace
+// 16-rank blocks of a shrink workgroup
+int rank_blocks(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
+// Shrink workgroups that fit the CUs of an MI355X at once (registers: one of
+// four waves with large tiles, else two).
+int slots_log2(int mt) { return mt == 1 ? 9 : 8; }
 
-// K splits of the shrink: the number that a workgroup's steps and the rounds of
-// workgroups, two on each CU of an MI355X, make fastest; a workgroup costs about
-// three steps beside its own. 1 to 16, each wave at least one step.
-int lora_splits(int64_t M, int64_t K, int R, int n) {
-  const int mt = shrink_mt(M, n);
-  const int64_t tiles = (M + 16 * mt - 1) / (16 * mt) + std::min<int64_t>(n, M) / 2, groups = (R + 63) / 64;
-  const int64_t steps = K / 64, most = std::min<int64_t>(16, std::max<int64_t>(1, steps / SHRINK_WAVES));
-  int best = 1;
-  double least = 0;
-  for (int s = 1; s <= most; ++s) {
-    const int64_t rounds = (tiles * groups * s + 511) / 512;
-    const double cost = (double)rounds * ((double)steps / (s * SHRINK_WAVES) + 3.0);
-    if (s == 1 || cost < least) {
-      best = s;
-      least = cost;
-    }
-  }
-  return best;
+hipError_t launch_expand(const LoraArgs& p, int mt, hipStream_t s) {
+  const int groups = (p.N + 63) / 64;
+  // runs of column groups: as many workgroups as fit the CUs of an MI355X at once,
+  // since each joins the tile's splits anew. 4096 x 7168, rank 64: 31.2 us at two
+  // per CU, 41.3 at three (two rounds, the second half empty), 36.8 at four
+  const int64_t runs = std::max<int64_t>(1, (mt == 1 ? 4 : 2) * 256 / lora_tiles(p.M, p.n, mt));
+  const int each = (int)((groups + runs * EXPAND_WAVES - 1) / (runs * EXPAND_WAVES));
+  const int run = each * EXPAND_WAVES, all_runs = (groups + run - 1) / run;
+  const unsigned grid = (unsigned)(lora_tiles(p.M, p.n, mt) * all_runs);
+  auto go = [&](auto d, auto m, auto r) {
+    k_lora_expand<decltype(d)::value, decltype(m)::value, decltype(r)::value><<<grid, 64 * EXPAND_WAVES, 0, s>>>(p, run, all_runs);
+  };
+  auto by_r = [&](auto d, auto m) {
+    if (p.R <= 32) go(d, m, std::integral_constant<int, 32>());
+    else if (p.R <= 64) go(d, m, std::integral_constant<int, 64>());
+    else go(d, m, std::integral_constant<int, 128>());
+  };
+  auto by_mt = [&](auto d) {
+    if (mt == 1) by_r(d, std::integral_constant<int, 1>());
+    else by_r(d, std::integral_constant<int, BIG_MT>());
+  };
+  if (p.dt == DT_BF16) by_mt(DtC<DT_BF16>());
+  else by_mt(DtC<DT_F16>());
+  return hipGetLastError();
 }
 
-hipError_t launch_lora_shrink(const LoraArgs& p, hipStream_t s) {
-  const int mt = shrink_mt(p.M, p.n);
-  const int rt = p.R <= 16 ? 1 : p.R <= 32 ? 2 : 4;
-  const unsigned grid = (unsigned)(lora_tiles(p.M, p.n, mt) * p.splits * ((p.R + 16 * rt - 1) / (16 * rt)));
+}  // namespace
+
+// Workgroups that may share one unit's K: what fills the slots, 16 at most.
+int lora_parts(int64_t M, int n) {
+  const int mt = row_blocks(M, n);
+  const int64_t tiles = std::max<int64_t>(1, M / (16 * mt));
+  return (int)std::min<int64_t>(16, 2 + ((1 << slots_log2(mt)) + tiles - 1) / tiles);
+}
+
+hipError_t launch_lora(const LoraArgs& args, hipStream_t s) {
+  LoraArgs p = args;
+  const int mt = row_blocks(p.M, p.n), rt = rank_blocks(p.R);
+  const int steps = std::max(p.K / 64, 1), parts = lora_parts(p.M, p.n);
+  p.slots_log2 = slots_log2(mt);
+  // a run of q = ceil(steps / (parts - 1)) steps or more touches a unit at most `parts` times
+  p.least = std::max(SHRINK_WAVES, (steps + parts - 2) / (parts - 1));
+  const int64_t units = lora_tiles(p.M, p.n, mt) << (p.R > 64);
+  const unsigned grid = (unsigned)std::min<int64_t>(1 << p.slots_log2, (units * steps + p.least - 1) / p.least);
   auto go = [&](auto d, auto m, auto r) {
     k_lora_shrink<decltype(d)::value, decltype(m)::value, decltype(r)::value><<<grid, 64 * SHRINK_WAVES, 0, s>>>(p);
   };
@@ -467,38 +530,12 @@ hipError_t launch_lora_shrink(const LoraArgs& p, hipStream_t s) {
   };
   auto by_mt = [&](auto d) {
     if (mt == 1) by_rt(d, std::integral_constant<int, 1>());
-    else by_rt(d, std::integral_constant<int, SHRINK_MT>());
+    else by_rt(d, std::integral_constant<int, BIG_MT>());
   };
   if (p.dt == DT_BF16) by_mt(DtC<DT_BF16>());
   else by_mt(DtC<DT_F16>());
-  return hipGetLastError();
-}
-
-hipError_t launch_lora_expand(const LoraArgs& p, hipStream_t s) {
-  const int mt = expand_mt(p.M, p.n);
-  const int groups = (p.N + 63) / 64;
-  // runs of column groups: as many workgroups as fit the CUs of an MI355X at once,
-  // since each joins the tile's splits anew. 4096 x 7168, rank 64: 31.2 us at two
-  // per CU, 41.3 at three (two rounds, the second half empty), 36.8 at four
-  const int64_t runs = std::max<int64_t>(1, (mt == 1 ? 4 : 2) * 256 / lora_tiles(p.M, p.n, mt));
-  const int each = (int)((groups + runs * EXPAND_WAVES - 1) / (runs * EXPAND_WAVES));
-  const int run = each * EXPAND_WAVES;
-  const unsigned grid = (unsigned)(lora_tiles(p.M, p.n, mt) * ((groups + run - 1) / run));
-  auto go = [&](auto d, auto m, auto r) {
-    k_lora_expand<decltype(d)::value, decltype(m)::value, decltype(r)::value><<<grid, 64 * EXPAND_WAVES, 0, s>>>(p, run);
-  };
-  auto by_r = [&](auto d, auto m) {
-    if (p.R <= 32) go(d, m, std::integral_constant<int, 32>());
-    else if (p.R <= 64) go(d, m, std::integral_constant<int, 64>());
-    else go(d, m, std::integral_constant<int, 128>());
-  };
-  auto by_mt = [&](auto d) {
-    if (mt == 1) by_r(d, std::integral_constant<int, 1>());
-    else by_r(d, std::integral_constant<int, EXPAND_MT>());
-  };
-  if (p.dt == DT_BF16) by_mt(DtC<DT_BF16>());
-  else by_mt(DtC<DT_F16>());
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : launch_expand(p, mt, s);
 }
 
 }  // namespace mx

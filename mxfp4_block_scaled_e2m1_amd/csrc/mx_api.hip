@@ -1742,7 +1742,7 @@ size_t mx_lora_add_workspace_size(int64_t M, int64_t K, int64_t R, int32_t n) {
   if (M < 0 || K < 8 || R < 8 || n < 1 || M > (1 << 24) || K > (1 << 20) || R > LORA_MAX_RANK || n > ROUTE_MAX_EXPERTS)
     return 0;
   Carve c(nullptr);
-  c.take((size_t)lora_splits(M, K, (int)R, n) * (size_t)M * (size_t)R * 4);
+  c.take((size_t)lora_parts(M, n) * (size_t)M * (size_t)R * 4);
   return c.off;
 }
 
@@ -1755,6 +1755,7 @@ mx_status mx_lora_add(mx_dtype dt, const void* x, int64_t ldx, int64_t M, int64_
   if (M < 0 || M > (1 << 24)) return fail(MX_ERR_SHAPE, "M %lld not in [0, 2^24]", (long long)M);
   if (K < 8 || K % 8 != 0 || K > (1 << 20)) return fail(MX_ERR_SHAPE, "K %lld must be a multiple of 8 in [8, 2^20]", (long long)K);
   if (N < 8 || N % 8 != 0 || N > (1 << 20)) return fail(MX_ERR_SHAPE, "N %lld must be a multiple of 8 in [8, 2^20]", (long long)N);
+  if (M * K > LORA_MAX_MK) return fail(MX_ERR_SHAPE, "M %lld x K %lld is above 2^38", (long long)M, (long long)K);
   if (R < 8 || R % 8 != 0 || R > LORA_MAX_RANK)
     return fail(MX_ERR_SHAPE, "rank %lld must be a multiple of 8 in [8, %d]", (long long)R, LORA_MAX_RANK);
   if (n < 1 || n > ROUTE_MAX_EXPERTS) return fail(MX_ERR_SHAPE, "%d adapters not in [1, %d]", n, ROUTE_MAX_EXPERTS);
@@ -1800,9 +1801,8 @@ mx_status mx_lora_add(mx_dtype dt, const void* x, int64_t ldx, int64_t M, int64_
   p.adapter_off = adapter_off; p.row_token = row_token;
   p.y = y; p.ldy = ldy;
   p.part = (float*)workspace;
-  p.splits = lora_splits(M, K, (int)R, n);
-  MX_HIP(phase("lora_shrink", s, [&] { return launch_lora_shrink(p, s); }), "lora_shrink");
-  MX_HIP(phase("lora_expand", s, [&] { return launch_lora_expand(p, s); }), "lora_expand");
+  p.slots_log2 = p.least = 0;
+  MX_HIP(phase("lora_add", s, [&] { return launch_lora(p, s); }), "lora_add");
   return ok();
 }
 

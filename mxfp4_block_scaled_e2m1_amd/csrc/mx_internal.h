@@ -315,12 +315,15 @@ struct LoraArgs {
   const int32_t* row_token;     // [M] token of each sorted row
   void* y;                      // [M, N], rows ldy elements apart
   int64_t ldy;
-  float* part;                  // [splits][M][R]
-  int splits;
+  float* part;                  // [lora_parts()][M][R]
+  // set by launch_lora: the shrink's workgroups (at most 2^slots_log2) and the
+  // fewest K steps that one takes
+  int slots_log2, least;
 };
-int lora_splits(int64_t M, int64_t K, int R, int n);
-hipError_t launch_lora_shrink(const LoraArgs& p, hipStream_t s);
-hipError_t launch_lora_expand(const LoraArgs& p, hipStream_t s);
+int lora_parts(int64_t M, int n);
+// Two kernels. M * K <= LORA_MAX_MK keeps the count of K steps in 32 bits.
+constexpr int64_t LORA_MAX_MK = (int64_t)1 << 38;
+hipError_t launch_lora(const LoraArgs& p, hipStream_t s);
 
 // Measurement probes (probe.hip). mode 0: reads into registers, 1: into LDS;
 // loads_per_wave 8 or 32; bytes a multiple of loads_per_wave KiB; out holds
