@@ -447,7 +447,7 @@ def _need(cond, what):
 
 def _tensor(t, name, dtype, shape, device):
     """t as a device pointer, once its type, shape, device and layout are as said."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device.index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}: got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}"
                          f"{'' if t.is_contiguous() else ', not contiguous'}")
@@ -455,7 +455,7 @@ def _tensor(t, name, dtype, shape, device):
 
 
 def _dtype(t, name):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("libmxfp4 takes device tensors")
     dt = MX_DT.get(t.dtype)
     if dt is None:
@@ -466,18 +466,20 @@ def _dtype(t, name):
 def _run(fn, device, stream, scratch, *args):
     """fn(*args, stream) on `device`; `scratch` is memory of this call's own that the stream goes on using."""
     if stream is None:
-        # torch.cuda.current_stream(device).cuda_stream without the Stream object, which costs
-        # as much as the library call
+        # torch.cuda.current_stream(device).cuda_stream and current_device() without what they
+        # build and check on the way, which costs as much as the library call
         s = torch._C._cuda_getCurrentRawStream(device.index)
     else:
         s = stream.cuda_stream
         if scratch is not None:
             scratch.record_stream(stream)
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, s))
+    if torch._C._cuda_getDevice() == device.index:
+        status = fn(*args, s)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, s))
+            status = fn(*args, s)
+    if status != 0:
+        _check(status)
 
 
 def _out(out, name, like, stream):
@@ -521,7 +523,7 @@ def moe_sort(topk_ids, E: int, expert_off=None, row_slot=None, slot_row=None, wo
     """mx_moe_sort: int32 topk_ids [T, k] -> (expert_off [E+1], row_slot [T*k], slot_row [T, k]), all int32."""
     T, k = topk_ids.shape
     dev, i32 = topk_ids.device, torch.int32
-    _need(dev.type == "cuda", "libmxfp4 takes device tensors")
+    _need(topk_ids.is_cuda, "libmxfp4 takes device tensors")
     _need(1 <= E <= 512, f"E {E} not in [1, 512]")
     ids = _tensor(topk_ids, "topk_ids", i32, (T, k), dev)
     expert_off, op = _new(expert_off, "expert_off", (E + 1,), i32, dev, stream)

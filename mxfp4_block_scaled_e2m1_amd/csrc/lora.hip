@@ -10,10 +10,11 @@
 // moving x, y and the adapters in use, so both are bound by memory: by HBM for
 // prompts, by latency for a few tokens.
 //
-// v stays fp32-accurate: for the matrix unit each value is split into two
-// 16-bit halves, hi + lo, after a power-of-two scaling of the token's row
-// (rounding v to one bf16 would be off by up to 2^-9 of every product, and fp16 could
-// overflow); the second product costs no memory traffic. y is rounded once.
+// v is formed in fp32. For the matrix unit each value is split into two 16-bit
+// halves, hi + lo, in fp16 after a power-of-two scaling of the token's row (it could
+// overflow otherwise): within 2^-17 of the value in bf16, 2^-21 in fp16. One bf16
+// would be off by up to 2^-9 of every product; the second matrix product costs no
+// memory traffic. y is rounded once.
 #include <algorithm>
 #include <type_traits>
 
@@ -126,7 +127,7 @@ __device__ __forceinline__ void wave_sync() {
 // Parts of v, [part][sorted row][R]: per unit MT x RT blocks of 16 tokens x 16 ranks.
 // A matrix operand wants 16 rows side by side in the lanes, but a load whose
 // neighbouring lanes are in different rows takes the address path one row at a time
-// (4096 x 7168, rank 64: 39 us that way even with x in L2). So a wave loads whole
+// (4096 x 7168, rank 64: 39 us that way, 35 with x in L2). So a wave loads whole
 // 128-byte lines, eight lanes each, the rows of a 64-wide step of K, turns them
 // in an LDS area of its own (pitch 144: conflict-free) and has the next
 // two steps' loads in flight meanwhile. The waves take a workgroup's steps in turn,

@@ -253,6 +253,8 @@ void dispatch_dt(DType dt, F&& f) {
 // expert_off [E+1], row_slot [P] (-1 past the last routed pair), slot_row [P]
 // (-1: id outside [0, E)). tile_base [E+1] and block_counts [chunks, E] are
 // scratch, not used when sort_in_one_block().
+// One workgroup against two launches, us on the GPU: 2048 pairs 4.3 and 6.1, 4096
+// pairs 6.6 and 6.3 (48 experts) or 5.7 and 6.9 (8), and a launch less on the host.
 constexpr int64_t SORT_ONE_BLOCK = 4096;
 // One workgroup sorts all pairs: its counts, one per expert and 64 pairs, fit LDS.
 inline bool sort_in_one_block(int64_t P, int n_experts) {
