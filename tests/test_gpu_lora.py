@@ -73,7 +73,9 @@ def test_without_scale_and_without_tokens(mx):
 
 
 @pytest.mark.parametrize("M,K,N,R,n", [(1, 7168, 1536, 64, 4), (64, 7168, 7168, 16, 32), (700, 7168, 1536, 128, 3),
-                                       (300, 1536, 7168, 40, 100), (2100, 520, 1000, 24, 6)])
+                                       (300, 1536, 7168, 40, 100), (2100, 520, 1000, 24, 6),
+                                       (2500, 256, 264, 128, 3), (2304, 1032, 64, 72, 4), (2100, 40, 72, 16, 2),
+                                       (4500, 128, 64, 8, 512), (5000, 64, 136, 56, 1)])
 @pytest.mark.parametrize("name", ["bf16", "fp16"])
 def test_whole_numbers_come_out_exactly(mx, M, K, N, R, n, name):
     """Small whole numbers keep every sum exact in fp32 and every v exact in its halves, so that the output is
@@ -154,3 +156,20 @@ def test_more_than_2_to_the_31_elements(mx):
     mx.lora_add(y, x, a, b, *_plan(mx, adapter, n))
     ref = around.lora_add(np.zeros((40, N)), x64, a64, b64, adapter[-40:])
     assert torch.equal(y[-40:].cpu(), torch.from_numpy(ref).to(torch.bfloat16)) and not y[:-40].any()
+
+
+@pytest.mark.parametrize("M,busy", [(1, 0), (40, 1), (4100, 5), (4100, 3000), (4100, 0)])
+def test_adapters_of_few_of_the_tokens(mx, M, busy):
+    """Most tokens without an adapter, most adapters without a token, all of an adapter's tokens in one place."""
+    K, N, R, n = 192, 136, 24, 300
+    rng = np.random.default_rng(busy)
+    x, x64 = pair(rng.integers(-2, 3, size=(M, K)), "fp16")
+    y, y64 = pair(rng.integers(-8, 9, size=(M, N)), "fp16")
+    a, a64 = pair(rng.integers(-1, 2, size=(n, R, K)), "fp16")
+    b, b64 = pair(rng.integers(-1, 2, size=(n, N, R)), "fp16")
+    adapter = np.full(M, -1)
+    adapter[M - busy:] = 297
+    adapter[:min(busy, 2)] = (0, 299)[:min(busy, 2)]
+    mx.lora_add(y, x, a, b, *_plan(mx, adapter, n))
+    ref = around.lora_add(y64, x64, a64, b64, adapter)
+    assert torch.equal(y.cpu(), torch.from_numpy(ref).to(torch.float16))
