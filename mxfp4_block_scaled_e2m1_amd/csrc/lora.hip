@@ -336,25 +336,41 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
   };
   const int g0 = (mine_at - index * runs) * run, g1 = min(groups, g0 + run);
   if (g0 + wave < g1) fetch(g0 + wave, 0);                   // on its way while v is formed
-  // v of the tile: RP / 4 lanes per row, four ranks each; the sum of the parts,
-  // eight loads at a time, in their order
+  // v of the tile: RP / 4 lanes per row, four ranks each, ITER rows per thread; the
+  // sum of the parts in their order, eight loads in flight (row by row they cost a
+  // tile of 64 rows and 128 ranks eight latencies: 1024 + 1024 columns of 8192 tokens
+  // took 28.1 us and take 25.1)
   constexpr int PER = RP / 4, ROWS = 64 / PER;
-  const int r = (lane & (PER - 1)) * 4;
-  for (int row = wave * ROWS + lane / PER; row < TM; row += EXPAND_WAVES * ROWS) {
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (r < p.R && row < tile.rows) {
-      const float* src = p.part + (int64_t)(tile.row0 + row) * p.R + r;
-      const int64_t next = (int64_t)p.M * p.R;
-      const int unit = (index << rlog) + (r >> 6), parts = share.last(unit) - share.first(unit) + 1;
-      for (int s = 0; s < parts; s += 8) {
-        f32x4 u[8];
+  constexpr int ITER = TM > EXPAND_WAVES * ROWS ? TM / (EXPAND_WAVES * ROWS) : 1, AHEAD = 8 / ITER;
+  const int r = (lane & (PER - 1)) * 4, vrow = wave * ROWS + lane / PER;
+  f32x4 vs[ITER];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = *(const f32x4*)(src + (int64_t)min(s + i, parts - 1) * next);
+  for (int i = 0; i < ITER; ++i) vs[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (r < p.R) {
+    const int unit = (index << rlog) + (r >> 6), parts = share.last(unit) - share.first(unit) + 1;
+    const float* src[ITER];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (s + i < parts) v += u[i];
-      }
+    for (int i = 0; i < ITER; ++i)     // rows past the tile repeat the last one: never used
+      src[i] = p.part + (int64_t)(tile.row0 + min(vrow + i * EXPAND_WAVES * ROWS, tile.rows - 1)) * p.R + r;
+    const int64_t next = (int64_t)p.M * p.R;
+    for (int s = 0; s < parts; s += AHEAD) {
+      f32x4 u[AHEAD][ITER];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) u[j][i] = *(const f32x4*)(src[i] + (int64_t)min(s + j, parts - 1) * next);
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+        for (int i = 0; i < ITER; ++i)
+          if (s + j < parts) vs[i] += u[j][i];
     }
+  }
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const int row = vrow + i * EXPAND_WAVES * ROWS;
+    if (row >= TM) continue;
+    const f32x4 v = vs[i];
     float down = 1.0f, up = 1.0f;
     if constexpr (DT == DT_F16) {
       // 2^-e with 2^e the exponent of the row's largest value, where that is an
@@ -461,12 +477,15 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
 
 // 16-row blocks per tile. A tile holds one adapter's rows, so it is no larger than
 // an adapter's share; and a larger one reads A and B less often but leaves fewer
-// workgroups to the expand, so it takes many rows to pay: 7168 x 7168, rank 64, 8
-// adapters, one block against four: 1024 tokens 24.1 and 26.1 us, 4096 tokens 63.8 and 51.9.
+// workgroups, so it takes many rows and much to read of each to pay. One block
+// against four, rank 64, 4 adapters, us: 1024 tokens of 7168 + 7168 columns 24.1 and
+// 26.1, 4096 of them 48.2 and 41.3; 4096 tokens of 2048 + 512 14.7 and 15.1, of
+// 2048 + 2048 20.5 and 20.2; 8192 tokens of 512 + 512 14.6 and 15.3, of 2048 + 2048
+// 31.9 and 29.3.
 constexpr int BIG_MT = 4;
-int row_blocks(int64_t M, int n) {
-  const int64_t share = M / std::min<int64_t>(n, std::max<int64_t>(M, 1));
-  return M >= 2048 && share >= 16 * BIG_MT ? BIG_MT : 1;
+bool big_rows(int64_t M, int n) { return M >= 2048 && M / n >= 16 * BIG_MT; }
+int row_blocks(const LoraArgs& p) {
+  return big_rows(p.M, p.n) && (int64_t)p.M * (p.K + p.N) >= (int64_t)1 << 24 ? BIG_MT : 1;
 }
 // Upper bound of the tiles of mt 16-row blocks: every adapter adds one partly filled at most.
 int64_t lora_tiles(int64_t M, int n, int mt) { return M / (16 * mt) + std::min<int64_t>(n, M); }
@@ -476,6 +495,11 @@ int rank_blocks(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
 // Shrink workgroups that fit the CUs of an MI355X at once (registers: one of
 // four waves with large tiles, else two).
 int slots_log2(int mt) { return mt == 1 ? 9 : 8; }
+// Workgroups that may share one unit's K: what fills the slots, 16 at most.
+int shrink_parts(int64_t M, int mt) {
+  const int64_t tiles = std::max<int64_t>(1, M / (16 * mt));
+  return (int)std::min<int64_t>(16, 2 + ((1 << slots_log2(mt)) + tiles - 1) / tiles);
+}
 
 hipError_t launch_expand(const LoraArgs& p, int mt, hipStream_t s) {
   const int groups = (p.N + 63) / 64;
@@ -505,17 +529,15 @@ hipError_t launch_expand(const LoraArgs& p, int mt, hipStream_t s) {
 
 }  // namespace
 
-// Workgroups that may share one unit's K: what fills the slots, 16 at most.
+// The workspace is asked for without N, so it holds the parts of either tile.
 int lora_parts(int64_t M, int n) {
-  const int mt = row_blocks(M, n);
-  const int64_t tiles = std::max<int64_t>(1, M / (16 * mt));
-  return (int)std::min<int64_t>(16, 2 + ((1 << slots_log2(mt)) + tiles - 1) / tiles);
+  return std::max(shrink_parts(M, 1), big_rows(M, n) ? shrink_parts(M, BIG_MT) : 0);
 }
 
 hipError_t launch_lora(const LoraArgs& args, hipStream_t s) {
   LoraArgs p = args;
-  const int mt = row_blocks(p.M, p.n), rt = rank_blocks(p.R);
-  const int steps = std::max(p.K / 64, 1), parts = lora_parts(p.M, p.n);
+  const int mt = row_blocks(p), rt = rank_blocks(p.R);
+  const int steps = std::max(p.K / 64, 1), parts = shrink_parts(p.M, mt);
   p.slots_log2 = slots_log2(mt);
   // a run of q = ceil(steps / (parts - 1)) steps or more touches a unit at most `parts` times
   p.least = std::max(SHRINK_WAVES, (steps + parts - 2) / (parts - 1));

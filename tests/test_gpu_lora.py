@@ -173,3 +173,35 @@ def test_adapters_of_few_of_the_tokens(mx, M, busy):
     mx.lora_add(y, x, a, b, *_plan(mx, adapter, n))
     ref = around.lora_add(y64, x64, a64, b64, adapter)
     assert torch.equal(y.cpu(), torch.from_numpy(ref).to(torch.float16))
+
+
+@pytest.mark.parametrize("M,K,N,R,n", [(2100, 7176, 824, 24, 6), (2500, 256, 6480, 128, 3), (2304, 1032, 6256, 72, 4),
+                                       (2100, 40, 7960, 16, 2), (4500, 128, 3608, 8, 70), (5000, 64, 3296, 56, 1),
+                                       (70000, 136, 104, 40, 5)])
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+def test_prompts_of_wide_rows(mx, M, K, N, R, n, name):
+    """M (K + N) of 2^24 and more: the large tiles, at ranks, widths and shares that do not fill them."""
+    test_whole_numbers_come_out_exactly(mx, M, K, N, R, n, name)
+
+
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+def test_prompts_of_wide_rows_in_ordinary_numbers(mx, name):
+    rng = np.random.default_rng(12)
+    _case(mx, 2100, 4104, 4000, 88, 3, rng.integers(-1, 4, size=2100), name, 13)
+
+
+@pytest.mark.parametrize("busy", [0, 5, 63, 64, 65, 3000])
+def test_prompts_with_adapters_of_few_of_the_tokens(mx, busy):
+    """As test_adapters_of_few_of_the_tokens, in large tiles: one filled partly, exactly, and one row over."""
+    M, K, N, R, n = 4100, 2056, 2048, 24, 60
+    rng = np.random.default_rng(busy)
+    x, x64 = pair(rng.integers(-2, 3, size=(M, K)), "bf16")
+    y, y64 = pair(rng.integers(-8, 9, size=(M, N)), "bf16")
+    a, a64 = pair(rng.integers(-1, 2, size=(n, R, K)), "bf16")
+    b, b64 = pair(rng.integers(-1, 2, size=(n, N, R)), "bf16")
+    adapter = np.full(M, -1)
+    adapter[M - busy:] = 57
+    adapter[:min(busy, 2)] = (0, 59)[:min(busy, 2)]
+    mx.lora_add(y, x, a, b, *_plan(mx, adapter, n))
+    ref = around.lora_add(y64, x64, a64, b64, adapter)
+    assert torch.equal(y.cpu(), torch.from_numpy(ref).to(torch.bfloat16))
