@@ -61,8 +61,8 @@ __device__ __forceinline__ void walk_rows(int64_t T, int groups, int group, Fetc
 // (v * threads + tid) * N. A workgroup holds blockDim / (64 gw) such groups, which
 // take rows side by side, and strides over the rows. GATE: the gate kind. PF: the
 // next row's pieces are loaded before this row's sums are waited for: with
-// one workgroup on a CU the sums would otherwise leave HBM idle, and more
-// workgroups are slower (the streams they make spread over HBM).
+// one or two workgroups on a CU the sums would otherwise leave HBM idle, and many
+// are slower (the streams they make spread over HBM).
 template <int DT, int RDT, int N, int V, int GATE, bool PF, bool AL>
 __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a, int gw) {
   __shared__ float red_all[16 * 2 * 16];                 // per group 2 * 16
@@ -468,13 +468,20 @@ void dispatch_pair(DType dt, DType rdt, F&& f) {
 static int piece(DType dt) { return dt == DT_F32 ? 4 : 8; }
 bool block_norm_aligned(DType dt, int H, uintptr_t all_pointers) { return H % piece(dt) == 0 && all_pointers % 16 == 0; }
 
-// One workgroup of up to 16 waves per CU of an MI355X. Measured on 4096 x 7168,
-// bf16 beside an fp32 residual, before the prefetch: 14 waves on every CU 65.9 us,
-// twice as many workgroups 68.8, four times 72.6; 7 waves, V = 2: 67.6 to 76.1.
+// One workgroup of up to 16 waves per CU of an MI355X. The way back keeps it so (4096
+// rows and more; 8192 x 7168 bf16 112 us, 120 with two), and so do rows of more than a
+// piece per thread and unaligned ones (8192 x 4290 bf16: 63.8 us, two 64.7).
 constexpr int ROW_GRID = 256;
-// Groups per workgroup: as many as there are rows for on every CU.
-int row_groups(int64_t T, int waves) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(16 / waves, (T + ROW_GRID - 1) / ROW_GRID));
+// The norm itself takes two, whose rows' sums and stores fall in each other's gaps, as
+// long as the rows they spread over HBM do not cost more. One against two, bf16, us:
+// 1000 x 7168 14.0 and 12.5, 4096 x 7168 48.5 and 44.9 (fp32 residual 69.3 and 68.3),
+// 16384 x 4096 97.7 and 97.0, 16384 x 7168 175 and 182.
+int norm_grid(int64_t T, int H, int V, bool aligned) {
+  return aligned && V == 1 && T * H <= (int64_t)1 << 26 ? 2 * ROW_GRID : ROW_GRID;
+}
+// Groups per workgroup: as many as there are rows for in every workgroup.
+int row_groups(int64_t T, int waves, int grid) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(16 / waves, (T + grid - 1) / grid));
 }
 
 // An upper bound of the workgroups of the way back, each with a partial sum.
@@ -497,8 +504,8 @@ void dispatch_shape(int H, int V, bool aligned, F&& f) {
 
 hipError_t launch_block_norm(const BlockNormArgs& a, bool aligned, hipStream_t s) {
   const RowShape sh = row_shape(a.H, piece(a.dt), 16);
-  const int groups = row_groups(a.T, sh.waves);
-  const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, ROW_GRID);
+  const int most = norm_grid(a.T, a.H, sh.V, aligned), groups = row_groups(a.T, sh.waves, most);
+  const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, most);
   const int threads = 64 * sh.waves * groups;
   dispatch_pair(a.dt, a.rdt, [&](auto d, auto r) {
     constexpr int D = decltype(d)::value, R = decltype(r)::value;
@@ -515,7 +522,7 @@ hipError_t launch_block_norm(const BlockNormArgs& a, bool aligned, hipStream_t s
 
 hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, bool aligned, hipStream_t s) {
   const RowShape sh = row_shape(a.H, piece(a.dt), 16);
-  const int groups = row_groups(a.T, sh.waves);
+  const int groups = row_groups(a.T, sh.waves, ROW_GRID);
   const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, ROW_GRID);
   const size_t lds = groups > 1 ? (size_t)groups * a.H * 4 : 0;
   const int threads = 64 * sh.waves * groups;
