@@ -503,13 +503,28 @@ int shrink_parts(int64_t M, int mt) {
 
 hipError_t launch_expand(const LoraArgs& p, int mt, hipStream_t s) {
   const int groups = (p.N + 63) / 64;
-  // runs of column groups: as many workgroups as fit the CUs of an MI355X at once,
-  // since each joins the tile's splits anew. 4096 x 7168, rank 64: 31.2 us at two
-  // per CU, 41.3 at three (two rounds, the second half empty), 36.8 at four
-  const int64_t runs = std::max<int64_t>(1, (mt == 1 ? 4 : 2) * 256 / lora_tiles(p.M, p.n, mt));
-  const int each = (int)((groups + runs * EXPAND_WAVES - 1) / (runs * EXPAND_WAVES));
-  const int run = each * EXPAND_WAVES, all_runs = (groups + run - 1) / run;
-  const unsigned grid = (unsigned)(lora_tiles(p.M, p.n, mt) * all_runs);
+  // Runs of column groups, `each` per wave. Workgroups that do not fit the CUs of an
+  // MI355X at once (two of large tiles, else four) wait for another round, and each
+  // forms the tile's v anew, half a group of a wave's time: of what fills one to
+  // eight rounds, the one of the least rounds x (each + 1/2). 7168 columns, rank 64:
+  // 4096 tokens 31.2 us in one full round, 41.3 in one and a half, 36.8 in two; with
+  // x of 7168 columns, 8 adapters, the most that one round holds against this, us: 8192
+  // tokens 89 and 83, 20000 tokens 229 and 198, 34000 tokens 364 and 315.
+  const int64_t tiles = lora_tiles(p.M, p.n, mt), slots = (mt == 1 ? 4 : 2) * 256;
+  int run = 0, all_runs = 0;
+  for (int64_t k = 1, least = INT64_MAX; k <= 8; ++k) {
+    const int64_t runs = std::max<int64_t>(1, k * slots / tiles);
+    const int each = (int)((groups + runs * EXPAND_WAVES - 1) / (runs * EXPAND_WAVES));
+    const int some = (groups + each * EXPAND_WAVES - 1) / (each * EXPAND_WAVES);
+    const int64_t cost = (tiles * some + slots - 1) / slots * (2 * each + 1);
+    if (cost < least) {
+      least = cost;
+      run = each * EXPAND_WAVES;
+      all_runs = some;
+    }
+    if (each == 1) break;              // no shorter runs
+  }
+  const unsigned grid = (unsigned)(tiles * all_runs);
   auto go = [&](auto d, auto m, auto r) {
     k_lora_expand<decltype(d)::value, decltype(m)::value, decltype(r)::value><<<grid, 64 * EXPAND_WAVES, 0, s>>>(p, run, all_runs);
   };

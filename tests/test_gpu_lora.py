@@ -205,3 +205,9 @@ def test_prompts_with_adapters_of_few_of_the_tokens(mx, busy):
     mx.lora_add(y, x, a, b, *_plan(mx, adapter, n))
     ref = around.lora_add(y64, x64, a64, b64, adapter)
     assert torch.equal(y.cpu(), torch.from_numpy(ref).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("M,K,N,R,n", [(9000, 64, 2056, 16, 8), (21000, 32, 1096, 8, 4), (36000, 16, 520, 72, 2),
+                                       (1500, 64, 5000, 8, 90)])
+def test_more_tiles_than_one_round_of_workgroups(mx, M, K, N, R, n):
+    test_whole_numbers_come_out_exactly(mx, M, K, N, R, n, "bf16")
