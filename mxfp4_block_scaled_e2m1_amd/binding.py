@@ -463,16 +463,14 @@ def _dtype(t, name):
     return dt
 
 
-def _run(fn, device, stream, scratch, *args):
-    """fn(*args, stream) on `device`; `scratch` is memory of this call's own that the stream goes on using."""
+def _run(fn, device, stream, *args):
+    """fn(*args, stream) on `device`."""
     if stream is None:
         # torch.cuda.current_stream(device).cuda_stream and current_device() without what they
         # build and check on the way, which costs as much as the library call
         s = torch._C._cuda_getCurrentRawStream(device.index)
     else:
         s = stream.cuda_stream
-        if scratch is not None:
-            scratch.record_stream(stream)
     if torch._C._cuda_getDevice() == device.index:
         status = fn(*args, s)
     else:
@@ -482,14 +480,21 @@ def _run(fn, device, stream, scratch, *args):
         _check(status)
 
 
+def _made(stream, make, *args, **kwargs):
+    """make(...): an output that a call on the given `stream` makes itself, from that stream's memory. A block of the
+    current stream's may still be in use there by work that `stream` does not wait for. The current stream is
+    made known to the tensor, since the caller will mostly go on with it there."""
+    with torch.cuda.stream(stream):
+        t = make(*args, **kwargs)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _out(out, name, like, stream):
-    """(`out` or a new tensor, its pointer): of the type, shape and device of the contiguous `like`. A new one
-    is made known to `stream` where that is not the current one."""
+    """(`out` or a new tensor, its pointer): of the type, shape and device of the contiguous `like`."""
     if out is not None:
         return out, _tensor(out, name, like.dtype, like.shape, like.device)
-    out = torch.empty_like(like)
-    if stream is not None:
-        out.record_stream(stream)
+    out = torch.empty_like(like) if stream is None else _made(stream, torch.empty_like, like)
     return out, out.data_ptr()
 
 
@@ -498,20 +503,27 @@ def _new(out, name, shape, dtype, device, stream):
     if out is not None:
         return out, _tensor(out, name, dtype, shape, device)
     # torch.empty, which takes a third longer
-    out = torch.empty_strided(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype=dtype, device=device)
-    if stream is not None:
-        out.record_stream(stream)
+    strides = (1,) if len(shape) == 1 else (shape[1], 1)
+    if stream is None:
+        out = torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    else:
+        out = _made(stream, torch.empty_strided, shape, strides, dtype=dtype, device=device)
     return out, out.data_ptr()
 
 
-def _scratch(workspace, nbytes, device):
-    """(tensor to keep if it is the call's own, pointer, bytes)"""
+def _scratch(workspace, nbytes, device, stream):
+    """(tensor to keep until the call has been made, pointer, bytes). Memory of the call's own is the call's stream's:
+    let go of afterwards, it comes back for later work of that stream only."""
     if workspace is not None:
         _need(workspace.device == device and workspace.is_contiguous(), f"workspace must be contiguous and on {device}")
-        return None, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if nbytes == 0:
         return None, None, 0
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        with torch.cuda.stream(stream):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return ws, ws.data_ptr(), nbytes
 
 
@@ -530,8 +542,8 @@ def moe_sort(topk_ids, E: int, expert_off=None, row_slot=None, slot_row=None, wo
     row_slot, rp = _new(row_slot, "row_slot", (T * k,), i32, dev, stream)
     slot_row, sp = _out(slot_row, "slot_row", topk_ids, stream)
     L = lib()
-    ws, wp, wn = _scratch(workspace, int(L.mx_moe_sort_workspace_size(T, k, E)), dev)
-    _run(L.mx_moe_sort, dev, stream, ws, ids, T, k, E, op, rp, sp, wp, wn)
+    ws, wp, wn = _scratch(workspace, int(L.mx_moe_sort_workspace_size(T, k, E)), dev, stream)
+    _run(L.mx_moe_sort, dev, stream, ids, T, k, E, op, rp, sp, wp, wn)
     return expert_off, row_slot, slot_row
 
 
@@ -543,7 +555,7 @@ def moe_permute(x, slot_row, out=None, stream=None):
     dev = x.device
     dt = _dtype(x, "x")
     out, op = _new(out, "out", (T * k if out is None else out.shape[0], H), x.dtype, dev, stream)
-    _run(lib().mx_moe_permute, dev, stream, None, dt, _tensor(x, "x", x.dtype, (T, H), dev), T, H,
+    _run(lib().mx_moe_permute, dev, stream, dt, _tensor(x, "x", x.dtype, (T, H), dev), T, H,
          _tensor(slot_row, "slot_row", torch.int32, (T, k), dev), k, out.shape[0], op)
     return out
 
@@ -555,7 +567,7 @@ def moe_unpermute(ys, slot_row, topk_w=None, out=None, stream=None):
     dev = ys.device
     dt = _dtype(ys, "ys")
     out, op = _new(out, "out", (T, H), ys.dtype, dev, stream)
-    _run(lib().mx_moe_unpermute, dev, stream, None, dt, _tensor(ys, "ys", ys.dtype, (rows, H), dev), rows, H,
+    _run(lib().mx_moe_unpermute, dev, stream, dt, _tensor(ys, "ys", ys.dtype, (rows, H), dev), rows, H,
          _tensor(slot_row, "slot_row", torch.int32, (T, k), dev),
          None if topk_w is None else _tensor(topk_w, "topk_w", torch.float32, (T, k), dev), T, k, op)
     return out
@@ -570,11 +582,10 @@ def moe_unpermute_grad(d_y, ys, slot_row, topk_w, d_ys=None, d_w=None, stream=No
     dt = _dtype(ys, "ys")
     yp = _tensor(ys, "ys", ys.dtype, (rows, H), dev)
     if d_ys is None:
-        with torch.cuda.stream(stream):
-            d_ys = torch.zeros_like(ys)
+        d_ys = torch.zeros_like(ys) if stream is None else _made(stream, torch.zeros_like, ys)
     wp = _tensor(topk_w, "topk_w", torch.float32, (T, k), dev)
     d_w, dwp = _out(d_w, "d_w", topk_w, stream)
-    _run(lib().mx_moe_unpermute_grad, dev, stream, None, dt, _tensor(d_y, "d_y", ys.dtype, (T, H), dev), yp, rows, H,
+    _run(lib().mx_moe_unpermute_grad, dev, stream, dt, _tensor(d_y, "d_y", ys.dtype, (T, H), dev), yp, rows, H,
          _tensor(slot_row, "slot_row", torch.int32, (T, k), dev), wp, T, k,
          _tensor(d_ys, "d_ys", ys.dtype, (rows, H), dev), dwp)
     return d_ys, d_w
@@ -616,7 +627,7 @@ def block_norm(residual, w_pre=None, y=None, w_post=None, gate=None, res_scale: 
             _new(normed, "normed", (T, H), adt, dev, stream)
     else:
         _need(normed is None, "normed needs w_pre")
-    _run(lib().mx_block_norm, dev, stream, None, dt, rdt, yp, res,
+    _run(lib().mx_block_norm, dev, stream, dt, rdt, yp, res,
          None if w_post is None else _tensor(w_post, "w_post", adt, (H,), dev), kind,
          None if gate is None else _tensor(gate, "gate", adt, gshape, dev), res_scale,
          None if w_pre is None else _tensor(w_pre, "w_pre", adt, (H,), dev), eps, T, H, ro, no)
@@ -652,8 +663,8 @@ def block_norm_grad(residual_out, w_pre=None, d_normed=None, d_residual_out=None
     d_residual, dr_p = _out(d_residual, "d_residual", residual_out, stream)
     d_y, dy_p = none if y is None else _out(d_y, "d_y", y, stream)
     L = lib()
-    ws, wp, wn = _scratch(workspace, int(L.mx_block_norm_grad_workspace_size(T, H)), dev)
-    _run(L.mx_block_norm_grad, dev, stream, ws, dt, rdt, yp, rp, act(w_post, "w_post", (H,)), kind,
+    ws, wp, wn = _scratch(workspace, int(L.mx_block_norm_grad_workspace_size(T, H)), dev, stream)
+    _run(L.mx_block_norm_grad, dev, stream, dt, rdt, yp, rp, act(w_post, "w_post", (H,)), kind,
          act(gate, "gate", gshape), res_scale, act(w_pre, "w_pre", (H,)), eps, T, H, act(d_normed, "d_normed", (T, H)),
          None if d_residual_out is None else _tensor(d_residual_out, "d_residual_out", residual_out.dtype, (T, H), dev),
          dr_p, dy_p, gate_p, wpost_p, wpre_p, wp, wn)
@@ -684,8 +695,8 @@ def lora_add(y, x, a, b, adapter_off, row_token, scale=None, workspace=None, str
     yp, N, ldy = _rows(y, "y", x.dtype, M, dev)
     _need(kx == K, f"x has {kx} columns, a takes {K}")
     L = lib()
-    ws, wp, wn = _scratch(workspace, int(L.mx_lora_add_workspace_size(M, K, R, n)), dev)
-    _run(L.mx_lora_add, dev, stream, ws, dt, xp, ldx, M, K, _tensor(a, "a", x.dtype, (n, R, K), dev),
+    ws, wp, wn = _scratch(workspace, int(L.mx_lora_add_workspace_size(M, K, R, n)), dev, stream)
+    _run(L.mx_lora_add, dev, stream, dt, xp, ldx, M, K, _tensor(a, "a", x.dtype, (n, R, K), dev),
          _tensor(b, "b", x.dtype, (n, N, R), dev),
          None if scale is None else _tensor(scale, "scale", torch.float32, (n,), dev), n, R,
          _tensor(adapter_off, "adapter_off", torch.int32, (n + 1,), dev),

@@ -1,0 +1,222 @@
+"""Calls on a stream that is not the current one: where the memory comes from that a call makes itself.
+
+torch's allocator gives a freed block out again at once on the stream it was made on, although that stream's earlier
+work may still be using it. So what a call on stream s makes (outputs, workspaces) has to be s's memory: a block of the
+current stream's could still be read or written there. On the CPU the binding runs over stand-ins that note which
+stream was current when memory was made; on the GPU calls meet a just-freed block with work pending in it."""
+
+import contextlib
+import ctypes
+import types
+
+import numpy as np
+import pytest
+import torch
+
+BF16, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+DEVICE = torch.device("cuda", 0)
+
+
+class Tensor:
+    """A contiguous device tensor as the binding sees it."""
+    is_cuda, requires_grad, device = True, False, DEVICE
+
+    def __init__(self, shape, dtype=BF16, made_on=None):
+        self.shape, self.dtype, self.made_on = torch.Size(shape), dtype, made_on
+        self.told, self.T = [], self
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        s = [int(np.prod(self.shape[j + 1:], dtype=np.int64)) for j in range(len(self.shape))]
+        return tuple(s) if i is None else s[i]
+
+    def numel(self):
+        return int(np.prod(self.shape, dtype=np.int64))
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def data_ptr(self):
+        return id(self)
+
+    def get_device(self):
+        return self.device.index
+
+    def is_contiguous(self):
+        return True
+
+    def record_stream(self, s):
+        self.told.append(s)
+
+
+class Stream:
+    cuda_stream = 77
+
+    def __init__(self, device=DEVICE):
+        self.device = device
+
+
+CURRENT = Stream()
+
+
+class Torch:
+    """torch, but memory comes from a note of the current stream."""
+    Tensor = Tensor
+
+    def __init__(self):
+        self.now, self.made = CURRENT, []
+        self.cuda = types.SimpleNamespace(stream=self._stream, current_stream=lambda device=None: self.now,
+                                          device=contextlib.nullcontext)
+        self._C = types.SimpleNamespace(_cuda_getDevice=lambda: 0, _cuda_getCurrentRawStream=lambda i: 0)
+
+    def __getattr__(self, name):
+        return getattr(torch, name)
+
+    @contextlib.contextmanager
+    def _stream(self, s):
+        before, self.now = self.now, s or self.now
+        yield
+        self.now = before
+
+    def _make(self, shape, dtype):
+        self.made.append(Tensor((shape,) if isinstance(shape, int) else shape, dtype, self.now))
+        return self.made[-1]
+
+    def empty(self, shape, dtype, device):
+        return self._make(shape, dtype)
+
+    def empty_strided(self, shape, strides, dtype, device):
+        return self._make(shape, dtype)
+
+    def empty_like(self, t):
+        return self._make(t.shape, t.dtype)
+
+    zeros_like = empty_like
+
+    def tensor(self, values, dtype, device):
+        return self._make((len(values),), dtype)
+
+
+class Library:
+    """Every call succeeds and asks for a workspace."""
+
+    def __init__(self):
+        self.streams = []
+
+    def __getattr__(self, name):
+        if name.endswith("_size"):
+            return lambda *a: 512
+
+        def call(*a):
+            self.streams.append(a[-1].value if isinstance(a[-1], ctypes.c_void_p) else a[-1])
+            return 0
+        return call
+
+
+def t(*shape, dtype=BF16):
+    return Tensor(shape, dtype)
+
+
+def around(mx):
+    """name -> a call of each operator around the experts that makes all it can itself."""
+    x, w, ids, gw, off, tok = t(4, 64), t(64), t(4, 2, dtype=I32), t(4, 2, dtype=F32), t(3, dtype=I32), t(4, dtype=I32)
+    ys, a, b = t(8, 64), t(2, 8, 64), t(2, 32, 8)
+    return {
+        "moe_sort": lambda **k: mx.moe_sort(ids, 4, **k),
+        "moe_permute": lambda **k: mx.moe_permute(x, ids, **k),
+        "moe_unpermute": lambda **k: mx.moe_unpermute(ys, ids, gw, **k),
+        "moe_unpermute_grad": lambda **k: mx.moe_unpermute_grad(x, ys, ids, gw, **k),
+        "block_norm": lambda **k: mx.block_norm(x, w, y=x, w_post=w, gate=w, **k),
+        "block_norm, no block": lambda **k: mx.block_norm(x, w, **k),
+        "block_norm_grad": lambda **k: mx.block_norm_grad(x, w, x, d_residual_out=x, y=x, w_post=w, gate=w, **k),
+        "lora_add": lambda **k: mx.lora_add(t(4, 32), x, a, b, off, tok, **k),
+    }
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    from mxfp4_block_scaled_e2m1_amd import binding
+    f = types.SimpleNamespace(torch=Torch(), lib=Library(), binding=binding)
+    monkeypatch.setattr(binding, "torch", f.torch)
+    monkeypatch.setattr(binding, "lib", lambda: f.lib)
+    return f
+
+
+AROUND = sorted(around(None))
+
+
+def _check(f, call, makes=True):
+    s = Stream()
+    out = call(stream=s)
+    assert f.lib.streams == [s.cuda_stream]
+    assert (len(f.torch.made) > 0) == makes
+    assert all(m.made_on is s for m in f.torch.made)
+    # what goes to the caller is known to the stream that the caller is on
+    out = [o for o in (out if isinstance(out, tuple) else (out,)) if isinstance(o, Tensor) and o in f.torch.made]
+    assert all(CURRENT in o.told for o in out)
+    f.torch.made.clear()
+    call()
+    assert all(m.made_on is CURRENT for m in f.torch.made)
+
+
+@pytest.mark.parametrize("name", AROUND)
+def test_memory_of_a_call_is_the_given_streams(fake, name):
+    _check(fake, around(fake.binding)[name])
+
+
+# ------------------------------------------------------------------ on the GPU
+
+def _pending(block):
+    """Work on the current stream that ends by overwriting `block`: some tens of milliseconds of matrix products."""
+    a = torch.ones((4096, 4096), device="cuda")
+    for _ in range(24):
+        a = a @ a * 2.0 ** -12
+    block.fill_(0xFF)
+
+
+@pytest.mark.gpu
+def test_freed_blocks_of_the_current_stream_are_left_alone():
+    """On the current stream a block of every size that the calls ask for is written late and let go of early; the same
+    calls on another stream, with all outputs and workspaces their own, give what they give on an idle device."""
+    import mxfp4_block_scaled_e2m1_amd as mx
+    rng = np.random.default_rng(0)
+    T, H, k, E, R, n = 2048, 1024, 4, 16, 16, 3
+    mk = lambda *s: torch.from_numpy(rng.standard_normal(s)).to(BF16).cuda()
+    x, res, dn, w1, w2, gate = mk(T, H), mk(T, H), mk(T, H), mk(H), mk(H), mk(H)
+    a, b = mk(n, R, H), mk(n, H, R)
+    ids = torch.from_numpy(rng.integers(0, E, size=(T, k)).astype(np.int32)).cuda()
+    aid = torch.from_numpy(rng.integers(0, n, size=(T, 1)).astype(np.int32)).cuda()
+    gw = torch.rand((T, k), device="cuda")
+    off, tok, _ = mx.moe_sort(aid, n)
+    slot_row = mx.moe_sort(ids, E)[2]
+    ys = mk(T * k, H)
+    calls = {
+        "sort": (lambda **s: mx.moe_sort(ids, E, **s), [4 * (E + 1), 4 * T * k, mx.moe_sort_workspace_size(T, k, E)]),
+        "permute": (lambda **s: mx.moe_permute(x, slot_row, **s), [2 * T * k * H]),
+        "unpermute": (lambda **s: mx.moe_unpermute(ys, slot_row, gw, **s), [2 * T * H]),
+        "unpermute_grad": (lambda **s: mx.moe_unpermute_grad(dn, ys, slot_row, gw, **s), [2 * T * k * H, 4 * T * k]),
+        "norm": (lambda **s: mx.block_norm(res, w1, y=x, w_post=w2, gate=gate, **s), [2 * T * H] * 2),
+        "norm_grad": (lambda **s: mx.block_norm_grad(res, w1, dn, d_residual_out=res, y=x, w_post=w2, gate=gate, **s),
+                      [2 * T * H, 2 * T * H, 4 * H, 4 * H, 4 * H, mx.block_norm_grad_workspace_size(T, H)]),
+        "lora": (lambda **s: mx.lora_add(y, x, a, b, off, tok, **s), [mx.lora_add_workspace_size(T, H, R, n)]),
+    }
+    side = torch.cuda.Stream()
+    for name, (call, sizes) in calls.items():
+        print(name, flush=True)
+        y = x.clone()
+        want = call()
+        want = [v.clone() for v in (want if isinstance(want, tuple) else (want,))]
+        y = x.clone()
+        torch.cuda.synchronize()
+        blocks = [torch.empty(s, dtype=U8, device="cuda") for s in sizes]
+        held = {v.data_ptr() for v in blocks}
+        for v in blocks:
+            _pending(v)
+        del blocks, v
+        got = call(stream=side)
+        got = got if isinstance(got, tuple) else (got,)
+        assert not held & {v.data_ptr() for v in got}, name
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), name
