@@ -133,22 +133,40 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _made(stream, make, *args, **kwargs):
+    """make(...): an output that a call on the given `stream` makes itself, from that stream's memory. A block of the
+    current stream's may still be in use there by work that `stream` does not wait for. The current stream is
+    made known to the tensor, since the caller will mostly go on with it there."""
+    with torch.cuda.stream(stream):
+        t = make(*args, **kwargs)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty for an output of a call on `stream` (None: the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _made(stream, torch.empty, shape, dtype=dtype, device=device)
+
+
 def _fmt(f) -> int:
     return MX_FMT[f] if isinstance(f, str) else int(f)
 
 
-def _global(g, device):
+def _global(g, device, stream=None):
     """An NVFP4 global scale as the library takes it: a one-element fp32 device
     tensor (passed through), a Python float (copied into a new device tensor),
     or None. Returns the tensor, which the caller keeps alive until the call
-    that reads it has run (stream order makes a temporary safe)."""
+    that reads it has been made (a temporary is memory of that call's stream)."""
     if g is None:
         return None
     if isinstance(g, torch.Tensor):
         if g.dtype != torch.float32 or g.numel() != 1:
             raise ValueError("a global scale tensor must hold one fp32 value")
         return g
-    return torch.tensor([float(g)], dtype=torch.float32, device=device)
+    with torch.cuda.stream(stream):
+        return torch.tensor([float(g)], dtype=torch.float32, device=device)
 
 
 # ---------------------------------------------------------------------------
@@ -157,8 +175,8 @@ def dequant(fmt, codes, scales, rows: int, cols: int, global_scale=None, out=Non
     """mx_dequant -> bf16 tensor [rows, cols]. global_scale (NVFP4): float or
     one-element fp32 device tensor."""
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=codes.device)
-    g = _global(global_scale, codes.device)
+        out = _empty((rows, cols), torch.bfloat16, codes.device, stream)
+    g = _global(global_scale, codes.device, stream)
     _check(lib().mx_dequant(_fmt(fmt), _ptr(codes), _ptr(scales), _ptr(g), rows, cols,
                             _ptr(out), _stream(stream)))
     return out
@@ -172,10 +190,10 @@ def quantize_act(fmt, x, global_scale=None, codes=None, scales=None, stream=None
     per = 16 if f == MX_FMT["nvfp4"] else 32
     if codes is None:
         width = cols if f == MX_FMT["mxfp8"] else cols // 2
-        codes = torch.empty((rows, width), dtype=torch.uint8, device=x.device)
+        codes = _empty((rows, width), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty((rows, cols // per), dtype=torch.uint8, device=x.device)
-    g = _global(global_scale, x.device)
+        scales = _empty((rows, cols // per), torch.uint8, x.device, stream)
+    g = _global(global_scale, x.device, stream)
     _check(lib().mx_quantize_act(f, _ptr(x), rows, cols, _ptr(g), _ptr(codes), _ptr(scales),
                                  _stream(stream)))
     return codes, scales
@@ -189,10 +207,15 @@ def grouped_expert_mlp_workspace_size(T, hidden, inter, k, E, requant="mxfp4") -
     return int(lib().mx_grouped_expert_mlp_workspace_size(T, hidden, inter, k, E, _fmt(requant)))
 
 
-def _workspace(nbytes, device, workspace):
+def _workspace(nbytes, device, workspace, stream):
+    """`workspace`, or memory of the call's stream: let go of afterwards, it comes back for later work of that
+    stream only."""
     if workspace is not None:
         return workspace
-    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if stream is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
 
 
 def packed_weight_scales_size(hidden, inter, E=1) -> int:
@@ -206,7 +229,7 @@ def pack_weight_scales(w1s, w3s, w2s, out=None, stream=None):
     inter, hidden = w1s.shape[-2], 32 * w1s.shape[-1]
     nbytes = packed_weight_scales_size(hidden, inter, E)
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=w1s.device)
+        out = _empty(nbytes, torch.uint8, w1s.device, stream)
     _check(lib().mx_pack_weight_scales(_ptr(w1s), _ptr(w3s), _ptr(w2s), hidden, inter, E, _ptr(out),
                                        out.numel(), _stream(stream)))
     return out
@@ -223,7 +246,7 @@ def pack_weight_codes(w1, w3, w2, out=None, stream=None):
     inter, hidden = w1.shape[-2], 2 * w1.shape[-1]
     nbytes = packed_weight_codes_size(hidden, inter, E)
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=w1.device)
+        out = _empty(nbytes, torch.uint8, w1.device, stream)
     _check(lib().mx_pack_weight_codes(_ptr(w1), _ptr(w3), _ptr(w2), hidden, inter, E, _ptr(out), out.numel(),
                                       _stream(stream)))
     return out
@@ -236,10 +259,10 @@ def expert_mlp(x, w1, w1s, w3, w3s, w2, w2s, requant="mxfp4", requant_global=Non
     M, hidden = x.shape
     inter = w1.shape[0]
     if out is None:
-        out = torch.empty((M, hidden), dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, hidden), torch.bfloat16, x.device, stream)
     nbytes = expert_mlp_workspace_size(M, hidden, inter, requant)
-    ws = _workspace(nbytes, x.device, workspace)
-    g = _global(requant_global, x.device)
+    ws = _workspace(nbytes, x.device, workspace, stream)
+    g = _global(requant_global, x.device, stream)
     _check(lib().mx_expert_mlp(_ptr(x), M, hidden, inter, _ptr(w1), _ptr(w1s), _ptr(w3), _ptr(w3s),
                                _ptr(w2), _ptr(w2s), _ptr(packed_scales), _ptr(packed_codes), _fmt(requant),
                                _ptr(g), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
@@ -253,8 +276,8 @@ def expert_mlp_noalloc(x, w1, w1s, w3, w3s, w2, w2s, requant="mxfp4", requant_gl
     M, hidden = x.shape
     inter = w1.shape[0]
     if out is None:
-        out = torch.empty((M, hidden), dtype=torch.bfloat16, device=x.device)
-    g = _global(requant_global, x.device)
+        out = _empty((M, hidden), torch.bfloat16, x.device, stream)
+    g = _global(requant_global, x.device, stream)
     _check(lib().mx_expert_mlp_noalloc(_ptr(x), M, hidden, inter, _ptr(w1), _ptr(w1s), _ptr(w3), _ptr(w3s),
                                        _ptr(w2), _ptr(w2s), _ptr(packed_scales), _ptr(packed_codes),
                                        _fmt(requant), _ptr(g), _ptr(out), _stream(stream)))
@@ -270,10 +293,10 @@ def grouped_expert_mlp(x, topk_ids, topk_w, w1, w1s, w3, w3s, w2, w2s, requant="
     k = topk_ids.shape[1]
     E, inter = w1.shape[0], w1.shape[1]
     if out is None:
-        out = torch.empty((T, hidden), dtype=torch.bfloat16, device=x.device)
+        out = _empty((T, hidden), torch.bfloat16, x.device, stream)
     nbytes = grouped_expert_mlp_workspace_size(T, hidden, inter, k, E, requant)
-    ws = _workspace(nbytes, x.device, workspace)
-    g = _global(requant_global, x.device)
+    ws = _workspace(nbytes, x.device, workspace, stream)
+    g = _global(requant_global, x.device, stream)
     _check(lib().mx_grouped_expert_mlp(_ptr(x), T, hidden, inter, _ptr(topk_ids), _ptr(topk_w), k, E,
                                        _ptr(w1), _ptr(w1s), _ptr(w3), _ptr(w3s), _ptr(w2), _ptr(w2s),
                                        _ptr(packed_scales), _ptr(packed_codes), _fmt(requant), _ptr(g),
@@ -292,9 +315,9 @@ def nvfp4_global_warmup(x, w1, w1s, w3, w3s, topk_ids=None, topk_w=None, packed_
     k = topk_ids.shape[1] if routed else 0
     E = w1.shape[0] if routed else 1
     if out is None:
-        out = torch.empty((1,), dtype=torch.float32, device=x.device)
+        out = _empty((1,), torch.float32, x.device, stream)
     nbytes = int(lib().mx_nvfp4_global_warmup_workspace_size(T, hidden, inter, k, E))
-    ws = _workspace(nbytes, x.device, workspace)
+    ws = _workspace(nbytes, x.device, workspace, stream)
     _check(lib().mx_nvfp4_global_warmup(_ptr(x), T, hidden, inter, _ptr(topk_ids), _ptr(topk_w), k, E,
                                         _ptr(w1), _ptr(w1s), _ptr(w3), _ptr(w3s), _ptr(packed_scales), _ptr(out),
                                         _ptr(ws), ws.numel(), _stream(stream)))
@@ -305,7 +328,7 @@ def debug_gemm_f32(a, a_s, b, b_s, out=None, stream=None):
     """mx_debug_gemm_f32: C [M, N] = A . B^T for MXFP4 A [M, K/2] and B [N, K/2]."""
     M, N, K = a.shape[0], b.shape[0], 2 * a.shape[1]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=a.device)
+        out = _empty((M, N), torch.float32, a.device, stream)
     _check(lib().mx_debug_gemm_f32(_ptr(a), _ptr(a_s), _ptr(b), _ptr(b_s), M, N, K, _ptr(out),
                                    _stream(stream)))
     return out
@@ -326,7 +349,7 @@ def profile_stop():
 def probe_mfma_fp4(operands, iters: int, workgroups: int, out=None, stream=None):
     """mx_probe_mfma_fp4: operands uint32 [512, 16] (device); returns float32 [workgroups, 512]."""
     if out is None:
-        out = torch.empty((workgroups, 512), dtype=torch.float32, device=operands.device)
+        out = _empty((workgroups, 512), torch.float32, operands.device, stream)
     _check(lib().mx_probe_mfma_fp4(_ptr(operands), iters, workgroups, _ptr(out), _stream(stream)))
     return out
 
@@ -334,7 +357,7 @@ def probe_mfma_fp4(operands, iters: int, workgroups: int, out=None, stream=None)
 def probe_read(src, mode: int, loads_per_wave: int, workgroups: int, out=None, stream=None):
     """mx_probe_read over all bytes of src; returns the per-wave XOR words (int32 [workgroups * 4])."""
     if out is None:
-        out = torch.empty(workgroups * 4, dtype=torch.int32, device=src.device)
+        out = _empty(workgroups * 4, torch.int32, src.device, stream)
     nbytes = src.numel() * src.element_size()
     _check(lib().mx_probe_read(mode, loads_per_wave, workgroups, _ptr(src), nbytes, _ptr(out), _stream(stream)))
     return out
@@ -358,8 +381,8 @@ def fp8_block_linear(x, w, w_s, out=None, workspace=None, stream=None):
     M, K = x.shape
     N = w.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    ws = _workspace(fp8_block_linear_workspace_size(M, K), x.device, workspace)
+        out = _empty((M, N), torch.bfloat16, x.device, stream)
+    ws = _workspace(fp8_block_linear_workspace_size(M, K), x.device, workspace, stream)
     _check(lib().mx_fp8_block_linear(_ptr(x), M, K, _ptr(w), _ptr(w_s), N, _ptr(out), _ptr(ws), ws.numel(),
                                      _stream(stream)))
     return out
@@ -374,8 +397,8 @@ def nvfp4_linear(x, w, w_s, w_global: float, x_global: float, out=None, workspac
     M, K = x.shape
     N = w.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    ws = _workspace(nvfp4_linear_workspace_size(M, K), x.device, workspace)
+        out = _empty((M, N), torch.bfloat16, x.device, stream)
+    ws = _workspace(nvfp4_linear_workspace_size(M, K), x.device, workspace, stream)
     _check(lib().mx_nvfp4_linear(_ptr(x), M, K, _ptr(w), _ptr(w_s), float(w_global), N, float(x_global), _ptr(out),
                                  _ptr(ws), ws.numel(), _stream(stream)))
     return out
@@ -391,8 +414,8 @@ def nvfp4_expert_mlp(x, w1, w1s, w1g, w3, w3s, w3g, w2, w2s, w2g, x_global, h_gl
     M, hidden = x.shape
     inter = w1.shape[0]
     if out is None:
-        out = torch.empty((M, hidden), dtype=torch.bfloat16, device=x.device)
-    ws = _workspace(nvfp4_expert_mlp_workspace_size(M, hidden, inter), x.device, workspace)
+        out = _empty((M, hidden), torch.bfloat16, x.device, stream)
+    ws = _workspace(nvfp4_expert_mlp_workspace_size(M, hidden, inter), x.device, workspace, stream)
     _check(lib().mx_nvfp4_expert_mlp(_ptr(x), M, hidden, inter, _ptr(w1), _ptr(w1s), float(w1g), _ptr(w3),
                                      _ptr(w3s), float(w3g), _ptr(w2), _ptr(w2s), float(w2g), float(x_global),
                                      float(h_global), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
@@ -410,8 +433,8 @@ def grouped_nvfp4_expert_mlp(x, topk_ids, topk_w, w1, w1s, w1g, w3, w3s, w3g, w2
     k = topk_ids.shape[1]
     E, inter = w1.shape[0], w1.shape[1]
     if out is None:
-        out = torch.empty((T, hidden), dtype=torch.bfloat16, device=x.device)
-    ws = _workspace(grouped_nvfp4_expert_mlp_workspace_size(T, hidden, inter, k, E), x.device, workspace)
+        out = _empty((T, hidden), torch.bfloat16, x.device, stream)
+    ws = _workspace(grouped_nvfp4_expert_mlp_workspace_size(T, hidden, inter, k, E), x.device, workspace, stream)
     _check(lib().mx_grouped_nvfp4_expert_mlp(_ptr(x), T, hidden, inter, _ptr(topk_ids), _ptr(topk_w), k, E,
                                              _ptr(w1), _ptr(w1s), _ptr(w1g), _ptr(w3), _ptr(w3s), _ptr(w3g),
                                              _ptr(w2), _ptr(w2s), _ptr(w2g), float(x_global), float(h_global),
@@ -428,8 +451,8 @@ def fp8_expert_mlp(x, w1, w1s, w3, w3s, w2, w2s, out=None, workspace=None, strea
     M, hidden = x.shape
     inter = w1.shape[0]
     if out is None:
-        out = torch.empty((M, hidden), dtype=torch.bfloat16, device=x.device)
-    ws = _workspace(fp8_expert_mlp_workspace_size(M, hidden, inter), x.device, workspace)
+        out = _empty((M, hidden), torch.bfloat16, x.device, stream)
+    ws = _workspace(fp8_expert_mlp_workspace_size(M, hidden, inter), x.device, workspace, stream)
     _check(lib().mx_fp8_expert_mlp(_ptr(x), M, hidden, inter, _ptr(w1), _ptr(w1s), _ptr(w3), _ptr(w3s), _ptr(w2),
                                    _ptr(w2s), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
     return out
@@ -478,16 +501,6 @@ def _run(fn, device, stream, *args):
             status = fn(*args, s)
     if status != 0:
         _check(status)
-
-
-def _made(stream, make, *args, **kwargs):
-    """make(...): an output that a call on the given `stream` makes itself, from that stream's memory. A block of the
-    current stream's may still be in use there by work that `stream` does not wait for. The current stream is
-    made known to the tensor, since the caller will mostly go on with it there."""
-    with torch.cuda.stream(stream):
-        t = make(*args, **kwargs)
-    t.record_stream(torch.cuda.current_stream(t.device))
-    return t
 
 
 def _out(out, name, like, stream):

@@ -166,6 +166,37 @@ def test_memory_of_a_call_is_the_given_streams(fake, name):
     _check(fake, around(fake.binding)[name])
 
 
+def quantised(mx):
+    """The same of the calls on quantised operands."""
+    x, c, w, ws = t(4, 64), t(4, 32, dtype=U8), t(64, 32, dtype=U8), t(64, 2, dtype=U8)
+    ids, gw, e, es, eg = t(4, 2, dtype=I32), t(4, 2, dtype=F32), t(3, 64, 32, dtype=U8), t(3, 64, 2, dtype=U8), t(3, dtype=F32)
+    one, all_ = (w, ws, w, ws, w, ws), (e, es, e, es, e, es)
+    return {
+        "dequant": lambda **k: mx.dequant("nvfp4", c, ws, 4, 64, 0.5, **k),
+        "quantize_act": lambda **k: mx.quantize_act("nvfp4", x, 0.5, **k),
+        "pack_weight_scales": lambda **k: mx.pack_weight_scales(ws, ws, ws, **k),
+        "pack_weight_codes": lambda **k: mx.pack_weight_codes(w, w, w, **k),
+        "expert_mlp": lambda **k: mx.expert_mlp(x, *one, requant="nvfp4", requant_global=0.5, **k),
+        "expert_mlp_noalloc": lambda **k: mx.expert_mlp_noalloc(x, *one, requant="nvfp4", requant_global=0.5, **k),
+        "grouped_expert_mlp": lambda **k: mx.grouped_expert_mlp(x, ids, gw, *all_, requant="nvfp4", requant_global=0.5, **k),
+        "nvfp4_global_warmup": lambda **k: mx.nvfp4_global_warmup(x, w, ws, w, ws, **k),
+        "debug_gemm_f32": lambda **k: mx.debug_gemm_f32(c, ws, c, ws, **k),
+        "probe_mfma_fp4": lambda **k: mx.probe_mfma_fp4(t(512, 16, dtype=I32), 1, 1, **k),
+        "probe_read": lambda **k: mx.probe_read(x, 0, 8, 1, **k),
+        "fp8_block_linear": lambda **k: mx.fp8_block_linear(x, w, ws, **k),
+        "nvfp4_linear": lambda **k: mx.nvfp4_linear(x, w, ws, 0.5, 0.5, **k),
+        "nvfp4_expert_mlp": lambda **k: mx.nvfp4_expert_mlp(x, w, ws, 0.5, w, ws, 0.5, w, ws, 0.5, 0.5, 0.5, **k),
+        "grouped_nvfp4_expert_mlp": lambda **k: mx.grouped_nvfp4_expert_mlp(x, ids, gw, e, es, eg, e, es, eg, e, es, eg,
+                                                                            0.5, 0.5, **k),
+        "fp8_expert_mlp": lambda **k: mx.fp8_expert_mlp(x, *one, **k),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(quantised(None)))
+def test_memory_of_a_quantised_call_is_the_given_streams(fake, name):
+    _check(fake, quantised(fake.binding)[name])
+
+
 # ------------------------------------------------------------------ on the GPU
 
 def _pending(block):
@@ -209,6 +240,41 @@ def test_freed_blocks_of_the_current_stream_are_left_alone():
         want = call()
         want = [v.clone() for v in (want if isinstance(want, tuple) else (want,))]
         y = x.clone()
+        torch.cuda.synchronize()
+        blocks = [torch.empty(s, dtype=U8, device="cuda") for s in sizes]
+        held = {v.data_ptr() for v in blocks}
+        for v in blocks:
+            _pending(v)
+        del blocks, v
+        got = call(stream=side)
+        got = got if isinstance(got, tuple) else (got,)
+        assert not held & {v.data_ptr() for v in got}, name
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), name
+
+
+@pytest.mark.gpu
+def test_freed_blocks_are_left_alone_by_quantised_calls():
+    """The same of quantisation, one expert and routed experts."""
+    import mxfp4_block_scaled_e2m1_amd as mx
+    import workloads as W
+    T, H, I, E, k = 512, 512, 256, 4, 2
+    d = W.grouped(tokens=T, n_experts=E, k=k, seed=1, hidden=H, inter=I)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    w = [dev(d[n]) for n in ("w1", "w1s", "w3", "w3s", "w2", "w2s")]
+    x = dev(d["x"].view(np.int16)).view(BF16)
+    ids, gw = dev(d["ids"]), dev(d["w"])
+    calls = {
+        "quantize": (lambda **s: mx.quantize_act("mxfp4", x, **s), [T * H // 2, T * H // 32]),
+        "expert": (lambda **s: mx.expert_mlp(x, *(v[0] for v in w), **s), [2 * T * H, mx.expert_mlp_workspace_size(T, H, I)]),
+        "routed": (lambda **s: mx.grouped_expert_mlp(x, ids, gw, *w, **s),
+                   [2 * T * H, mx.grouped_expert_mlp_workspace_size(T, H, I, k, E)]),
+    }
+    side = torch.cuda.Stream()
+    for name, (call, sizes) in calls.items():
+        print(name, flush=True)
+        want = call()
+        want = [v.clone() for v in (want if isinstance(want, tuple) else (want,))]
         torch.cuda.synchronize()
         blocks = [torch.empty(s, dtype=U8, device="cuda") for s in sizes]
         held = {v.data_ptr() for v in blocks}
