@@ -493,6 +493,7 @@ def _run(fn, device, stream, *args):
         # build and check on the way, which costs as much as the library call
         s = torch._C._cuda_getCurrentRawStream(device.index)
     else:
+        _need(stream.device == device, f"stream is on {stream.device}, the tensors on {device}")
         s = stream.cuda_stream
     if torch._C._cuda_getDevice() == device.index:
         status = fn(*args, s)

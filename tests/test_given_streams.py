@@ -166,6 +166,13 @@ def test_memory_of_a_call_is_the_given_streams(fake, name):
     _check(fake, around(fake.binding)[name])
 
 
+@pytest.mark.parametrize("name", AROUND)
+def test_a_stream_of_another_device_is_refused(fake, name):
+    with pytest.raises(ValueError, match="stream is on cuda:1, the tensors on cuda:0"):
+        around(fake.binding)[name](stream=Stream(torch.device("cuda", 1)))
+    assert not fake.lib.streams
+
+
 def quantised(mx):
     """The same of the calls on quantised operands."""
     x, c, w, ws = t(4, 64), t(4, 32, dtype=U8), t(64, 32, dtype=U8), t(64, 2, dtype=U8)
