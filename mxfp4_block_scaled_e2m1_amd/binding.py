@@ -461,15 +461,35 @@ def fp8_expert_mlp(x, w1, w1s, w3, w3s, w2, w2s, out=None, workspace=None, strea
 # ---------------------------------------------------------------------------
 # The operators around the experts. Their tensors are checked here against each
 # other (type, shape, device), since the library sees pointers only; a call runs
-# on the tensors' device, on its current stream unless one is given.
+# on the tensors' device, on its current stream unless one is given. Autograd
+# records none of them: the gradients are calls of their own (for a
+# torch.autograd.Function, whose passes run without recording), and a call that
+# autograd would have to record raises.
 
 def _need(cond, what):
     if not cond:
         raise ValueError(what)
 
 
+def _unrecorded(name):
+    """Where autograd records: a result would silently miss the gradient of `name`, or `name`, if written, its history."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, and autograd does not record this call: call it under "
+                         "torch.no_grad() or in a torch.autograd.Function")
+
+
+def _wrote(given):
+    """Tells autograd that the caller's tensors among these were written, as an operation of torch's in place does: an
+    operation that has saved one for its backward pass then raises there instead of reading the new values."""
+    given = [t for t in given if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def _tensor(t, name, dtype, shape, device):
     """t as a device pointer, once its type, shape, device and layout are as said."""
+    if t.requires_grad:
+        _unrecorded(name)
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device.index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}: got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}"
@@ -547,6 +567,7 @@ def moe_sort_workspace_size(T, k, E) -> int:
 
 def moe_sort(topk_ids, E: int, expert_off=None, row_slot=None, slot_row=None, workspace=None, stream=None):
     """mx_moe_sort: int32 topk_ids [T, k] -> (expert_off [E+1], row_slot [T*k], slot_row [T, k]), all int32."""
+    given = (expert_off, row_slot, slot_row)
     T, k = topk_ids.shape
     dev, i32 = topk_ids.device, torch.int32
     _need(topk_ids.is_cuda, "libmxfp4 takes device tensors")
@@ -558,12 +579,14 @@ def moe_sort(topk_ids, E: int, expert_off=None, row_slot=None, slot_row=None, wo
     L = lib()
     ws, wp, wn = _scratch(workspace, int(L.mx_moe_sort_workspace_size(T, k, E)), dev, stream)
     _run(L.mx_moe_sort, dev, stream, ids, T, k, E, op, rp, sp, wp, wn)
+    _wrote(given)
     return expert_off, row_slot, slot_row
 
 
 def moe_permute(x, slot_row, out=None, stream=None):
     """mx_moe_permute: x [T, H] to its rows of out [rows, H] (default: a new [T*k, H], whose other rows are
     whatever they are)."""
+    given = (out,)
     T, H = x.shape
     k = slot_row.shape[1]
     dev = x.device
@@ -571,11 +594,13 @@ def moe_permute(x, slot_row, out=None, stream=None):
     out, op = _new(out, "out", (T * k if out is None else out.shape[0], H), x.dtype, dev, stream)
     _run(lib().mx_moe_permute, dev, stream, dt, _tensor(x, "x", x.dtype, (T, H), dev), T, H,
          _tensor(slot_row, "slot_row", torch.int32, (T, k), dev), k, out.shape[0], op)
+    _wrote(given)
     return out
 
 
 def moe_unpermute(ys, slot_row, topk_w=None, out=None, stream=None):
     """mx_moe_unpermute: ys [rows, H] -> y [T, H], weighted by fp32 topk_w [T, k] (None: 1)."""
+    given = (out,)
     rows, H = ys.shape
     T, k = slot_row.shape
     dev = ys.device
@@ -584,12 +609,14 @@ def moe_unpermute(ys, slot_row, topk_w=None, out=None, stream=None):
     _run(lib().mx_moe_unpermute, dev, stream, dt, _tensor(ys, "ys", ys.dtype, (rows, H), dev), rows, H,
          _tensor(slot_row, "slot_row", torch.int32, (T, k), dev),
          None if topk_w is None else _tensor(topk_w, "topk_w", torch.float32, (T, k), dev), T, k, op)
+    _wrote(given)
     return out
 
 
 def moe_unpermute_grad(d_y, ys, slot_row, topk_w, d_ys=None, d_w=None, stream=None):
     """mx_moe_unpermute_grad -> (d_ys [rows, H], d_w [T, k] fp32). Without d_ys, rows that no slot names come
     back as zeros; a given d_ys keeps them."""
+    given = (d_ys, d_w)
     rows, H = ys.shape
     T, k = slot_row.shape
     dev = ys.device
@@ -602,6 +629,7 @@ def moe_unpermute_grad(d_y, ys, slot_row, topk_w, d_ys=None, d_w=None, stream=No
     _run(lib().mx_moe_unpermute_grad, dev, stream, dt, _tensor(d_y, "d_y", ys.dtype, (T, H), dev), yp, rows, H,
          _tensor(slot_row, "slot_row", torch.int32, (T, k), dev), wp, T, k,
          _tensor(d_ys, "d_ys", ys.dtype, (rows, H), dev), dwp)
+    _wrote(given)
     return d_ys, d_w
 
 
@@ -622,6 +650,7 @@ def block_norm(residual, w_pre=None, y=None, w_post=None, gate=None, res_scale: 
                residual_out=None, normed=None, stream=None):
     """mx_block_norm -> (normed [T, H] or None without w_pre, residual_out [T, H] or, without y, the residual).
     gate: None, [H] (per channel), [T, 1] (per token) or [T, H]."""
+    given = (residual_out, normed)
     T, H = residual.shape
     dev = residual.device
     rdt = _dtype(residual, "residual")
@@ -645,6 +674,7 @@ def block_norm(residual, w_pre=None, y=None, w_post=None, gate=None, res_scale: 
          None if w_post is None else _tensor(w_post, "w_post", adt, (H,), dev), kind,
          None if gate is None else _tensor(gate, "gate", adt, gshape, dev), res_scale,
          None if w_pre is None else _tensor(w_pre, "w_pre", adt, (H,), dev), eps, T, H, ro, no)
+    _wrote(given)
     return normed, (residual if y is None else residual_out)
 
 
@@ -656,6 +686,7 @@ def block_norm_grad(residual_out, w_pre=None, d_normed=None, d_residual_out=None
                     res_scale: float = 1.0, eps: float = 1e-6, d_residual=None, d_y=None, workspace=None, stream=None):
     """mx_block_norm_grad at the stored residual_out (without y: the residual) -> (d_residual, dw_pre, d_y, dw_post,
     d_gate); None for what there is none of. dw_pre, dw_post and the d_gate of a [H] or [T, 1] gate are fp32."""
+    given = (d_residual, d_y)
     T, H = residual_out.shape
     dev, f32 = residual_out.device, torch.float32
     rdt = _dtype(residual_out, "residual_out")
@@ -682,6 +713,7 @@ def block_norm_grad(residual_out, w_pre=None, d_normed=None, d_residual_out=None
          act(gate, "gate", gshape), res_scale, act(w_pre, "w_pre", (H,)), eps, T, H, act(d_normed, "d_normed", (T, H)),
          None if d_residual_out is None else _tensor(d_residual_out, "d_residual_out", residual_out.dtype, (T, H), dev),
          dr_p, dy_p, gate_p, wpost_p, wpre_p, wp, wn)
+    _wrote(given)
     return d_residual, dw_pre, d_y, dw_post, d_gate
 
 
@@ -691,6 +723,8 @@ def lora_add_workspace_size(M, K, R, n) -> int:
 
 def _rows(t, name, dtype, rows, device):
     """(pointer, width, row stride) of a matrix whose rows are contiguous."""
+    if t.requires_grad:
+        _unrecorded(name)
     if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.device != device or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a {dtype} matrix of {rows} rows with contiguous columns on {device}: got "
                          f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
@@ -715,6 +749,7 @@ def lora_add(y, x, a, b, adapter_off, row_token, scale=None, workspace=None, str
          None if scale is None else _tensor(scale, "scale", torch.float32, (n,), dev), n, R,
          _tensor(adapter_off, "adapter_off", torch.int32, (n + 1,), dev),
          _tensor(row_token, "row_token", torch.int32, (M,), dev), yp, ldy, N, wp, wn)
+    _wrote((y,))
     return y
 
 
