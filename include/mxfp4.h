@@ -638,9 +638,9 @@ MX_API size_t mx_block_norm_grad_workspace_size(int64_t T, int64_t H);
  *   adapter_off [n+1], row_token [M]: expert_off and row_slot of mx_moe_sort over
  *     the tokens' adapter ids (k = 1, E = n), made once and used for every
  *     projection of a step; tokens with an id outside [0, n) keep their y.
- * x . A^T is formed in fp32 and enters the second product as two 16-bit halves,
- * within 2^-17 of each value (fp16: 2^-21, or 2^-23 of the token's largest); the
- * sum is fp32 and y is rounded once.
+ * x . A^T is formed in fp32 and enters the second product whole (fp16: what is
+ * below 2^-38 of the token's largest value is cut off); the sum is fp32 and y is
+ * rounded once.
  * R a multiple of 8 up to 128 (adapters of smaller rank are padded with zero
  * rows of A and zero columns of B), K and N multiples of 8 up to 2^20,
  * M <= 2^24, M * K <= 2^38, 1 <= n <= 512, ldx >= K and ldy >= N multiples of 8.

@@ -10,11 +10,14 @@
 // moving x, y and the adapters in use, so both are bound by memory: by HBM for
 // prompts, by latency for a few tokens.
 //
-// v is formed in fp32. For the matrix unit each value is split into two 16-bit
-// halves, hi + lo, in fp16 after a power-of-two scaling of the token's row (it could
-// overflow otherwise): within 2^-17 of the value in bf16, 2^-21 in fp16. One bf16
-// would be off by up to 2^-9 of every product; the second matrix product costs no
-// memory traffic. y is rounded once.
+// v is formed in fp32. For the matrix unit each value is cut into three 16-bit
+// pieces that add up to it: in bf16 exactly (8 bits each), in fp16, after a
+// power-of-two scaling of the token's row, exactly down to 2^-15 of the row's
+// largest value and to within 2^-38 of that one below. So the second product is off
+// by fp32's own rounding only, also where it cancels y. (Two pieces, 16 bits of v in
+// bf16, left 2^-17 of each product; the third costs matrix and LDS cycles but no memory
+// traffic: 7168 + 7168 columns, 4096 tokens, rank 64 40.6 -> 42.1 us, 8192 tokens, rank
+// 128 92.4 -> 98.5.) y is rounded once.
 #include <algorithm>
 #include <type_traits>
 
@@ -38,6 +41,30 @@ __device__ __forceinline__ f32x4 mma(u32v4 a, u32v4 b, f32x4 c) {
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                   0);
+}
+
+// Three pieces of each of u0, u1, packed in pairs: piece[0] + piece[1] + piece[2] = u, each cut off towards
+// zero, so that the next takes what is left exactly. An inf or NaN travels in the first alone (a NaN that
+// arithmetic gave has its highest mantissa bit set, which the first piece keeps).
+template <int DT>
+__device__ __forceinline__ void cut3(float u0, float u1, uint32_t (&piece)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    float h0, h1;
+    if constexpr (DT == DT_BF16) {
+      const uint32_t w0 = __float_as_uint(u0), w1 = __float_as_uint(u1);
+      piece[i] = __builtin_amdgcn_perm(w1, w0, 0x07060302u);   // the upper halves
+      h0 = __uint_as_float(w0 & 0xFFFF0000u);
+      h1 = __uint_as_float(w1 & 0xFFFF0000u);
+    } else {
+      piece[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(u0, u1));
+      h0 = lo_f32<DT>(piece[i]);
+      h1 = hi_f32<DT>(piece[i]);
+    }
+    const bool f0 = i > 0 || fabsf(u0) < INFINITY, f1 = i > 0 || fabsf(u1) < INFINITY;
+    u0 = f0 ? u0 - h0 : 0.0f;
+    u1 = f1 ? u1 - h1 : 0.0f;
+  }
 }
 
 // A tile is up to TM sorted rows of one adapter, adapters in order. How many there
@@ -289,9 +316,11 @@ template <int DT, int MT, int RP>
 __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, int run, int runs) {
   constexpr int TM = 16 * MT, VP = RP + 8;                   // pitch of v in 16-bit elements
   constexpr int RH = RP < 64 ? RP : 64, HALVES = RP / RH;    // ranks at a time
-  constexpr int BP = RH * 2 + 16, CP = 64 * 4 + 16;          // pitches in bytes: of B, of the products
+  // and in the area: of large tiles of many ranks half of them, which leaves LDS for two workgroups
+  constexpr int SH = MT > 1 && RP > 64 ? 32 : RH;
+  constexpr int BP = SH * 2 + 16, CP = 64 * 4 + 16;          // pitches in bytes: of B, of the products
   constexpr int AREA = 64 * BP > 16 * CP ? 64 * BP : 16 * CP;
-  __shared__ __attribute__((aligned(16))) uint16_t vh[TM * VP], vl[TM * VP];
+  __shared__ __attribute__((aligned(16))) uint16_t vp[3][TM * VP];   // v's pieces
   __shared__ __attribute__((aligned(16))) uint8_t lds[EXPAND_WAVES * AREA];
   __shared__ float fac[TM];                                  // scale * 2^e
   const int groups = (p.N + 63) / 64;                        // of 64 columns
@@ -319,7 +348,7 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
     const int flat = i * 64 + lane;
     const int row = RP == 32 ? flat / per_row : flat >> 3, piece = RP == 32 ? flat - row * per_row : flat & 7;
     bsrc[i] = RP == 32 ? flat * 8 : row * p.R;
-    bput[i] = row * BP + piece * 16;
+    bput[i] = row * BP + piece % (SH / 8) * 16;
   }
   const uint16_t* bm = (const uint16_t*)p.b + (int64_t)tile.adapter * p.N * p.R;
   u32v4 bv[BI];
@@ -373,28 +402,22 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
     const f32x4 v = vs[i];
     float down = 1.0f, up = 1.0f;
     if constexpr (DT == DT_F16) {
-      // 2^-e with 2^e the exponent of the row's largest value, where that is an
-      // ordinary number; bf16 has fp32's range and needs none
+      // 2^(14 - e) with 2^e the exponent of the row's largest value, so that the pieces
+      // use what fp16 has on both sides; bf16 has fp32's range and needs none
       float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
       for (int d = PER / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
-      const uint32_t ex = __float_as_uint(amax) >> 23;
-      if (ex >= 2 && ex <= 252) {
-        down = __uint_as_float((254u - ex) << 23);
-        up = __uint_as_float(ex << 23);
+      const uint32_t ex = max(__float_as_uint(amax) >> 23, 15u);      // 2^126 at most
+      if (ex < 255) {
+        down = __uint_as_float((268u - ex) << 23);
+        up = __uint_as_float((ex - 14u) << 23);
       }
     }
-    uint32_t h[2], l[2];
+    uint32_t c0[3], c1[3];
+    cut3<DT>(v[0] * down, v[1] * down, c0);
+    cut3<DT>(v[2] * down, v[3] * down, c1);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float u0 = v[2 * i] * down, u1 = v[2 * i + 1] * down;
-      h[i] = pack2<DT>(u0, u1);
-      const float h0 = lo_f32<DT>(h[i]), h1 = hi_f32<DT>(h[i]);
-      // an inf or NaN travels in hi alone
-      l[i] = pack2<DT>(fabsf(h0) < INFINITY ? u0 - h0 : 0.0f, fabsf(h1) < INFINITY ? u1 - h1 : 0.0f);
-    }
-    *(u32v2*)(vh + row * VP + r) = u32v2{h[0], h[1]};
-    *(u32v2*)(vl + row * VP + r) = u32v2{l[0], l[1]};
+    for (int j = 0; j < 3; ++j) *(u32v2*)(vp[j] + row * VP + r) = u32v2{c0[j], c1[j]};
     if (r == 0) fac[row] = scale * up;
   }
   // y pieces: token 8 i + lane / 8 of the tile, columns 8 (lane % 8) of the group;
@@ -420,31 +443,39 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
       for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
-      wave_sync();
 #pragma unroll
-      for (int i = 0; i < BI; ++i)
-        if (RP != 32 || i < per_row) *(u32v4*)(area + bput[i]) = bv[i];
-      wave_sync();
-      // the next piece, or at the end this one again: no condition on the loads
-      if (h + 1 < HALVES) fetch(g, h + 1);
-      else fetch(min(g + EXPAND_WAVES, groups - 1), 0);
+      for (int part = 0; part < RH; part += SH) {
+        wave_sync();
+        if (SH == RH || (lane & 7) / (SH / 8) == part / SH) {
 #pragma unroll
-      for (int k = 0; k < RH; k += 32) {
-        const int r0 = h * RH + k + q * 8;
-        u32v4 bf[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          bf[j] = *(const u32v4*)(area + (16 * j + c) * BP + k * 2 + q * 16);
-          if (r0 >= p.R) bf[j] = u32v4{0, 0, 0, 0};          // past the rank: whatever LDS held
+          for (int i = 0; i < BI; ++i)
+            if (RP != 32 || i < per_row) *(u32v4*)(area + bput[i]) = bv[i];
+        }
+        wave_sync();
+        // the next piece, or at the end this one again: no condition on the loads
+        if (part + SH == RH) {
+          if (h + 1 < HALVES) fetch(g, h + 1);
+          else fetch(min(g + EXPAND_WAVES, groups - 1), 0);
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int w = (m * 16 + c) * VP + r0;
-          const u32v4 hi = *(const u32v4*)(vh + w), lo = *(const u32v4*)(vl + w);
+        for (int k = 0; k < SH; k += 32) {
+          if (h * RH + part + k >= p.R) break;               // nothing but padding
+          const int r0 = h * RH + part + k + q * 8;
+          u32v4 bf[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            acc[m][j] = mma<DT>(bf[j], lo, acc[m][j]);
-            acc[m][j] = mma<DT>(bf[j], hi, acc[m][j]);
+            bf[j] = *(const u32v4*)(area + (16 * j + c) * BP + k * 2 + q * 16);
+            if (r0 >= p.R) bf[j] = u32v4{0, 0, 0, 0};        // past the rank: whatever LDS held
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const int w = (m * 16 + c) * VP + r0;
+#pragma unroll
+            for (int i = 2; i >= 0; --i) {                   // the small pieces first
+              const u32v4 v = *(const u32v4*)(vp[i] + w);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[m][j] = mma<DT>(bf[j], v, acc[m][j]);
+            }
           }
         }
       }
@@ -526,7 +557,8 @@ hipError_t launch_expand(const LoraArgs& p, int mt, hipStream_t s) {
   }
   const unsigned grid = (unsigned)(tiles * all_runs);
   auto go = [&](auto d, auto m, auto r) {
-    k_lora_expand<decltype(d)::value, decltype(m)::value, decltype(r)::value><<<grid, 64 * EXPAND_WAVES, 0, s>>>(p, run, all_runs);
+    k_lora_expand<decltype(d)::value, decltype(m)::value, decltype(r)::value>
+        <<<grid, 64 * EXPAND_WAVES, 0, s>>>(p, run, all_runs);
   };
   auto by_r = [&](auto d, auto m) {
     if (p.R <= 32) go(d, m, std::integral_constant<int, 32>());

@@ -211,3 +211,64 @@ def test_prompts_with_adapters_of_few_of_the_tokens(mx, busy):
                                        (1500, 64, 5000, 8, 90)])
 def test_more_tiles_than_one_round_of_workgroups(mx, M, K, N, R, n):
     test_whole_numbers_come_out_exactly(mx, M, K, N, R, n, "bf16")
+
+
+@pytest.mark.parametrize("M,N,R,n", [(1, 72, 8, 1), (40, 136, 24, 3), (70, 264, 128, 2), (150, 64, 56, 1),
+                                     (2100, 8000, 24, 3), (2050, 8200, 64, 2), (2200, 7800, 128, 2)])
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+def test_where_the_adapter_cancels_the_projection(mx, M, N, R, n, name):
+    """The inner product's low bits count: each column takes one rank, y holds that product rounded to its type
+    with the other sign, and what is left is exact. v is a whole number of up to 22 bits times 2^-s, s up to 14 from
+    rank to rank, so that fp16's pieces reach its smallest subnormals (2^22 2^-s next to 1)."""
+    K = 8
+    rng = np.random.default_rng(M + R)
+    xv = np.zeros((M, K))
+    for i, size in enumerate((1.0, 2.0 ** 7, 2.0 ** 15)):
+        xv[:, i] = size * rng.choice([-1, 1], size=M)
+    step = 2.0 ** -rng.integers(0, 15, size=(n, R, 1))
+    x, x64 = pair(xv, name)
+    a, a64 = pair(rng.integers(-127, 128, size=(n, R, K)) * step, name)
+    bv = np.zeros((n, N, R))
+    bv[:, np.arange(N), np.arange(N) % R] = rng.choice([-1, 1], size=(n, N))
+    b, b64 = pair(bv, name)
+    adapter = rng.integers(0, n, size=M)
+    scale, s64 = pair(np.full(n, 2.0 ** -8), "fp32")
+    delta = np.zeros((M, N))
+    for i in range(n):
+        t = adapter == i
+        delta[t] = 2.0 ** -8 * ((x64[t] @ a64[i].T) @ b64[i].T)          # exact in 64 bits
+    y, y64 = pair(-delta, name)
+    mx.lora_add(y, x, a, b, *_plan(mx, adapter, n), scale=scale)
+    left = torch.from_numpy(y64 + delta)
+    assert (left != 0).any()
+    assert torch.equal(y.cpu(), left.to(y.dtype))
+
+
+@pytest.mark.parametrize("M,N,R,n", [(1, 72, 8, 1), (40, 136, 24, 3), (70, 264, 128, 2), (150, 64, 56, 1),
+                                     (2100, 8000, 24, 3), (2050, 8200, 64, 2), (2200, 7800, 128, 2)])
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+def test_where_two_ranks_cancel(mx, M, N, R, n, name):
+    """Each column takes the difference of two ranks' v, whole numbers of up to 22 bits times 2^-s that differ in the
+    last 8 only: the difference fits either type and comes out exactly."""
+    K = 8
+    rng = np.random.default_rng(M + R + 1)
+    xv = np.zeros((M, K))
+    for i, size in enumerate((1.0, 2.0 ** 7, 2.0 ** 15)):
+        xv[:, i] = size * rng.choice([-1, 1], size=M)
+    av = rng.integers(-127, 128, size=(n, R, K)).astype(np.float64)
+    av[:, 1::2, 1:] = av[:, 0::2, 1:]
+    av *= np.repeat(2.0 ** -rng.integers(0, 15, size=(n, R // 2, 1)), 2, axis=1)
+    x, x64 = pair(xv, name)
+    a, a64 = pair(av, name)
+    bv = np.zeros((n, N, R))
+    at = 2 * (np.arange(N) % (R // 2))
+    bv[:, np.arange(N), at], bv[:, np.arange(N), at + 1] = 1, -1
+    b, b64 = pair(bv, name)
+    adapter = rng.integers(0, n, size=M)
+    y, y64 = pair(np.zeros((M, N)), name)
+    for i in range(n):
+        t = adapter == i
+        y64[t] = (x64[t] @ a64[i].T) @ b64[i].T                           # exact in 64 bits
+    mx.lora_add(y, x, a, b, *_plan(mx, adapter, n))
+    assert (y64 != 0).any()
+    assert np.array_equal(f64(y), y64)
