@@ -67,6 +67,17 @@ __device__ __forceinline__ void cut3(float u0, float u1, uint32_t (&piece)[3]) {
   }
 }
 
+// acc + 0 * (two elements): NaN if one is infinite or NaN.
+template <int DT>
+__device__ __forceinline__ float dot0(uint32_t w, float acc) {
+  if constexpr (DT == DT_BF16) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, 0u), acc, false);
+  } else {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), __builtin_bit_cast(f16x2, 0u), acc, false);
+  }
+}
+
 // A tile is up to TM sorted rows of one adapter, adapters in order. How many there
 // are, and where each lies, is only known on the device: every wave looks at
 // the adapters' offsets itself, 64 at a time.
@@ -431,6 +442,34 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
   }
   uint8_t* area = lds + wave * AREA;
   __syncthreads();
+  // An infinite B: its products with a value's pieces (zeros, mostly) do not add up to the
+  // one with the value, and NaN comes out. Those sums once more, by the formula. (Looking
+  // for them takes 0.3 us of 42 at 4096 tokens of 7168 + 7168 columns, rank 64.)
+  auto by_formula = [&](f32x4 (&acc)[MT][4], int n0) {
+    const uint16_t* br = bm + (int64_t)min(n0 + lane, p.N - 1) * p.R;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      wave_sync();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *(f32x4*)(area + c * CP + (16 * j + 4 * q) * 4) = acc[m][j];
+      wave_sync();
+#pragma unroll 1
+      for (int row = 0; row < 16; ++row) {
+        float* out = (float*)(area + row * CP) + lane;
+        if (*out == *out) continue;
+        const uint16_t* vr = &vp[0][(16 * m + row) * VP];
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int k = 0; k < p.R && sum == sum; ++k)
+          sum = fmaf(lo_f32<DT>(vr[k]) + (lo_f32<DT>(vr[TM * VP + k]) + lo_f32<DT>(vr[2 * TM * VP + k])),
+                     lo_f32<DT>(br[k]), sum);
+        *out = sum;
+      }
+      wave_sync();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[m][j] = *(const f32x4*)(area + c * CP + (16 * j + 4 * q) * 4);
+    }
+  };
   for (int g = g0 + wave; g < g1; g += EXPAND_WAVES) {
     const int n0 = g * 64, n = min(n0 + lcol, p.N - 8);     // N % 8 == 0
     Raw<DT, 8> y[2 * MT];
@@ -441,6 +480,7 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float odd = 0.0f;                // large tiles: NaN from the first infinite (or NaN) B on
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
 #pragma unroll
@@ -466,6 +506,8 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
           for (int j = 0; j < 4; ++j) {
             bf[j] = *(const u32v4*)(area + (16 * j + c) * BP + k * 2 + q * 16);
             if (r0 >= p.R) bf[j] = u32v4{0, 0, 0, 0};        // past the rank: whatever LDS held
+#pragma unroll
+            for (int i = 0; i < (MT > 1 ? 4 : 0); ++i) odd = dot0<DT>(bf[j][i], odd);
           }
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
@@ -480,6 +522,14 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
         }
       }
     }
+    // whether to look for such sums: of a large tile by its operands, of a small one by its fewer sums
+    bool look = odd != odd;
+    if constexpr (MT == 1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        look |= __builtin_isunordered(acc[0][j][0], acc[0][j][1]) || __builtin_isunordered(acc[0][j][2], acc[0][j][3]);
+    }
+    if (__ballot(look)) by_formula(acc, n0);
     // product j: columns 16 j + 4 q .. + 3 of token c
 #pragma unroll
     for (int m = 0; m < MT; ++m) {

@@ -272,3 +272,42 @@ def test_where_two_ranks_cancel(mx, M, N, R, n, name):
     mx.lora_add(y, x, a, b, *_plan(mx, adapter, n))
     assert (y64 != 0).any()
     assert np.array_equal(f64(y), y64)
+
+
+@pytest.mark.parametrize("M,N,R", [(1, 72, 8), (40, 136, 24), (70, 264, 56), (90, 80, 72), (2100, 7992, 16),
+                                   (2050, 8200, 64), (2200, 7800, 128)])
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+@pytest.mark.parametrize("where", ["A", "B"])
+def test_infinite_weights(mx, M, N, R, name, where):
+    """Infinities and NaN in A or in B, next to v of one and of more pieces, zeros and large values: +-inf and NaN where
+    the formula has them, the rest the exact sum rounded once."""
+    K, n = 64, 3
+    rng = np.random.default_rng(R)
+    xv = rng.integers(-2, 3, size=(M, K)).astype(np.float64)
+    xv[::3] *= 2.0 ** rng.integers(-6, 7, size=K)           # v of many bits
+    xv[1::5] = 0.0                                          # v = 0: 0 * inf is NaN
+    xv[:, 7], xv[:, 8] = 1.0, 2.0 ** 6
+    av, bv = rng.integers(-1, 2, size=(n, R, K)).astype(np.float64), rng.integers(-1, 2, size=(n, N, R)) * 0.25
+    av[:, :, 7] = 0.0
+    if where == "A":
+        # an adapter with an infinite and a large v, of which the columns take some, and one with v that is NaN
+        av[1, 2, 7], av[1, 3, 7] = -np.inf, 2.0 ** (15 if name == "fp16" else 100)
+        av[1, 3, 8], av[2, 4, 9] = av[1, 3, 7], np.nan
+    else:
+        bv[1, 3, 5], bv[1, 11, 0], bv[1, 11, 1], bv[1, 20, 2] = np.inf, -np.inf, np.inf, np.nan
+        bv[1, N - 1], bv[1, N - 2, R - 1] = np.inf, -np.inf
+    x = pair(xv, name)[0]
+    a = pair(av, name)[0]
+    b = pair(bv, name)[0]
+    y = pair(rng.integers(-4, 5, size=(M, N)), name)[0]
+    adapter = (np.arange(M) // 2 + 1) % n
+    ref, xd, ad, bd = y.double(), x.double(), a.double(), b.double()      # product by product: 0 * inf is NaN
+    for i in range(n):
+        t = torch.from_numpy(np.nonzero(adapter == i)[0]).cuda()
+        v = sum(xd[t, k, None] * ad[i, :, k] for k in range(K))
+        ref[t] += sum(v[:, r, None] * bd[i, :, r] for r in range(R))
+    ref = ref.to(y.dtype)
+    mx.lora_add(y, x, a, b, *_plan(mx, adapter, n))
+    assert torch.isinf(ref).any() and torch.isnan(ref).any()
+    assert torch.equal(y.isnan(), ref.isnan())
+    assert torch.equal(y[~ref.isnan()], ref[~ref.isnan()])
