@@ -200,3 +200,19 @@ def test_more_than_2_to_the_31_elements(mx):
     assert torch.equal(dys[rows - 1], x[0]) and torch.equal(dys[1], x[1])
     ref = (f64(x) ** 2).sum(1, keepdims=True).repeat(2, 1)
     within(dw, ref, depth(H) * U * ref)
+
+
+@pytest.mark.parametrize("P,k,E", [(512 * 1024 - 1, 1, 200), (512 * 1024, 4, 512), (512 * 1024 + 1, 1, 1),
+                                   (513 * 1024, 8, 200), (600 * 1024 + 300, 1, 512), (1 << 20, 8, 48)])
+def test_sort_past_the_chunks_that_scan_themselves(mx, P, k, E):
+    """Up to 512 chunks every scatter workgroup sums the histograms itself, beyond a kernel of its own does: both sides
+    of the border, the last chunk whole and not, ids outside the experts on both sides."""
+    assert P % k == 0
+    rng = np.random.default_rng(P + E)
+    _check_sort(mx, rng.integers(-E // 4 - 1, E + E // 4 + 2, size=(P // k, k)).astype(np.int32), E)
+
+
+@pytest.mark.parametrize("P", [512 * 1024, 512 * 1024 + 1024])
+def test_sort_of_many_slots_on_one_expert_or_none(mx, P):
+    for fill in (-1, 6, 7):
+        _check_sort(mx, np.full((P, 1), fill, np.int32), 7)
