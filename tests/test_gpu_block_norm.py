@@ -310,3 +310,40 @@ def test_more_than_2_to_the_31_elements(mx):
     du = np.abs(f64(t["gate"]) * f64(r[0]))
     for i, mass in ((1, np.abs(f64(t["dn"])) * rh), (3, du * yh)):
         within(g[i], f64(r[i]), 1.02 * 8 * U * mass.sum(0))
+
+
+# rows of more than one piece per thread (beyond 8192 elements, in fp32 4096), more of them than workgroups: every
+# workgroup goes through its sums' LDS and its one row buffer several times
+LONG = [(300, 8200, "bf16", "bf16"), (530, 16384, "bf16", "fp32"), (300, 12345, "fp16", "fp16"), (530, 16383, "fp16", "fp32"),
+        (530, 4100, "fp32", "fp32"), (300, 8192, "fp32", "fp32"), (270, 16384, "fp32", "fp32"), (300, 9001, "fp32", "fp32")]
+KINDS = [("none", False), ("channel", True), ("token", True), ("token", False), ("full", True)]
+LONG = [shape + KINDS[(i + j) % 5] for i, shape in enumerate(LONG) for j in (0, 2)]      # each shape with two kinds
+
+
+@pytest.mark.parametrize("T,H,name,res_name,gate,post", LONG)
+def test_forward_of_many_long_rows(mx, T, H, name, res_name, gate, post):
+    _forward(mx, T, H, name, res_name, gate, post)
+
+
+@pytest.mark.parametrize("T,H,name,res_name,gate,post", LONG)
+def test_grad_of_many_long_rows(mx, T, H, name, res_name, gate, post):
+    t, h = _inputs(T, H, name, res_name, gate, post)
+    _grad(mx, t, h, name, res_name)
+
+
+@pytest.mark.parametrize("T,H", [(530, 8200), (300, 16384)])
+def test_parts_of_many_long_rows(mx, T, H):
+    """Without the block, without the next norm: one sum a row, or none, and a barrier that stands for the other."""
+    t, h = _inputs(T, H, "bf16", "bf16", "channel", True)
+    n, _ = mx.block_norm(t["residual"], t["w_pre"], eps=EPS)
+    ref, _ = around.block_norm(h["residual"], h["w_pre"], eps=EPS)
+    within(n, ref, 1.02 * (np.abs(ref) * (depth(H) * U / 2 + 8 * U) + rounded(ref, "bf16")))
+    none, added = mx.block_norm(t["residual"], None, y=t["y"], w_post=t["w_post"], gate=t["gate"], eps=EPS)
+    assert none is None
+    _, r, _, er = _bounds({**h, "w_pre": None}, 1.0)
+    within(added, r, 1.02 * (er + rounded(r, "bf16")))
+
+    def cut(*names):
+        return {k: None if k in names else v for k, v in t.items()}, {k: None if k in names else v for k, v in h.items()}
+    _grad(mx, *cut("y", "w_post", "gate"), "bf16", "bf16")
+    _grad(mx, *cut("w_pre", "dn"), "bf16", "bf16")
