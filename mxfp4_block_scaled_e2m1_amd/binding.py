@@ -636,13 +636,13 @@ def moe_unpermute_grad(d_y, ys, slot_row, topk_w, d_ys=None, d_w=None, stream=No
 def _gate(gate, T, H):
     """(mx_gate, shape of the gate) from the gate's shape: None, [H], [T, 1] or [T, H]."""
     if gate is None:
-        return 0, None
+        return MX_GATE["none"], None
     if gate.shape == (H,):
-        return 1, (H,)
+        return MX_GATE["channel"], (H,)
     if gate.shape == (T, H) and H > 1:
-        return 3, (T, H)
+        return MX_GATE["full"], (T, H)
     if gate.shape == (T, 1):
-        return 2, (T, 1)
+        return MX_GATE["token"], (T, 1)
     raise ValueError(f"gate of shape {tuple(gate.shape)}: [H], [T, 1] or [T, H] is taken, T {T}, H {H}")
 
 
@@ -704,7 +704,7 @@ def block_norm_grad(residual_out, w_pre=None, d_normed=None, d_residual_out=None
     none = (None, None)
     dw_pre, wpre_p = none if w_pre is None else _new(None, "dw_pre", (H,), f32, dev, stream)
     dw_post, wpost_p = none if w_post is None else _new(None, "dw_post", (H,), f32, dev, stream)
-    d_gate, gate_p = none if gate is None else _new(None, "d_gate", gshape, adt if kind == 3 else f32, dev, stream)
+    d_gate, gate_p = none if gate is None else _new(None, "d_gate", gshape, adt if kind == MX_GATE["full"] else f32, dev, stream)
     d_residual, dr_p = _out(d_residual, "d_residual", residual_out, stream)
     d_y, dy_p = none if y is None else _out(d_y, "d_y", y, stream)
     L = lib()
