@@ -164,3 +164,50 @@ def test_freed_blocks_are_left_alone_by_quantised_calls():
         assert not held & {v.data_ptr() for v in got}, name
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, want)), name
+
+
+@pytest.mark.gpu
+def test_given_streams_under_capture():
+    """Captured on the capturing stream, given by name, and on one that forks from it and joins it again, with outputs
+    and workspaces of the calls' own: replays give what eager calls give, also after other work on both streams."""
+    import mxfp4_block_scaled_e2m1_amd as mx
+    rng = np.random.default_rng(1)
+    T, H, k, E, R, n = 1500, 512, 3, 8, 24, 4
+    mk = lambda *s: torch.from_numpy(rng.standard_normal(s)).to(BF16).cuda()
+    x, w, y0, a, b = mk(T, H), mk(H), mk(T, H), mk(n, R, H), mk(n, H, R)
+    ids = torch.from_numpy(rng.integers(-1, E, size=(T, k)).astype(np.int32)).cuda()
+    aid = torch.from_numpy(rng.integers(-1, n, size=(T, 1)).astype(np.int32)).cuda()
+    gw = torch.rand((T, k), device="cuda")
+
+    def step(s):
+        norm, r = mx.block_norm(x, w, y=y0, w_post=w, stream=s)
+        slot_row = mx.moe_sort(ids, E, stream=s)[2]
+        xs = mx.moe_permute(norm, slot_row, stream=s)
+        back = mx.moe_unpermute(xs, slot_row, gw, stream=s)
+        off, tok, _ = mx.moe_sort(aid, n, stream=s)
+        mx.lora_add(back, x, a, b, off, tok, stream=s)
+        grads = mx.block_norm_grad(r, w, back, y=y0, w_post=w, stream=s)
+        return (back, r) + grads[:4]
+
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    want = [v.clone() for v in step(None)]
+    torch.cuda.synchronize()
+    for fork in (False, True):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=main):
+            if fork:
+                side.wait_stream(main)
+                got = step(side)
+                main.wait_stream(side)
+            else:
+                got = step(main)
+        for _ in range(3):
+            for v in got:
+                v.zero_()
+            junk = step(main), step(side), step(None)
+            torch.cuda.synchronize()
+            del junk
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(got, want)), fork
+        del got, g
