@@ -597,7 +597,7 @@ MX_API mx_status mx_moe_unpermute_grad(mx_dtype dt, const void* d_y, const void*
  *   residual, residual_out [T, H] of type res_dt: dt, or MX_DT_F32.
  * residual_out may be residual, and normed may be y (in place); no other
  * overlap. 1 <= H <= 16384, eps >= 0, res_scale finite. Sums of squares are fp32:
- * |values| up to about 10^17. Alignment: one element (H a multiple of 8 with all
+ * |values| up to about 10^17, and with eps 0 not a whole row below 10^-17. Alignment: one element (H a multiple of 8 with all
  * pointers 16-byte aligned is faster).
  */
 MX_API mx_status mx_block_norm(mx_dtype dt, mx_dtype res_dt, const void* y, const void* residual, const void* w_post,

@@ -468,9 +468,12 @@ void dispatch_pair(DType dt, DType rdt, F&& f) {
 static int piece(DType dt) { return dt == DT_F32 ? 4 : 8; }
 bool block_norm_aligned(DType dt, int H, uintptr_t all_pointers) { return H % piece(dt) == 0 && all_pointers % 16 == 0; }
 
-// One workgroup of up to 16 waves per CU of an MI355X. The way back keeps it so (4096
-// rows and more; 8192 x 7168 bf16 112 us, 120 with two), and so do rows of more than a
-// piece per thread and unaligned ones (8192 x 4290 bf16: 63.8 us, two 64.7).
+// One workgroup of up to 16 waves per CU of an MI355X. The way back keeps it so, at any
+// count of rows: one against two, token gate, bf16, us: 300 x 7168 19.6 and 23.0, 1024
+// x 4096 22.3 and 26.9, 1537 x 1024 14.4 and 13.9, 2048 x 1024 14.2 and 15.0, 3000 x
+// 7168 61.2 and 68.2, 4096 x 7168 77.3 and 84.4; fp32, full gate: 300 x 1000 9.4 and
+// 9.8, 1537 x 1000 17.0 and 19.6. So do rows of more than a piece per thread and
+// unaligned ones (8192 x 4290 bf16: 63.8 us, two 64.7).
 constexpr int ROW_GRID = 256;
 // The norm itself takes two, whose rows' sums and stores fall in each other's gaps, as
 // long as the rows they spread over HBM do not cost more. One against two, bf16, us:
@@ -533,7 +536,11 @@ hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, bool aligned, hipS
       dispatch_gate(a.gate_kind, [&](auto g) {
         constexpr int V = decltype(v)::value, G = decltype(g)::value;
         // a full gate beside an fp32 residual, or unaligned rows: the next row would not
-        // fit the registers
+        // fit the 128 registers that a thread of a full workgroup has. Rows of more than
+        // a piece per thread do not fit by themselves: 4 to 338 registers of those
+        // variants (20 and more of unaligned full gates) go to scratch, and they take
+        // twice the time of what they move (4096 x 16384 bf16, channel gate: 316 us, 149
+        // to move).
         constexpr bool AL = decltype(al)::value;
         constexpr bool PF = V == 1 && AL && !(G == GATE_FULL && D != DT_F32 && R == DT_F32);
         k_block_norm_grad<D, R, decltype(n)::value, V, G, PF, AL>

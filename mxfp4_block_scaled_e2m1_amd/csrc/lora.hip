@@ -559,10 +559,10 @@ __global__ __launch_bounds__(64 * EXPAND_WAVES) void k_lora_expand(LoraArgs p, i
 // 16-row blocks per tile. A tile holds one adapter's rows, so it is no larger than
 // an adapter's share; and a larger one reads A and B less often but leaves fewer
 // workgroups, so it takes many rows and much to read of each to pay. One block
-// against four, rank 64, 4 adapters, us: 1024 tokens of 7168 + 7168 columns 24.1 and
-// 26.1, 4096 of them 48.2 and 41.3; 4096 tokens of 2048 + 512 14.7 and 15.1, of
-// 2048 + 2048 20.5 and 20.2; 8192 tokens of 512 + 512 14.6 and 15.3, of 2048 + 2048
-// 31.9 and 29.3.
+// against four, rank 64, 4 adapters, us: 1024 tokens of 7168 + 7168 columns 21.8 and
+// 22.9, 4096 of them 51.6 and 44.0; 4096 tokens of 2048 + 512 15.0 and 15.8, of
+// 2048 + 2048 21.2 and 21.0; 8192 tokens of 512 + 512 15.0 and 15.9, of 1024 + 1024
+// 21.4 and 20.5, of 2048 + 2048 34.8 and 30.4.
 constexpr int BIG_MT = 4;
 bool big_rows(int64_t M, int n) { return M >= 2048 && M / n >= 16 * BIG_MT; }
 int row_blocks(const LoraArgs& p) {
@@ -587,10 +587,9 @@ hipError_t launch_expand(const LoraArgs& p, int mt, hipStream_t s) {
   // Runs of column groups, `each` per wave. Workgroups that do not fit the CUs of an
   // MI355X at once (two of large tiles, else four) wait for another round, and each
   // forms the tile's v anew, half a group of a wave's time: of what fills one to
-  // eight rounds, the one of the least rounds x (each + 1/2). 7168 columns, rank 64:
-  // 4096 tokens 31.2 us in one full round, 41.3 in one and a half, 36.8 in two; with
-  // x of 7168 columns, 8 adapters, the most that one round holds against this, us: 8192
-  // tokens 89 and 83, 20000 tokens 229 and 198, 34000 tokens 364 and 315.
+  // eight rounds, the one of the least rounds x (each + 1/2). 7168 + 7168 columns, rank
+  // 64, 8 adapters, the most that one round holds against this, us: 4096 tokens 43.0
+  // and 42.9, 8192 85 and 77, 20000 216 and 188, 34000 366 and 317.
   const int64_t tiles = lora_tiles(p.M, p.n, mt), slots = (mt == 1 ? 4 : 2) * 256;
   int run = 0, all_runs = 0;
   for (int64_t k = 1, least = INT64_MAX; k <= 8; ++k) {

@@ -42,8 +42,9 @@ __device__ __forceinline__ char* at(void* p, int64_t i) { return (char*)p + i * 
 
 // The same vector at any element's address: the hardware and its ABI take
 // unaligned global accesses, so a row that does not start on 16 bytes still moves 16
-// bytes a lane (element by element, norms of 4096 x 4097 bf16 took 194 us
-// instead of 28, their gradient 680 instead of 48).
+// bytes a lane. 4096 rows of bf16, post-norm and channel gate, us per call in a
+// graph: 4096 columns 25.9, their gradient 47.7; 4097 columns 40.8 and 75.6 (element
+// by element 194 and 680).
 typedef uint32_t u32v4_any __attribute__((ext_vector_type(4), aligned(2)));
 
 // N consecutive elements as they lie in memory, at element i of a row: one
