@@ -7,8 +7,8 @@
  * which allocates its workspace and synchronises once when it is created and
  * destroyed, and keeps the buffers it was created over. Work is enqueued on the caller's HIP
  * stream (`stream` is a hipStream_t; NULL means the default stream). Tensors are
- * row-major and contiguous (mx_lora_add takes row strides). bf16 tensors are
- * passed as uint16_t bit patterns, those of several types (mx_dtype) as void*;
+ * row-major and contiguous (mx_lora_add, mx_w4_linear and mx_cache_write take row
+ * strides). bf16 tensors are passed as uint16_t bit patterns, those of several types (mx_dtype) as void*;
  * FP4 codes and E8M0/E4M3 scales are raw bytes (a checkpoint's int8 storage is
  * read as unsigned bytes).
  *
@@ -94,7 +94,8 @@ typedef enum mx_format {
   MX_FMT_MXFP4 = 0,      /* E2M1 codes + E8M0 per 1x32 */
   MX_FMT_FP8_B128 = 1,   /* float8_e4m3fn + E8M0 per 128x128 block (dequant only) */
   MX_FMT_NVFP4 = 2,      /* E2M1 codes + E4M3 per 1x16 + fp32 global scale */
-  MX_FMT_MXFP8 = 3,      /* float8_e4m3fn codes + E8M0 per 1x32 (activation quantisation only) */
+  MX_FMT_MXFP8 = 3,      /* float8_e4m3fn codes + E8M0 per 1x32 (activations, the cache) */
+  MX_FMT_INT4 = 4,       /* codes 0..15 with a scale and a zero point per group (mx_w4_linear) */
   /* not formats: they make every int32 value a valid mx_format, so a caller's
    * unknown value reaches the library's check (MX_ERR_FORMAT) with defined
    * behaviour in C++ as in C */
@@ -103,7 +104,7 @@ typedef enum mx_format {
 } mx_format;
 
 /* Element type of the activations the operators around the experts take
- * (mx_moe_*, mx_block_norm*, mx_lora_add). */
+ * (mx_moe_*, mx_block_norm*, mx_lora_add, mx_w4_linear, mx_cache_*). */
 typedef enum mx_dtype {
   MX_DT_BF16 = 0,
   MX_DT_F16 = 1,
@@ -122,6 +123,14 @@ typedef enum mx_gate {
   MX_GATE_RESERVED_MIN_ = -2147483647 - 1,
   MX_GATE_RESERVED_MAX_ = 2147483647
 } mx_gate;
+
+/* What a router's logits z become. */
+typedef enum mx_score {
+  MX_SCORE_SOFTMAX = 0,  /* softmax of z over the experts */
+  MX_SCORE_SIGMOID = 1,  /* 1 / (1 + e^-z), each expert for itself */
+  MX_SCORE_RESERVED_MIN_ = -2147483647 - 1,
+  MX_SCORE_RESERVED_MAX_ = 2147483647
+} mx_score;
 
 /*
  * mx_dequant -- dequantise a block-scaled matrix to bf16. The operation is the
@@ -652,6 +661,106 @@ MX_API mx_status mx_lora_add(mx_dtype dt, const void* x, int64_t ldx, int64_t M,
                              const int32_t* row_token, void* y, int64_t ldy, int64_t N, void* workspace,
                              size_t ws_bytes, void* stream);
 MX_API size_t mx_lora_add_workspace_size(int64_t M, int64_t K, int64_t R, int32_t n);
+
+/*
+ * mx_moe_gate -- the router: the k experts of each token and their weights, as
+ * mx_grouped_expert_mlp and mx_moe_sort take them.
+ *   logits [T, E] of type dt; s = their scores (mx_score)
+ *   bias   [E] fp32, or NULL: added to the scores for the choice only
+ *   topk_ids [T, k] int32: the experts of the largest s + bias, the largest first, of
+ *            equal ones the lower index
+ *   topk_w   [T, k] fp32: scale * s of each, with renorm != 0 over the sum of the
+ *            token's k scores (0 where that sum is 0)
+ * An expert whose logit is -inf is off: its score is 0 and it is not chosen. Where
+ * fewer than k are on, the slots left over have the id -1 and the weight 0. The
+ * choice is made on the logits themselves (no bias) or on s + bias in 64 bits. A NaN
+ * logit comes behind every number; with softmax scores the token's weights are NaN.
+ * 1 <= E <= 512, 1 <= k <= min(E, 64), 0 <= T <= 2^26, scale finite. Alignment: one element.
+ * The outputs must not overlap each other or an input.
+ *
+ * mx_moe_balance -- the balance loss of each sequence of a batch, and the load of
+ * each expert. With p the scores as shares of one (softmax: the scores; sigmoid:
+ * over their sum), n tokens in sequence q, and c[q, e] its slots that name e:
+ *   counts [S, E] int32 = c
+ *   loss   [S] fp32 = coef * E / (k n^2) * sum_e c[q, e] * sum_t p[t, e]
+ *          (1 * coef where both load and shares are even; 0 for n = 0)
+ *   seq_off [S+1] int32: sequence q has the tokens seq_off[q] .. seq_off[q+1] - 1;
+ *          tokens outside every sequence are left out. NULL: S is 1, all T tokens.
+ *   topk_ids [T, k] int32; ids outside [0, E) are not counted.
+ * 1 <= S <= 2^20, S * E <= 2^28, k >= 1, T * k <= 2^30, coef finite. The sums run in a
+ * fixed order for given sizes. workspace: mx_moe_balance_workspace_size(T, E, S)
+ * bytes, 256-byte aligned (0 bytes for few tokens a sequence: workspace may then be NULL).
+ *
+ * mx_moe_gate_grad -- the gradient of both for the logits:
+ *   d_logits [T, E] of type dt, given
+ *   d_w [T, k] fp32, the gradient of topk_w (NULL: none), and
+ *   d_loss [S] fp32, that of loss, with the counts of mx_moe_balance (NULL, both: none)
+ * at the given topk_ids, which count as constants, as counts do (an id may stand
+ * twice; slots outside [0, E) have no part). renorm, scale, coef, seq_off and S as in
+ * the forward calls. 0 for experts that are off. Not both d_w and d_loss NULL.
+ */
+MX_API mx_status mx_moe_gate(mx_dtype dt, const void* logits, int64_t T, int32_t E, mx_score score, const float* bias,
+                             int32_t k, int32_t renorm, float scale, int32_t* topk_ids, float* topk_w, void* stream);
+MX_API mx_status mx_moe_balance(mx_dtype dt, const void* logits, int64_t T, int32_t E, mx_score score,
+                                const int32_t* topk_ids, int32_t k, const int32_t* seq_off, int64_t S, float coef,
+                                float* loss, int32_t* counts, void* workspace, size_t ws_bytes, void* stream);
+MX_API size_t mx_moe_balance_workspace_size(int64_t T, int32_t E, int64_t S);
+MX_API mx_status mx_moe_gate_grad(mx_dtype dt, const void* logits, int64_t T, int32_t E, mx_score score,
+                                  const int32_t* topk_ids, int32_t k, int32_t renorm, float scale, const float* d_w,
+                                  const int32_t* counts, const int32_t* seq_off, int64_t S, float coef,
+                                  const float* d_loss, void* d_logits, void* stream);
+
+/*
+ * mx_w4_linear -- a linear layer of activations as they are (mx_nvfp4_linear and
+ * mx_fp8_block_linear quantise them) with 4-bit weights and group scales, from one
+ * token to many:
+ *   y[t, n] = sum_c x[t, c] * (code[n, c] - zero[n, c / group]) * scale[n, c / group]
+ *   x [M, K], rows ldx elements apart; y [M, N], rows ldy elements apart; both of
+ *   type dt (MX_DT_BF16 or MX_DT_F16)
+ *   w [N, K/2]: two codes a byte, column 2j in the low nibble
+ *   MX_FMT_MXFP4: E2M1 codes, scales [N, K/32] E8M0; group is 32, zeros NULL
+ *   MX_FMT_INT4:  codes 0 .. 15, scales [N, K/group] of type dt, zeros [N, K/group]
+ *                 bytes, or NULL for 8; group 32, 64 or 128
+ * Codes enter the products exactly, a group's scale multiplies an fp32 sum, and y is
+ * rounded once. A token with an infinite or NaN activation has no finite y.
+ * K a multiple of group up to 2^20, 1 <= N <= 2^20, 0 <= M <= 2^20, ldx a multiple of 8 of at least K,
+ * ldy >= N, both at most 2^30. workspace: mx_w4_linear_workspace_size(M, K, N) bytes,
+ * 256-byte aligned (0 bytes for most sizes: it may then be NULL). Alignment: x and w 16
+ * bytes, y and an INT4 scale one element. y overlaps no input.
+ */
+MX_API mx_status mx_w4_linear(mx_dtype dt, const void* x, int64_t ldx, int64_t M, int64_t K, mx_format fmt,
+                              const uint8_t* w, const void* scales, const uint8_t* zeros, int32_t group, int64_t N,
+                              void* y, int64_t ldy, void* workspace, size_t ws_bytes, void* stream);
+MX_API size_t mx_w4_linear_workspace_size(int64_t M, int64_t K, int64_t N);
+
+/*
+ * A paged cache whose rows are held in MX_FMT_MXFP8 or MX_FMT_MXFP4 (the formats and
+ * the rounding of mx_quantize_act): codes [pages, page_size, width] (MXFP4: width / 2)
+ * and scales [pages, page_size, width / 32].
+ *
+ * mx_cache_write -- the row of slot slots[t] = page * page_size + place takes x[t]:
+ *   x [T, width] of type dt, rows ldx elements apart; slots [T] int32. A slot
+ *   outside [0, pages * page_size) is skipped (padding: -1). No two tokens may name
+ *   one slot. Rows that no token names are left as they are.
+ * mx_cache_read -- the rows of B sequences, each rounded once to dt:
+ *   out [rows, width]; seq_off [B+1] int32, in ascending order: sequence b's rows
+ *   are out[seq_off[b]] .. out[seq_off[b+1] - 1], at its positions 0, 1, ..
+ *   page_table [B, table_width] int32: position i is at place i % page_size of page
+ *   page_table[b, i / page_size]
+ * A position whose page is outside [0, pages) or past the table reads as zeros (a
+ * sequence of fewer than all positions is read by a table and offsets of its own).
+ * Rows of out before seq_off[0] and from seq_off[B] on are left as they are.
+ * width a multiple of 32 up to 2^16, page_size >= 1, pages * page_size < 2^31,
+ * 0 <= T, rows < 2^31, T * width < 2^34, ldx a multiple of 8 of at least width and at most 2^30,
+ * B >= 0, table_width >= 0, B * table_width < 2^40.
+ * Alignment: x, codes and out 16 bytes. Outputs overlap no input.
+ */
+MX_API mx_status mx_cache_write(mx_format fmt, mx_dtype dt, const void* x, int64_t ldx, int64_t T, int64_t width,
+                                const int32_t* slots, int64_t pages, int64_t page_size, uint8_t* codes,
+                                uint8_t* scales, void* stream);
+MX_API mx_status mx_cache_read(mx_format fmt, const uint8_t* codes, const uint8_t* scales, int64_t pages,
+                               int64_t page_size, int64_t width, const int32_t* page_table, int64_t table_width,
+                               const int32_t* seq_off, int64_t B, int64_t rows, mx_dtype dt, void* out, void* stream);
 
 /*
  * Measurement probes (not steps of the pages' pipeline): kernels whose measured

@@ -22,7 +22,8 @@ LIB_PATH = os.environ.get("MXFP4_LIB") or os.path.join(HERE, "libmxfp4.so")
 
 MX_DT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 MX_GATE = {"none": 0, "channel": 1, "token": 2, "full": 3}
-MX_FMT = {"mxfp4": 0, "fp8_b128": 1, "nvfp4": 2, "mxfp8": 3}
+MX_FMT = {"mxfp4": 0, "fp8_b128": 1, "nvfp4": 2, "mxfp8": 3, "int4": 4}
+MX_SCORE = {"softmax": 0, "sigmoid": 1}
 STATUS = {0: "MX_OK", 1: "MX_ERR_NULL", 2: "MX_ERR_SHAPE", 3: "MX_ERR_ALIGN", 4: "MX_ERR_FORMAT",
           5: "MX_ERR_WORKSPACE", 6: "MX_ERR_HIP", 7: "MX_ERR_VALUE"}
 
@@ -83,6 +84,14 @@ SIGNATURES = {
     "mx_block_norm_grad_workspace_size": (_SZ, [_I64, _I64]),
     "mx_lora_add": (_I32, [_I32, _P, _I64, _I64, _I64, _P, _P, _P, _I32, _I64, _P, _P, _P, _I64, _I64, _P, _SZ, _P]),
     "mx_lora_add_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
+    "mx_moe_gate": (_I32, [_I32, _P, _I64, _I32, _I32, _P, _I32, _I32, _F, _P, _P, _P]),
+    "mx_moe_balance": (_I32, [_I32, _P, _I64, _I32, _I32, _P, _I32, _P, _I64, _F, _P, _P, _P, _SZ, _P]),
+    "mx_moe_balance_workspace_size": (_SZ, [_I64, _I32, _I64]),
+    "mx_moe_gate_grad": (_I32, [_I32, _P, _I64, _I32, _I32, _P, _I32, _I32, _F, _P, _P, _P, _I64, _F, _P, _P, _P]),
+    "mx_w4_linear": (_I32, [_I32, _P, _I64, _I64, _I64, _I32, _P, _P, _P, _I32, _I64, _P, _I64, _P, _SZ, _P]),
+    "mx_w4_linear_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "mx_cache_write": (_I32, [_I32, _I32, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P]),
+    "mx_cache_read": (_I32, [_I32, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _I64, _I64, _I32, _P, _P]),
     "mx_probe_mfma_fp4": (_I32, [_P, _I64, _I32, _P, _P]),
     "mx_probe_read": (_I32, [_I32, _I32, _I32, _P, _I64, _P, _P]),
     "mx_probe_copy": (_I32, [_P, _P, _I64, _P]),
@@ -758,6 +767,178 @@ def lora_add(y, x, a, b, adapter_off, row_token, scale=None, workspace=None, str
          _tensor(row_token, "row_token", torch.int32, (M,), dev), yp, ldy, N, wp, wn)
     _wrote((y,))
     return y
+
+
+def _score(score):
+    s = MX_SCORE.get(score)
+    if s is None:
+        raise ValueError(f"score {score!r}: softmax or sigmoid is taken")
+    return s
+
+
+def moe_gate(logits, k: int, score="softmax", bias=None, renorm: bool = True, scale: float = 1.0, topk_ids=None,
+             topk_w=None, stream=None):
+    """mx_moe_gate: logits [T, E] -> (topk_ids [T, k] int32, topk_w [T, k] fp32). bias [E] fp32 has a part in the
+    choice only."""
+    given = (topk_ids, topk_w)
+    T, E = logits.shape
+    dev = logits.device
+    dt = _dtype(logits, "logits")
+    if not 1 <= k <= min(E, 64):
+        raise ValueError(f"k {k} not in [1, min(E {E}, 64)]")
+    lp = _tensor(logits, "logits", logits.dtype, (T, E), dev)
+    bp = None if bias is None else _tensor(bias, "bias", torch.float32, (E,), dev)
+    topk_ids, ip = _new(topk_ids, "topk_ids", (T, k), torch.int32, dev, stream)
+    topk_w, wp = _new(topk_w, "topk_w", (T, k), torch.float32, dev, stream)
+    _run(lib().mx_moe_gate, dev, stream, dt, lp, T, E, _score(score), bp, k, renorm, scale, ip, wp)
+    _wrote(given)
+    return topk_ids, topk_w
+
+
+@functools.lru_cache(4096)
+def moe_balance_workspace_size(T, E, S) -> int:
+    return int(lib().mx_moe_balance_workspace_size(T, E, S))
+
+
+def _sequences(seq_off, dev):
+    """(pointer, number of sequences): one of all tokens without seq_off."""
+    if seq_off is None:
+        return None, 1
+    S = seq_off.shape[0] - 1
+    if S < 1:
+        raise ValueError("seq_off needs two entries at least")
+    return _tensor(seq_off, "seq_off", torch.int32, (S + 1,), dev), S
+
+
+def moe_balance(logits, topk_ids, seq_off=None, score="softmax", coef: float = 1.0, loss=None, counts=None,
+                workspace=None, stream=None):
+    """mx_moe_balance: logits [T, E], topk_ids [T, k] -> (loss [S] fp32, counts [S, E] int32) of the S sequences with the
+    tokens seq_off[q] .. seq_off[q + 1] - 1 (int32 seq_off [S + 1]; None: one of all tokens)."""
+    given = (loss, counts)
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    dev = logits.device
+    dt = _dtype(logits, "logits")
+    lp = _tensor(logits, "logits", logits.dtype, (T, E), dev)
+    ip = _tensor(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    op, S = _sequences(seq_off, dev)
+    loss, xp = _new(loss, "loss", (S,), torch.float32, dev, stream)
+    counts, cp = _new(counts, "counts", (S, E), torch.int32, dev, stream)
+    ws, wp, wn = _scratch(workspace, moe_balance_workspace_size(T, E, S), dev, stream)
+    _run(lib().mx_moe_balance, dev, stream, dt, lp, T, E, _score(score), ip, k, op, S, coef, xp, cp, wp, wn)
+    _wrote(given)
+    return loss, counts
+
+
+def moe_gate_grad(logits, topk_ids, d_w=None, counts=None, d_loss=None, seq_off=None, score="softmax",
+                  renorm: bool = True, scale: float = 1.0, coef: float = 1.0, d_logits=None, stream=None):
+    """mx_moe_gate_grad -> d_logits [T, E]: the gradient of moe_gate's weights (d_w [T, k] fp32) and of moe_balance's
+    losses (d_loss [S] fp32, with its counts [S, E]) at the given topk_ids; either may be None."""
+    given = (d_logits,)
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    dev, f32 = logits.device, torch.float32
+    dt = _dtype(logits, "logits")
+    _need(d_w is not None or d_loss is not None, "d_w and d_loss are both None: nothing to do")
+    _need((counts is None) == (d_loss is None), "counts and d_loss go together")
+    lp = _tensor(logits, "logits", logits.dtype, (T, E), dev)
+    ip = _tensor(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    wp = None if d_w is None else _tensor(d_w, "d_w", f32, (T, k), dev)
+    op, S = _sequences(seq_off, dev)
+    cp = None if counts is None else _tensor(counts, "counts", torch.int32, (S, E), dev)
+    xp = None if d_loss is None else _tensor(d_loss, "d_loss", f32, (S,), dev)
+    d_logits, dp = _out(d_logits, "d_logits", logits, stream)
+    _run(lib().mx_moe_gate_grad, dev, stream, dt, lp, T, E, _score(score), ip, k, renorm, scale, wp, cp, op, S, coef, xp,
+         dp)
+    _wrote(given)
+    return d_logits
+
+
+@functools.lru_cache(4096)
+def w4_linear_workspace_size(M, K, N) -> int:
+    return int(lib().mx_w4_linear_workspace_size(M, K, N))
+
+
+def w4_linear(x, w, w_s, zeros=None, out=None, workspace=None, stream=None):
+    """mx_w4_linear: x [M, K] (bf16 or fp16) . w^T -> y [M, N], for packed 4-bit w [N, K/2]. uint8 w_s [N, K/32]: MXFP4
+    with its E8M0 scales; w_s [N, K/group] of x's type: INT4 with those scales and zero points zeros [N, K/group]
+    uint8 (None: 8), group 32, 64 or 128. x and out may be column ranges of wider matrices."""
+    given = (out,)
+    M, dev = x.shape[0], x.device
+    dt = _dtype(x, "x")
+    xp, K, ldx = _rows(x, "x", x.dtype, M, dev)
+    N, groups = w_s.shape
+    wp = _tensor(w, "w", torch.uint8, (N, K // 2), dev)
+    group = K // groups if groups and K % groups == 0 else 0
+    if w_s.dtype is torch.uint8:
+        fmt = MX_FMT["mxfp4"]
+        _need(group == 32, f"w_s of {groups} columns: MXFP4 has one scale per 32 of the {K}")
+        _need(zeros is None, "MXFP4 has no zeros")
+    else:
+        fmt = MX_FMT["int4"]
+        _need(group in (32, 64, 128), f"w_s of {groups} columns: one scale per 32, 64 or 128 of the {K} is taken")
+    sp = _tensor(w_s, "w_s", torch.uint8 if w_s.dtype is torch.uint8 else x.dtype, (N, groups), dev)
+    zp = None if zeros is None else _tensor(zeros, "zeros", torch.uint8, (N, groups), dev)
+    if out is None:
+        out, yp = _new(None, "out", (M, N), x.dtype, dev, stream)
+        ldy = N
+    else:
+        yp, n, ldy = _rows(out, "out", x.dtype, M, dev)
+        _need(n == N, f"out has {n} columns, w {N} rows")
+    ws, kp, kn = _scratch(workspace, w4_linear_workspace_size(M, K, N), dev, stream)
+    _run(lib().mx_w4_linear, dev, stream, dt, xp, ldx, M, K, fmt, wp, sp, zp, group, N, yp, ldy, kp, kn)
+    _wrote(given)
+    return out
+
+
+def _cache(fmt, codes, scales, dev):
+    """(mx_format, pages, page_size, width, pointers) of a cache."""
+    f = MX_FMT.get(fmt) if fmt in ("mxfp8", "mxfp4") else None
+    if f is None:
+        raise ValueError(f"format {fmt!r}: the cache holds mxfp8 or mxfp4")
+    pages, page_size, blocks = scales.shape
+    width = 32 * blocks
+    return (f, pages, page_size, width,
+            _tensor(codes, "codes", torch.uint8, (pages, page_size, width if fmt == "mxfp8" else width // 2), dev),
+            _tensor(scales, "scales", torch.uint8, (pages, page_size, blocks), dev))
+
+
+def cache_write(fmt, x, slots, codes, scales, stream=None):
+    """mx_cache_write: x [T, width] to the rows slots [T] (int32, page * page_size + place; -1: none) of the cache codes
+    [pages, page_size, width] (mxfp4: width / 2) and scales [pages, page_size, width / 32], in place. x may be a column
+    range of a wider matrix. Returns (codes, scales)."""
+    T, dev = x.shape[0], x.device
+    dt = _dtype(x, "x")
+    f, pages, page_size, width, cp, sp = _cache(fmt, codes, scales, dev)
+    xp, n, ldx = _rows(x, "x", x.dtype, T, dev)
+    _need(n == width, f"x has {n} columns, the cache {width}")
+    _run(lib().mx_cache_write, dev, stream, f, dt, xp, ldx, T, width, _tensor(slots, "slots", torch.int32, (T,), dev),
+         pages, page_size, cp, sp)
+    _wrote((codes, scales))
+    return codes, scales
+
+
+def cache_read(fmt, codes, scales, page_table, seq_off, rows=None, dtype=torch.bfloat16, out=None, stream=None):
+    """mx_cache_read -> out [rows, width]: the rows seq_off[b] .. seq_off[b + 1] - 1 (int32 seq_off [B + 1]) are the
+    first positions of sequence b, at the pages page_table[b] (int32 [B, table_width]). Rows outside every sequence are
+    whatever they are, or what a given out has."""
+    given = (out,)
+    dev = codes.device
+    _need(codes.is_cuda, "libmxfp4 takes device tensors")
+    f, pages, page_size, width, cp, sp = _cache(fmt, codes, scales, dev)
+    B, table_width = page_table.shape
+    tp = _tensor(page_table, "page_table", torch.int32, (B, table_width), dev)
+    fp = _tensor(seq_off, "seq_off", torch.int32, (B + 1,), dev)
+    if out is None:
+        _need(rows is not None, "rows or out is needed")
+    else:
+        _need(rows is None or rows == out.shape[0], f"out has {out.shape[0]} rows, not {rows}")
+        rows, dtype = out.shape[0], out.dtype
+    out, op = _new(out, "out", (rows, width), dtype, dev, stream)
+    _run(lib().mx_cache_read, dev, stream, f, cp, sp, pages, page_size, width, tp, table_width, fp, B, rows,
+         _dtype(out, "out"), op)
+    _wrote(given)
+    return out
 
 
 class MoeRunner:

@@ -1452,6 +1452,16 @@ mx_status check_apart(const Span& out, std::initializer_list<Span> all, std::ini
   return MX_OK;
 }
 
+// x [.., K] and y [.., N] of 16-bit elements may be interleaved column ranges of one
+// matrix: only equal or row-overlapping ranges are refused.
+mx_status check_columns(const Span& x, int64_t ldx, int64_t K, const Span& y, int64_t ldy, int64_t N) {
+  if (!overlaps(x, y)) return MX_OK;
+  const int64_t bytes = (const char*)y.p - (const char*)x.p, d = bytes / 2;
+  const int64_t col = ldx == ldy ? ((d % ldx) + ldx) % ldx : 0;
+  if (ldx != ldy || bytes % 2 != 0 || col < K || col + N > ldx) return fail(MX_ERR_VALUE, "y overlaps x");
+  return MX_OK;
+}
+
 mx_status check_slots(int64_t T, int32_t k) {
   if (T < 0) return fail(MX_ERR_SHAPE, "token count %lld is negative", (long long)T);
   if (k < 1) return fail(MX_ERR_SHAPE, "k %d must be at least 1", k);
@@ -1781,19 +1791,12 @@ mx_status mx_lora_add(mx_dtype dt, const void* x, int64_t ldx, int64_t M, int64_
   MX_REQUIRE_ALIGN(workspace, 256);
   const size_t need = mx_lora_add_workspace_size(M, K, R, n);
   if (ws_bytes < need) return fail(MX_ERR_WORKSPACE, "workspace %zu bytes < required %zu", ws_bytes, need);
-  // x and y may be interleaved column ranges of one matrix: only equal or
-  // row-overlapping ranges are refused
   const Span sa{"a", a, n * R * K * 2}, sb{"b", b, n * R * N * 2}, sc{"scale", scale, (int64_t)n * 4},
       so{"adapter_off", adapter_off, ((int64_t)n + 1) * 4}, st{"row_token", row_token, M * 4},
       sx{"x", x, ((M - 1) * ldx + K) * 2}, sy{"y", y, ((M - 1) * ldy + N) * 2}, sw{"workspace", workspace, (int64_t)need};
   MX_TRY(check_apart(sw, {sa, sb, sc, so, st, sx, sy}));
   MX_TRY(check_apart(sy, {sa, sb, sc, so, st}));
-  if (overlaps(sx, sy)) {
-    const int64_t d = ((const char*)y - (const char*)x) / 2;
-    const int64_t col = ldx == ldy ? ((d % ldx) + ldx) % ldx : 0;
-    if (ldx != ldy || ((const char*)y - (const char*)x) % 2 != 0 || col < K || col + N > ldx)
-      return fail(MX_ERR_VALUE, "y overlaps x");
-  }
+  MX_TRY(check_columns(sx, ldx, K, sy, ldy, N));
   LoraArgs p;
   p.dt = (DType)dt;
   p.x = x; p.ldx = ldx; p.M = (int)M; p.K = (int)K; p.N = (int)N; p.R = (int)R; p.n = n;
@@ -1803,6 +1806,283 @@ mx_status mx_lora_add(mx_dtype dt, const void* x, int64_t ldx, int64_t M, int64_
   p.part = (float*)workspace;
   p.slots_log2 = p.least = 0;
   MX_HIP(phase("lora_add", s, [&] { return launch_lora(p, s); }), "lora_add");
+  return ok();
+}
+
+// ---------------------------------------------------------------- the router
+namespace {
+
+mx_status check_router(mx_dtype dt, int64_t T, int32_t E, mx_score score, int32_t k) {
+  MX_TRY(check_dtype(dt));
+  if (score != MX_SCORE_SOFTMAX && score != MX_SCORE_SIGMOID) return fail(MX_ERR_FORMAT, "unknown score %d", (int)score);
+  if (T < 0 || T > ((int64_t)1 << 26)) return fail(MX_ERR_SHAPE, "token count %lld not in [0, 2^26]", (long long)T);
+  if (E < 1 || E > ROUTE_MAX_EXPERTS) return fail(MX_ERR_SHAPE, "E %d not in [1, %d]", E, ROUTE_MAX_EXPERTS);
+  return check_slots(T, k);
+}
+
+mx_status check_sequences(int32_t E, const int32_t* seq_off, int64_t S, float coef) {
+  if (S < 1 || S > (1 << 20) || S * E > ((int64_t)1 << 28))
+    return fail(MX_ERR_SHAPE, "%lld sequences not in [1, 2^20], or more than 2^28 / E", (long long)S);
+  if (seq_off == nullptr && S != 1) return fail(MX_ERR_NULL, "seq_off is NULL for %lld sequences", (long long)S);
+  MX_REQUIRE_ALIGN(seq_off, 4);
+  if (!std::isfinite(coef)) return fail(MX_ERR_VALUE, "coef %g is not finite", (double)coef);
+  return MX_OK;
+}
+
+}  // namespace
+
+mx_status mx_moe_gate(mx_dtype dt, const void* logits, int64_t T, int32_t E, mx_score score, const float* bias,
+                      int32_t k, int32_t renorm, float scale, int32_t* topk_ids, float* topk_w, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_router(dt, T, E, score, k));
+  if (k > E || k > MAX_TOPK) return fail(MX_ERR_SHAPE, "k %d above E %d or %d", k, E, MAX_TOPK);
+  if (!std::isfinite(scale)) return fail(MX_ERR_VALUE, "scale %g is not finite", (double)scale);
+  if (T == 0) return ok();
+  const int es = dt_bytes((DType)dt);
+  MX_REQUIRE_PTR(logits);
+  MX_REQUIRE_PTR(topk_ids);
+  MX_REQUIRE_PTR(topk_w);
+  MX_REQUIRE_ALIGN(logits, es);
+  MX_REQUIRE_ALIGN(bias, 4);
+  MX_REQUIRE_ALIGN(topk_ids, 4);
+  MX_REQUIRE_ALIGN(topk_w, 4);
+  const Span sl{"logits", logits, T * E * es}, sb{"bias", bias, (int64_t)E * 4}, si{"topk_ids", topk_ids, T * k * 4},
+      sw{"topk_w", topk_w, T * k * 4};
+  MX_TRY(check_apart(si, {sl, sb, sw}));
+  MX_TRY(check_apart(sw, {sl, sb}));
+  MX_HIP(phase("moe_gate", s,
+               [&] {
+                 return launch_gate(logits, (DType)dt, T, E, score == MX_SCORE_SIGMOID, bias, k, renorm != 0, scale,
+                                    topk_ids, topk_w, s);
+               }),
+         "moe_gate");
+  return ok();
+}
+
+size_t mx_moe_balance_workspace_size(int64_t T, int32_t E, int64_t S) {
+  if (T < 0 || T > ((int64_t)1 << 26) || E < 1 || E > ROUTE_MAX_EXPERTS || S < 1 || S > (1 << 20) ||
+      S * E > ((int64_t)1 << 28))
+    return 0;
+  const int parts = balance_splits(T, S);
+  if (parts == 1) return 0;
+  Carve c(nullptr);
+  c.take((size_t)(S * parts * E) * 8);
+  return c.off;
+}
+
+mx_status mx_moe_balance(mx_dtype dt, const void* logits, int64_t T, int32_t E, mx_score score, const int32_t* topk_ids,
+                         int32_t k, const int32_t* seq_off, int64_t S, float coef, float* loss, int32_t* counts,
+                         void* workspace, size_t ws_bytes, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_router(dt, T, E, score, k));
+  MX_TRY(check_sequences(E, seq_off, S, coef));
+  const int es = dt_bytes((DType)dt);
+  if (T > 0) {
+    MX_REQUIRE_PTR(logits);
+    MX_REQUIRE_PTR(topk_ids);
+  }
+  MX_REQUIRE_PTR(loss);
+  MX_REQUIRE_PTR(counts);
+  MX_REQUIRE_ALIGN(logits, es);
+  MX_REQUIRE_ALIGN(topk_ids, 4);
+  MX_REQUIRE_ALIGN(loss, 4);
+  MX_REQUIRE_ALIGN(counts, 4);
+  const size_t need = mx_moe_balance_workspace_size(T, E, S);
+  if (need > 0) {
+    MX_REQUIRE_PTR(workspace);
+    MX_REQUIRE_ALIGN(workspace, 256);
+  }
+  if (ws_bytes < need) return fail(MX_ERR_WORKSPACE, "workspace %zu bytes < required %zu", ws_bytes, need);
+  const Span sl{"logits", logits, T * E * es}, si{"topk_ids", topk_ids, T * k * 4},
+      so{"seq_off", seq_off, (S + 1) * 4}, sx{"loss", loss, S * 4}, sc{"counts", counts, S * E * 4},
+      ws{"workspace", workspace, (int64_t)need};
+  MX_TRY(check_apart(sx, {sl, si, so, sc, ws}));
+  MX_TRY(check_apart(sc, {sl, si, so, ws}));
+  MX_TRY(check_apart(ws, {sl, si, so}));
+  MX_HIP(phase("moe_balance", s,
+               [&] {
+                 return launch_balance(logits, (DType)dt, T, E, score == MX_SCORE_SIGMOID, topk_ids, k, seq_off, S,
+                                       coef, (float*)workspace, loss, counts, s);
+               }),
+         "moe_balance");
+  return ok();
+}
+
+mx_status mx_moe_gate_grad(mx_dtype dt, const void* logits, int64_t T, int32_t E, mx_score score,
+                           const int32_t* topk_ids, int32_t k, int32_t renorm, float scale, const float* d_w,
+                           const int32_t* counts, const int32_t* seq_off, int64_t S, float coef, const float* d_loss,
+                           void* d_logits, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_router(dt, T, E, score, k));
+  if (k > MAX_TOPK) return fail(MX_ERR_SHAPE, "k %d above %d", k, MAX_TOPK);
+  if (!std::isfinite(scale)) return fail(MX_ERR_VALUE, "scale %g is not finite", (double)scale);
+  MX_TRY(check_sequences(E, seq_off, S, coef));
+  if (T == 0) return ok();          // d_w of no tokens may be NULL
+  if ((counts == nullptr) != (d_loss == nullptr)) return fail(MX_ERR_NULL, "counts and d_loss go together");
+  if (d_w == nullptr && d_loss == nullptr) return fail(MX_ERR_NULL, "d_w and d_loss are both NULL: nothing to do");
+  const int es = dt_bytes((DType)dt);
+  MX_REQUIRE_PTR(logits);
+  MX_REQUIRE_PTR(topk_ids);
+  MX_REQUIRE_PTR(d_logits);
+  MX_REQUIRE_ALIGN(logits, es);
+  MX_REQUIRE_ALIGN(topk_ids, 4);
+  MX_REQUIRE_ALIGN(d_w, 4);
+  MX_REQUIRE_ALIGN(counts, 4);
+  MX_REQUIRE_ALIGN(d_loss, 4);
+  MX_REQUIRE_ALIGN(d_logits, es);
+  MX_TRY(check_apart({"d_logits", d_logits, T * E * es}, {{"logits", logits, T * E * es},
+                                                          {"topk_ids", topk_ids, T * k * 4},
+                                                          {"d_w", d_w, T * k * 4},
+                                                          {"counts", counts, S * E * 4},
+                                                          {"seq_off", seq_off, (S + 1) * 4},
+                                                          {"d_loss", d_loss, S * 4}}));
+  MX_HIP(phase("moe_gate_grad", s,
+               [&] {
+                 return launch_gate_grad(logits, (DType)dt, T, E, score == MX_SCORE_SIGMOID, topk_ids, k, renorm != 0,
+                                         scale, d_w, counts, seq_off, S, coef, d_loss, d_logits, s);
+               }),
+         "moe_gate_grad");
+  return ok();
+}
+
+// ---------------------------------------------------------------- 4-bit weights with group scales
+size_t mx_w4_linear_workspace_size(int64_t M, int64_t K, int64_t N) {
+  if (M < 0 || M > (1 << 20) || K < 32 || K > (1 << 20) || N < 1 || N > (1 << 20)) return 0;
+  return 0;
+}
+
+mx_status mx_w4_linear(mx_dtype dt, const void* x, int64_t ldx, int64_t M, int64_t K, mx_format fmt, const uint8_t* w,
+                       const void* scales, const uint8_t* zeros, int32_t group, int64_t N, void* y, int64_t ldy,
+                       void* workspace, size_t ws_bytes, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_dtype(dt));
+  if (dt == MX_DT_F32) return fail(MX_ERR_FORMAT, "w4_linear takes bf16 or fp16, not fp32");
+  if (fmt != MX_FMT_MXFP4 && fmt != MX_FMT_INT4)
+    return fail(MX_ERR_FORMAT, "w4_linear takes MXFP4 or INT4 weights, not format %d", (int)fmt);
+  const bool int4 = fmt == MX_FMT_INT4;
+  if (group != 32 && !(int4 && (group == 64 || group == 128)))
+    return fail(MX_ERR_SHAPE, "group %d: %s", group, int4 ? "32, 64 or 128 columns" : "MXFP4 has 32 columns");
+  if (!int4 && zeros != nullptr) return fail(MX_ERR_VALUE, "zeros must be NULL for MXFP4");
+  if (M < 0 || M > (1 << 20)) return fail(MX_ERR_SHAPE, "M %lld not in [0, 2^20]", (long long)M);
+  if (K < group || K % group != 0 || K > (1 << 20))
+    return fail(MX_ERR_SHAPE, "K %lld must be a multiple of the group's %d columns up to 2^20", (long long)K, group);
+  if (N < 1 || N > (1 << 20)) return fail(MX_ERR_SHAPE, "N %lld not in [1, 2^20]", (long long)N);
+  if (ldx < K || ldx % 8 != 0 || ldx > ((int64_t)1 << 30))
+    return fail(MX_ERR_SHAPE, "ldx %lld must be a multiple of 8 of at least K", (long long)ldx);
+  if (ldy < N || ldy > ((int64_t)1 << 30)) return fail(MX_ERR_SHAPE, "ldy %lld not in [N, 2^30]", (long long)ldy);
+  if (M == 0) return ok();
+  MX_REQUIRE_PTR(x);
+  MX_REQUIRE_PTR(w);
+  MX_REQUIRE_PTR(scales);
+  MX_REQUIRE_PTR(y);
+  MX_REQUIRE_ALIGN(x, 16);
+  MX_REQUIRE_ALIGN(w, 16);
+  MX_REQUIRE_ALIGN(scales, int4 ? 2 : 1);
+  MX_REQUIRE_ALIGN(y, 2);
+  const size_t need = mx_w4_linear_workspace_size(M, K, N);
+  if (need > 0) {
+    MX_REQUIRE_PTR(workspace);
+    MX_REQUIRE_ALIGN(workspace, 256);
+  }
+  if (ws_bytes < need) return fail(MX_ERR_WORKSPACE, "workspace %zu bytes < required %zu", ws_bytes, need);
+  const int64_t groups = N * (K / group);
+  const Span sw{"w", w, N * K / 2}, ss{"scales", scales, groups * (int4 ? 2 : 1)}, sz{"zeros", zeros, groups},
+      sx{"x", x, ((M - 1) * ldx + K) * 2}, sy{"y", y, ((M - 1) * ldy + N) * 2}, wk{"workspace", workspace, (int64_t)need};
+  MX_TRY(check_apart(wk, {sw, ss, sz, sx, sy}));
+  MX_TRY(check_apart(sy, {sw, ss, sz}));
+  MX_TRY(check_columns(sx, ldx, K, sy, ldy, N));
+  W4Args a;
+  a.dt = (DType)dt;
+  a.int4 = int4;
+  a.x = x; a.ldx = ldx; a.M = M; a.K = K; a.N = N;
+  a.w = w; a.scales = scales; a.zeros = zeros;
+  a.group_log2 = group == 32 ? 5 : group == 64 ? 6 : 7;
+  a.y = y; a.ldy = ldy;
+  MX_HIP(phase("w4_linear", s, [&] { return launch_w4(a, s); }), "w4_linear");
+  return ok();
+}
+
+// ---------------------------------------------------------------- quantised cache
+namespace {
+
+mx_status check_cache(mx_format fmt, mx_dtype dt, int64_t pages, int64_t page_size, int64_t width) {
+  if (fmt != MX_FMT_MXFP8 && fmt != MX_FMT_MXFP4)
+    return fail(MX_ERR_FORMAT, "the cache holds MXFP8 or MXFP4, not format %d", (int)fmt);
+  MX_TRY(check_dtype(dt));
+  if (width < 32 || width % 32 != 0 || width > (1 << 16))
+    return fail(MX_ERR_SHAPE, "width %lld must be a multiple of 32 in [32, 2^16]", (long long)width);
+  const int64_t most = ((int64_t)1 << 31) - 1;
+  if (pages < 0 || page_size < 1 || page_size > most || pages > most / page_size)
+    return fail(MX_ERR_SHAPE, "%lld pages of %lld rows: not at least one row a page and below 2^31 rows",
+                (long long)pages, (long long)page_size);
+  return MX_OK;
+}
+
+}  // namespace
+
+mx_status mx_cache_write(mx_format fmt, mx_dtype dt, const void* x, int64_t ldx, int64_t T, int64_t width,
+                         const int32_t* slots, int64_t pages, int64_t page_size, uint8_t* codes, uint8_t* scales,
+                         void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_cache(fmt, dt, pages, page_size, width));
+  if (T < 0 || T > ((int64_t)1 << 31) - 1 || T >= ((int64_t)1 << 34) / width)
+    return fail(MX_ERR_SHAPE, "T %lld x width %lld not below 2^34, or T not in [0, 2^31)", (long long)T, (long long)width);
+  if (ldx < width || ldx % 8 != 0 || ldx > ((int64_t)1 << 30))
+    return fail(MX_ERR_SHAPE, "ldx %lld must be a multiple of 8 of at least the width", (long long)ldx);
+  if (T == 0 || pages == 0) return ok();
+  const int es = dt_bytes((DType)dt);
+  const bool fp8 = fmt == MX_FMT_MXFP8;
+  MX_REQUIRE_PTR(x);
+  MX_REQUIRE_PTR(slots);
+  MX_REQUIRE_PTR(codes);
+  MX_REQUIRE_PTR(scales);
+  MX_REQUIRE_ALIGN(x, 16);
+  MX_REQUIRE_ALIGN(slots, 4);
+  MX_REQUIRE_ALIGN(codes, 16);
+  const int64_t n = pages * page_size;
+  const Span sx{"x", x, ((T - 1) * ldx + width) * es}, sl{"slots", slots, T * 4},
+      sc{"codes", codes, n * (fp8 ? width : width / 2)}, ss{"scales", scales, n * (width / 32)};
+  MX_TRY(check_apart(sc, {sx, sl, ss}));
+  MX_TRY(check_apart(ss, {sx, sl}));
+  MX_HIP(phase("cache_write", s,
+               [&] { return launch_cache_write(x, (DType)dt, ldx, T, width, fp8, slots, n, codes, scales, s); }),
+         "cache_write");
+  return ok();
+}
+
+mx_status mx_cache_read(mx_format fmt, const uint8_t* codes, const uint8_t* scales, int64_t pages, int64_t page_size,
+                        int64_t width, const int32_t* page_table, int64_t table_width, const int32_t* seq_off, int64_t B,
+                        int64_t rows, mx_dtype dt, void* out, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  MX_TRY(check_cache(fmt, dt, pages, page_size, width));
+  if (rows < 0 || rows > ((int64_t)1 << 31) - 1) return fail(MX_ERR_SHAPE, "rows %lld not in [0, 2^31)", (long long)rows);
+  if (B < 0 || table_width < 0 || B > ((int64_t)1 << 31) - 1 || (B > 0 && table_width >= ((int64_t)1 << 40) / B))
+    return fail(MX_ERR_SHAPE, "page table of %lld x %lld", (long long)B, (long long)table_width);
+  if (rows == 0 || B == 0) return ok();
+  const int es = dt_bytes((DType)dt);
+  const bool fp8 = fmt == MX_FMT_MXFP8;
+  if (pages > 0) {
+    MX_REQUIRE_PTR(codes);
+    MX_REQUIRE_PTR(scales);
+  }
+  if (table_width > 0) MX_REQUIRE_PTR(page_table);
+  MX_REQUIRE_PTR(seq_off);
+  MX_REQUIRE_PTR(out);
+  MX_REQUIRE_ALIGN(codes, 16);
+  MX_REQUIRE_ALIGN(page_table, 4);
+  MX_REQUIRE_ALIGN(seq_off, 4);
+  MX_REQUIRE_ALIGN(out, 16);
+  const int64_t n = pages * page_size;
+  MX_TRY(check_apart({"out", out, rows * width * es}, {{"codes", codes, n * (fp8 ? width : width / 2)},
+                                                       {"scales", scales, n * (width / 32)},
+                                                       {"page_table", page_table, B * table_width * 4},
+                                                       {"seq_off", seq_off, (B + 1) * 4}}));
+  MX_HIP(phase("cache_read", s,
+               [&] {
+                 return launch_cache_read(codes, scales, pages, page_size, width, fp8, page_table, table_width, seq_off,
+                                          B, rows, out, (DType)dt, s);
+               }),
+         "cache_read");
   return ok();
 }
 

@@ -327,6 +327,44 @@ int lora_parts(int64_t M, int n);
 constexpr int64_t LORA_MAX_MK = (int64_t)1 << 38;
 hipError_t launch_lora(const LoraArgs& p, hipStream_t s);
 
+// ---- The router (router.hip) -------------------------------------------------------
+constexpr int MAX_TOPK = 64;
+hipError_t launch_gate(const void* logits, DType dt, int64_t T, int E, bool sigmoid, const float* bias, int k,
+                       bool renorm, float scale, int32_t* ids, float* w, hipStream_t s);
+// Parts that a sequence's tokens are summed in; `part` holds S * parts * E floats and as
+// many ints (not used with one part).
+int balance_splits(int64_t T, int64_t S);
+hipError_t launch_balance(const void* logits, DType dt, int64_t T, int E, bool sigmoid, const int32_t* ids, int k,
+                          const int32_t* seq_off, int64_t S, float coef, float* part, float* loss, int32_t* counts,
+                          hipStream_t s);
+// d_w, or counts with d_loss, may be null.
+hipError_t launch_gate_grad(const void* logits, DType dt, int64_t T, int E, bool sigmoid, const int32_t* ids, int k,
+                            bool renorm, float scale, const float* d_w, const int32_t* counts, const int32_t* seq_off,
+                            int64_t S, float coef, const float* d_loss, void* d_logits, hipStream_t s);
+
+// ---- 4-bit weights with group scales (w4.hip) ----------------------------------------
+struct W4Args {
+  DType dt;                     // DT_BF16 or DT_F16
+  bool int4;                    // else MXFP4
+  const void* x;                // [M, K], rows ldx elements apart
+  int64_t ldx, M, K, N;
+  const uint8_t* w;             // [N, K/2]
+  const void* scales;           // [N, K >> group_log2]: E8M0 bytes, or elements of dt
+  const uint8_t* zeros;         // INT4: [N, K >> group_log2] or null (8)
+  int group_log2;               // 5, 6 or 7
+  void* y;                      // [M, N], rows ldy elements apart
+  int64_t ldy;
+};
+hipError_t launch_w4(const W4Args& a, hipStream_t s);
+
+// ---- Quantised cache (cache.hip) ------------------------------------------------------
+// fp8: MXFP8, else MXFP4. width % 32 == 0, T * width / 8 below 2^32.
+hipError_t launch_cache_write(const void* x, DType dt, int64_t ldx, int64_t T, int64_t width, bool fp8,
+                              const int32_t* slots, int64_t n_slots, uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_cache_read(const uint8_t* codes, const uint8_t* scales, int64_t pages, int64_t page_size,
+                             int64_t width, bool fp8, const int32_t* page_table, int64_t table_width,
+                             const int32_t* seq_off, int64_t B, int64_t rows, void* out, DType dt, hipStream_t s);
+
 // Measurement probes (probe.hip). mode 0: reads into registers, 1: into LDS;
 // loads_per_wave 8 or 32; bytes a multiple of loads_per_wave KiB; out holds
 // workgroups * 4 words. operands: 512 x 16 words; out: workgroups * 512 floats.
