@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmxfp4.so")
 SOURCES = ["mx_api.hip", "gemm.hip", "gemm_nv.hip", "decode.hip", "elementwise.hip", "route.hip", "pack.hip", "fp8_linear.hip",
-           "moe_rows.hip", "block_norm.hip", "lora.hip", "router.hip", "w4.hip",
+           "moe_rows.hip", "block_norm.hip", "lora.hip", "router.hip", "w4.hip", "w4_gemm.hip",
            "cache.hip", "probe.hip"]
 
 HIPCC_FLAGS = [

@@ -1947,8 +1947,12 @@ mx_status mx_moe_gate_grad(mx_dtype dt, const void* logits, int64_t T, int32_t E
 
 // ---------------------------------------------------------------- 4-bit weights with group scales
 size_t mx_w4_linear_workspace_size(int64_t M, int64_t K, int64_t N) {
-  if (M < 0 || M > (1 << 20) || K < 32 || K > (1 << 20) || N < 1 || N > (1 << 20)) return 0;
-  return 0;
+  if (M < 0 || M > (1 << 20) || K < 32 || K > (1 << 20) || N < 1 || N > (1 << 20) || M <= W4_FEW) return 0;
+  Carve c(nullptr);
+  c.take((size_t)(K / 32 * N) * 4);
+  c.take((size_t)(K / 32 * N) * 4);
+  c.take(W4_TABLE_GRID * 4);
+  return c.off;
 }
 
 mx_status mx_w4_linear(mx_dtype dt, const void* x, int64_t ldx, int64_t M, int64_t K, mx_format fmt, const uint8_t* w,
@@ -1998,6 +2002,10 @@ mx_status mx_w4_linear(mx_dtype dt, const void* x, int64_t ldx, int64_t M, int64
   a.w = w; a.scales = scales; a.zeros = zeros;
   a.group_log2 = group == 32 ? 5 : group == 64 ? 6 : 7;
   a.y = y; a.ldy = ldy;
+  Carve c(need > 0 ? workspace : nullptr);
+  a.scale_table = (float*)c.take((size_t)(K / 32 * N) * 4);
+  a.zero_table = (uint32_t*)c.take((size_t)(K / 32 * N) * 4);
+  a.large = (int*)c.take(W4_TABLE_GRID * 4);
   MX_HIP(phase("w4_linear", s, [&] { return launch_w4(a, s); }), "w4_linear");
   return ok();
 }

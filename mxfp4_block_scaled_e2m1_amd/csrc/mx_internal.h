@@ -354,8 +354,16 @@ struct W4Args {
   int group_log2;               // 5, 6 or 7
   void* y;                      // [M, N], rows ldy elements apart
   int64_t ldy;
+  // many tokens: [K / 32][N] each, and one flag per workgroup that makes them
+  float* scale_table;
+  uint32_t* zero_table;
+  int* large;
 };
+constexpr int W4_TABLE_GRID = 512;
+// More tokens go through the tiled product.
+constexpr int64_t W4_FEW = 64;
 hipError_t launch_w4(const W4Args& a, hipStream_t s);
+hipError_t launch_w4_gemm(const W4Args& a, hipStream_t s);
 
 // ---- Quantised cache (cache.hip) ------------------------------------------------------
 // fp8: MXFP8, else MXFP4. width % 32 == 0, T * width / 8 below 2^32.

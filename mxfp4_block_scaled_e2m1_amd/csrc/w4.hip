@@ -10,14 +10,11 @@
 // 32 activations, which one more MFMA with ones gives in the lanes that need it.
 #include <algorithm>
 
-#include "rows.h"
+#include "w4_expand.h"
 
 namespace mx {
 
 namespace {
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 template <int DT>
 __device__ __forceinline__ f32x4 mfma(u32v4 a, u32v4 b, f32x4 c) {
@@ -31,19 +28,6 @@ __device__ __forceinline__ f32x4 mfma(u32v4 a, u32v4 b, f32x4 c) {
 template <int DT>
 constexpr uint32_t ONES = DT == DT_BF16 ? 0x3F803F80u : 0x3C003C00u;
 
-// Two FP8 bytes (E4M3, half H of w) times 2^9 as 16-bit values: the bytes 0 .. 15 are
-// the subnormals and the first binade, code * 2^-9, so this is the code itself.
-template <int DT, bool H>
-__device__ __forceinline__ uint32_t int_pair(uint32_t w) {
-  if constexpr (DT == DT_BF16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 512.0f, H));
-  else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 512.0f, H));
-}
-template <int DT, int SEL>
-__device__ __forceinline__ uint32_t fp4_pair(uint32_t w) {
-  if constexpr (DT == DT_BF16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, SEL));
-  else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, SEL));
-}
-
 // Eight codes (a dword, the low nibble first) as 16-bit values in their order.
 template <int DT, bool INT>
 __device__ __forceinline__ u32v4 expand(uint32_t d) {
@@ -52,7 +36,7 @@ __device__ __forceinline__ u32v4 expand(uint32_t d) {
     const uint32_t a = __builtin_amdgcn_perm(hi, lo, 0x05010400u), b = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
     return u32v4{int_pair<DT, false>(a), int_pair<DT, true>(a), int_pair<DT, false>(b), int_pair<DT, true>(b)};
   } else {
-    return u32v4{fp4_pair<DT, 0>(d), fp4_pair<DT, 1>(d), fp4_pair<DT, 2>(d), fp4_pair<DT, 3>(d)};
+    return expand_fp4<DT>(d, 1.0f);
   }
 }
 
@@ -64,10 +48,6 @@ __device__ __forceinline__ void transpose4(uint32_t (&d)[4]) {
   auto e = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
   auto f = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
   d[0] = e[0]; d[1] = e[1]; d[2] = f[0]; d[3] = f[1];
-}
-
-__device__ __forceinline__ float e8m0(uint32_t b) {
-  return b == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, (int)b - 127);
 }
 
 // Scale of a row's 32 columns at block `blk` (columns 32 blk ..).
@@ -189,12 +169,15 @@ __global__ __launch_bounds__(64 * W4_WAVES) void k_w4(W4Args a) {
 }  // namespace
 
 hipError_t launch_w4(const W4Args& a, hipStream_t s) {
+  if (a.M > W4_FEW) return launch_w4_gemm(a, s);
   const auto go = [&](auto d, auto in) {
     constexpr int D = decltype(d)::value;
     constexpr bool I = decltype(in)::value;
     const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.M + 63) / 64));
-    if (a.M <= 16) k_w4<D, I, 1, 1><<<dim3(grid.x, 1), 64 * W4_WAVES, 0, s>>>(a);
-    else k_w4<D, I, 1, 4><<<grid, 64 * W4_WAVES, 0, s>>>(a);
+    if (a.M <= 16)
+      k_w4<D, I, 1, 1><<<dim3(grid.x, 1), 64 * W4_WAVES, 0, s>>>(a);
+    else
+      k_w4<D, I, 1, 4><<<grid, 64 * W4_WAVES, 0, s>>>(a);
   };
   if (a.dt == DT_BF16) {
     if (a.int4) go(DtC<DT_BF16>(), std::true_type());
