@@ -16,6 +16,7 @@
 // The scales come as a table [K / 32][N] of fp32 that a small kernel before makes (the
 // rows of scales are neither aligned nor next to each other for a stage).
 #include <algorithm>
+#include <cstdlib>
 
 #include "w4_expand.h"
 
@@ -23,15 +24,22 @@ namespace mx {
 
 namespace {
 
-constexpr int TT = 512;                   // threads
-constexpr int TM = 256, TN = 256;         // tokens, weight rows
 constexpr int TK = 64;                    // columns of a stage
-constexpr int X_BYTES = TM * TK * 2, W_BYTES = TN * TK / 2, S_BYTES = 2 * TN * 4;
-constexpr int SLOT = X_BYTES + W_BYTES + 2 * S_BYTES;   // the second table: zero points
 constexpr int SLOTS = 3;
-// The output tile takes the stages' place: rows of 512 bytes at a pitch that spreads them over the banks.
-constexpr int Y_PITCH = TN * 2 + 8;
-constexpr int SMEM = SLOTS * SLOT > TM * Y_PITCH ? SLOTS * SLOT : TM * Y_PITCH;
+
+// A workgroup's tile: WM x WN waves of 32 I tokens x 32 J weight rows each.
+template <int WM, int WN, int I, int J>
+struct Tile {
+  static constexpr int IB = I, JB = J, WAVES_M = WM, WAVES_N = WN, THREADS = 64 * WM * WN;
+  static constexpr int TM = 32 * I * WM, TN = 32 * J * WN;
+  static constexpr int X_BYTES = TM * TK * 2, W_BYTES = TN * TK / 2, S_BYTES = 2 * TN * 4;
+  static constexpr int SLOT = X_BYTES + W_BYTES + 2 * S_BYTES;   // the second table: zero points
+  // The output tile takes the stages' place, its rows at a pitch that spreads them over the banks.
+  static constexpr int Y_PITCH = TN * 2 + 8;
+  static constexpr int SMEM = SLOTS * SLOT > TM * Y_PITCH ? SLOTS * SLOT : TM * Y_PITCH;
+  static constexpr int X_COPIES = X_BYTES / (16 * THREADS);
+  static_assert(W_BYTES == 16 * THREADS && 2 * TN == THREADS, "one copy of codes and one table entry a thread");
+};
 
 // Copies of 16 or 4 bytes a lane to LDS, lane i's to base + 16 i or 4 i. Inline, so that the compiler does not
 // wait for them before every LDS read: the loop waits for a stage's copies itself.
@@ -56,47 +64,60 @@ __device__ __forceinline__ f32x16 mfma32(u32v4 a, u32v4 b, const f32x16& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// Until no more than N of the wave's copies are under way and its LDS reads are done, then the barrier.
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+  static_assert(N == 0 || (N >= 4 && N <= 7), "a wait for each count");
+  if constexpr (N == 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else if constexpr (N == 4) asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else if constexpr (N == 5) asm volatile("s_waitcnt vmcnt(5) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else if constexpr (N == 6) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // The tile's products. GROUPS: scaled sums per block of 32 columns (1) or per stage (2, groups of
 // 64 or more); 0: scales in the expansion.
-template <int DT, bool INT, int GROUPS>
+template <class T, int DT, bool INT, int GROUPS>
 __device__ __forceinline__ void w4_tile(const W4Args& a, uint8_t* smem, int64_t t0, int64_t n0) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r32 = lane & 31, h = lane >> 5, wn = wave & 3, wm = wave >> 2;
+  constexpr int TM = T::TM, TN = T::TN, IB = T::IB, JB = T::JB, XC = T::X_COPIES;
+  constexpr int X_BYTES = T::X_BYTES, W_BYTES = T::W_BYTES, S_BYTES = T::S_BYTES, SLOT = T::SLOT, Y_PITCH = T::Y_PITCH;
+  const int r32 = lane & 31, h = lane >> 5, wn = wave % T::WAVES_N, wm = wave / T::WAVES_N;
   const int blocks = (int)(a.K / 32), stages = (blocks + 1) / 2;
 
-  // this thread's chunks: 4 of the activations, 1 of the codes, one entry of each table
-  const char* xs[4];
-  int xc[4];
+  // this thread's chunks of the activations and the codes, and its entry of each table
+  const char* xs[XC];
+  int xc[XC];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int p = (wave * 4 + c) * 64 + lane, r = p >> 3;
+  for (int c = 0; c < XC; ++c) {
+    const int p = (wave * XC + c) * 64 + lane, r = p >> 3;
     xc[c] = (p & 7) ^ ((r >> 1) & 7);
     xs[c] = at<DT>(a.x, min(t0 + r, a.M - 1) * a.ldx) + xc[c] * 16;
   }
   const int wr = tid >> 1, wc = (tid & 1) ^ ((wr >> 3) & 1);
   const uint8_t* ws = a.w + min(n0 + wr, a.N - 1) * (a.K / 2) + wc * 16;
-  const int sb = tid >> 8;                            // the block of the stage whose table entry this thread copies
-  const float* ss = a.scale_table + min(n0 + (tid & 255), a.N - 1);
-  const uint32_t* zs = a.zero_table + min(n0 + (tid & 255), a.N - 1);
+  const int sb = tid / TN;                            // the block of the stage whose table entry this thread copies
+  const float* ss = a.scale_table + min(n0 + tid % TN, a.N - 1);
+  const uint32_t* zs = a.zero_table + min(n0 + tid % TN, a.N - 1);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)smem;
-  auto issue = [&](int st) {                           // 6 copies, INT 7
+  auto issue = [&](int st) {                           // XC + 2 copies, INT one more
     const uint32_t base = lds0 + (uint32_t)(st % SLOTS) * SLOT;
     // the last stage may have one block: its second half is the first again, and not used
     const bool whole = 2 * st + 1 < blocks;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      copy16(xs[c] + (int64_t)st * (TK * 2) - (whole || xc[c] < 4 ? 0 : 64), base + (wave * 4 + c) * 1024);
+    for (int c = 0; c < XC; ++c)
+      copy16(xs[c] + (int64_t)st * (TK * 2) - (whole || xc[c] < 4 ? 0 : 64), base + (wave * XC + c) * 1024);
     copy16(ws + (int64_t)st * (TK / 2) - (whole || wc == 0 ? 0 : 16), base + X_BYTES + wave * 1024);
     const int64_t blk = 2 * st + (whole ? sb : 0);
     copy4(ss + blk * a.N, base + X_BYTES + W_BYTES + wave * 256);
     if constexpr (INT) copy4(zs + blk * a.N, base + X_BYTES + W_BYTES + S_BYTES + wave * 256);
   };
 
-  f32x16 acc[4][2];
+  f32x16 acc[IB][JB];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < IB; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < JB; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
@@ -105,22 +126,23 @@ __device__ __forceinline__ void w4_tile(const W4Args& a, uint8_t* smem, int64_t 
   for (int st = 0; st < stages; ++st) {
     // stage st is there (a later one may be on its way), and all waves are done with the stage before
     if (st + 1 < stages) {
-      if constexpr (INT) asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    } else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      wait_barrier<XC + 2 + INT>();
+    } else {
+      wait_barrier<0>();
+    }
     if (st + 2 < stages) issue(st + 2);
     const uint8_t* sx = smem + (st % SLOTS) * SLOT;
     const uint8_t* sw = sx + X_BYTES;
     const float* sc = (const float*)(sw + W_BYTES);
     const bool whole = 2 * st + 1 < blocks;
     // lane (row, h) has columns 16 h .. 16 h + 15 of a block: step 2 b + m takes 8 m .. 8 m + 7 of them
-    u32v4 w[2][4];
-    float scale[2][2];
+    u32v4 w[JB][4];
+    float scale[JB][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < JB; ++j)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int r = wn * 64 + j * 32 + r32;
+        const int r = (wn * JB + j) * 32 + r32;
         const u32v2 d = *(const u32v2*)(sw + w_off(r, b) + 8 * h);
         scale[j][b] = sc[b * TN + r];
         uint32_t zero = 0;
@@ -132,24 +154,24 @@ __device__ __forceinline__ void w4_tile(const W4Args& a, uint8_t* smem, int64_t 
         }
       }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < IB; ++i) {
       u32v4 x[4];
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        x[s] = *(const u32v4*)(sx + x_off(wm * 128 + i * 32 + r32, 4 * (s >> 1) + 2 * h + (s & 1)));
+        x[s] = *(const u32v4*)(sx + x_off((wm * IB + i) * 32 + r32, 4 * (s >> 1) + 2 * h + (s & 1)));
       if constexpr (GROUPS == 0) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           if (s == 2 && !whole) break;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<DT>(x[s], w[j][s], acc[i][j]);
+          for (int j = 0; j < JB; ++j) acc[i][j] = mfma32<DT>(x[s], w[j][s], acc[i][j]);
         }
       } else {
 #pragma unroll
         for (int b = 0; b < 2; b += GROUPS) {
           if (b == 1 && !whole) break;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < JB; ++j) {
             f32x16 p;
 #pragma unroll
             for (int v = 0; v < 16; ++v) p[v] = 0.0f;
@@ -166,20 +188,20 @@ __device__ __forceinline__ void w4_tile(const W4Args& a, uint8_t* smem, int64_t 
   // lane (r32, h) has weight row r32 of a block and tokens 8 (v / 4) + 4 h + v % 4: through LDS, and out in whole rows
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < IB; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < JB; ++j)
 #pragma unroll
       for (int v = 0; v < 16; v += 2) {
         const uint32_t d = pack2<DT>(acc[i][j][v], acc[i][j][v + 1]);
-        const int t = wm * 128 + i * 32 + 8 * (v / 4) + 4 * h + v % 4;
-        uint8_t* p = smem + t * Y_PITCH + (wn * 64 + j * 32 + r32) * 2;
+        const int t = (wm * IB + i) * 32 + 8 * (v / 4) + 4 * h + v % 4;
+        uint8_t* p = smem + t * Y_PITCH + ((wn * JB + j) * 32 + r32) * 2;
         *(uint16_t*)p = (uint16_t)d;
         *(uint16_t*)(p + Y_PITCH) = (uint16_t)(d >> 16);
       }
   __syncthreads();
   const bool al = a.ldy % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
-  for (int p = tid; p < TM * (TN / 8); p += TT) {
+  for (int p = tid; p < TM * (TN / 8); p += T::THREADS) {
     const int r = p / (TN / 8), c = p % (TN / 8) * 8;
     const int64_t t = t0 + r, n = n0 + c;
     if (t >= a.M || n >= a.N) continue;
@@ -237,43 +259,51 @@ __global__ __launch_bounds__(256) void k_w4_tables(W4Args a) {
   }
 }
 
-template <int DT, bool INT>
-__global__ __launch_bounds__(TT, 1) void k_w4_gemm(W4Args a, int tiles_m, int tiles_n, int per_xcd) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[SMEM];
+template <class T, int DT, bool INT>
+__global__ __launch_bounds__(T::THREADS, 2) void k_w4_gemm(W4Args a, int tiles_m, int tiles_n, int per_xcd) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::SMEM];
   // consecutive workgroups are on different XCDs: each XCD takes a run of tiles, four token tiles by all of the rows'
   const int L = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
   if (L >= tiles_m * tiles_n) return;
   const int band = L / (4 * tiles_n), m0 = band * 4, high = min(4, tiles_m - m0), i = L - band * 4 * tiles_n;
-  const int64_t t0 = (int64_t)(m0 + i % high) * TM, n0 = (int64_t)(i / high) * TN;
+  const int64_t t0 = (int64_t)(m0 + i % high) * T::TM, n0 = (int64_t)(i / high) * T::TN;
   if constexpr (INT) {
-    if (a.group_log2 == 5) w4_tile<DT, true, 1>(a, smem, t0, n0);
-    else w4_tile<DT, true, 2>(a, smem, t0, n0);
+    if (a.group_log2 == 5) w4_tile<T, DT, true, 1>(a, smem, t0, n0);
+    else w4_tile<T, DT, true, 2>(a, smem, t0, n0);
   } else if constexpr (DT == DT_BF16) {
-    const bool large = __syncthreads_or(threadIdx.x < W4_TABLE_GRID ? a.large[threadIdx.x] : 0);
-    if (large) w4_tile<DT, false, 1>(a, smem, t0, n0);
-    else w4_tile<DT, false, 0>(a, smem, t0, n0);
+    int seen = 0;
+    for (int i = threadIdx.x; i < W4_TABLE_GRID; i += T::THREADS) seen |= a.large[i];
+    const bool large = __syncthreads_or(seen);
+    if (large) w4_tile<T, DT, false, 1>(a, smem, t0, n0);
+    else w4_tile<T, DT, false, 0>(a, smem, t0, n0);
   } else {
-    w4_tile<DT, false, 1>(a, smem, t0, n0);
+    w4_tile<T, DT, false, 1>(a, smem, t0, n0);
   }
 }
 
 }  // namespace
 
 hipError_t launch_w4_gemm(const W4Args& a, hipStream_t s) {
-  const int tm = (int)((a.M + TM - 1) / TM), tn = (int)((a.N + TN - 1) / TN), per_xcd = (tm * tn + 7) / 8;
-  const auto go = [&](auto d, auto in) {
+  const auto go = [&](auto tile, auto d, auto in) {
+    typedef decltype(tile) T;
     constexpr int D = decltype(d)::value;
     constexpr bool I = decltype(in)::value;
+    const int tm = (int)((a.M + T::TM - 1) / T::TM), tn = (int)((a.N + T::TN - 1) / T::TN), per_xcd = (tm * tn + 7) / 8;
     k_w4_tables<D, I><<<W4_TABLE_GRID, 256, 0, s>>>(a);
-    k_w4_gemm<D, I><<<8 * per_xcd, TT, 0, s>>>(a, tm, tn, per_xcd);
+    k_w4_gemm<T, D, I><<<8 * per_xcd, T::THREADS, 0, s>>>(a, tm, tn, per_xcd);
   };
-  if (a.dt == DT_BF16) {
-    if (a.int4) go(DtC<DT_BF16>(), std::true_type());
-    else go(DtC<DT_BF16>(), std::false_type());
-  } else {
-    if (a.int4) go(DtC<DT_F16>(), std::true_type());
-    else go(DtC<DT_F16>(), std::false_type());
-  }
+  const auto types = [&](auto tile) {
+    if (a.dt == DT_BF16) {
+      if (a.int4) go(tile, DtC<DT_BF16>(), std::true_type());
+      else go(tile, DtC<DT_BF16>(), std::false_type());
+    } else {
+      if (a.int4) go(tile, DtC<DT_F16>(), std::true_type());
+      else go(tile, DtC<DT_F16>(), std::false_type());
+    }
+  };
+  static const bool small = getenv("W4SMALL") != nullptr;
+  if (small) types(Tile<2, 2, 2, 2>());
+  else types(Tile<2, 4, 4, 2>());
   return hipGetLastError();
 }
 
