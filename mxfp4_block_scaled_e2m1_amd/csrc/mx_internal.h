@@ -354,6 +354,7 @@ struct W4Args {
   int group_log2;               // 5, 6 or 7
   void* y;                      // [M, N], rows ldy elements apart
   int64_t ldy;
+  bool whole_dwords;            // few tokens: rows of scales and zero points are aligned dwords (set by launch_w4)
   // many tokens: [K / 32][N] each, and one flag per workgroup that makes them
   float* scale_table;
   uint32_t* zero_table;
@@ -361,7 +362,7 @@ struct W4Args {
 };
 constexpr int W4_TABLE_GRID = 512;
 // More tokens go through the tiled product.
-constexpr int64_t W4_FEW = 64;
+constexpr int64_t W4_FEW = 16;
 hipError_t launch_w4(const W4Args& a, hipStream_t s);
 hipError_t launch_w4_gemm(const W4Args& a, hipStream_t s);
 

@@ -3,20 +3,22 @@
 // MXFP4: E2M1 codes, one E8M0 byte per 32 columns, no zero. INT4: codes 0 .. 15, a scale
 // of the activations' type and a zero point (8 without) per 32, 64 or 128 columns.
 //
-// Here for few tokens (w4_gemm.hip has many): a pass over the weights, which HBM bounds.
-// The codes less their zero points become 16-bit values exactly and enter
-// V_MFMA_F32_16X16X32 as they are; the scale multiplies the fp32 sum of its group. So no
-// weight is rounded, and every scale that fp32 holds does its work (an MXFP4 scale is far
-// outside fp16, and scale * code of INT4 needs 15 bits where bf16 has 8).
+// Here for up to 16 tokens (w4_gemm.hip has more): a pass over the weights, which HBM
+// bounds. The codes become 16-bit values exactly and enter V_MFMA_F32_16X16X32 as they
+// are; the scale multiplies the fp32 sum of its group, of which an INT4 zero point has
+// taken its part of the sum of the activations (one more MFMA, with ones). So no weight is
+// rounded, and every scale that fp32 holds does its work (an MXFP4 scale is far outside
+// fp16, and scale * code of INT4 needs 15 bits where bf16 has 8). An MXFP4 byte of up to
+// 252 times a code is a bf16 number, and goes into the expansion.
 //
-// A workgroup has 16 NT weight rows and 16 MT tokens; its waves share K in steps of 128
-// columns and add up through LDS at the end. Rows come in by copies straight to LDS
-// (GLOBAL_LOAD_LDS), each of 16 rows x 64 bytes, four neighbouring lanes a row's 64: a
-// step's codes of 16 rows, or the activations of 16 tokens in a block of 32 columns. (A
-// load in the matrix operand's own layout has neighbouring lanes in different rows, and
-// the address path takes it apart lane by lane: 64 tokens of 7168 -> 7168 took 42 to 89
-// us.) Every wave has copies of its own under way, DW steps of codes and RX blocks of
-// activations ahead, and waits for nobody else's.
+// A workgroup has 16 NT weight rows; W waves share K in steps of 128 columns and add up
+// through LDS at the end. Rows come in by copies straight to LDS (GLOBAL_LOAD_LDS), each
+// of 16 rows x 64 bytes, four neighbouring lanes a row's 64: a step's codes of 16 rows, or
+// activations. (A load in the matrix operand's own layout has neighbouring lanes in
+// different rows, and the address path takes it apart lane by lane: one token of 7168 ->
+// 7168 took 19 us, 16 took 34.) Every wave has copies of its own under way, DW steps of
+// codes and RX pieces of activations ahead, and waits for nobody else's. One wave more
+// brings the scales, whose rows lie at any alignment, through its registers.
 #include <algorithm>
 
 #include "w4_expand.h"
@@ -44,45 +46,35 @@ __device__ __forceinline__ void transpose4(uint32_t (&d)[4]) {
   d[0] = e[0]; d[1] = e[1]; d[2] = f[0]; d[3] = f[1];
 }
 
+template <int DT>
+constexpr uint32_t ONES = DT == DT_BF16 ? 0x3F803F80u : 0x3C003C00u;
+
 // Words at any address.
 typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef uint16_t u16_any __attribute__((aligned(1)));
 
-// The scales (and zero points) of a row's step of 128 columns. GL: log2 of a group's columns.
+// The scales (and zero points) of a row are streams of dwords, of which a step of 128 columns has SB (ZB) bytes. GL: log2
+// of a group's columns.
 template <int DT, bool INT, int GL>
 struct Scales {
-  static constexpr int N = 128 >> GL;
-  static constexpr int SW = INT && N == 4 ? 2 : 1, WORDS = INT ? SW + 1 : 1;   // as they lie in memory, then the zero points
-  uint32_t w[WORDS];
-  // row: the row's scales; zeros: its zero points, or null; step: which 128 columns
-  __device__ __forceinline__ void load(const uint8_t* row, const uint8_t* zeros, int64_t step) {
-    if constexpr (!INT) {
-      w[0] = *(const u32_any*)(row + 4 * step);
-    } else {
-      const uint8_t* p = row + 2 * N * step;
-      if constexpr (N == 1) w[0] = *(const uint16_t*)p;
-      else w[0] = *(const u32_any*)p;
-      if constexpr (N == 4) w[1] = *(const u32_any*)(p + 4);
-      w[SW] = 0x08080808u;
-      if (zeros != nullptr) {
-        if constexpr (N == 1) w[SW] = zeros[step];
-        else if constexpr (N == 2) w[SW] = *(const u16_any*)(zeros + 2 * step);
-        else w[SW] = *(const u32_any*)(zeros + 4 * step);
-      }
-    }
-  }
+  static constexpr int SB = INT ? 256 >> GL : 4, ZB = INT ? 128 >> GL : 0;
+  uint32_t w[SB == 8 ? 2 : 1], z;
   __device__ __forceinline__ float scale(int g) const {
     if constexpr (!INT) return e8m0((w[0] >> (8 * g)) & 0xFFu);
     else return g % 2 ? hi_f32<DT>(w[g / 2]) : lo_f32<DT>(w[g / 2]);
   }
-  __device__ __forceinline__ uint32_t zero(int g) const {
-    if constexpr (INT) return zero_bits<DT>((w[SW] >> (8 * g)) & 0xFFu);
-    else return 0;
-  }
+  // MXFP4: the same by its exponent alone, for the conversions
+  __device__ __forceinline__ float power(int g) const { return __uint_as_float(((w[0] >> (8 * g)) & 0xFFu) << 23); }
+  __device__ __forceinline__ float zero(int g) const { return (float)((z >> (8 * g)) & 0xFFu); }
 };
 
-// A copy of 16 bytes a lane to LDS, lane i's to lds + 16 i. Inline, so that the compiler does not wait
-// for it before every LDS read; wait_copies<N>() does until no more than N of the wave's are under way.
+// The dwords of a row's steps in LDS: four neighbouring ones of each of a tile's 16 rows side by side, 256 bytes, for
+// each of the NT tiles. Dword e of row r of tile k.
+template <int NT>
+__device__ __forceinline__ int stream_at(int e, int k, int r) { return ((e >> 2) * NT + k) * 64 + r * 4 + (e & 3); }
+
+// Copies of 16 or 4 bytes a lane to LDS, lane i's to lds + 16 i or 4 i. Inline, so that the compiler does not
+// wait for them before every LDS read; wait_copies<N>() does until no more than N of the wave's are under way.
 __device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
 }
@@ -90,201 +82,243 @@ template <int N>
 __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void copy4(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
+}
+// Barrier that does not wait for copies under way; LDS writes and reads are complete before it.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 // The wave's LDS reads are done: a copy may take their place.
 __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-template <int DT, bool INT>
-__device__ __forceinline__ u32v4 expand(uint32_t d, uint32_t zero) {
-  if constexpr (INT) return expand_int<DT>(d, zero);
-  else return expand_fp4<DT>(d, 1.0f);
-}
-
 constexpr int CHUNK = 64;     // steps whose scales are in LDS together
 
-// LDS of a workgroup: each wave's copies, then the scales; the sums at the end take their place.
-template <int WORDS, int NT, int MT, int W, int DW, int RX>
-constexpr int W4_RING = W * (DW * NT + RX * MT) * 1024;
-template <int WORDS, int NT, int MT, int W, int DW, int RX>
-constexpr int W4_SMEM = W4_RING<WORDS, NT, MT, W, DW, RX> + WORDS * CHUNK * (16 * NT + 1) * 4;
+// LDS of a workgroup: each wave's copies, then the scales and the zero points; the sums at the end take their place.
+template <int NT, int W, int DW, int RX>
+constexpr int W4_RING = W * (DW * NT + RX) * 1024;
+template <int NT>
+constexpr int w4_stream(int bytes) { return CHUNK * bytes * 16 * NT; }
 
-template <int DT, bool INT, int GL, int NT, int MT, int W, int DW, int RX>
+// T: tokens, 4, 8 or 16. A copy of activations is 16 rows of 64 bytes: T tokens in 16 / T blocks of 32 columns, so that
+// of few tokens more of K is under way in the same place.
+template <int DT, bool INT, int GL, int NT, int T, int W, int DW, int RX>
 __global__ __launch_bounds__(64 * W) void k_w4(W4Args a) {
   typedef Scales<DT, INT, GL> Sc;
-  constexpr int RING = W4_RING<Sc::WORDS, NT, MT, W, DW, RX>, SMEM = W4_SMEM<Sc::WORDS, NT, MT, W, DW, RX>;
+  constexpr int RING = W4_RING<NT, W, DW, RX>, SMEM = RING + w4_stream<NT>(Sc::SB) + w4_stream<NT>(Sc::ZB);
   constexpr int G = 128 >> GL, B = 4 / G;        // groups of a step, blocks of 32 columns of a group
-  constexpr int PITCH = 16 * NT + 1;             // of a step's scales
-  static_assert(SMEM >= W * NT * MT * 1024 && SMEM <= 160 * 1024, "LDS");
-  static_assert(RX >= 2 && RX + 4 <= 4 * DW && RX * MT + NT < 64, "the waits for the copies");
+  constexpr int PB = 16 / T, P = 4 / PB;         // blocks of a copy of activations, such copies of a step
+  static_assert(SMEM >= W * NT * 1024 && SMEM <= 160 * 1024, "LDS");
+  static_assert(RX >= 2 && RX + P <= P * DW && RX + NT < 64, "the waits for the copies");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[SMEM];
-  uint32_t* sw = (uint32_t*)(smem + RING);
+  uint32_t* const ssc = (uint32_t*)(smem + RING);
+  uint32_t* const szp = (uint32_t*)(smem + RING + w4_stream<NT>(Sc::SB));
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16 * NT, t0 = (int64_t)blockIdx.y * 16 * MT;
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * NT;
   const int steps = (int)(a.K / 128);
   const int64_t groups = a.K >> GL;
   // what this lane copies: of row lane / 4 the 16 bytes that stand at lane % 4 in LDS. Chunk c of row i stands at c ^
   // (i / 4 % 4), so that 16 rows' reads of one chunk fall in 16 bank groups.
   const int cr = lane >> 2, cc = (lane & 3) ^ ((lane >> 4) & 3);
   const uint8_t* wsrc[NT];
-  const char* xsrc[MT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) wsrc[i] = a.w + min(n0 + 16 * i + cr, a.N - 1) * (a.K / 2) + 16 * cc;
-#pragma unroll
-  for (int j = 0; j < MT; ++j) xsrc[j] = at<DT>(a.x, min(t0 + 16 * j + cr, a.M - 1) * a.ldx) + 16 * cc;
-  uint8_t* ring = smem + wave * (DW * NT + RX * MT) * 1024;
-  const uint32_t lds = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)ring;
+  const char* xsrc = at<DT>(a.x, min((int64_t)(cr % T), a.M - 1) * a.ldx) + cr / T * 64 + 16 * cc;
+  uint8_t* ring = smem + wave * (DW * NT + RX) * 1024;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)smem;
+  const uint32_t lds = lds0 + wave * (DW * NT + RX) * 1024;
   const uint32_t at16 = r * 64 + ((q ^ (r >> 2)) << 4);       // where this lane reads row r's chunk q
-  f32x4 acc[NT][MT];
+  const u32v4 ones = {ONES<DT>, ONES<DT>, ONES<DT>, ONES<DT>};
+  f32x4 acc[NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   for (int c0 = 0; c0 < steps; c0 += CHUNK) {
     const int cn = min(CHUNK, steps - c0);
-    const int mine = wave < cn ? (cn - wave + W - 1) / W : 0;      // steps c0 + wave, c0 + wave + W, ..
-    const int blocks = 4 * mine;
+    const int mine = wave < min(W, cn) ? (cn - wave + W - 1) / W : 0;      // steps c0 + wave, c0 + wave + W, ..
+    const int pieces = P * mine;                                           // copies of activations
     auto copy_w = [&](int i) {
 #pragma unroll
       for (int k = 0; k < NT; ++k)
         copy16(wsrc[k] + (int64_t)(c0 + wave + W * i) * 64, lds + ((i % DW) * NT + k) * 1024);
     };
     auto copy_x = [&](int n) {
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-        copy16(xsrc[j] + ((int64_t)(c0 + wave + W * (n >> 2)) * 256 + (n & 3) * 64),
-               lds + (DW * NT + (n % RX) * MT + j) * 1024);
+      copy16(xsrc + ((int64_t)(c0 + wave + W * (n / P)) * 256 + n % P * (PB * 64)), lds + (DW * NT + n % RX) * 1024);
     };
+    // the scales, as dwords where their rows are whole dwords, else through registers
+    const int es = (cn * Sc::SB + 3) / 4, ez = a.zeros == nullptr ? 0 : (cn * Sc::ZB + 3) / 4;     // dwords of a row
+    if (a.whole_dwords) {
+      const int us = (es + 3) / 4 * NT, uz = (ez + 3) / 4 * NT;
+      for (int u = wave; u < us + uz; u += W) {
+        const bool z = u >= us;
+        const int v = z ? u - us : u, k = v % NT, e = min(v / NT * 4 + (lane & 3), (z ? ez : es) - 1);
+        const int64_t n = min(n0 + 16 * k + (lane >> 2), a.N - 1);
+        const uint8_t* src = z ? a.zeros + n * groups + (int64_t)c0 * Sc::ZB
+                               : (const uint8_t*)a.scales + n * groups * (INT ? 2 : 1) + (int64_t)c0 * Sc::SB;
+        copy4(src + 4 * e, lds0 + RING + (z ? w4_stream<NT>(Sc::SB) : 0) + v * 256);
+      }
+    } else {
+      for (int i = threadIdx.x; i < es * 16 * NT; i += 64 * W) {
+        const int row = i / es, e = i - row * es;
+        const uint8_t* p = (const uint8_t*)a.scales + min(n0 + row, a.N - 1) * groups * (INT ? 2 : 1) + (int64_t)c0 * Sc::SB + 4 * e;
+        ssc[stream_at<NT>(e, row >> 4, row & 15)] = 4 * e + 4 <= cn * Sc::SB ? *(const u32_any*)p : *(const uint16_t*)p;
+      }
+      for (int i = threadIdx.x; i < ez * 16 * NT; i += 64 * W) {
+        const int row = i / ez, e = i - row * ez;
+        const uint8_t* p = a.zeros + min(n0 + row, a.N - 1) * groups + (int64_t)c0 * Sc::ZB + 4 * e;
+        uint32_t v = 0;
+        for (int b = 0; b < min(4, cn * Sc::ZB - 4 * e); ++b) v |= (uint32_t)p[b] << (8 * b);
+        szp[stream_at<NT>(e, row >> 4, row & 15)] = v;
+      }
+    }
     // all codes that the ring takes, then the activations
     for (int i = 0; i < min(DW, mine); ++i) copy_w(i);
-    for (int n = 0; n < min(RX, blocks); ++n) copy_x(n);
-    for (int i = threadIdx.x; i < cn * 16 * NT; i += 64 * W) {
-      const int row = i / cn, s = i - row * cn;
-      const int64_t n = min(n0 + row, a.N - 1);
-      Sc t;
-      t.load((const uint8_t*)a.scales + n * groups * (INT ? 2 : 1), a.zeros == nullptr ? nullptr : a.zeros + n * groups,
-             c0 + s);
-#pragma unroll
-      for (int k = 0; k < Sc::WORDS; ++k) sw[(k * CHUNK + s) * PITCH + row] = t.w[k];
-    }
-    __syncthreads();
+    for (int n = 0; n < min(RX, pieces); ++n) copy_x(n);
+    if (mine >= DW && pieces >= RX) wait_copies<DW * NT + RX>();
+    else wait_copies<0>();
+    lds_barrier();                 // the scales are there
     for (int i = 0; i < mine; ++i) {
       uint32_t d[NT][4];
       Sc sc[NT];
+      const int s = wave + W * i;
+      bool fold = !INT && DT == DT_BF16;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        u32v4 x[B][MT];
+        u32v4 x[B];
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-          const int n = 4 * i + g * B + b;
-          // Copied after block n's activations were those of RX - 1 more blocks (near the end fewer: then all is
-          // waited for), and, if the step before ended at most RX blocks ago and had any to copy, its codes. Step i's
-          // own codes were copied before block 4 i's activations, since RX + 4 <= 4 DW.
-          constexpr int X = (RX - 1) * MT;
-          if (n + RX > blocks) wait_copies<0>();
-          else if (g * B + b < RX && i > 0 && i - 1 + DW < mine) wait_copies<X + NT>();
-          else wait_copies<X>();
-          if (g * B + b == 0) {
+          const int blk = g * B + b, m = blk / PB, n = P * i + m;
+          // Copied after piece n of the activations were RX - 1 more (near the end fewer: then all is waited for), and, if
+          // the step before ended at most RX pieces ago and had any to copy, its codes. Step i's own codes were copied
+          // before piece P i, since RX + P <= P DW.
+          if (blk % PB == 0) {
+            if (n + RX > pieces) wait_copies<0>();
+            else if (m < RX && i > 0 && i - 1 + DW < mine) wait_copies<RX - 1 + NT>();
+            else wait_copies<RX - 1>();
+          }
+          if (blk == 0) {
+            uint32_t big = 0;
 #pragma unroll
             for (int k = 0; k < NT; ++k) {
               const u32v4 v = *(const u32v4*)(ring + ((i % DW) * NT + k) * 1024 + at16);
 #pragma unroll
               for (int e = 0; e < 4; ++e) d[k][e] = v[e];
 #pragma unroll
-              for (int e = 0; e < Sc::WORDS; ++e) sc[k].w[e] = sw[(e * CHUNK + wave + W * i) * PITCH + 16 * k + r];
+              for (int e = 0; e < (Sc::SB + 3) / 4; ++e) {
+                sc[k].w[e] = ssc[stream_at<NT>(Sc::SB == 8 ? 2 * s + e : s * Sc::SB / 4, k, r)];
+                if constexpr (Sc::SB == 2) sc[k].w[e] >>= 16 * (s & 1);
+              }
+              if constexpr (INT) {
+                sc[k].z = 0x08080808u;
+                if (a.zeros != nullptr) sc[k].z = szp[stream_at<NT>(s * Sc::ZB / 4, k, r)] >> (8 * (s * Sc::ZB & 3));
+              }
               transpose4(d[k]);      // block b's codes: columns 8 q .. 8 q + 7 of it in d[k][b]
+              if constexpr (!INT) big |= ((sc[k].w[0] & 0x7F7F7F7Fu) + 0x03030303u) & sc[k].w[0];   // bit 7 of bytes above 252
             }
+            if (__any((big & 0x80808080u) != 0)) fold = false;
+          }
+          const int row = blk % PB * T + r % T;
+          x[b] = *(const u32v4*)(ring + (DW * NT + n % RX) * 1024 + row * 64 + ((q ^ (row >> 2 & 3)) << 4));
+          wait_reads();
+          if (blk % PB == PB - 1 && n + RX < pieces) copy_x(n + RX);
+        }
+        if (fold) {
+#pragma unroll
+          for (int k = 0; k < NT; ++k)
+            acc[k] = mfma<DT>(x[0], expand_fp4<DT>(d[k][g], sc[k].power(g)), acc[k]);
+        } else {
+          f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+          if constexpr (INT) {
+#pragma unroll
+            for (int b = 0; b < B; ++b) sum = mfma<DT>(x[b], ones, sum);
           }
 #pragma unroll
-          for (int j = 0; j < MT; ++j) x[b][j] = *(const u32v4*)(ring + (DW * NT + (n % RX) * MT + j) * 1024 + at16);
-          wait_reads();
-          if (n + RX < blocks) copy_x(n + RX);
-        }
-#pragma unroll
-        for (int k = 0; k < NT; ++k) {
-          const float scale = sc[k].scale(g);
-          const uint32_t zero = sc[k].zero(g);
-          u32v4 wv[B];
-#pragma unroll
-          for (int b = 0; b < B; ++b) wv[b] = expand<DT, INT>(d[k][g * B + b], zero);
-#pragma unroll
-          for (int j = 0; j < MT; ++j) {
+          for (int k = 0; k < NT; ++k) {
             f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int b = 0; b < B; ++b) p = mfma<DT>(x[b][j], wv[b], p);
+            for (int b = 0; b < B; ++b) {
+              if constexpr (INT) p = mfma<DT>(x[b], expand_code<DT>(d[k][g * B + b]), p);
+              else p = mfma<DT>(x[b], expand_fp4<DT>(d[k][g * B + b], 1.0f), p);
+            }
+            const float scale = sc[k].scale(g), zero = sc[k].zero(g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[k][j][e] = fmaf(scale, p[e], acc[k][j][e]);
+            for (int e = 0; e < 4; ++e) acc[k][e] = fmaf(scale, INT ? fmaf(-zero, sum[e], p[e]) : p[e], acc[k][e]);
           }
         }
       }
       if (i + DW < mine) copy_w(i + DW);
     }
-    __syncthreads();               // the scales' place is free
+    lds_barrier();                 // the scales' place is free
   }
-  // up to three blocks behind the last whole step, by the wave that has the fewest steps
+  // up to three blocks behind the last whole step, by the wave that may have a step less
   if (GL < 7 && wave == W - 1) {
     for (int blk = 4 * steps; blk < (int)(a.K / 32); ++blk) {
+      const u32v4 x = *(const u32v4*)(at<DT>(a.x, min((int64_t)r, a.M - 1) * a.ldx + 8 * q) + (int64_t)blk * 64);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int64_t n = min(n0 + 16 * i + r, a.N - 1);
+      for (int k = 0; k < NT; ++k) {
+        const int64_t n = min(n0 + 16 * k + r, a.N - 1);
         const int g = blk >> (GL - 5);
+        const uint32_t d = *(const uint32_t*)(a.w + n * (a.K / 2) + (int64_t)blk * 16 + 4 * q);
+        f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
         float scale;
-        uint32_t zero = 0;
         if constexpr (INT) {
+          const float zero = a.zeros != nullptr ? (float)a.zeros[n * groups + g] : 8.0f;
+          const f32x4 sum = mfma<DT>(x, ones, p);
           scale = Raw<DT, 1>{{((const uint16_t*)a.scales)[n * groups + g]}}.get(0);
-          zero = zero_bits<DT>(a.zeros != nullptr ? a.zeros[n * groups + g] : 8u);
+          p = mfma<DT>(x, expand_code<DT>(d), p);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = fmaf(-zero, sum[e], p[e]);
         } else {
           scale = e8m0(((const uint8_t*)a.scales)[n * groups + g]);
+          p = mfma<DT>(x, expand_fp4<DT>(d, 1.0f), p);
         }
-        const u32v4 wv = expand<DT, INT>(*(const uint32_t*)(a.w + n * (a.K / 2) + (int64_t)blk * 16 + 4 * q), zero);
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          const f32x4 p = mfma<DT>(*(const u32v4*)(at<DT>(a.x, min(t0 + 16 * j + r, a.M - 1) * a.ldx + 8 * q) + (int64_t)blk * 64), wv, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(scale, p[e], acc[i][j][e]);
-        }
+        for (int e = 0; e < 4; ++e) acc[k][e] = fmaf(scale, p[e], acc[k][e]);
       }
     }
   }
 
   // lane (r, q) has tokens 4 q + e of weight row r
-  float(*part)[NT * MT][4][64] = (float(*)[NT * MT][4][64])smem;
+  float(*part)[NT][4][64] = (float(*)[NT][4][64])smem;
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int k = 0; k < NT; ++k)
 #pragma unroll
-    for (int j = 0; j < MT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) part[wave][i * MT + j][e][lane] = acc[i][j][e];
+    for (int e = 0; e < 4; ++e) part[wave][k][e][lane] = acc[k][e];
   __syncthreads();
-  const int rows = (int)min(a.M - t0, (int64_t)16 * MT);
-  for (int o = threadIdx.x; o < rows * 16 * NT; o += 64 * W) {
+  for (int o = threadIdx.x; o < (int)a.M * 16 * NT; o += 64 * W) {
     const int t = o / (16 * NT), n = o % (16 * NT);
     if (n0 + n >= a.N) continue;
-    const float* p = &part[0][n / 16 * MT + t / 16][t % 4][t % 16 / 4 * 16 + n % 16];
+    const float* p = &part[0][n / 16][t % 4][t / 4 * 16 + n % 16];
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < W; ++i) sum += p[i * (NT * MT * 4 * 64)];
+    for (int i = 0; i < W; ++i) sum += p[i * (NT * 4 * 64)];
     Raw<DT, 1> out;
     out.set(&sum);
-    out.store(at<DT>(a.y, (t0 + t) * a.ldy + n0), (uint32_t)n);
+    out.store(at<DT>(a.y, (int64_t)t * a.ldy + n0), (uint32_t)n);
   }
 }
 
 }  // namespace
 
-hipError_t launch_w4(const W4Args& a, hipStream_t s) {
-  if (a.M > W4_FEW) return launch_w4_gemm(a, s);
+hipError_t launch_w4(const W4Args& args, hipStream_t s) {
+  if (args.M > W4_FEW) return launch_w4_gemm(args, s);
+  W4Args a = args;
+  const int64_t groups = a.K >> a.group_log2;
+  a.whole_dwords = ((uintptr_t)a.scales | (uintptr_t)a.zeros) % 4 == 0 && groups * (a.int4 ? 2 : 1) % 4 == 0 &&
+                   (a.zeros == nullptr || groups % 4 == 0);
   const auto go = [&](auto d, auto in, auto gl) {
     constexpr int DT = decltype(d)::value, GL = decltype(gl)::value;
     constexpr bool I = decltype(in)::value;
     const unsigned one = (unsigned)((a.N + 15) / 16), two = (unsigned)((a.N + 31) / 32);
-    if (a.M <= 16) {
-      if (two >= 192) k_w4<DT, I, GL, 2, 1, 8, 3, 6><<<two, 512, 0, s>>>(a);
-      else k_w4<DT, I, GL, 1, 1, 8, 4, 8><<<one, 512, 0, s>>>(a);
-    } else if (a.M <= 32) {
-      k_w4<DT, I, GL, 2, 2, 8, 2, 4><<<two, 512, 0, s>>>(a);
+    const bool wide = two >= 192;      // 32 rows a workgroup leave few compute units without one
+    if (a.M <= 4) {
+      if (wide) k_w4<DT, I, GL, 2, 4, 8, 6, 4><<<two, 512, 0, s>>>(a);
+      else k_w4<DT, I, GL, 1, 4, 16, 4, 3><<<one, 1024, 0, s>>>(a);
+    } else if (a.M <= 8) {
+      if (wide) k_w4<DT, I, GL, 2, 8, 8, 4, 6><<<two, 512, 0, s>>>(a);
+      else k_w4<DT, I, GL, 1, 8, 16, 4, 4><<<one, 1024, 0, s>>>(a);
     } else {
-      k_w4<DT, I, GL, 2, 4, 8, 2, 3><<<two, 512, 0, s>>>(a);
+      if (wide) k_w4<DT, I, GL, 2, 16, 8, 3, 8><<<two, 512, 0, s>>>(a);
+      else k_w4<DT, I, GL, 1, 16, 16, 3, 5><<<one, 1024, 0, s>>>(a);
     }
   };
   const auto types = [&](auto in, auto gl) {

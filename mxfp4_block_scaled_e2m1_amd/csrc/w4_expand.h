@@ -37,6 +37,14 @@ __device__ __forceinline__ uint32_t sign_magnitude(uint32_t q, uint32_t z) {
   return (v ^ ((neg - one) | 0x80808080u)) + one;
 }
 
+// Eight codes 0 .. 15.
+template <int DT>
+__device__ __forceinline__ u32v4 expand_code(uint32_t d) {
+  const uint32_t lo = d & 0x0F0F0F0Fu, hi = (d >> 4) & 0x0F0F0F0Fu;
+  const uint32_t a = __builtin_amdgcn_perm(hi, lo, 0x05010400u), b = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+  return u32v4{int_pair<DT, false>(a), int_pair<DT, true>(a), int_pair<DT, false>(b), int_pair<DT, true>(b)};
+}
+
 // A zero point 0 .. 15 as expand_int takes it: four bytes, or two fp16.
 template <int DT>
 __device__ __forceinline__ uint32_t zero_bits(uint32_t z) {

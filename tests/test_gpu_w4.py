@@ -127,6 +127,24 @@ def test_scales_of_the_whole_range(mx, M):
         assert (np.isinf(y[far]) & (np.sign(y[far]) == np.sign(ref[far]))).all()
 
 
+@pytest.mark.parametrize("M", [1, 6, 14, 30, 64, 300])
+@pytest.mark.parametrize("size", [-60, 40, 120])
+def test_scales_that_are_bf16_numbers(mx, M, size):
+    """Bytes of up to 252, whose products with codes bf16 holds, and no other: from subnormal weights with large
+    activations to the largest."""
+    K, N = 256, 253
+    rng = np.random.default_rng(2)
+    w = rng.integers(0, 256, size=(N, K // 2)).astype(np.uint8)
+    s = np.tile(np.arange(N)[:, None], (1, K // 32)).astype(np.uint8)
+    x, xr = pair(2.0 ** size * rng.standard_normal((M, K)), "bf16")
+    v, m = o.w4_weights(w, s)
+    y = f64(mx.w4_linear(x, torch.from_numpy(w).cuda(), torch.from_numpy(s).cuda()))
+    ref, most = xr @ v.T, np.abs(xr) @ m.T
+    inside = most < torch.finfo(torch.float32).max / 2
+    tol = 2 * U * 80 * most + half_step("bf16") * np.abs(ref) * 1.01 + 2.0 ** -132
+    assert inside.sum() > 100 * M and (np.abs(y - ref)[inside] <= tol[inside]).all()
+
+
 @pytest.mark.parametrize("M", [1, 12, 70, 300])
 @pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
 def test_activations_that_are_not_finite(mx, M, bad):
