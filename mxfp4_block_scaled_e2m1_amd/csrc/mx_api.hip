@@ -1948,10 +1948,14 @@ mx_status mx_moe_gate_grad(mx_dtype dt, const void* logits, int64_t T, int32_t E
 // ---------------------------------------------------------------- 4-bit weights with group scales
 size_t mx_w4_linear_workspace_size(int64_t M, int64_t K, int64_t N) {
   if (M < 0 || M > (1 << 20) || K < 32 || K > (1 << 20) || N < 1 || N > (1 << 20) || M <= W4_FEW) return 0;
+  const W4Plan p = w4_plan(M, K, N);
   Carve c(nullptr);
-  c.take((size_t)(K / 32 * N) * 4);
-  c.take((size_t)(K / 32 * N) * 4);
-  c.take(W4_TABLE_GRID * 4);
+  if (p.splits > 1) c.take((size_t)p.splits * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4);
+  if (p.tables) {
+    c.take((size_t)(K / 32 * N) * 4);
+    c.take((size_t)(K / 32 * N) * 4);
+    c.take(W4_TABLE_GRID * 4);
+  }
   return c.off;
 }
 
@@ -2002,10 +2006,22 @@ mx_status mx_w4_linear(mx_dtype dt, const void* x, int64_t ldx, int64_t M, int64
   a.w = w; a.scales = scales; a.zeros = zeros;
   a.group_log2 = group == 32 ? 5 : group == 64 ? 6 : 7;
   a.y = y; a.ldy = ldy;
-  Carve c(need > 0 ? workspace : nullptr);
-  a.scale_table = (float*)c.take((size_t)(K / 32 * N) * 4);
-  a.zero_table = (uint32_t*)c.take((size_t)(K / 32 * N) * 4);
-  a.large = (int*)c.take(W4_TABLE_GRID * 4);
+  const int64_t row = K / group;
+  a.whole_dwords = ((uintptr_t)scales | (uintptr_t)zeros) % 4 == 0 && row * (int4 ? 2 : 1) % 4 == 0 &&
+                   (zeros == nullptr || row % 4 == 0);
+  a.part = a.scale_table = nullptr;
+  a.zero_table = nullptr;
+  a.large = nullptr;
+  if (need > 0) {
+    const W4Plan p = w4_plan(M, K, N);
+    Carve c(workspace);
+    if (p.splits > 1) a.part = (float*)c.take((size_t)p.splits * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4);
+    if (p.tables) {
+      a.scale_table = (float*)c.take((size_t)(K / 32 * N) * 4);
+      a.zero_table = (uint32_t*)c.take((size_t)(K / 32 * N) * 4);
+      a.large = (int*)c.take(W4_TABLE_GRID * 4);
+    }
+  }
   MX_HIP(phase("w4_linear", s, [&] { return launch_w4(a, s); }), "w4_linear");
   return ok();
 }

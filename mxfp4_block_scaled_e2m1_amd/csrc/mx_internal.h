@@ -354,15 +354,23 @@ struct W4Args {
   int group_log2;               // 5, 6 or 7
   void* y;                      // [M, N], rows ldy elements apart
   int64_t ldy;
-  bool whole_dwords;            // few tokens: rows of scales and zero points are aligned dwords (set by launch_w4)
+  bool whole_dwords;            // rows of scales and zero points are aligned dwords
+  // sums of parts of K, [w4_plan().splits][M][N rounded up to 4]
+  float* part;
   // many tokens: [K / 32][N] each, and one flag per workgroup that makes them
   float* scale_table;
   uint32_t* zero_table;
   int* large;
 };
 constexpr int W4_TABLE_GRID = 512;
-// More tokens go through the tiled product.
-constexpr int64_t W4_FEW = 16;
+constexpr int64_t W4_FEW = 16;  // up to so many tokens: w4.hip, else w4_gemm.hip
+// How a product of more tokens is shared out: tiles of `tokens` x 128 rows whose K is cut
+// into `splits` parts, or (tables) whole tiles of 256 x 256 that read the tables.
+struct W4Plan {
+  int tokens, splits;
+  bool tables;
+};
+W4Plan w4_plan(int64_t M, int64_t K, int64_t N);
 hipError_t launch_w4(const W4Args& a, hipStream_t s);
 hipError_t launch_w4_gemm(const W4Args& a, hipStream_t s);
 

@@ -49,10 +49,6 @@ __device__ __forceinline__ void transpose4(uint32_t (&d)[4]) {
 template <int DT>
 constexpr uint32_t ONES = DT == DT_BF16 ? 0x3F803F80u : 0x3C003C00u;
 
-// Words at any address.
-typedef uint32_t u32_any __attribute__((aligned(1)));
-typedef uint16_t u16_any __attribute__((aligned(1)));
-
 // The scales (and zero points) of a row are streams of dwords, of which a step of 128 columns has SB (ZB) bytes. GL: log2
 // of a group's columns.
 template <int DT, bool INT, int GL>
@@ -68,49 +64,25 @@ struct Scales {
   __device__ __forceinline__ float zero(int g) const { return (float)((z >> (8 * g)) & 0xFFu); }
 };
 
-// The dwords of a row's steps in LDS: four neighbouring ones of each of a tile's 16 rows side by side, 256 bytes, for
-// each of the NT tiles. Dword e of row r of tile k.
-template <int NT>
-__device__ __forceinline__ int stream_at(int e, int k, int r) { return ((e >> 2) * NT + k) * 64 + r * 4 + (e & 3); }
-
-// Copies of 16 or 4 bytes a lane to LDS, lane i's to lds + 16 i or 4 i. Inline, so that the compiler does not
-// wait for them before every LDS read; wait_copies<N>() does until no more than N of the wave's are under way.
-__device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
-}
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void copy4(const void* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
-}
-// Barrier that does not wait for copies under way; LDS writes and reads are complete before it.
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-// The wave's LDS reads are done: a copy may take their place.
-__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-
 constexpr int CHUNK = 64;     // steps whose scales are in LDS together
 
 // LDS of a workgroup: each wave's copies, then the scales and the zero points; the sums at the end take their place.
 template <int NT, int W, int DW, int RX>
 constexpr int W4_RING = W * (DW * NT + RX) * 1024;
-template <int NT>
-constexpr int w4_stream(int bytes) { return CHUNK * bytes * 16 * NT; }
-
 // T: tokens, 4, 8 or 16. A copy of activations is 16 rows of 64 bytes: T tokens in 16 / T blocks of 32 columns, so that
 // of few tokens more of K is under way in the same place.
 template <int DT, bool INT, int GL, int NT, int T, int W, int DW, int RX>
 __global__ __launch_bounds__(64 * W) void k_w4(W4Args a) {
   typedef Scales<DT, INT, GL> Sc;
-  constexpr int RING = W4_RING<NT, W, DW, RX>, SMEM = RING + w4_stream<NT>(Sc::SB) + w4_stream<NT>(Sc::ZB);
+  constexpr int RING = W4_RING<NT, W, DW, RX>, ZEROS = RING + stream_bytes(CHUNK * Sc::SB, NT);
+  constexpr int SMEM = ZEROS + stream_bytes(CHUNK * Sc::ZB, NT);
   constexpr int G = 128 >> GL, B = 4 / G;        // groups of a step, blocks of 32 columns of a group
   constexpr int PB = 16 / T, P = 4 / PB;         // blocks of a copy of activations, such copies of a step
   static_assert(SMEM >= W * NT * 1024 && SMEM <= 160 * 1024, "LDS");
   static_assert(RX >= 2 && RX + P <= P * DW && RX + NT < 64, "the waits for the copies");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[SMEM];
   uint32_t* const ssc = (uint32_t*)(smem + RING);
-  uint32_t* const szp = (uint32_t*)(smem + RING + w4_stream<NT>(Sc::SB));
+  uint32_t* const szp = (uint32_t*)(smem + ZEROS);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16 * NT;
@@ -124,7 +96,7 @@ __global__ __launch_bounds__(64 * W) void k_w4(W4Args a) {
   for (int i = 0; i < NT; ++i) wsrc[i] = a.w + min(n0 + 16 * i + cr, a.N - 1) * (a.K / 2) + 16 * cc;
   const char* xsrc = at<DT>(a.x, min((int64_t)(cr % T), a.M - 1) * a.ldx) + cr / T * 64 + 16 * cc;
   uint8_t* ring = smem + wave * (DW * NT + RX) * 1024;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)smem;
+  const uint32_t lds0 = lds_address(smem);
   const uint32_t lds = lds0 + wave * (DW * NT + RX) * 1024;
   const uint32_t at16 = r * 64 + ((q ^ (r >> 2)) << 4);       // where this lane reads row r's chunk q
   const u32v4 ones = {ONES<DT>, ONES<DT>, ONES<DT>, ONES<DT>};
@@ -145,30 +117,14 @@ __global__ __launch_bounds__(64 * W) void k_w4(W4Args a) {
       copy16(xsrc + ((int64_t)(c0 + wave + W * (n / P)) * 256 + n % P * (PB * 64)), lds + (DW * NT + n % RX) * 1024);
     };
     // the scales, as dwords where their rows are whole dwords, else through registers
-    const int es = (cn * Sc::SB + 3) / 4, ez = a.zeros == nullptr ? 0 : (cn * Sc::ZB + 3) / 4;     // dwords of a row
+    const Stream scales = {(const uint8_t*)a.scales, groups * (INT ? 2 : 1), (int64_t)c0 * Sc::SB, cn * Sc::SB};
+    const Stream zeros = {a.zeros, groups, (int64_t)c0 * Sc::ZB, a.zeros == nullptr ? 0 : cn * Sc::ZB};
     if (a.whole_dwords) {
-      const int us = (es + 3) / 4 * NT, uz = (ez + 3) / 4 * NT;
-      for (int u = wave; u < us + uz; u += W) {
-        const bool z = u >= us;
-        const int v = z ? u - us : u, k = v % NT, e = min(v / NT * 4 + (lane & 3), (z ? ez : es) - 1);
-        const int64_t n = min(n0 + 16 * k + (lane >> 2), a.N - 1);
-        const uint8_t* src = z ? a.zeros + n * groups + (int64_t)c0 * Sc::ZB
-                               : (const uint8_t*)a.scales + n * groups * (INT ? 2 : 1) + (int64_t)c0 * Sc::SB;
-        copy4(src + 4 * e, lds0 + RING + (z ? w4_stream<NT>(Sc::SB) : 0) + v * 256);
-      }
+      stream_copies<NT, W>(scales, n0, a.N, lds0 + RING, wave, lane);
+      if (INT) stream_copies<NT, W>(zeros, n0, a.N, lds0 + ZEROS, wave, lane);
     } else {
-      for (int i = threadIdx.x; i < es * 16 * NT; i += 64 * W) {
-        const int row = i / es, e = i - row * es;
-        const uint8_t* p = (const uint8_t*)a.scales + min(n0 + row, a.N - 1) * groups * (INT ? 2 : 1) + (int64_t)c0 * Sc::SB + 4 * e;
-        ssc[stream_at<NT>(e, row >> 4, row & 15)] = 4 * e + 4 <= cn * Sc::SB ? *(const u32_any*)p : *(const uint16_t*)p;
-      }
-      for (int i = threadIdx.x; i < ez * 16 * NT; i += 64 * W) {
-        const int row = i / ez, e = i - row * ez;
-        const uint8_t* p = a.zeros + min(n0 + row, a.N - 1) * groups + (int64_t)c0 * Sc::ZB + 4 * e;
-        uint32_t v = 0;
-        for (int b = 0; b < min(4, cn * Sc::ZB - 4 * e); ++b) v |= (uint32_t)p[b] << (8 * b);
-        szp[stream_at<NT>(e, row >> 4, row & 15)] = v;
-      }
+      stream_loads<NT, 64 * W>(scales, n0, a.N, ssc);
+      if (INT) stream_loads<NT, 64 * W>(zeros, n0, a.N, szp);
     }
     // all codes that the ring takes, then the activations
     for (int i = 0; i < min(DW, mine); ++i) copy_w(i);
@@ -299,12 +255,8 @@ __global__ __launch_bounds__(64 * W) void k_w4(W4Args a) {
 
 }  // namespace
 
-hipError_t launch_w4(const W4Args& args, hipStream_t s) {
-  if (args.M > W4_FEW) return launch_w4_gemm(args, s);
-  W4Args a = args;
-  const int64_t groups = a.K >> a.group_log2;
-  a.whole_dwords = ((uintptr_t)a.scales | (uintptr_t)a.zeros) % 4 == 0 && groups * (a.int4 ? 2 : 1) % 4 == 0 &&
-                   (a.zeros == nullptr || groups % 4 == 0);
+hipError_t launch_w4(const W4Args& a, hipStream_t s) {
+  if (a.M > W4_FEW) return launch_w4_gemm(a, s);
   const auto go = [&](auto d, auto in, auto gl) {
     constexpr int DT = decltype(d)::value, GL = decltype(gl)::value;
     constexpr bool I = decltype(in)::value;

@@ -1,4 +1,5 @@
-// 4-bit codes to 16-bit values, and the operand types of the 16-bit matrix instructions (w4.hip, w4_gemm.hip).
+// Shared by the linear layer's kernels (w4.hip, w4_gemm.hip): 4-bit codes to 16-bit values, copies to LDS, and the rows of
+// scales and zero points in LDS.
 #pragma once
 
 #include "rows.h"
@@ -72,6 +73,66 @@ __device__ __forceinline__ u32v4 expand_int(uint32_t d, uint32_t zero) {
 
 __device__ __forceinline__ float e8m0(uint32_t b) {
   return b == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, (int)b - 127);
+}
+
+// Copies of 16 or 4 bytes a lane to LDS, lane i's to lds + 16 i or 4 i. Inline, so that the compiler does not
+// wait for them before every LDS read; wait_copies<N>() does until no more than N of the wave's are under way.
+__device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void copy4(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// The wave's LDS reads are done: a copy may take their place.
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// Barrier that does not wait for copies under way; LDS writes and reads are complete before it.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
+}
+
+// Words at any address.
+typedef uint32_t u32_any __attribute__((aligned(1)));
+
+// Rows of scales or zero points as streams of dwords, for NT tiles of 16 rows: in LDS four neighbouring dwords of each of a
+// tile's rows stand side by side, 256 bytes. Dword e of row r of tile k:
+template <int NT>
+__device__ __forceinline__ int stream_at(int e, int k, int r) { return ((e >> 2) * NT + k) * 64 + r * 4 + (e & 3); }
+constexpr int stream_bytes(int bytes, int tiles) { return (bytes + 15) / 16 * 256 * tiles; }
+
+struct Stream {
+  const uint8_t* base;      // row n at base + n * row_bytes
+  int64_t row_bytes, off;   // the stream starts at byte `off` of a row, a multiple of four
+  int bytes;                // and has so many
+};
+// By copies, where rows are whole aligned dwords; returns how many the wave issued. Row 0 is row n0 of N.
+template <int NT, int W>
+__device__ __forceinline__ int stream_copies(const Stream& s, int64_t n0, int64_t N, uint32_t lds, int wave, int lane) {
+  const int dwords = (s.bytes + 3) / 4, units = (dwords + 3) / 4 * NT;
+  int n = 0;
+  for (int u = wave; u < units; u += W, ++n) {
+    const int e = min(u / NT * 4 + (lane & 3), dwords - 1);
+    copy4(s.base + min(n0 + 16 * (u % NT) + (lane >> 2), N - 1) * s.row_bytes + s.off + 4 * e, lds + u * 256);
+  }
+  return n;
+}
+// Through registers, at any alignment.
+template <int NT, int THREADS>
+__device__ __forceinline__ void stream_loads(const Stream& s, int64_t n0, int64_t N, uint32_t* dst) {
+  const int dwords = (s.bytes + 3) / 4;
+  for (int i = threadIdx.x; i < dwords * 16 * NT; i += THREADS) {
+    const int row = i / dwords, e = i - row * dwords;
+    const uint8_t* p = s.base + min(n0 + row, N - 1) * s.row_bytes + s.off + 4 * e;
+    uint32_t v = 0;
+    if (4 * e + 4 <= s.bytes) v = *(const u32_any*)p;
+    else
+      for (int b = 0; b < s.bytes - 4 * e; ++b) v |= (uint32_t)p[b] << (8 * b);
+    dst[stream_at<NT>(e, row >> 4, row & 15)] = v;
+  }
 }
 
 }  // namespace mx

@@ -38,17 +38,9 @@ struct Tile {
   static constexpr int Y_PITCH = TN * 2 + 8;
   static constexpr int SMEM = SLOTS * SLOT > TM * Y_PITCH ? SLOTS * SLOT : TM * Y_PITCH;
   static constexpr int X_COPIES = X_BYTES / (16 * THREADS);
+  static constexpr int Y_BYTES = TM * Y_PITCH;
   static_assert(W_BYTES == 16 * THREADS && 2 * TN == THREADS, "one copy of codes and one table entry a thread");
 };
-
-// Copies of 16 or 4 bytes a lane to LDS, lane i's to base + 16 i or 4 i. Inline, so that the compiler does not
-// wait for them before every LDS read: the loop waits for a stage's copies itself.
-__device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
-}
-__device__ __forceinline__ void copy4(const void* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
-}
 
 // 16-byte chunk c (of 8) of activation row r: 16 rows at one chunk fall in 16 bank groups.
 __device__ __forceinline__ int x_off(int r, int c) { return r * (TK * 2) + ((c ^ ((r >> 1) & 7)) << 4); }
@@ -64,145 +56,133 @@ __device__ __forceinline__ f32x16 mfma32(u32v4 a, u32v4 b, const f32x16& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// Until no more than N of the wave's copies are under way and its LDS reads are done, then the barrier.
-template <int N>
-__device__ __forceinline__ void wait_barrier() {
-  static_assert(N == 0 || (N >= 4 && N <= 7), "a wait for each count");
-  if constexpr (N == 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  else if constexpr (N == 4) asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  else if constexpr (N == 5) asm volatile("s_waitcnt vmcnt(5) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  else if constexpr (N == 6) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  else asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// The tile's products. GROUPS: scaled sums per block of 32 columns (1) or per stage (2, groups of
-// 64 or more); 0: scales in the expansion.
-template <class T, int DT, bool INT, int GROUPS>
-__device__ __forceinline__ void w4_tile(const W4Args& a, uint8_t* smem, int64_t t0, int64_t n0) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  constexpr int TM = T::TM, TN = T::TN, IB = T::IB, JB = T::JB, XC = T::X_COPIES;
-  constexpr int X_BYTES = T::X_BYTES, W_BYTES = T::W_BYTES, S_BYTES = T::S_BYTES, SLOT = T::SLOT, Y_PITCH = T::Y_PITCH;
-  const int r32 = lane & 31, h = lane >> 5, wn = wave % T::WAVES_N, wm = wave / T::WAVES_N;
-  const int blocks = (int)(a.K / 32), stages = (blocks + 1) / 2;
-
-  // this thread's chunks of the activations and the codes, and its entry of each table
+// Where a thread stands in its tile: what it copies of a stage, and which rows its wave multiplies.
+template <class T, int DT>
+struct Place {
+  static constexpr int XC = T::X_COPIES;
+  int tid, lane, wave, r32, h, wn, wm;
   const char* xs[XC];
-  int xc[XC];
+  int xc[XC], wc;
+  const uint8_t* ws;
+  __device__ __forceinline__ Place(const W4Args& a, int64_t t0, int64_t n0) {
+    tid = threadIdx.x;
+    lane = tid & 63;
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    r32 = lane & 31;
+    h = lane >> 5;
+    wn = wave % T::WAVES_N;
+    wm = wave / T::WAVES_N;
 #pragma unroll
-  for (int c = 0; c < XC; ++c) {
-    const int p = (wave * XC + c) * 64 + lane, r = p >> 3;
-    xc[c] = (p & 7) ^ ((r >> 1) & 7);
-    xs[c] = at<DT>(a.x, min(t0 + r, a.M - 1) * a.ldx) + xc[c] * 16;
+    for (int c = 0; c < XC; ++c) {
+      const int p = (wave * XC + c) * 64 + lane, r = p >> 3;
+      xc[c] = (p & 7) ^ ((r >> 1) & 7);
+      xs[c] = at<DT>(a.x, min(t0 + r, a.M - 1) * a.ldx) + xc[c] * 16;
+    }
+    const int wr = tid >> 1;
+    wc = (tid & 1) ^ ((wr >> 3) & 1);
+    ws = a.w + min(n0 + wr, a.N - 1) * (a.K / 2) + wc * 16;
   }
-  const int wr = tid >> 1, wc = (tid & 1) ^ ((wr >> 3) & 1);
-  const uint8_t* ws = a.w + min(n0 + wr, a.N - 1) * (a.K / 2) + wc * 16;
-  const int sb = tid / TN;                            // the block of the stage whose table entry this thread copies
-  const float* ss = a.scale_table + min(n0 + tid % TN, a.N - 1);
-  const uint32_t* zs = a.zero_table + min(n0 + tid % TN, a.N - 1);
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)smem;
-  auto issue = [&](int st) {                           // XC + 2 copies, INT one more
-    const uint32_t base = lds0 + (uint32_t)(st % SLOTS) * SLOT;
-    // the last stage may have one block: its second half is the first again, and not used
-    const bool whole = 2 * st + 1 < blocks;
+  // The copies of the 64 columns from block `blk` on to `slot`: XC + 1 a thread. `whole` is false where there is one block of
+  // 32 left: the second is then the first again, and not used.
+  __device__ __forceinline__ void issue(int64_t blk, bool whole, uint32_t slot) const {
 #pragma unroll
     for (int c = 0; c < XC; ++c)
-      copy16(xs[c] + (int64_t)st * (TK * 2) - (whole || xc[c] < 4 ? 0 : 64), base + (wave * XC + c) * 1024);
-    copy16(ws + (int64_t)st * (TK / 2) - (whole || wc == 0 ? 0 : 16), base + X_BYTES + wave * 1024);
-    const int64_t blk = 2 * st + (whole ? sb : 0);
-    copy4(ss + blk * a.N, base + X_BYTES + W_BYTES + wave * 256);
-    if constexpr (INT) copy4(zs + blk * a.N, base + X_BYTES + W_BYTES + S_BYTES + wave * 256);
-  };
+      copy16(xs[c] + blk * 64 - (whole || xc[c] < 4 ? 0 : 64), slot + (wave * XC + c) * 1024);
+    copy16(ws + blk * 16 - (whole || wc == 0 ? 0 : 16), slot + T::X_BYTES + wave * 1024);
+  }
+};
 
-  f32x16 acc[IB][JB];
+// A stage's products. GROUPS: scaled sums per block of 32 columns (1) or for both together (2,
+// groups of 64 or more); 0: scales in the expansion. scale_zero(j, b, row, scale, zero) gives block
+// b's of the tile's weight row `row`. Lane (row, h) has columns 16 h .. 16 h + 15 of a block: step 2 b + m
+// takes 8 m .. 8 m + 7 of them.
+template <class T, int DT, bool INT, int GROUPS, class F>
+__device__ __forceinline__ void stage_products(const Place<T, DT>& me, const uint8_t* sx, bool whole, F&& scale_zero,
+                                               f32x16 (&acc)[T::IB][T::JB]) {
+  constexpr int IB = T::IB, JB = T::JB;
+  const uint8_t* sw = sx + T::X_BYTES;
+  u32v4 w[JB][4];
+  float scale[JB][2];
 #pragma unroll
-  for (int i = 0; i < IB; ++i)
+  for (int j = 0; j < JB; ++j)
 #pragma unroll
-    for (int j = 0; j < JB; ++j)
+    for (int b = 0; b < 2; ++b) {
+      const int r = (me.wn * JB + j) * 32 + me.r32;
+      const u32v2 d = *(const u32v2*)(sw + w_off(r, b) + 8 * me.h);
+      uint32_t zero = 0;
+      scale_zero(b, r, scale[j][b], zero);
 #pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-
-  issue(0);
-  if (stages > 1) issue(1);
-  for (int st = 0; st < stages; ++st) {
-    // stage st is there (a later one may be on its way), and all waves are done with the stage before
-    if (st + 1 < stages) {
-      wait_barrier<XC + 2 + INT>();
-    } else {
-      wait_barrier<0>();
-    }
-    if (st + 2 < stages) issue(st + 2);
-    const uint8_t* sx = smem + (st % SLOTS) * SLOT;
-    const uint8_t* sw = sx + X_BYTES;
-    const float* sc = (const float*)(sw + W_BYTES);
-    const bool whole = 2 * st + 1 < blocks;
-    // lane (row, h) has columns 16 h .. 16 h + 15 of a block: step 2 b + m takes 8 m .. 8 m + 7 of them
-    u32v4 w[JB][4];
-    float scale[JB][2];
-#pragma unroll
-    for (int j = 0; j < JB; ++j)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int r = (wn * JB + j) * 32 + r32;
-        const u32v2 d = *(const u32v2*)(sw + w_off(r, b) + 8 * h);
-        scale[j][b] = sc[b * TN + r];
-        uint32_t zero = 0;
-        if constexpr (INT) zero = __float_as_uint(sc[S_BYTES / 4 + b * TN + r]);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if constexpr (INT) w[j][2 * b + m] = expand_int<DT>(d[m], zero);
-          else w[j][2 * b + m] = expand_fp4<DT>(d[m], GROUPS == 0 ? scale[j][b] : 1.0f);
-        }
+      for (int m = 0; m < 2; ++m) {
+        const uint32_t c = m == 0 ? d[0] : d[1];
+        if constexpr (INT) w[j][2 * b + m] = expand_int<DT>(c, zero);
+        else w[j][2 * b + m] = expand_fp4<DT>(c, GROUPS == 0 ? scale[j][b] : 1.0f);
       }
+    }
 #pragma unroll
-    for (int i = 0; i < IB; ++i) {
-      u32v4 x[4];
+  for (int i = 0; i < IB; ++i) {
+    u32v4 x[4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        x[s] = *(const u32v4*)(sx + x_off((wm * IB + i) * 32 + r32, 4 * (s >> 1) + 2 * h + (s & 1)));
-      if constexpr (GROUPS == 0) {
+    for (int s = 0; s < 4; ++s)
+      x[s] = *(const u32v4*)(sx + x_off((me.wm * IB + i) * 32 + me.r32, 4 * (s >> 1) + 2 * me.h + (s & 1)));
+    if constexpr (GROUPS == 0) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          if (s == 2 && !whole) break;
+      for (int s = 0; s < 4; ++s) {
+        if (s == 2 && !whole) break;
 #pragma unroll
-          for (int j = 0; j < JB; ++j) acc[i][j] = mfma32<DT>(x[s], w[j][s], acc[i][j]);
-        }
-      } else {
+        for (int j = 0; j < JB; ++j) acc[i][j] = mfma32<DT>(x[s], w[j][s], acc[i][j]);
+      }
+    } else {
 #pragma unroll
-        for (int b = 0; b < 2; b += GROUPS) {
-          if (b == 1 && !whole) break;
+      for (int b = 0; b < 2; b += GROUPS) {
+        if (b == 1 && !whole) break;
 #pragma unroll
-          for (int j = 0; j < JB; ++j) {
-            f32x16 p;
+        for (int j = 0; j < JB; ++j) {
+          f32x16 p;
 #pragma unroll
-            for (int v = 0; v < 16; ++v) p[v] = 0.0f;
+          for (int v = 0; v < 16; ++v) p[v] = 0.0f;
 #pragma unroll
-            for (int s = 2 * b; s < 2 * b + 2 * GROUPS; ++s) p = mfma32<DT>(x[s], w[j][s], p);
+          for (int s = 2 * b; s < 2 * b + 2 * GROUPS; ++s) p = mfma32<DT>(x[s], w[j][s], p);
 #pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(scale[j][b], p[v], acc[i][j][v]);
-          }
+          for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(scale[j][b], p[v], acc[i][j][v]);
         }
       }
     }
   }
+}
 
-  // lane (r32, h) has weight row r32 of a block and tokens 8 (v / 4) + 4 h + v % 4: through LDS, and out in whole rows
+template <class T>
+__device__ __forceinline__ void clear(f32x16 (&acc)[T::IB][T::JB]) {
+#pragma unroll
+  for (int i = 0; i < T::IB; ++i)
+#pragma unroll
+    for (int j = 0; j < T::JB; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+}
+
+// The finished tile: lane (r32, h) has weight row r32 of a block and tokens 8 (v / 4) + 4 h + v % 4. Through LDS, and
+// out in whole rows.
+template <class T, int DT>
+__device__ __forceinline__ void store_tile(const W4Args& a, const Place<T, DT>& me, uint8_t* smem, int64_t t0, int64_t n0,
+                                           const f32x16 (&acc)[T::IB][T::JB]) {
+  constexpr int Y_PITCH = T::Y_PITCH;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < IB; ++i)
+  for (int i = 0; i < T::IB; ++i)
 #pragma unroll
-    for (int j = 0; j < JB; ++j)
+    for (int j = 0; j < T::JB; ++j)
 #pragma unroll
       for (int v = 0; v < 16; v += 2) {
         const uint32_t d = pack2<DT>(acc[i][j][v], acc[i][j][v + 1]);
-        const int t = (wm * IB + i) * 32 + 8 * (v / 4) + 4 * h + v % 4;
-        uint8_t* p = smem + t * Y_PITCH + ((wn * JB + j) * 32 + r32) * 2;
+        const int t = (me.wm * T::IB + i) * 32 + 8 * (v / 4) + 4 * me.h + v % 4;
+        uint8_t* p = smem + t * Y_PITCH + ((me.wn * T::JB + j) * 32 + me.r32) * 2;
         *(uint16_t*)p = (uint16_t)d;
         *(uint16_t*)(p + Y_PITCH) = (uint16_t)(d >> 16);
       }
   __syncthreads();
   const bool al = a.ldy % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
-  for (int p = tid; p < TM * (TN / 8); p += T::THREADS) {
-    const int r = p / (TN / 8), c = p % (TN / 8) * 8;
+  for (int p = me.tid; p < T::TM * (T::TN / 8); p += T::THREADS) {
+    const int r = p / (T::TN / 8), c = p % (T::TN / 8) * 8;
     const int64_t t = t0 + r, n = n0 + c;
     if (t >= a.M || n >= a.N) continue;
     uint16_t* out = (uint16_t*)a.y + t * a.ldy + n;
@@ -216,6 +196,43 @@ __device__ __forceinline__ void w4_tile(const W4Args& a, uint8_t* smem, int64_t 
       for (int i = 0; i < (int)(a.N - n); ++i) out[i] = in[i];
     }
   }
+}
+
+// The whole K of a tile, scales from the tables. The loop issues XC + 2 copies a stage, INT one more.
+template <class T, int DT, bool INT, int GROUPS>
+__device__ __forceinline__ void w4_tile(const W4Args& a, uint8_t* smem, int64_t t0, int64_t n0) {
+  constexpr int TN = T::TN, SCALES = T::X_BYTES + T::W_BYTES, ZEROS = SCALES + T::S_BYTES, C = T::X_COPIES + 2 + INT;
+  const Place<T, DT> me(a, t0, n0);
+  const int blocks = (int)(a.K / 32), stages = (blocks + 1) / 2;
+  const int sb = me.tid / TN;                         // the block of the stage whose table entry this thread copies
+  const float* ss = a.scale_table + min(n0 + me.tid % TN, a.N - 1);
+  const uint32_t* zs = a.zero_table + min(n0 + me.tid % TN, a.N - 1);
+  const uint32_t lds0 = lds_address(smem);
+  auto issue = [&](int st) {
+    const uint32_t slot = lds0 + (uint32_t)(st % SLOTS) * T::SLOT;
+    const bool whole = 2 * st + 1 < blocks;
+    me.issue(2 * st, whole, slot);
+    const int64_t blk = 2 * st + (whole ? sb : 0);
+    copy4(ss + blk * a.N, slot + SCALES + me.wave * 256);
+    if constexpr (INT) copy4(zs + blk * a.N, slot + ZEROS + me.wave * 256);
+  };
+  f32x16 acc[T::IB][T::JB];
+  clear<T>(acc);
+  issue(0);
+  if (stages > 1) issue(1);
+  for (int st = 0; st < stages; ++st) {
+    // stage st is there (a later one may be on its way), and all waves are done with the stage before
+    if (st + 1 < stages) wait_copies<C>();
+    else wait_copies<0>();
+    lds_barrier();
+    if (st + 2 < stages) issue(st + 2);
+    const uint8_t* slot = smem + (st % SLOTS) * T::SLOT;
+    stage_products<T, DT, INT, GROUPS>(me, slot, 2 * st + 1 < blocks, [&](int b, int r, float& scale, uint32_t& zero) {
+      scale = ((const float*)(slot + SCALES))[b * TN + r];
+      if constexpr (INT) zero = ((const uint32_t*)(slot + ZEROS))[b * TN + r];
+    }, acc);
+  }
+  store_tile<T, DT>(a, me, smem, t0, n0, acc);
 }
 
 // Scales (and zero points) as fp32, block by block of 32 columns; large[]: whether the workgroup saw an E8M0 byte above 252.
@@ -281,29 +298,188 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_w4_gemm(W4Args a, int tiles_m
   }
 }
 
+// Fewer tokens: tiles of 128 weight rows and all or 128 of the tokens, K cut into parts for as many workgroups as the
+// compute units take. The part's scales are in LDS as they are, CAP steps of 128 columns at a time.
+template <class T, int SL, int CAP, int DT, bool INT, int GL>
+struct Part {
+  static constexpr int SB = INT ? 256 >> GL : 4, ZB = INT ? 128 >> GL : 0;     // bytes of a row's step
+  static constexpr int SLOT = T::X_BYTES + T::W_BYTES, SCALES = SL * SLOT;
+  // three steps more: a stream starts at a dword
+  static constexpr int ZEROS = SCALES + stream_bytes((CAP + 3) * SB, T::TN / 16);
+  static constexpr int RING = ZEROS + stream_bytes((CAP + 3) * ZB, T::TN / 16);
+  static constexpr int SMEM = RING > T::Y_BYTES ? RING : T::Y_BYTES;
+
+  // The products of blocks b0 .. b1 - 1, whose first step's scales are a0's in the streams.
+  template <int GROUPS>
+  static __device__ __forceinline__ void run(const Place<T, DT>& me, const W4Args& a, uint8_t* smem, int b0, int b1, int a0,
+                                             int issued, f32x16 (&acc)[T::IB][T::JB]) {
+    constexpr int C = T::X_COPIES + 1, NT = T::TN / 16;
+    const uint32_t* ssc = (const uint32_t*)(smem + SCALES);
+    const uint32_t* szp = (const uint32_t*)(smem + ZEROS);
+    const int stages = (b1 - b0 + 1) / 2;
+    for (int st = 0; st < stages; ++st) {
+      // stage st is there, up to SL - 2 later ones on their way, and all waves are done with the stage before
+      if (st + SL - 1 <= stages) wait_copies<(SL - 2) * C>();
+      else wait_copies<0>();
+      lds_barrier();
+      const int next = st + SL - 1;
+      if (next < stages) me.issue(b0 + 2 * next, b0 + 2 * next + 1 < b1, lds_address(smem) + next % SL * SLOT);
+      const int rel = b0 + 2 * st - 4 * a0;
+      stage_products<T, DT, INT, GROUPS>(me, smem + st % SL * SLOT, b0 + 2 * st + 1 < b1,
+                                         [&](int b, int r, float& scale, uint32_t& zero) {
+        const int g = (rel + b) >> (GL - 5);
+        if constexpr (INT) {
+          const uint32_t w = ssc[stream_at<NT>(g >> 1, r >> 4, r & 15)] >> (16 * (g & 1));
+          scale = lo_f32<DT>(w);
+          zero = zero_bits<DT>(a.zeros == nullptr ? 8u : szp[stream_at<NT>(g >> 2, r >> 4, r & 15)] >> (8 * (g & 3)) & 0xFFu);
+        } else {
+          const uint32_t w = ssc[stream_at<NT>(g >> 2, r >> 4, r & 15)] >> (8 * (g & 3)) & 0xFFu;
+          scale = GROUPS == 0 ? __uint_as_float(w << 23) : e8m0(w);
+        }
+      }, acc);
+    }
+  }
+};
+
+template <class T, int SL, int CAP, int DT, bool INT, int GL>
+__global__ __launch_bounds__(T::THREADS, 2) void k_w4_part(W4Args a, int tiles_m, int tiles_n, int splits, int per_xcd) {
+  typedef Part<T, SL, CAP, DT, INT, GL> P;
+  constexpr int NT = T::TN / 16, W = T::THREADS / 64, C = T::X_COPIES + 1;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[P::SMEM];
+  // an XCD takes a run of tiles, those of the same tokens and part of K side by side
+  const int L = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  if (L >= tiles_m * tiles_n * splits) return;
+  const int nt = L % tiles_n, mt = L / tiles_n % tiles_m, sp = L / tiles_n / tiles_m;
+  const int64_t t0 = (int64_t)mt * T::TM, n0 = (int64_t)nt * T::TN;
+  const Place<T, DT> me(a, t0, n0);
+  const int blocks = (int)(a.K / 32), steps = (blocks + 3) / 4;
+  const int s0 = (int)((int64_t)steps * sp / splits), s1 = (int)((int64_t)steps * (sp + 1) / splits);
+  const int64_t groups = a.K >> GL;
+  f32x16 acc[T::IB][T::JB];
+  clear<T>(acc);
+  for (int c0 = s0; c0 < s1; c0 += CAP) {
+    const int c1 = min(c0 + CAP, s1), a0 = c0 & ~3, b0 = 4 * c0, b1 = min(4 * c1, blocks), n = b1 - 4 * a0;
+    const Stream scales = {(const uint8_t*)a.scales, groups * (INT ? 2 : 1), (int64_t)a0 * P::SB, (n * P::SB + 3) / 4};
+    const Stream zeros = {a.zeros, groups, (int64_t)a0 * P::ZB, a.zeros == nullptr ? 0 : (n * P::ZB + 3) / 4};
+    if (c0 > s0) lds_barrier();
+    if (a.whole_dwords) {
+      stream_copies<NT, W>(scales, n0, a.N, lds_address(smem) + P::SCALES, me.wave, me.lane);
+      if (INT) stream_copies<NT, W>(zeros, n0, a.N, lds_address(smem) + P::ZEROS, me.wave, me.lane);
+    } else {
+      stream_loads<NT, T::THREADS>(scales, n0, a.N, (uint32_t*)(smem + P::SCALES));
+      if (INT) stream_loads<NT, T::THREADS>(zeros, n0, a.N, (uint32_t*)(smem + P::ZEROS));
+    }
+    const int stages = (b1 - b0 + 1) / 2, first = min(SL - 1, stages);
+    for (int st = 0; st < first; ++st)
+      me.issue(b0 + 2 * st, b0 + 2 * st + 1 < b1, lds_address(smem) + st * P::SLOT);
+    if (first == SL - 1) wait_copies<(SL - 1) * C>();
+    else wait_copies<0>();
+    lds_barrier();                 // the scales are there
+    if constexpr (INT) {
+      P::template run<(GL == 5 ? 1 : 2)>(me, a, smem, b0, b1, a0, first, acc);
+    } else if constexpr (DT == DT_BF16) {
+      bool large = false;
+      const int dwords = (scales.bytes + 3) / 4;
+      for (int i = me.tid; i < dwords * T::TN; i += T::THREADS) {
+        const int e = i / T::TN, r = i % T::TN;
+        const uint32_t w = ((const uint32_t*)(smem + P::SCALES))[stream_at<NT>(e, r >> 4, r & 15)];
+        large |= ((((w & 0x7F7F7F7Fu) + 0x03030303u) & w) & 0x80808080u) != 0;   // a byte above 252
+      }
+      if (__syncthreads_or(large)) P::template run<1>(me, a, smem, b0, b1, a0, first, acc);
+      else P::template run<0>(me, a, smem, b0, b1, a0, first, acc);
+    } else {
+      P::template run<1>(me, a, smem, b0, b1, a0, first, acc);
+    }
+  }
+  if (splits == 1) {
+    store_tile<T, DT>(a, me, smem, t0, n0, acc);
+    return;
+  }
+  const int64_t pitch = (a.N + 3) / 4 * 4;
+#pragma unroll
+  for (int i = 0; i < T::IB; ++i)
+#pragma unroll
+    for (int j = 0; j < T::JB; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int64_t t = t0 + (me.wm * T::IB + i) * 32 + 8 * (v / 4) + 4 * me.h + v % 4;
+        const int64_t n = n0 + (me.wn * T::JB + j) * 32 + me.r32;
+        if (t < a.M && n < a.N) a.part[(sp * a.M + t) * pitch + n] = acc[i][j][v];
+      }
+}
+
+// y = the sum of the parts of K, in their order; four columns a thread.
+template <int DT>
+__global__ __launch_bounds__(256) void k_w4_sum(W4Args a, int splits) {
+  const int64_t pitch = (a.N + 3) / 4 * 4, quads = pitch / 4;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.M * quads; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / quads, n = (i - t * quads) * 4;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) v += *(const f32x4*)(a.part + ((int64_t)s * a.M + t) * pitch + n);
+    uint16_t* out = (uint16_t*)a.y + t * a.ldy + n;
+    const uint32_t lo = pack2<DT>(v[0], v[1]), hi = pack2<DT>(v[2], v[3]);
+    if (n + 4 <= a.N) {
+      typedef u32v2 u32v2_any __attribute__((aligned(2)));
+      *(u32v2_any*)out = u32v2{lo, hi};
+    } else {
+      for (int e = 0; e < (int)(a.N - n); ++e) out[e] = (uint16_t)((e < 2 ? lo : hi) >> (16 * (e & 1)));
+    }
+  }
+}
+
 }  // namespace
 
+W4Plan w4_plan(int64_t M, int64_t K, int64_t N) {
+  if (M <= W4_FEW) return {16, 1, false};
+  const int64_t large = ((M + 255) / 256) * ((N + 255) / 256);
+  static const char* eL = getenv("W4L");
+  if (large >= (eL ? atoi(eL) : 160)) return {256, 1, true};
+  const int tokens = M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const int64_t tiles = ((M + tokens - 1) / tokens) * ((N + 127) / 128), steps = (K + 127) / 128;
+  static const char* eS = getenv("W4S");
+  int64_t splits = std::max<int64_t>(1, (eS ? atoi(eS) : 448) / tiles);
+  splits = std::min({splits, std::max<int64_t>(1, steps / 2), (int64_t)16});
+  return {tokens, (int)splits, false};
+}
+
 hipError_t launch_w4_gemm(const W4Args& a, hipStream_t s) {
-  const auto go = [&](auto tile, auto d, auto in) {
-    typedef decltype(tile) T;
-    constexpr int D = decltype(d)::value;
+  const W4Plan plan = w4_plan(a.M, a.K, a.N);
+  const auto go = [&](auto d, auto in, auto gl) {
+    constexpr int D = decltype(d)::value, GL = decltype(gl)::value;
     constexpr bool I = decltype(in)::value;
-    const int tm = (int)((a.M + T::TM - 1) / T::TM), tn = (int)((a.N + T::TN - 1) / T::TN), per_xcd = (tm * tn + 7) / 8;
-    k_w4_tables<D, I><<<W4_TABLE_GRID, 256, 0, s>>>(a);
-    k_w4_gemm<T, D, I><<<8 * per_xcd, T::THREADS, 0, s>>>(a, tm, tn, per_xcd);
-  };
-  const auto types = [&](auto tile) {
-    if (a.dt == DT_BF16) {
-      if (a.int4) go(tile, DtC<DT_BF16>(), std::true_type());
-      else go(tile, DtC<DT_BF16>(), std::false_type());
-    } else {
-      if (a.int4) go(tile, DtC<DT_F16>(), std::true_type());
-      else go(tile, DtC<DT_F16>(), std::false_type());
+    if (plan.tables) {
+      typedef Tile<2, 4, 4, 2> T;
+      const int tm = (int)((a.M + T::TM - 1) / T::TM), tn = (int)((a.N + T::TN - 1) / T::TN), per_xcd = (tm * tn + 7) / 8;
+      k_w4_tables<D, I><<<W4_TABLE_GRID, 256, 0, s>>>(a);
+      k_w4_gemm<T, D, I><<<8 * per_xcd, T::THREADS, 0, s>>>(a, tm, tn, per_xcd);
+      return;
     }
+    const auto part = [&](auto tile, auto slots, auto cap) {
+      typedef decltype(tile) T;
+      const int tm = (int)((a.M + T::TM - 1) / T::TM), tn = (int)((a.N + T::TN - 1) / T::TN);
+      const int per_xcd = (tm * tn * plan.splits + 7) / 8;
+      k_w4_part<T, decltype(slots)::value, decltype(cap)::value, D, I, GL><<<8 * per_xcd, T::THREADS, 0, s>>>(
+          a, tm, tn, plan.splits, per_xcd);
+      if (plan.splits > 1) {
+        const int64_t quads = a.M * ((a.N + 3) / 4);
+        k_w4_sum<D><<<(unsigned)std::min<int64_t>((quads + 255) / 256, 4096), 256, 0, s>>>(a, plan.splits);
+      }
+    };
+    using std::integral_constant;
+    if (plan.tokens == 32) part(Tile<1, 4, 1, 1>(), integral_constant<int, 5>(), integral_constant<int, 16>());
+    else if (plan.tokens == 64) part(Tile<1, 4, 2, 1>(), integral_constant<int, 4>(), integral_constant<int, 16>());
+    else part(Tile<2, 2, 2, 2>(), integral_constant<int, 3>(), integral_constant<int, 8>());
   };
-  static const bool small = getenv("W4SMALL") != nullptr;
-  if (small) types(Tile<2, 2, 2, 2>());
-  else types(Tile<2, 4, 4, 2>());
+  const auto types = [&](auto in, auto gl) {
+    if (a.dt == DT_BF16) go(DtC<DT_BF16>(), in, gl);
+    else go(DtC<DT_F16>(), in, gl);
+  };
+  using std::integral_constant;
+  if (!a.int4) types(std::false_type(), integral_constant<int, 5>());
+  else if (a.group_log2 == 5) types(std::true_type(), integral_constant<int, 5>());
+  else if (a.group_log2 == 6) types(std::true_type(), integral_constant<int, 6>());
+  else types(std::true_type(), integral_constant<int, 7>());
   return hipGetLastError();
 }
 
