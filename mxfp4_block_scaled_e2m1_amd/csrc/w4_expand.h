@@ -83,6 +83,10 @@ __device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
 __device__ __forceinline__ void copy4(const void* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
 }
+// The same from a base that all lanes share and a lane's offset of 32 bits: the base moves on in scalar registers.
+__device__ __forceinline__ void copy16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
+}
 template <int N>
 __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");

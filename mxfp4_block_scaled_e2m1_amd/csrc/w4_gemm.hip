@@ -16,7 +16,6 @@
 // The scales come as a table [K / 32][N] of fp32 that a small kernel before makes (the
 // rows of scales are neither aligned nor next to each other for a stage).
 #include <algorithm>
-#include <cstdlib>
 
 #include "w4_expand.h"
 
@@ -39,7 +38,6 @@ struct Tile {
   static constexpr int SMEM = SLOTS * SLOT > TM * Y_PITCH ? SLOTS * SLOT : TM * Y_PITCH;
   static constexpr int X_COPIES = X_BYTES / (16 * THREADS);
   static constexpr int Y_BYTES = TM * Y_PITCH;
-  static_assert(W_BYTES == 16 * THREADS && 2 * TN == THREADS, "one copy of codes and one table entry a thread");
 };
 
 // 16-byte chunk c (of 8) of activation row r: 16 rows at one chunk fall in 16 bank groups.
@@ -56,51 +54,26 @@ __device__ __forceinline__ f32x16 mfma32(u32v4 a, u32v4 b, const f32x16& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// Where a thread stands in its tile: what it copies of a stage, and which rows its wave multiplies.
+// Which rows of its tile a wave multiplies.
 template <class T, int DT>
 struct Place {
-  static constexpr int XC = T::X_COPIES;
-  int tid, lane, wave, r32, h, wn, wm;
-  const char* xs[XC];
-  int xc[XC], wc;
-  const uint8_t* ws;
-  __device__ __forceinline__ Place(const W4Args& a, int64_t t0, int64_t n0) {
-    tid = threadIdx.x;
-    lane = tid & 63;
-    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    r32 = lane & 31;
-    h = lane >> 5;
+  int r32, h, wn, wm;
+  __device__ __forceinline__ explicit Place(int wave) {
+    r32 = threadIdx.x & 31;
+    h = threadIdx.x >> 5 & 1;
     wn = wave % T::WAVES_N;
     wm = wave / T::WAVES_N;
-#pragma unroll
-    for (int c = 0; c < XC; ++c) {
-      const int p = (wave * XC + c) * 64 + lane, r = p >> 3;
-      xc[c] = (p & 7) ^ ((r >> 1) & 7);
-      xs[c] = at<DT>(a.x, min(t0 + r, a.M - 1) * a.ldx) + xc[c] * 16;
-    }
-    const int wr = tid >> 1;
-    wc = (tid & 1) ^ ((wr >> 3) & 1);
-    ws = a.w + min(n0 + wr, a.N - 1) * (a.K / 2) + wc * 16;
-  }
-  // The copies of the 64 columns from block `blk` on to `slot`: XC + 1 a thread. `whole` is false where there is one block of
-  // 32 left: the second is then the first again, and not used.
-  __device__ __forceinline__ void issue(int64_t blk, bool whole, uint32_t slot) const {
-#pragma unroll
-    for (int c = 0; c < XC; ++c)
-      copy16(xs[c] + blk * 64 - (whole || xc[c] < 4 ? 0 : 64), slot + (wave * XC + c) * 1024);
-    copy16(ws + blk * 16 - (whole || wc == 0 ? 0 : 16), slot + T::X_BYTES + wave * 1024);
   }
 };
 
 // A stage's products. GROUPS: scaled sums per block of 32 columns (1) or for both together (2,
-// groups of 64 or more); 0: scales in the expansion. scale_zero(j, b, row, scale, zero) gives block
-// b's of the tile's weight row `row`. Lane (row, h) has columns 16 h .. 16 h + 15 of a block: step 2 b + m
-// takes 8 m .. 8 m + 7 of them.
-template <class T, int DT, bool INT, int GROUPS, class F>
-__device__ __forceinline__ void stage_products(const Place<T, DT>& me, const uint8_t* sx, bool whole, F&& scale_zero,
-                                               f32x16 (&acc)[T::IB][T::JB]) {
+// groups of 64 or more); 0: scales in the expansion. codes(b, row) is where the 16 bytes of block b
+// of the tile's weight row `row` are, scale_zero(b, row, scale, zero) gives that block's. Lane (row, h)
+// has columns 16 h .. 16 h + 15 of a block: step 2 b + m takes 8 m .. 8 m + 7 of them.
+template <class T, int DT, bool INT, int GROUPS, class C, class F>
+__device__ __forceinline__ void stage_products(const Place<T, DT>& me, const uint8_t* sx, bool whole, C&& codes,
+                                               F&& scale_zero, f32x16 (&acc)[T::IB][T::JB]) {
   constexpr int IB = T::IB, JB = T::JB;
-  const uint8_t* sw = sx + T::X_BYTES;
   u32v4 w[JB][4];
   float scale[JB][2];
 #pragma unroll
@@ -108,7 +81,7 @@ __device__ __forceinline__ void stage_products(const Place<T, DT>& me, const uin
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int r = (me.wn * JB + j) * 32 + me.r32;
-      const u32v2 d = *(const u32v2*)(sw + w_off(r, b) + 8 * me.h);
+      const u32v2 d = *(const u32v2*)(codes(b, r) + 8 * me.h);
       uint32_t zero = 0;
       scale_zero(b, r, scale[j][b], zero);
 #pragma unroll
@@ -181,7 +154,7 @@ __device__ __forceinline__ void store_tile(const W4Args& a, const Place<T, DT>& 
       }
   __syncthreads();
   const bool al = a.ldy % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
-  for (int p = me.tid; p < T::TM * (T::TN / 8); p += T::THREADS) {
+  for (int p = threadIdx.x; p < T::TM * (T::TN / 8); p += T::THREADS) {
     const int r = p / (T::TN / 8), c = p % (T::TN / 8) * 8;
     const int64_t t = t0 + r, n = n0 + c;
     if (t >= a.M || n >= a.N) continue;
@@ -202,19 +175,37 @@ __device__ __forceinline__ void store_tile(const W4Args& a, const Place<T, DT>& 
 template <class T, int DT, bool INT, int GROUPS>
 __device__ __forceinline__ void w4_tile(const W4Args& a, uint8_t* smem, int64_t t0, int64_t n0) {
   constexpr int TN = T::TN, SCALES = T::X_BYTES + T::W_BYTES, ZEROS = SCALES + T::S_BYTES, C = T::X_COPIES + 2 + INT;
-  const Place<T, DT> me(a, t0, n0);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Place<T, DT> me(wave);
   const int blocks = (int)(a.K / 32), stages = (blocks + 1) / 2;
-  const int sb = me.tid / TN;                         // the block of the stage whose table entry this thread copies
-  const float* ss = a.scale_table + min(n0 + me.tid % TN, a.N - 1);
-  const uint32_t* zs = a.zero_table + min(n0 + me.tid % TN, a.N - 1);
+  static_assert(T::W_BYTES == 16 * T::THREADS && 2 * TN == T::THREADS, "one copy of codes and one table entry a thread");
+  // this thread's chunks of the activations and the codes, and its entry of each table
+  constexpr int XC = T::X_COPIES;
+  const char* xs[XC];
+  int xc[XC];
+#pragma unroll
+  for (int c = 0; c < XC; ++c) {
+    const int p = (wave * XC + c) * 64 + lane, r = p >> 3;
+    xc[c] = (p & 7) ^ ((r >> 1) & 7);
+    xs[c] = at<DT>(a.x, min(t0 + r, a.M - 1) * a.ldx) + xc[c] * 16;
+  }
+  const int wr = tid >> 1, wc = (tid & 1) ^ ((wr >> 3) & 1);
+  const uint8_t* ws = a.w + min(n0 + wr, a.N - 1) * (a.K / 2) + wc * 16;
+  const int sb = tid / TN;                            // the block of the stage whose table entry this thread copies
+  const float* ss = a.scale_table + min(n0 + tid % TN, a.N - 1);
+  const uint32_t* zs = a.zero_table + min(n0 + tid % TN, a.N - 1);
   const uint32_t lds0 = lds_address(smem);
   auto issue = [&](int st) {
     const uint32_t slot = lds0 + (uint32_t)(st % SLOTS) * T::SLOT;
+    // the last stage may have one block: its second is the first again, and not used
     const bool whole = 2 * st + 1 < blocks;
-    me.issue(2 * st, whole, slot);
+#pragma unroll
+    for (int c = 0; c < XC; ++c)
+      copy16(xs[c] + (int64_t)st * (TK * 2) - (whole || xc[c] < 4 ? 0 : 64), slot + (wave * XC + c) * 1024);
+    copy16(ws + (int64_t)st * (TK / 2) - (whole || wc == 0 ? 0 : 16), slot + T::X_BYTES + wave * 1024);
     const int64_t blk = 2 * st + (whole ? sb : 0);
-    copy4(ss + blk * a.N, slot + SCALES + me.wave * 256);
-    if constexpr (INT) copy4(zs + blk * a.N, slot + ZEROS + me.wave * 256);
+    copy4(ss + blk * a.N, slot + SCALES + wave * 256);
+    if constexpr (INT) copy4(zs + blk * a.N, slot + ZEROS + wave * 256);
   };
   f32x16 acc[T::IB][T::JB];
   clear<T>(acc);
@@ -227,10 +218,13 @@ __device__ __forceinline__ void w4_tile(const W4Args& a, uint8_t* smem, int64_t 
     lds_barrier();
     if (st + 2 < stages) issue(st + 2);
     const uint8_t* slot = smem + (st % SLOTS) * T::SLOT;
-    stage_products<T, DT, INT, GROUPS>(me, slot, 2 * st + 1 < blocks, [&](int b, int r, float& scale, uint32_t& zero) {
-      scale = ((const float*)(slot + SCALES))[b * TN + r];
-      if constexpr (INT) zero = ((const uint32_t*)(slot + ZEROS))[b * TN + r];
-    }, acc);
+    stage_products<T, DT, INT, GROUPS>(
+        me, slot, 2 * st + 1 < blocks, [&](int b, int r) { return slot + T::X_BYTES + w_off(r, b); },
+        [&](int b, int r, float& scale, uint32_t& zero) {
+          scale = ((const float*)(slot + SCALES))[b * TN + r];
+          if constexpr (INT) zero = ((const uint32_t*)(slot + ZEROS))[b * TN + r];
+        },
+        acc);
   }
   store_tile<T, DT>(a, me, smem, t0, n0, acc);
 }
@@ -298,114 +292,216 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_w4_gemm(W4Args a, int tiles_m
   }
 }
 
-// Fewer tokens: tiles of 128 weight rows and all or 128 of the tokens, K cut into parts for as many workgroups as the
-// compute units take. The part's scales are in LDS as they are, CAP steps of 128 columns at a time.
-template <class T, int SL, int CAP, int DT, bool INT, int GL>
+// Fewer tokens: tiles of 128 weight rows and 32, 64 or 128 tokens, K cut into parts for as many workgroups as there are
+// compute units. 16 waves in KG groups: a step is KG stages of 64 columns, one for each group, whose sums meet at the end;
+// with one stage a step and four waves the chain from barrier over LDS and expansion to the products was most of it
+// (64 tokens of 7168 -> 7168: 30 us). The codes come in units of 256 columns, a row's whole 128 byte line (with 32
+// bytes a copy, four copies wait for one line, and the lines after it are asked for late), WS - 1 units ahead; the
+// activations, from L2, one step ahead. The scales of CAP units are in LDS as they are.
+constexpr int UNIT = 8;       // blocks of a unit of codes
+template <class T, int KG, int WS, int CAP, int DT, bool INT, int GL>
 struct Part {
-  static constexpr int SB = INT ? 256 >> GL : 4, ZB = INT ? 128 >> GL : 0;     // bytes of a row's step
-  static constexpr int SLOT = T::X_BYTES + T::W_BYTES, SCALES = SL * SLOT;
-  // three steps more: a stream starts at a dword
-  static constexpr int ZEROS = SCALES + stream_bytes((CAP + 3) * SB, T::TN / 16);
-  static constexpr int RING = ZEROS + stream_bytes((CAP + 3) * ZB, T::TN / 16);
-  static constexpr int SMEM = RING > T::Y_BYTES ? RING : T::Y_BYTES;
+  static constexpr int SB = INT ? 256 >> GL : 4, ZB = INT ? 128 >> GL : 0;     // bytes of a row's 128 columns
+  static constexpr int THREADS = T::THREADS * KG, P = 4 / KG;                  // steps of a unit
+  static constexpr int UNIT_BYTES = T::TN * 16 * UNIT, CW = UNIT_BYTES / (16 * THREADS);
+  static constexpr int STEP_BYTES = T::X_BYTES * KG, CX = STEP_BYTES / (16 * THREADS);
+  static constexpr int CODES = 2 * STEP_BYTES, SCALES = CODES + WS * UNIT_BYTES, WL = WS - 1;
+  // two steps more: a stream starts at a multiple of 512 columns
+  static constexpr int ZEROS = SCALES + stream_bytes((2 * CAP + 2) * SB, T::TN / 16);
+  static constexpr int RING = ZEROS + stream_bytes((2 * CAP + 2) * ZB, T::TN / 16);
+  static constexpr int SUMS = KG * T::TM * T::TN * 4;
+  static constexpr int SMEM = RING > SUMS ? RING : SUMS;
+  static_assert(CW >= 1 && CX >= 1 && WL * P > 1 && SMEM <= 160 * 1024, "whole copies, the waits for them, LDS");
 
-  // The products of blocks b0 .. b1 - 1, whose first step's scales are a0's in the streams.
+  const W4Args& a;
+  uint8_t* smem;
+  uint32_t lds;
+  int tid, lane, wave, kg;
+  const char *x, *w;          // the tile's first token and row
+  uint32_t ws[CW], xs[CX];    // what this thread copies of a unit and of a step: the byte from there,
+  int wc[CW], xb[CX];         // and the block
+  int64_t t0;
+  int b0, b1, a0;             // the blocks that are multiplied, and the 128 columns that the streams start with
+
+  __device__ __forceinline__ Part(const W4Args& args, uint8_t* s, int64_t t, int64_t n0) : a(args), smem(s), t0(t) {
+    lds = lds_address(smem);
+    tid = threadIdx.x;
+    lane = tid & 63;
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    kg = wave / (T::THREADS / 64);
+    x = at<DT>(a.x, t0 * a.ldx);
+    w = (const char*)a.w + n0 * (a.K / 2);
+#pragma unroll
+    for (int c = 0; c < CW; ++c) {
+      const int q = (wave * CW + c) * 64 + lane, r = q >> 3;
+      wc[c] = (q & 7) ^ ((r >> 1) & 7);
+      ws[c] = (uint32_t)min((int64_t)r, a.N - 1 - n0) * (uint32_t)(a.K / 2) + wc[c] * 16;
+    }
+#pragma unroll
+    for (int c = 0; c < CX; ++c) {
+      xb[c] = 2 * (piece(c) / (T::X_BYTES / 16)) + (chunk(c) >> 2);
+      xs[c] = (uint32_t)(row(c) * a.ldx * 2) + xb[c] * 64 + (chunk(c) & 3) * 16;
+    }
+  }
+  // of a step's copies of activations: which 16 bytes in LDS, of which of the tile's tokens, of which 8 of a stage's columns
+  __device__ __forceinline__ int piece(int c) const { return (wave * CX + c) * 64 + lane; }
+  __device__ __forceinline__ int64_t row(int c) const {
+    return min((int64_t)(piece(c) % (T::X_BYTES / 16) >> 3), a.M - 1 - t0);
+  }
+  __device__ __forceinline__ int chunk(int c) const {
+    const int p = piece(c) % (T::X_BYTES / 16);
+    return (p & 7) ^ ((p >> 4) & 7);
+  }
+  __device__ __forceinline__ int steps() const { return (b1 - b0 + 2 * KG - 1) / (2 * KG); }
+  __device__ __forceinline__ int units() const { return (b1 - b0 + UNIT - 1) / UNIT; }
+  // what would lie behind the last block is the last block over again, and not used
+  __device__ __forceinline__ void copy_x(int n) const {
+    const int blk = b0 + 2 * KG * n;
+    const uint32_t slot = lds + (n & 1) * STEP_BYTES + wave * (CX * 1024);
+    const char* from = x + (int64_t)blk * 64;
+    if (a.ldx < (1 << 24) && blk + 2 * KG <= b1) {      // offsets below 2^32
+#pragma unroll
+      for (int c = 0; c < CX; ++c) copy16(from, xs[c], slot + c * 1024);
+    } else {
+#pragma unroll
+      for (int c = 0; c < CX; ++c)
+        copy16(x + row(c) * a.ldx * 2 + (int64_t)min(blk + xb[c], b1 - 1) * 64 + (chunk(c) & 3) * 16, slot + c * 1024);
+    }
+  }
+  __device__ __forceinline__ void copy_w(int u) const {
+    const int blk = b0 + UNIT * u, left = b1 - 1 - blk;
+    const uint32_t slot = lds + CODES + u % WS * UNIT_BYTES + wave * (CW * 1024);
+    const char* from = w + (int64_t)blk * 16;
+#pragma unroll
+    for (int c = 0; c < CW; ++c)
+      copy16(from, left >= UNIT - 1 ? ws[c] : ws[c] + (min(wc[c], left) - wc[c]) * 16, slot + c * 1024);
+  }
+  __device__ __forceinline__ void start() const {
+    for (int u = 0; u < min(WL, units()); ++u) copy_w(u);
+    copy_x(0);
+  }
+  // Until no more copies are under way than start() issued.
+  __device__ __forceinline__ void wait_before_start() const {
+    if (units() >= WL) wait_copies<WL * CW + CX>();
+    else wait_copies<0>();
+  }
   template <int GROUPS>
-  static __device__ __forceinline__ void run(const Place<T, DT>& me, const W4Args& a, uint8_t* smem, int b0, int b1, int a0,
-                                             int issued, f32x16 (&acc)[T::IB][T::JB]) {
-    constexpr int C = T::X_COPIES + 1, NT = T::TN / 16;
-    const uint32_t* ssc = (const uint32_t*)(smem + SCALES);
-    const uint32_t* szp = (const uint32_t*)(smem + ZEROS);
-    const int stages = (b1 - b0 + 1) / 2;
-    for (int st = 0; st < stages; ++st) {
-      // stage st is there, up to SL - 2 later ones on their way, and all waves are done with the stage before
-      if (st + SL - 1 <= stages) wait_copies<(SL - 2) * C>();
+  __device__ __forceinline__ void run(const Place<T, DT>& me, f32x16 (&acc)[T::IB][T::JB]) const {
+    constexpr int NT = T::TN / 16;
+    // of row r: where dword e is from where dword 0 is
+    const auto dword = [](const uint8_t* s, int e, int r) {
+      return ((const uint32_t*)s)[stream_at<NT>(0, r >> 4, r & 15) + stream_at<NT>(e, 0, 0)];
+    };
+    const int n = steps(), last = units();
+    for (int i = 0; i < n; ++i) {
+      // Step i's activations are waited for, and with them its unit's codes, which were copied before. Copied after them
+      // was the unit that the step before copied, if that was a unit's first step and there was one to copy. All waves
+      // are then done with the step before.
+      if (i > 0 && (i - 1) % P == 0 && (i - 1) / P + WL < last) wait_copies<CW>();
       else wait_copies<0>();
       lds_barrier();
-      const int next = st + SL - 1;
-      if (next < stages) me.issue(b0 + 2 * next, b0 + 2 * next + 1 < b1, lds_address(smem) + next % SL * SLOT);
-      const int rel = b0 + 2 * st - 4 * a0;
-      stage_products<T, DT, INT, GROUPS>(me, smem + st % SL * SLOT, b0 + 2 * st + 1 < b1,
-                                         [&](int b, int r, float& scale, uint32_t& zero) {
-        const int g = (rel + b) >> (GL - 5);
-        if constexpr (INT) {
-          const uint32_t w = ssc[stream_at<NT>(g >> 1, r >> 4, r & 15)] >> (16 * (g & 1));
-          scale = lo_f32<DT>(w);
-          zero = zero_bits<DT>(a.zeros == nullptr ? 8u : szp[stream_at<NT>(g >> 2, r >> 4, r & 15)] >> (8 * (g & 3)) & 0xFFu);
-        } else {
-          const uint32_t w = ssc[stream_at<NT>(g >> 2, r >> 4, r & 15)] >> (8 * (g & 3)) & 0xFFu;
-          scale = GROUPS == 0 ? __uint_as_float(w << 23) : e8m0(w);
-        }
-      }, acc);
+      if (i + 1 < n) copy_x(i + 1);
+      if (i % P == 0 && i / P + WL < last) copy_w(i / P + WL);
+      const int blk = b0 + 2 * (KG * i + kg), rel = blk - 4 * a0, at = 2 * (KG * (i % P) + kg);
+      if (blk >= b1) continue;
+      const uint8_t* unit = smem + CODES + i / P % WS * UNIT_BYTES;
+      stage_products<T, DT, INT, GROUPS>(
+          me, smem + (i & 1) * STEP_BYTES + kg * T::X_BYTES, blk + 1 < b1,
+          [&](int k, int r) { return unit + x_off(r, at + k); },
+          [&](int k, int r, float& scale, uint32_t& zero) {
+            const int g = (rel + k) >> (GL - 5);
+            if constexpr (INT) {
+              scale = lo_f32<DT>(dword(smem + SCALES, g >> 1, r) >> (16 * (g & 1)));
+              zero = zero_bits<DT>(a.zeros == nullptr ? 8u : dword(smem + ZEROS, g >> 2, r) >> (8 * (g & 3)) & 0xFFu);
+            } else {
+              const uint32_t w = dword(smem + SCALES, g >> 2, r) >> (8 * (g & 3)) & 0xFFu;
+              scale = GROUPS == 0 ? __uint_as_float(w << 23) : e8m0(w);
+            }
+          },
+          acc);
     }
   }
 };
 
-template <class T, int SL, int CAP, int DT, bool INT, int GL>
-__global__ __launch_bounds__(T::THREADS, 2) void k_w4_part(W4Args a, int tiles_m, int tiles_n, int splits, int per_xcd) {
-  typedef Part<T, SL, CAP, DT, INT, GL> P;
-  constexpr int NT = T::TN / 16, W = T::THREADS / 64, C = T::X_COPIES + 1;
+template <class T, int KG, int WS, int CAP, int DT, bool INT, int GL>
+__global__ __launch_bounds__(T::THREADS* KG) void k_w4_part(W4Args a, int tiles_m, int tiles_n, int splits, int per_xcd) {
+  typedef Part<T, KG, WS, CAP, DT, INT, GL> P;
+  constexpr int NT = T::TN / 16, W = P::THREADS / 64;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[P::SMEM];
   // an XCD takes a run of tiles, those of the same tokens and part of K side by side
   const int L = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
   if (L >= tiles_m * tiles_n * splits) return;
   const int nt = L % tiles_n, mt = L / tiles_n % tiles_m, sp = L / tiles_n / tiles_m;
   const int64_t t0 = (int64_t)mt * T::TM, n0 = (int64_t)nt * T::TN;
-  const Place<T, DT> me(a, t0, n0);
-  const int blocks = (int)(a.K / 32), steps = (blocks + 3) / 4;
-  const int s0 = (int)((int64_t)steps * sp / splits), s1 = (int)((int64_t)steps * (sp + 1) / splits);
+  P p(a, smem, t0, n0);
+  const Place<T, DT> me(p.wave % (T::THREADS / 64));
+  const int blocks = (int)(a.K / 32), units = (blocks + UNIT - 1) / UNIT;
+  const int u0 = units * sp / splits, u1 = units * (sp + 1) / splits;     // (units and splits are small)
   const int64_t groups = a.K >> GL;
   f32x16 acc[T::IB][T::JB];
   clear<T>(acc);
-  for (int c0 = s0; c0 < s1; c0 += CAP) {
-    const int c1 = min(c0 + CAP, s1), a0 = c0 & ~3, b0 = 4 * c0, b1 = min(4 * c1, blocks), n = b1 - 4 * a0;
-    const Stream scales = {(const uint8_t*)a.scales, groups * (INT ? 2 : 1), (int64_t)a0 * P::SB, (n * P::SB + 3) / 4};
-    const Stream zeros = {a.zeros, groups, (int64_t)a0 * P::ZB, a.zeros == nullptr ? 0 : (n * P::ZB + 3) / 4};
-    if (c0 > s0) lds_barrier();
+  for (int c0 = u0; c0 < u1; c0 += CAP) {
+    p.b0 = UNIT * c0;
+    p.b1 = min(UNIT * min(c0 + CAP, u1), blocks);
+    p.a0 = (2 * c0) & ~3;
+    const int n = p.b1 - 4 * p.a0;
+    const Stream scales = {(const uint8_t*)a.scales, groups * (INT ? 2 : 1), (int64_t)p.a0 * P::SB, (n * P::SB + 3) / 4};
+    const Stream zeros = {a.zeros, groups, (int64_t)p.a0 * P::ZB, a.zeros == nullptr ? 0 : (n * P::ZB + 3) / 4};
+    if (c0 > u0) lds_barrier();
     if (a.whole_dwords) {
-      stream_copies<NT, W>(scales, n0, a.N, lds_address(smem) + P::SCALES, me.wave, me.lane);
-      if (INT) stream_copies<NT, W>(zeros, n0, a.N, lds_address(smem) + P::ZEROS, me.wave, me.lane);
+      stream_copies<NT, W>(scales, n0, a.N, p.lds + P::SCALES, p.wave, p.lane);
+      if (INT) stream_copies<NT, W>(zeros, n0, a.N, p.lds + P::ZEROS, p.wave, p.lane);
     } else {
-      stream_loads<NT, T::THREADS>(scales, n0, a.N, (uint32_t*)(smem + P::SCALES));
-      if (INT) stream_loads<NT, T::THREADS>(zeros, n0, a.N, (uint32_t*)(smem + P::ZEROS));
+      stream_loads<NT, P::THREADS>(scales, n0, a.N, (uint32_t*)(smem + P::SCALES));
+      if (INT) stream_loads<NT, P::THREADS>(zeros, n0, a.N, (uint32_t*)(smem + P::ZEROS));
     }
-    const int stages = (b1 - b0 + 1) / 2, first = min(SL - 1, stages);
-    for (int st = 0; st < first; ++st)
-      me.issue(b0 + 2 * st, b0 + 2 * st + 1 < b1, lds_address(smem) + st * P::SLOT);
-    if (first == SL - 1) wait_copies<(SL - 1) * C>();
-    else wait_copies<0>();
+    p.start();
+    p.wait_before_start();
     lds_barrier();                 // the scales are there
     if constexpr (INT) {
-      P::template run<(GL == 5 ? 1 : 2)>(me, a, smem, b0, b1, a0, first, acc);
+      p.template run<(GL == 5 ? 1 : 2)>(me, acc);
     } else if constexpr (DT == DT_BF16) {
       bool large = false;
       const int dwords = (scales.bytes + 3) / 4;
-      for (int i = me.tid; i < dwords * T::TN; i += T::THREADS) {
+      for (int i = p.tid; i < dwords * T::TN; i += P::THREADS) {
         const int e = i / T::TN, r = i % T::TN;
         const uint32_t w = ((const uint32_t*)(smem + P::SCALES))[stream_at<NT>(e, r >> 4, r & 15)];
         large |= ((((w & 0x7F7F7F7Fu) + 0x03030303u) & w) & 0x80808080u) != 0;   // a byte above 252
       }
-      if (__syncthreads_or(large)) P::template run<1>(me, a, smem, b0, b1, a0, first, acc);
-      else P::template run<0>(me, a, smem, b0, b1, a0, first, acc);
+      if (__syncthreads_or(large)) p.template run<1>(me, acc);
+      else p.template run<0>(me, acc);
     } else {
-      P::template run<1>(me, a, smem, b0, b1, a0, first, acc);
+      p.template run<1>(me, acc);
     }
   }
-  if (splits == 1) {
-    store_tile<T, DT>(a, me, smem, t0, n0, acc);
-    return;
-  }
-  const int64_t pitch = (a.N + 3) / 4 * 4;
+  // the groups' sums, in their order
+  __syncthreads();
+  float* sums = (float*)smem;
 #pragma unroll
   for (int i = 0; i < T::IB; ++i)
 #pragma unroll
     for (int j = 0; j < T::JB; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const int64_t t = t0 + (me.wm * T::IB + i) * 32 + 8 * (v / 4) + 4 * me.h + v % 4;
-        const int64_t n = n0 + (me.wn * T::JB + j) * 32 + me.r32;
-        if (t < a.M && n < a.N) a.part[(sp * a.M + t) * pitch + n] = acc[i][j][v];
+        const int t = (me.wm * T::IB + i) * 32 + 8 * (v / 4) + 4 * me.h + v % 4, n = (me.wn * T::JB + j) * 32 + me.r32;
+        sums[(p.kg * T::TM + t) * T::TN + n] = acc[i][j][v];
       }
+  __syncthreads();
+  const int64_t pitch = (a.N + 3) / 4 * 4;
+  for (int o = p.tid; o < T::TM * T::TN; o += P::THREADS) {
+    const int64_t t = t0 + o / T::TN, n = n0 + o % T::TN;
+    if (t >= a.M || n >= a.N) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int g = 0; g < KG; ++g) v += sums[g * T::TM * T::TN + o];
+    if (splits > 1) {
+      a.part[(sp * a.M + t) * pitch + n] = v;
+    } else {
+      Raw<DT, 1> out;
+      out.set(&v);
+      out.store(at<DT>(a.y, t * a.ldy), (uint32_t)n);
+    }
+  }
 }
 
 // y = the sum of the parts of K, in their order; four columns a thread.
@@ -430,16 +526,15 @@ __global__ __launch_bounds__(256) void k_w4_sum(W4Args a, int splits) {
 
 }  // namespace
 
+// Measured, us, MXFP4 with bf16, K 7168 (a compute unit does a 256 x 256 tile in about 180 us, alone in 165): 1024 tokens to
+// 7168 rows 151 in parts, 183 in tiles of 256; 2048 tokens 340 and 217; 2048 tokens to 1536 rows 90 and 175.
 W4Plan w4_plan(int64_t M, int64_t K, int64_t N) {
   if (M <= W4_FEW) return {16, 1, false};
-  const int64_t large = ((M + 255) / 256) * ((N + 255) / 256);
-  static const char* eL = getenv("W4L");
-  if (large >= (eL ? atoi(eL) : 160)) return {256, 1, true};
+  if (((M + 255) / 256) * ((N + 255) / 256) >= 160) return {256, 1, true};
   const int tokens = M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  const int64_t tiles = ((M + tokens - 1) / tokens) * ((N + 127) / 128), steps = (K + 127) / 128;
-  static const char* eS = getenv("W4S");
-  int64_t splits = std::max<int64_t>(1, (eS ? atoi(eS) : 448) / tiles);
-  splits = std::min({splits, std::max<int64_t>(1, steps / 2), (int64_t)16});
+  const int64_t tiles = ((M + tokens - 1) / tokens) * ((N + 127) / 128), units = (K + 255) / 256;
+  // one workgroup is on a compute unit at a time: as many parts as leave none without work for long
+  const int64_t splits = std::min({std::max<int64_t>(1, 240 / tiles), units, (int64_t)16});
   return {tokens, (int)splits, false};
 }
 
@@ -455,21 +550,25 @@ hipError_t launch_w4_gemm(const W4Args& a, hipStream_t s) {
       k_w4_gemm<T, D, I><<<8 * per_xcd, T::THREADS, 0, s>>>(a, tm, tn, per_xcd);
       return;
     }
-    const auto part = [&](auto tile, auto slots, auto cap) {
+    const auto part = [&](auto tile, auto kg, auto ws) {
       typedef decltype(tile) T;
+      constexpr int KG = decltype(kg)::value, CAP = 8;
       const int tm = (int)((a.M + T::TM - 1) / T::TM), tn = (int)((a.N + T::TN - 1) / T::TN);
       const int per_xcd = (tm * tn * plan.splits + 7) / 8;
-      k_w4_part<T, decltype(slots)::value, decltype(cap)::value, D, I, GL><<<8 * per_xcd, T::THREADS, 0, s>>>(
-          a, tm, tn, plan.splits, per_xcd);
+      k_w4_part<T, KG, decltype(ws)::value, CAP, D, I, GL><<<8 * per_xcd, T::THREADS * KG, 0, s>>>(a, tm, tn, plan.splits,
+                                                                                                per_xcd);
       if (plan.splits > 1) {
         const int64_t quads = a.M * ((a.N + 3) / 4);
         k_w4_sum<D><<<(unsigned)std::min<int64_t>((quads + 255) / 256, 4096), 256, 0, s>>>(a, plan.splits);
       }
     };
     using std::integral_constant;
-    if (plan.tokens == 32) part(Tile<1, 4, 1, 1>(), integral_constant<int, 5>(), integral_constant<int, 16>());
-    else if (plan.tokens == 64) part(Tile<1, 4, 2, 1>(), integral_constant<int, 4>(), integral_constant<int, 16>());
-    else part(Tile<2, 2, 2, 2>(), integral_constant<int, 3>(), integral_constant<int, 8>());
+    const integral_constant<int, 2> c2;
+    const integral_constant<int, 3> c3;
+    const integral_constant<int, 4> c4;
+    if (plan.tokens == 32) part(Tile<1, 4, 1, 1>(), c4, c4);
+    else if (plan.tokens == 64) part(Tile<1, 4, 2, 1>(), c4, c3);
+    else part(Tile<2, 4, 2, 1>(), c2, c3);
   };
   const auto types = [&](auto in, auto gl) {
     if (a.dt == DT_BF16) go(DtC<DT_BF16>(), in, gl);
