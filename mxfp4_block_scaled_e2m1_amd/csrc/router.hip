@@ -95,11 +95,29 @@ __device__ __forceinline__ float logit(const char* row, int e) {
   return r.get(0);
 }
 
-// The lane's logits of a token; -inf behind the last expert.
+// The lane's logits of a token; -inf behind the last expert. Every load is made (of the last expert where there is none), so
+// that they go out one behind the other.
 template <int DT, int G, int V>
 __device__ __forceinline__ void load_logits(const char* row, int E, int l, float (&z)[V]) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) z[i] = i * G + l < E ? logit<DT>(row, i * G + l) : -INFINITY;
+  for (int i = 0; i < V; ++i) z[i] = logit<DT>(row, min(i * G + l, E - 1));
+#pragma unroll
+  for (int i = 0; i < V; ++i) z[i] = i * G + l < E ? z[i] : -INFINITY;
+}
+
+// e^d for d <= 0, to about a step and a half of fp32; 0 below 2^-126. The rounding of d / ln 2 goes back into the result:
+// without that a probability of e^-20 is off by 40 half steps.
+__device__ __forceinline__ float exp_down(float d) {
+  d = d < -104.0f ? -104.0f : d;               // (a NaN stays)
+  const float t = d * 0x1.715476p+0f;
+  const float r = fmaf(d, 0x1.4ae0cp-26f, fmaf(d, 0x1.715476p+0f, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, r * 0x1.62e43p-1f, e);
+}
+// 1 / (1 + e^-z), to about three steps.
+__device__ __forceinline__ float sigmoid_f32(float z) {
+  const float e = exp_down(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
+  return z < 0.0f ? e * r : r;
 }
 
 // The shares p of the lane's logits, 0 for all where no expert is on (or, of
@@ -117,7 +135,7 @@ __device__ __forceinline__ void shares(const float (&z)[V], bool sigmoid, float 
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    p[i] = sigmoid ? 1.0f / (1.0f + expf(-z[i])) : expf(z[i] - top);
+    p[i] = sigmoid ? sigmoid_f32(z[i]) : exp_down(z[i] - top);
     sum += p[i];
   }
   total = group_add<G>(sum);
@@ -235,7 +253,7 @@ __device__ __forceinline__ void slot_scores(const char* row, const int32_t* sel,
   float sum = 0.0f;
 #pragma unroll
   for (int q = 0; q < MAX_TOPK / G; ++q) {
-    s[q] = sigmoid ? 1.0f / (1.0f + expf(-z[q])) : expf(z[q] - top);
+    s[q] = sigmoid ? sigmoid_f32(z[q]) : exp_down(z[q] - top);
     sum += s[q];
   }
   if (renorm) total = group_add<G>(sum);
@@ -244,12 +262,115 @@ __device__ __forceinline__ void slot_scores(const char* row, const int32_t* sel,
   for (int q = 0; q < MAX_TOPK / G; ++q) s[q] = total == 0.0f ? 0.0f : s[q] / total;
 }
 
+// What 32 bits of s + b are off by at most: the exponential's argument is rounded to 2^-24 of itself, which moves a
+// sigmoid by 2^-24 |z| s (1 - s) < 2^-26 and a softmax's share by less than 2^-25; four more roundings, the softmax's sum of
+// up to 512 terms 16 a lane, and the sum with b. With room of as much again.
+__device__ __forceinline__ float key_error(bool sigmoid, float key) {
+  return (sigmoid ? 0x1p-20f : 0x1p-17f) + 0x1p-22f * fabsf(key);
+}
+
+// The choice with a bias: 32 bits of s + b leave few experts that can be among the k, and those alone are weighed in 64
+// bits, one a lane (64 bits of all: 14.7 us instead of 8.8 for 4096 tokens of 384 experts). False where there are more of
+// them than lanes. sel: the group's k places; list, key: its LDS.
+template <int G, int V>
+__device__ __forceinline__ bool choose_by_bias(const float (&z)[V], bool sigmoid, const float* bias, int E, int k, int l,
+                                               int32_t* sel, int32_t* count, uint16_t* list, uint64_t* keys,
+                                               float* cand_z) {
+  float m = 0.0f, sum = 0.0f, a[V];
+  if (!sigmoid) {
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, z[i]);
+    m = group_fmax<G>(m);
+    if (m == -INFINITY) m = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    a[i] = sigmoid ? sigmoid_f32(z[i]) : exp_down(z[i] - m);
+    sum += a[i];
+  }
+  float inv = 1.0f;
+  if (!sigmoid) inv = __builtin_amdgcn_rcpf(group_add<G>(sum));
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = i * G + l;
+    a[i] = fmaf(a[i], inv, e < E ? bias[e] : 0.0f);
+    key[i] = z[i] == -INFINITY ? 0u : max(place(a[i]), 1u);
+  }
+  // the k-th largest, equal ones together
+  uint32_t left[V], kth = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) left[i] = key[i];
+  int got = 0;                      // of all the wave's groups the slowest sets the pace
+  while (true) {
+    uint32_t b = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) b = max(b, left[i]);
+    b = group_max<G>(b);
+    if (got < k) kth = b;
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      n += left[i] == b;
+      left[i] = left[i] == b ? 0u : left[i];
+    }
+    got += (int)group_all<G>(n, [](uint32_t p, uint32_t q) { return p + q; });
+    if (__all(got >= k || b == 0)) break;
+  }
+  // kth 0: fewer than k are on, and all of them are chosen; 1: NaN among them, and all are weighed
+  const float t = kth <= 1u ? -INFINITY : __uint_as_float((kth >> 31) ? kth & 0x7FFFFFFFu : ~kth);
+  const float least = t - 2.0f * key_error(sigmoid, t);
+  if (l == 0) *count = 0;
+  wave_lds();
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (key[i] != 0 && !(a[i] < least)) {
+      const int at = atomicAdd(count, 1);
+      if (at < G) {
+        list[at] = (uint16_t)(i * G + l);
+        cand_z[at] = z[i];
+      }
+    }
+  wave_lds();
+  const int n = *count;
+  if (!__all(n <= G)) return false;
+  double total = 1.0;
+  if (!sigmoid) {
+    double part = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) part += exp((double)z[i] - (double)m);
+    total = group_add<G>(part);
+  }
+  const int e = l < n ? list[l] : 0;
+  uint64_t mine = 0;
+  if (l < n) {
+    const double zz = (double)cand_z[l];
+    mine = place((sigmoid ? 1.0 / (1.0 + exp(-zz)) : exp(zz - (double)m) / total) + (double)bias[e]);
+    keys[l] = mine;
+  }
+  for (int j = l; j < k; j += G) sel[j] = -1;
+  wave_lds();
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint64_t o = keys[j];
+    rank += o > mine || (o == mine && list[j] < e);
+  }
+  if (l < n && rank < k) sel[rank] = e;
+  wave_lds();
+  return true;
+}
+
 template <int DT, int G, int V, bool BIAS>
 __global__ __launch_bounds__(GATE_THREADS) void k_gate(const void* __restrict__ logits, int64_t T, int E, bool sigmoid,
                                                        const float* __restrict__ bias, int k, bool renorm, float scale,
                                                        int32_t* __restrict__ ids, float* __restrict__ w) {
   constexpr int PER = GATE_THREADS / G;
   __shared__ int32_t sel[PER][MAX_TOPK];
+  __shared__ uint64_t keys[BIAS ? PER : 1][G];
+  __shared__ float cand_z[BIAS ? PER : 1][G];
+  __shared__ int32_t count[BIAS ? PER : 1];
+  __shared__ uint16_t list[BIAS ? PER : 1][G];
   const int l = threadIdx.x % G, g = threadIdx.x / G;
   for (int64_t t0 = (int64_t)blockIdx.x * PER; t0 < T; t0 += (int64_t)gridDim.x * PER) {
     const bool live = t0 + g < T;
@@ -261,13 +382,18 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate(const void* __restrict__ 
       float p[V];
       shares<G, V>(z, false, p, top, total);
     }
-    Keys<G, V, BIAS> keys;
-    keys.make(z, sigmoid, bias, E, l);
-    for (int j = 0; j < k; ++j) {
-      const int e = keys.take(l);
-      if (l == 0) sel[g][j] = e;
+    bool chosen = false;
+    if constexpr (BIAS)
+      chosen = choose_by_bias<G, V>(z, sigmoid, bias, E, k, l, sel[g], &count[g], list[g], keys[g], cand_z[g]);
+    if (!chosen) {
+      Keys<G, V, BIAS> keys_of;
+      keys_of.make(z, sigmoid, bias, E, l);
+      for (int j = 0; j < k; ++j) {
+        const int e = keys_of.take(l);
+        if (l == 0) sel[g][j] = e;
+      }
+      wave_lds();
     }
-    wave_lds();
     float s[MAX_TOPK / G];
     slot_scores<DT, G>(row, sel[g], k, E, l, sigmoid, renorm, top, total, s);
 #pragma unroll
@@ -288,7 +414,7 @@ __device__ __forceinline__ void tokens_of(const int32_t* seq_off, int64_t q, int
   b = seq_off != nullptr ? min(max((int64_t)seq_off[q + 1], a), T) : T;
 }
 
-constexpr int BAL_THREADS = 512;
+constexpr int BAL_THREADS = 1024;
 constexpr int BAL_WAVES = BAL_THREADS / 64;
 
 // One expert's count and sum of shares in a sequence are summed by one thread, which
@@ -303,8 +429,8 @@ __device__ __forceinline__ void balance_out(int64_t q, int64_t n, int E, int k, 
   if (e == 0) loss[q] = coef * ((float)E / (float)k) * v[0];
 }
 
-// Workgroup (split, sequence): the sums of p and the counts over its part of the
-// sequence's tokens.
+// Workgroup (split, sequence): the sums of p and the counts over its part of the sequence's
+// tokens.
 template <int DT, int G, int V>
 __global__ __launch_bounds__(BAL_THREADS) void k_balance(const void* __restrict__ logits, int64_t T, int E, bool sigmoid,
                                                          const int32_t* __restrict__ ids, int k,
@@ -313,30 +439,35 @@ __global__ __launch_bounds__(BAL_THREADS) void k_balance(const void* __restrict_
                                                          float* __restrict__ loss, int32_t* __restrict__ counts) {
   constexpr int PER = BAL_THREADS / G;
   __shared__ float sums[BAL_WAVES][G * V];
-  __shared__ int32_t hist[BAL_THREADS];
+  __shared__ int32_t hist[512];
   __shared__ float red[16];
   const int64_t q = blockIdx.y;
   int64_t a, b;
   tokens_of(seq_off, q, T, a, b);
   const int64_t per = (b - a + gridDim.x - 1) / gridDim.x;
   const int64_t lo = min(b, a + per * blockIdx.x), hi = min(b, lo + per);
-  hist[threadIdx.x] = 0;
-  __syncthreads();
-  for (int64_t i = lo * k + threadIdx.x; i < hi * k; i += BAL_THREADS) {
-    const uint32_t e = (uint32_t)ids[i];
-    if (e < (uint32_t)E) atomicAdd(&hist[e], 1);
-  }
   const int l = threadIdx.x % G, g = threadIdx.x / G;
+  const int64_t slots = (hi - lo) * k;
+  uint32_t first = E;
+  if ((int64_t)threadIdx.x < slots) first = (uint32_t)ids[lo * k + threadIdx.x];
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+  if (threadIdx.x < 512) hist[threadIdx.x] = 0;
+  __syncthreads();
   for (int64_t t0 = lo; t0 < hi; t0 += PER) {
-    const bool live = t0 + g < hi;
     float z[V], p[V], top, total;
-    load_logits<DT, G, V>(at<DT>(logits, (live ? t0 + g : hi - 1) * E), E, l, z);
+    load_logits<DT, G, V>(at<DT>(logits, min(t0 + g, hi - 1) * E), E, l, z);
+    if (t0 == lo) {
+      if (first < (uint32_t)E) atomicAdd(&hist[first], 1);
+      for (int64_t i = threadIdx.x + BAL_THREADS; i < slots; i += BAL_THREADS) {
+        const uint32_t e = (uint32_t)ids[lo * k + i];
+        if (e < (uint32_t)E) atomicAdd(&hist[e], 1);
+      }
+    }
     shares<G, V>(z, sigmoid, p, top, total);
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] += live ? p[i] : 0.0f;
+    for (int i = 0; i < V; ++i) acc[i] += t0 + g < hi ? p[i] : 0.0f;
   }
   // over the wave's groups, then the waves
 #pragma unroll
@@ -355,7 +486,7 @@ __global__ __launch_bounds__(BAL_THREADS) void k_balance(const void* __restrict_
 #pragma unroll
     for (int i = 0; i < BAL_WAVES; ++i) p += sums[i][threadIdx.x];
   }
-  const int c = hist[threadIdx.x];
+  const int c = threadIdx.x < 512 ? hist[threadIdx.x] : 0;
   if (part_p == nullptr) {
     balance_out(q, b - a, E, k, coef, c, p, red, loss, counts);
   } else if ((int)threadIdx.x < E) {
@@ -365,26 +496,58 @@ __global__ __launch_bounds__(BAL_THREADS) void k_balance(const void* __restrict_
   }
 }
 
-// The parts of a sequence, in their order.
+// The parts of a sequence, in their order: runs of them side by side, then the runs.
 __global__ __launch_bounds__(BAL_THREADS) void k_balance_sum(const float* __restrict__ part_p,
                                                              const int32_t* __restrict__ part_c, int splits, int64_t T,
                                                              int E, int k, const int32_t* __restrict__ seq_off, float coef,
                                                              float* __restrict__ loss, int32_t* __restrict__ counts) {
-  __shared__ float red[16];
+  __shared__ float red[16], sum_p[BAL_THREADS];
+  __shared__ int32_t sum_c[BAL_THREADS];
   const int64_t q = blockIdx.x;
   int64_t a, b;
   tokens_of(seq_off, q, T, a, b);
+  const int runs = min(BAL_THREADS / E, 8), run = threadIdx.x / E, e = threadIdx.x - run * E;
   float p = 0.0f;
   int c = 0;
-  if ((int)threadIdx.x < E) {
-    const int64_t at = q * splits * E + threadIdx.x;
-#pragma unroll 8
-    for (int i = 0; i < splits; ++i) {
+  if (run < runs) {
+    const int64_t at = q * splits * E + e;
+#pragma unroll 16
+    for (int i = splits * run / runs; i < splits * (run + 1) / runs; ++i) {
       p += part_p[at + (int64_t)i * E];
       c += part_c[at + (int64_t)i * E];
     }
   }
+  sum_p[threadIdx.x] = p;
+  sum_c[threadIdx.x] = c;
+  __syncthreads();
+  if (run == 0) {
+    for (int i = 1; i < runs; ++i) {
+      p += sum_p[i * E + e];
+      c += sum_c[i * E + e];
+    }
+  }
   balance_out(q, b - a, E, k, coef, c, p, red, loss, counts);
+}
+
+// The last of the S + 1 offsets that is at or before t, G of them at a time; -1 where t is before all of them.
+template <int G>
+__device__ __forceinline__ int64_t sequence_of(const int32_t* seq_off, int64_t S, int64_t t, int l) {
+  int64_t lo = 0, n = S + 1;        // the last offset at or before t is one of lo .. lo + n - 1, or none
+  while (n > G) {
+    const int64_t step = (n + G - 1) / G, at = lo + step * l;
+    const uint32_t before = group_all<G>(step * l < n && seq_off[min(at, S)] <= t ? 1u : 0u,
+                                         [](uint32_t p, uint32_t q) { return p + q; });
+    if (before > 0) {
+      const int64_t skip = step * (int64_t)(before - 1);
+      lo += skip;
+      n = min(step, n - skip);
+    } else {
+      n = 1;
+    }
+  }
+  const uint32_t here = group_all<G>(l < n && seq_off[min(lo + l, S)] <= t ? 1u : 0u,
+                                     [](uint32_t p, uint32_t q) { return p + q; });
+  return here == 0 ? -1 : lo + here - 1;
 }
 
 struct GateGrad {
@@ -416,29 +579,35 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
     const int64_t t = live ? t0 + g : a.T - 1;
     const char* row = at<DT>(a.logits, t * E);
     float z[V], p[V], d[V], top, total;
+    // everything that hangs on nothing else is asked for first
     load_logits<DT, G, V>(row, E, l, z);
+    int32_t id[Q];
+    float dw[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int64_t j = t * k + min(q * G + l, k - 1);
+      id[q] = a.d_w != nullptr ? a.ids[j] : -1;
+      dw[q] = a.d_w != nullptr ? a.d_w[j] : 0.0f;
+    }
+    int64_t lo = 0;
+    if (a.counts != nullptr && a.seq_off != nullptr) lo = sequence_of<G>(a.seq_off, a.S, t, l);
+    lo = min(lo, a.S - 1);          // (behind the last sequence: it does not reach t)
     shares<G, V>(z, a.sigmoid, p, top, total);
 #pragma unroll
     for (int i = 0; i < V; ++i) d[i] = 0.0f;
     if (a.counts != nullptr) {
-      // the last sequence that starts at or before t, if it reaches t
-      int64_t lo = 0, n = a.S;
-      if (a.seq_off != nullptr) {
-        while (n > 1) {
-          const int64_t half = n >> 1;
-          if (a.seq_off[lo + half] <= t) { lo += half; n -= half; }
-          else n = half;
-        }
+      float f = 0.0f;
+      if (lo >= 0) {
+        int64_t first, last;
+        tokens_of(a.seq_off, lo, a.T, first, last);
+        const float inv = 1.0f / (float)max(last - first, (int64_t)1);
+        if (t >= first && t < last) f = a.coef * ((float)E / (float)k) * a.d_loss[lo] * inv * inv;
       }
-      int64_t first, last;
-      tokens_of(a.seq_off, lo, a.T, first, last);
-      const float inv = 1.0f / (float)max(last - first, (int64_t)1);
-      const float f = t >= first && t < last ? a.coef * ((float)E / (float)k) * a.d_loss[lo] * inv * inv : 0.0f;
       float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int e = i * G + l;
-        d[i] = e < E ? f * (float)a.counts[lo * E + e] : 0.0f;
+        d[i] = e < E && lo >= 0 ? f * (float)a.counts[lo * E + e] : 0.0f;
         dot = fmaf(p[i], d[i], dot);
       }
       dot = group_add<G>(dot);
@@ -449,16 +618,15 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const int j = q * G + l;
-        if (j < k) sel[g][j] = a.ids[t * k + j];
+        if (j < k) sel[g][j] = id[q];
       }
       wave_lds();
-      float s[Q], dw[Q], mean = 0.0f;
+      float s[Q], mean = 0.0f;
       slot_scores<DT, G>(row, sel[g], k, E, l, a.sigmoid, a.renorm, top, total, s);
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const int j = q * G + l;
-        const bool has = j < k && (unsigned)sel[g][j] < (unsigned)E;
-        dw[q] = has ? a.d_w[t * k + j] : 0.0f;
+        if (!(j < k && (unsigned)id[q] < (unsigned)E)) dw[q] = 0.0f;
         mean = fmaf(s[q], dw[q], mean);
       }
       mean = a.renorm ? group_add<G>(mean) : 0.0f;
@@ -488,7 +656,7 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = i * G + l;
-      if (a.sigmoid) d[i] *= 1.0f / (1.0f + expf(z[i]));
+      if (a.sigmoid) d[i] *= sigmoid_f32(-z[i]);
       Raw<DT, 1> o;
       o.set(&d[i]);
       if (live && e < E) o.store(out, (uint32_t)e);
@@ -500,11 +668,15 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
 template <class F>
 void dispatch_experts(int E, F&& f) {
   using std::integral_constant;
-  if (E <= 64) f(integral_constant<int, 16>(), integral_constant<int, 4>());
-  else if (E <= 128) f(integral_constant<int, 16>(), integral_constant<int, 8>());
-  else if (E <= 256) f(integral_constant<int, 32>(), integral_constant<int, 8>());
-  else if (E <= 384) f(integral_constant<int, 32>(), integral_constant<int, 12>());
-  else f(integral_constant<int, 32>(), integral_constant<int, 16>());
+  const integral_constant<int, 16> g16;
+  const integral_constant<int, 32> g32;
+  if (E <= 64) f(g16, integral_constant<int, 4>());
+  else if (E <= 128) f(g16, integral_constant<int, 8>());
+  else if (E <= 192) f(g32, integral_constant<int, 6>());
+  else if (E <= 256) f(g32, integral_constant<int, 8>());
+  else if (E <= 320) f(g32, integral_constant<int, 10>());
+  else if (E <= 384) f(g32, integral_constant<int, 12>());
+  else f(g32, integral_constant<int, 16>());
 }
 
 unsigned token_grid(int64_t T, int per) { return (unsigned)std::min<int64_t>((T + per - 1) / per, (int64_t)1 << 20); }
@@ -527,8 +699,8 @@ hipError_t launch_gate(const void* logits, DType dt, int64_t T, int E, bool sigm
 }
 
 int balance_splits(int64_t T, int64_t S) {
-  // at most 64 parts of a sequence, of 32 tokens or more on average, about 512 workgroups
-  return (int)std::max<int64_t>(1, std::min({(int64_t)64, T / S / 32, (512 + S - 1) / S}));
+  // parts of a sequence: of 32 tokens or more on average, at most 80, about 512 workgroups in all
+  return (int)std::max<int64_t>(1, std::min({(int64_t)80, T / S / 32, (512 + S - 1) / S}));
 }
 
 hipError_t launch_balance(const void* logits, DType dt, int64_t T, int E, bool sigmoid, const int32_t* ids, int k,

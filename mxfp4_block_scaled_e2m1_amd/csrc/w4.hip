@@ -122,13 +122,14 @@ __global__ __launch_bounds__(64 * W) void k_w4(W4Args a) {
     if (a.whole_dwords) {
       stream_copies<NT, W>(scales, n0, a.N, lds0 + RING, wave, lane);
       if (INT) stream_copies<NT, W>(zeros, n0, a.N, lds0 + ZEROS, wave, lane);
-    } else {
-      stream_loads<NT, 64 * W>(scales, n0, a.N, ssc);
-      if (INT) stream_loads<NT, 64 * W>(zeros, n0, a.N, szp);
     }
     // all codes that the ring takes, then the activations
     for (int i = 0; i < min(DW, mine); ++i) copy_w(i);
     for (int n = 0; n < min(RX, pieces); ++n) copy_x(n);
+    if (!a.whole_dwords) {
+      stream_loads<NT, 64 * W>(scales, n0, a.N, ssc);
+      if (INT) stream_loads<NT, 64 * W>(zeros, n0, a.N, szp);
+    }
     if (mine >= DW && pieces >= RX) wait_copies<DW * NT + RX>();
     else wait_copies<0>();
     lds_barrier();                 // the scales are there

@@ -451,11 +451,12 @@ __global__ __launch_bounds__(T::THREADS* KG) void k_w4_part(W4Args a, int tiles_
     if (a.whole_dwords) {
       stream_copies<NT, W>(scales, n0, a.N, p.lds + P::SCALES, p.wave, p.lane);
       if (INT) stream_copies<NT, W>(zeros, n0, a.N, p.lds + P::ZEROS, p.wave, p.lane);
-    } else {
+    }
+    p.start();
+    if (!a.whole_dwords) {
       stream_loads<NT, P::THREADS>(scales, n0, a.N, (uint32_t*)(smem + P::SCALES));
       if (INT) stream_loads<NT, P::THREADS>(zeros, n0, a.N, (uint32_t*)(smem + P::ZEROS));
     }
-    p.start();
     p.wait_before_start();
     lds_barrier();                 // the scales are there
     if constexpr (INT) {
