@@ -1863,10 +1863,8 @@ size_t mx_moe_balance_workspace_size(int64_t T, int32_t E, int64_t S) {
   if (T < 0 || T > ((int64_t)1 << 26) || E < 1 || E > ROUTE_MAX_EXPERTS || S < 1 || S > (1 << 20) ||
       S * E > ((int64_t)1 << 28))
     return 0;
-  const int parts = balance_splits(T, S);
-  if (parts == 1) return 0;
   Carve c(nullptr);
-  c.take((size_t)(S * parts * E) * 8);
+  c.take((size_t)(balance_parts(T, S) * E) * 8);
   return c.off;
 }
 

@@ -331,9 +331,8 @@ hipError_t launch_lora(const LoraArgs& p, hipStream_t s);
 constexpr int MAX_TOPK = 64;
 hipError_t launch_gate(const void* logits, DType dt, int64_t T, int E, bool sigmoid, const float* bias, int k,
                        bool renorm, float scale, int32_t* ids, float* w, hipStream_t s);
-// Parts that a sequence's tokens are summed in; `part` holds S * parts * E floats and as
-// many ints (not used with one part).
-int balance_splits(int64_t T, int64_t S);
+// Rows of E sums that `part` has room for, as floats and again as ints; 0 where it is not used.
+int64_t balance_parts(int64_t T, int64_t S);
 hipError_t launch_balance(const void* logits, DType dt, int64_t T, int E, bool sigmoid, const int32_t* ids, int k,
                           const int32_t* seq_off, int64_t S, float coef, float* part, float* loss, int32_t* counts,
                           hipStream_t s);

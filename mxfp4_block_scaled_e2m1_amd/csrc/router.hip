@@ -114,16 +114,23 @@ __device__ __forceinline__ float exp_down(float d) {
   const float e = __builtin_amdgcn_exp2f(t);
   return fmaf(e, r * 0x1.62e43p-1f, e);
 }
-// 1 / (1 + e^-z), to about three steps.
-__device__ __forceinline__ float sigmoid_f32(float z) {
+// 1 / (1 + e^-z), and what it leaves of 1 without the cancellation, to about three steps.
+__device__ __forceinline__ float sigmoid_f32(float z, float& rest) {
   const float e = exp_down(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
+  rest = z < 0.0f ? r : e * r;
   return z < 0.0f ? e * r : r;
+}
+__device__ __forceinline__ float sigmoid_f32(float z) {
+  float rest;
+  return sigmoid_f32(z, rest);
 }
 
 // The shares p of the lane's logits, 0 for all where no expert is on (or, of
-// sigmoids, none is above 0). Also the softmax's largest logit and sum.
+// sigmoids, none is above 0). Also the softmax's largest logit, the sum of the scores, and what the sigmoids leave of 1
+// (of a softmax: 1).
 template <int G, int V>
-__device__ __forceinline__ void shares(const float (&z)[V], bool sigmoid, float (&p)[V], float& top, float& total) {
+__device__ __forceinline__ void shares(const float (&z)[V], bool sigmoid, float (&p)[V], float (&rest)[V], float& top,
+                                       float& total) {
   top = 0.0f;
   if (!sigmoid) {
     float m = -INFINITY;
@@ -135,7 +142,8 @@ __device__ __forceinline__ void shares(const float (&z)[V], bool sigmoid, float 
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    p[i] = sigmoid ? sigmoid_f32(z[i]) : exp_down(z[i] - top);
+    rest[i] = 1.0f;
+    p[i] = sigmoid ? sigmoid_f32(z[i], rest[i]) : exp_down(z[i] - top);
     sum += p[i];
   }
   total = group_add<G>(sum);
@@ -269,96 +277,129 @@ __device__ __forceinline__ float key_error(bool sigmoid, float key) {
   return (sigmoid ? 0x1p-20f : 0x1p-17f) + 0x1p-22f * fabsf(key);
 }
 
-// The choice with a bias: 32 bits of s + b leave few experts that can be among the k, and those alone are weighed in 64
-// bits, one a lane (64 bits of all: 14.7 us instead of 8.8 for 4096 tokens of 384 experts). False where there are more of
-// them than lanes. sel: the group's k places; list, key: its LDS.
-template <int G, int V>
-__device__ __forceinline__ bool choose_by_bias(const float (&z)[V], bool sigmoid, const float* bias, int E, int k, int l,
-                                               int32_t* sel, int32_t* count, uint16_t* list, uint64_t* keys,
-                                               float* cand_z) {
-  float m = 0.0f, sum = 0.0f, a[V];
-  if (!sigmoid) {
-    m = -INFINITY;
+// A token's candidates: a group's lanes each have one.
+template <int G>
+struct Candidates {
+  uint64_t key[G];
+  float z[G];
+  uint16_t e[G];
+};
+
+// The choice for k <= G. The k-th largest of the lanes' largest keys is at most the k-th largest of all: the few keys from
+// there on (less, with a bias, what its 32 bits may be off) are all that can be chosen, and are ranked against each other,
+// one a lane. A round over all keys for each of the k instead took 7.5 us for 4096 tokens of 384 experts, and with the
+// bias, all sums in 64 bits, 14.7. Returns the lane's rank (k or more: not chosen; its logit and expert are then of no
+// use), or -1 for all where there are more candidates than lanes.
+template <int G, int V, bool BIAS>
+__device__ __forceinline__ int choose(const float (&z)[V], bool sigmoid, const float (&b)[V], const float* bias, int k,
+                                      int l, Candidates<G>& c, int& n, float& cz, int& ce) {
+  float m = 0.0f, a[V];
+  uint32_t key[V], most = 0;
+  if constexpr (BIAS) {
+    float sum = 0.0f, inv = 1.0f;
+    if (!sigmoid) {
+      m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = fmaxf(m, z[i]);
-    m = group_fmax<G>(m);
-    if (m == -INFINITY) m = 0.0f;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    a[i] = sigmoid ? sigmoid_f32(z[i]) : exp_down(z[i] - m);
-    sum += a[i];
-  }
-  float inv = 1.0f;
-  if (!sigmoid) inv = __builtin_amdgcn_rcpf(group_add<G>(sum));
-  uint32_t key[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = i * G + l;
-    a[i] = fmaf(a[i], inv, e < E ? bias[e] : 0.0f);
-    key[i] = z[i] == -INFINITY ? 0u : max(place(a[i]), 1u);
-  }
-  // the k-th largest, equal ones together
-  uint32_t left[V], kth = 0;
-#pragma unroll
-  for (int i = 0; i < V; ++i) left[i] = key[i];
-  int got = 0;                      // of all the wave's groups the slowest sets the pace
-  while (true) {
-    uint32_t b = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) b = max(b, left[i]);
-    b = group_max<G>(b);
-    if (got < k) kth = b;
-    uint32_t n = 0;
+      for (int i = 0; i < V; ++i) m = fmaxf(m, z[i]);
+      m = group_fmax<G>(m);
+      if (m == -INFINITY) m = 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      n += left[i] == b;
-      left[i] = left[i] == b ? 0u : left[i];
+      a[i] = sigmoid ? sigmoid_f32(z[i]) : exp_down(z[i] - m);
+      sum += a[i];
     }
-    got += (int)group_all<G>(n, [](uint32_t p, uint32_t q) { return p + q; });
-    if (__all(got >= k || b == 0)) break;
+    if (!sigmoid) inv = __builtin_amdgcn_rcpf(group_add<G>(sum));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      a[i] = fmaf(a[i], inv, b[i]);
+      key[i] = z[i] == -INFINITY ? 0u : max(place(a[i]), 1u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = place(z[i]);
   }
-  // kth 0: fewer than k are on, and all of them are chosen; 1: NaN among them, and all are weighed
-  const float t = kth <= 1u ? -INFINITY : __uint_as_float((kth >> 31) ? kth & 0x7FFFFFFFu : ~kth);
-  const float least = t - 2.0f * key_error(sigmoid, t);
-  if (l == 0) *count = 0;
-  wave_lds();
+#pragma unroll
+  for (int i = 0; i < V; ++i) most = max(most, key[i]);
+  uint32_t kth = 0;
+  for (int got = 0;;) {             // of the wave's groups the slowest sets the pace
+    const uint32_t top = group_max<G>(most);
+    if (got < k) kth = top;
+    got += (int)group_all<G>(most == top ? 1u : 0u, [](uint32_t p, uint32_t q) { return p + q; });
+    if (most == top) most = 0;
+    if (__all(got >= k || top == 0)) break;
+  }
+  uint32_t least = max(kth, 1u);
+  if constexpr (BIAS) {
+    // kth 0 or 1: fewer than k lanes have a number, and all keys are candidates
+    if (kth > 1u) {
+      const float t = __uint_as_float((kth >> 31) ? kth & 0x7FFFFFFFu : ~kth), s = t - 2.0f * key_error(sigmoid, t);
+      least = s == s ? max(place(s), 1u) : 1u;
+    } else {
+      least = 1u;
+    }
+  }
+  // the lanes' candidates one behind the other
+  uint32_t mine = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) mine += key[i] >= least || (BIAS && key[i] == 1u) ? 1u : 0u;
+  const auto add = [](uint32_t p, uint32_t q) { return p + q; };
+  uint32_t at = mine;
+  at += __builtin_amdgcn_update_dpp(0u, at, 0x111, 0xF, 0xF, false);      // row_shr 1, 2, 4, 8
+  at += __builtin_amdgcn_update_dpp(0u, at, 0x112, 0xF, 0xF, false);
+  at += __builtin_amdgcn_update_dpp(0u, at, 0x114, 0xF, 0xF, false);
+  at += __builtin_amdgcn_update_dpp(0u, at, 0x118, 0xF, 0xF, false);
+  uint32_t all = group_all<16>(mine, add);
+  at -= mine;
+  if constexpr (G == 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(all, all, false, false);
+    if (l >= 16) at += r[0];
+    all = r[0] + r[1];
+  }
+  n = (int)all;
+  if (!__all(n <= G)) return -1;
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (key[i] != 0 && !(a[i] < least)) {
-      const int at = atomicAdd(count, 1);
-      if (at < G) {
-        list[at] = (uint16_t)(i * G + l);
-        cand_z[at] = z[i];
-      }
+    if (key[i] >= least || (BIAS && key[i] == 1u)) {
+      c.e[at] = (uint16_t)(i * G + l);
+      c.z[at] = z[i];
+      if (!BIAS) c.key[at] = key[i];
+      ++at;
     }
-  wave_lds();
-  const int n = *count;
-  if (!__all(n <= G)) return false;
   double total = 1.0;
-  if (!sigmoid) {
-    double part = 0.0;
+  if constexpr (BIAS) {
+    if (!sigmoid) {
+      double part = 0.0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) part += exp((double)z[i] - (double)m);
-    total = group_add<G>(part);
+      for (int i = 0; i < V; ++i) part += exp((double)z[i] - (double)m);
+      total = group_add<G>(part);
+    }
   }
-  const int e = l < n ? list[l] : 0;
-  uint64_t mine = 0;
+  wave_lds();
+  uint64_t own = 0;
+  ce = -1;
+  cz = -INFINITY;
   if (l < n) {
-    const double zz = (double)cand_z[l];
-    mine = place((sigmoid ? 1.0 / (1.0 + exp(-zz)) : exp(zz - (double)m) / total) + (double)bias[e]);
-    keys[l] = mine;
+    ce = c.e[l];
+    cz = c.z[l];
+    if constexpr (BIAS) {
+      const double zz = (double)cz;
+      own = place((sigmoid ? 1.0 / (1.0 + exp(-zz)) : exp(zz - (double)m) / total) + (double)bias[ce]);
+      c.key[l] = own;
+    } else {
+      own = c.key[l];
+    }
   }
-  for (int j = l; j < k; j += G) sel[j] = -1;
-  wave_lds();
-  int rank = 0;
+  if (BIAS) wave_lds();
+  int rank = l < n ? 0 : G;
+  // (list positions are not in the order of experts)
+#pragma unroll 4
   for (int j = 0; j < n; ++j) {
-    const uint64_t o = keys[j];
-    rank += o > mine || (o == mine && list[j] < e);
+    const uint64_t o = c.key[j];
+    rank += o > own || (o == own && (int)c.e[j] < ce);
   }
-  if (l < n && rank < k) sel[rank] = e;
   wave_lds();
-  return true;
+  return rank;
 }
 
 template <int DT, int G, int V, bool BIAS>
@@ -367,33 +408,59 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate(const void* __restrict__ 
                                                        int32_t* __restrict__ ids, float* __restrict__ w) {
   constexpr int PER = GATE_THREADS / G;
   __shared__ int32_t sel[PER][MAX_TOPK];
-  __shared__ uint64_t keys[BIAS ? PER : 1][G];
-  __shared__ float cand_z[BIAS ? PER : 1][G];
-  __shared__ int32_t count[BIAS ? PER : 1];
-  __shared__ uint16_t list[BIAS ? PER : 1][G];
+  __shared__ Candidates<G> cand[PER];
   const int l = threadIdx.x % G, g = threadIdx.x / G;
   for (int64_t t0 = (int64_t)blockIdx.x * PER; t0 < T; t0 += (int64_t)gridDim.x * PER) {
     const bool live = t0 + g < T;
     const int64_t t = live ? t0 + g : T - 1;        // all lanes go along: DPP reads only active ones
     const char* row = at<DT>(logits, t * E);
-    float z[V], top = 0.0f, total = 1.0f;
+    float z[V], b[V], top = 0.0f, total = 1.0f;
     load_logits<DT, G, V>(row, E, l, z);
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = BIAS ? bias[min(i * G + l, E - 1)] : 0.0f;
     if (!sigmoid && !renorm) {
-      float p[V];
-      shares<G, V>(z, false, p, top, total);
+      float p[V], rest[V];
+      shares<G, V>(z, false, p, rest, top, total);
     }
-    bool chosen = false;
-    if constexpr (BIAS)
-      chosen = choose_by_bias<G, V>(z, sigmoid, bias, E, k, l, sel[g], &count[g], list[g], keys[g], cand_z[g]);
-    if (!chosen) {
-      Keys<G, V, BIAS> keys_of;
-      keys_of.make(z, sigmoid, bias, E, l);
-      for (int j = 0; j < k; ++j) {
-        const int e = keys_of.take(l);
-        if (l == 0) sel[g][j] = e;
+    int rank = -1, n = 0, e = 0;
+    float ze = 0.0f;
+    if (k <= G) rank = choose<G, V, BIAS>(z, sigmoid, b, bias, k, l, cand[g], n, ze, e);
+    if (rank >= 0) {
+      // a lane has a slot: the chosen expert's score, as slot_scores forms it
+      const bool mine = rank < k;
+      if (!mine) ze = -INFINITY;
+      if (!sigmoid && renorm) {
+        top = group_fmax<G>(ze);
+        if (top == -INFINITY) top = 0.0f;
       }
-      wave_lds();
+      float s = sigmoid ? sigmoid_f32(ze) : exp_down(ze - top);
+      if (renorm) {
+        // over the slots in their order, whichever lane they are in
+        if (mine) cand[g].z[rank] = s;
+        wave_lds();
+        total = group_add<G>(l < min(n, k) ? cand[g].z[l] : 0.0f);
+        wave_lds();
+      } else if (sigmoid) {
+        total = 1.0f;
+      }
+      s = total == 0.0f ? 0.0f : s / total;
+      if (live && mine) {
+        ids[t * k + rank] = e;
+        w[t * k + rank] = scale * s;
+      }
+      if (live && l >= n && l < k) {                 // fewer than k are on
+        ids[t * k + l] = -1;
+        w[t * k + l] = 0.0f;
+      }
+      continue;
     }
+    Keys<G, V, BIAS> keys;
+    keys.make(z, sigmoid, bias, E, l);
+    for (int j = 0; j < k; ++j) {
+      const int best = keys.take(l);
+      if (l == 0) sel[g][j] = best;
+    }
+    wave_lds();
     float s[MAX_TOPK / G];
     slot_scores<DT, G>(row, sel[g], k, E, l, sigmoid, renorm, top, total, s);
 #pragma unroll
@@ -412,121 +479,6 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate(const void* __restrict__ 
 __device__ __forceinline__ void tokens_of(const int32_t* seq_off, int64_t q, int64_t T, int64_t& a, int64_t& b) {
   a = seq_off != nullptr ? min(max((int64_t)seq_off[q], (int64_t)0), T) : 0;
   b = seq_off != nullptr ? min(max((int64_t)seq_off[q + 1], a), T) : T;
-}
-
-constexpr int BAL_THREADS = 1024;
-constexpr int BAL_WAVES = BAL_THREADS / 64;
-
-// One expert's count and sum of shares in a sequence are summed by one thread, which
-// has them as `c` and `p`; the workgroup sums the loss.
-__device__ __forceinline__ void balance_out(int64_t q, int64_t n, int E, int k, float coef, int c, float p, float* red,
-                                            float* loss, int32_t* counts) {
-  const int e = threadIdx.x;
-  if (e < E) counts[q * E + e] = c;
-  const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
-  float v[1] = {e < E ? ((float)c * inv) * (p * inv) : 0.0f};
-  group_sum<1>(v, red, BAL_WAVES, threadIdx.x & 63, threadIdx.x >> 6);
-  if (e == 0) loss[q] = coef * ((float)E / (float)k) * v[0];
-}
-
-// Workgroup (split, sequence): the sums of p and the counts over its part of the sequence's
-// tokens.
-template <int DT, int G, int V>
-__global__ __launch_bounds__(BAL_THREADS) void k_balance(const void* __restrict__ logits, int64_t T, int E, bool sigmoid,
-                                                         const int32_t* __restrict__ ids, int k,
-                                                         const int32_t* __restrict__ seq_off, float coef,
-                                                         float* __restrict__ part_p, int32_t* __restrict__ part_c,
-                                                         float* __restrict__ loss, int32_t* __restrict__ counts) {
-  constexpr int PER = BAL_THREADS / G;
-  __shared__ float sums[BAL_WAVES][G * V];
-  __shared__ int32_t hist[512];
-  __shared__ float red[16];
-  const int64_t q = blockIdx.y;
-  int64_t a, b;
-  tokens_of(seq_off, q, T, a, b);
-  const int64_t per = (b - a + gridDim.x - 1) / gridDim.x;
-  const int64_t lo = min(b, a + per * blockIdx.x), hi = min(b, lo + per);
-  const int l = threadIdx.x % G, g = threadIdx.x / G;
-  const int64_t slots = (hi - lo) * k;
-  uint32_t first = E;
-  if ((int64_t)threadIdx.x < slots) first = (uint32_t)ids[lo * k + threadIdx.x];
-  float acc[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-  if (threadIdx.x < 512) hist[threadIdx.x] = 0;
-  __syncthreads();
-  for (int64_t t0 = lo; t0 < hi; t0 += PER) {
-    float z[V], p[V], top, total;
-    load_logits<DT, G, V>(at<DT>(logits, min(t0 + g, hi - 1) * E), E, l, z);
-    if (t0 == lo) {
-      if (first < (uint32_t)E) atomicAdd(&hist[first], 1);
-      for (int64_t i = threadIdx.x + BAL_THREADS; i < slots; i += BAL_THREADS) {
-        const uint32_t e = (uint32_t)ids[lo * k + i];
-        if (e < (uint32_t)E) atomicAdd(&hist[e], 1);
-      }
-    }
-    shares<G, V>(z, sigmoid, p, top, total);
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] += t0 + g < hi ? p[i] : 0.0f;
-  }
-  // over the wave's groups, then the waves
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if constexpr (G == 16) {
-      const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i]), __float_as_uint(acc[i]), false, false);
-      acc[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    }
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i]), __float_as_uint(acc[i]), false, false);
-    acc[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    if ((threadIdx.x & 63) < G) sums[threadIdx.x >> 6][i * G + l] = acc[i];
-  }
-  __syncthreads();
-  float p = 0.0f;
-  if (threadIdx.x < G * V) {
-#pragma unroll
-    for (int i = 0; i < BAL_WAVES; ++i) p += sums[i][threadIdx.x];
-  }
-  const int c = threadIdx.x < 512 ? hist[threadIdx.x] : 0;
-  if (part_p == nullptr) {
-    balance_out(q, b - a, E, k, coef, c, p, red, loss, counts);
-  } else if ((int)threadIdx.x < E) {
-    const int64_t at = (q * gridDim.x + blockIdx.x) * E + threadIdx.x;
-    part_p[at] = p;
-    part_c[at] = c;
-  }
-}
-
-// The parts of a sequence, in their order: runs of them side by side, then the runs.
-__global__ __launch_bounds__(BAL_THREADS) void k_balance_sum(const float* __restrict__ part_p,
-                                                             const int32_t* __restrict__ part_c, int splits, int64_t T,
-                                                             int E, int k, const int32_t* __restrict__ seq_off, float coef,
-                                                             float* __restrict__ loss, int32_t* __restrict__ counts) {
-  __shared__ float red[16], sum_p[BAL_THREADS];
-  __shared__ int32_t sum_c[BAL_THREADS];
-  const int64_t q = blockIdx.x;
-  int64_t a, b;
-  tokens_of(seq_off, q, T, a, b);
-  const int runs = min(BAL_THREADS / E, 8), run = threadIdx.x / E, e = threadIdx.x - run * E;
-  float p = 0.0f;
-  int c = 0;
-  if (run < runs) {
-    const int64_t at = q * splits * E + e;
-#pragma unroll 16
-    for (int i = splits * run / runs; i < splits * (run + 1) / runs; ++i) {
-      p += part_p[at + (int64_t)i * E];
-      c += part_c[at + (int64_t)i * E];
-    }
-  }
-  sum_p[threadIdx.x] = p;
-  sum_c[threadIdx.x] = c;
-  __syncthreads();
-  if (run == 0) {
-    for (int i = 1; i < runs; ++i) {
-      p += sum_p[i * E + e];
-      c += sum_c[i * E + e];
-    }
-  }
-  balance_out(q, b - a, E, k, coef, c, p, red, loss, counts);
 }
 
 // The last of the S + 1 offsets that is at or before t, G of them at a time; -1 where t is before all of them.
@@ -548,6 +500,152 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* seq_off, int64_t S
   const uint32_t here = group_all<G>(l < n && seq_off[min(lo + l, S)] <= t ? 1u : 0u,
                                      [](uint32_t p, uint32_t q) { return p + q; });
   return here == 0 ? -1 : lo + here - 1;
+}
+
+constexpr int BAL_THREADS = 1024;
+constexpr int BAL_WAVES = BAL_THREADS / 64;
+
+// One expert's count and sum of shares in a sequence are summed by one thread, which
+// has them as `c` and `p`; the workgroup sums the loss.
+__device__ __forceinline__ void balance_out(int64_t q, int64_t n, int E, int k, float coef, int c, float p, float* red,
+                                            float* loss, int32_t* counts) {
+  const int e = threadIdx.x;
+  if (e < E) counts[q * E + e] = c;
+  const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
+  float v[1] = {e < E ? ((float)c * inv) * (p * inv) : 0.0f};
+  group_sum<1>(v, red, BAL_WAVES, threadIdx.x & 63, threadIdx.x >> 6);
+  if (e == 0) loss[q] = coef * ((float)E / (float)k) * v[0];
+}
+
+// The sums of p and the counts of tokens lo .. hi - 1, by one workgroup: those of expert threadIdx.x come back to a thread.
+template <int DT, int G, int V>
+__device__ __forceinline__ void balance_part(const void* logits, int E, bool sigmoid, const int32_t* ids, int k, int64_t lo,
+                                             int64_t hi, float (*sums)[G * V], int32_t* hist, float& p_sum, int32_t& c) {
+  constexpr int PER = BAL_THREADS / G;
+  const int l = threadIdx.x % G, g = threadIdx.x / G;
+  const int64_t slots = (hi - lo) * k;
+  uint32_t first = E;
+  if ((int64_t)threadIdx.x < slots) first = (uint32_t)ids[lo * k + threadIdx.x];
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+  if (threadIdx.x < 512) hist[threadIdx.x] = 0;
+  __syncthreads();
+  for (int64_t t0 = lo; t0 < hi; t0 += PER) {
+    float z[V], p[V], rest[V], top, total;
+    load_logits<DT, G, V>(at<DT>(logits, min(t0 + g, hi - 1) * E), E, l, z);
+    if (t0 == lo) {
+      if (first < (uint32_t)E) atomicAdd(&hist[first], 1);
+      for (int64_t i = threadIdx.x + BAL_THREADS; i < slots; i += BAL_THREADS) {
+        const uint32_t e = (uint32_t)ids[lo * k + i];
+        if (e < (uint32_t)E) atomicAdd(&hist[e], 1);
+      }
+    }
+    shares<G, V>(z, sigmoid, p, rest, top, total);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += t0 + g < hi ? p[i] : 0.0f;
+  }
+  // over the wave's groups, then the waves
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if constexpr (G == 16) {
+      const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i]), __float_as_uint(acc[i]), false, false);
+      acc[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i]), __float_as_uint(acc[i]), false, false);
+    acc[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    if ((threadIdx.x & 63) < G) sums[threadIdx.x >> 6][i * G + l] = acc[i];
+  }
+  __syncthreads();
+  p_sum = 0.0f;
+  if (threadIdx.x < G * V) {
+#pragma unroll
+    for (int i = 0; i < BAL_WAVES; ++i) p_sum += sums[i][threadIdx.x];
+  }
+  c = threadIdx.x < 512 ? hist[threadIdx.x] : 0;
+}
+
+// A workgroup to a sequence, for short ones.
+template <int DT, int G, int V>
+__global__ __launch_bounds__(BAL_THREADS) void k_balance(const void* __restrict__ logits, int64_t T, int E, bool sigmoid,
+                                                         const int32_t* __restrict__ ids, int k,
+                                                         const int32_t* __restrict__ seq_off, float coef,
+                                                         float* __restrict__ loss, int32_t* __restrict__ counts) {
+  __shared__ float sums[BAL_WAVES][G * V];
+  __shared__ int32_t hist[512];
+  __shared__ float red[16];
+  int64_t a, b;
+  tokens_of(seq_off, blockIdx.x, T, a, b);
+  float p;
+  int32_t c;
+  balance_part<DT, G, V>(logits, E, sigmoid, ids, k, a, b, sums, hist, p, c);
+  balance_out(blockIdx.x, b - a, E, k, coef, c, p, red, loss, counts);
+}
+
+// A workgroup to `chunk` tokens, for long ones: what they give each sequence that they are of. From chunk to chunk and
+// sequence to sequence one of the two moves on, so the part of (chunk, sequence) is row chunk + sequence of the parts, and
+// a sequence's parts are rows that follow one another.
+template <int DT, int G, int V>
+__global__ __launch_bounds__(BAL_THREADS) void k_balance_chunk(const void* __restrict__ logits, int64_t T, int E,
+                                                               bool sigmoid, const int32_t* __restrict__ ids, int k,
+                                                               const int32_t* __restrict__ seq_off, int64_t S, int chunk,
+                                                               float* __restrict__ part_p, int32_t* __restrict__ part_c) {
+  __shared__ float sums[BAL_WAVES][G * V];
+  __shared__ int32_t hist[512];
+  const int64_t lo = (int64_t)blockIdx.x * chunk, hi = min(lo + chunk, T);
+  int q = seq_off == nullptr ? 0 : max((int)sequence_of<G>(seq_off, S, lo, threadIdx.x % G), 0);
+  for (q = __builtin_amdgcn_readfirstlane(q); q < (int)S; ++q) {
+    int64_t a, b;
+    tokens_of(seq_off, q, T, a, b);
+    if (a >= hi) break;
+    a = max(a, lo);
+    b = min(b, hi);
+    if (a >= b) continue;
+    float p;
+    int32_t c;
+    balance_part<DT, G, V>(logits, E, sigmoid, ids, k, a, b, sums, hist, p, c);
+    if ((int)threadIdx.x < E) {
+      const int64_t at = (blockIdx.x + q) * E + threadIdx.x;
+      part_p[at] = p;
+      part_c[at] = c;
+    }
+    __syncthreads();
+  }
+}
+
+// A sequence's parts in their order: runs of them side by side, then the runs.
+__global__ __launch_bounds__(BAL_THREADS) void k_balance_sum(const float* __restrict__ part_p,
+                                                             const int32_t* __restrict__ part_c, int chunk, int64_t T,
+                                                             int E, int k, const int32_t* __restrict__ seq_off, float coef,
+                                                             float* __restrict__ loss, int32_t* __restrict__ counts) {
+  __shared__ float red[16], sum_p[BAL_THREADS];
+  __shared__ int32_t sum_c[BAL_THREADS];
+  const int64_t q = blockIdx.x;
+  int64_t a, b;
+  tokens_of(seq_off, q, T, a, b);
+  const int64_t c0 = a / chunk, parts = b > a ? (b - 1) / chunk - c0 + 1 : 0;
+  const int runs = min(BAL_THREADS / E, 8), run = threadIdx.x / E, e = threadIdx.x - run * E;
+  float p = 0.0f;
+  int c = 0;
+  if (run < runs) {
+    const int64_t at = (c0 + q) * E + e;
+    const int i1 = (int)(parts * (run + 1) / runs);
+#pragma unroll 16
+    for (int i = (int)(parts * run / runs); i < i1; ++i) {
+      p += part_p[at + (int64_t)i * E];
+      c += part_c[at + (int64_t)i * E];
+    }
+  }
+  sum_p[threadIdx.x] = p;
+  sum_c[threadIdx.x] = c;
+  __syncthreads();
+  if (run == 0) {
+    for (int i = 1; i < runs; ++i) {
+      p += sum_p[i * E + e];
+      c += sum_c[i * E + e];
+    }
+  }
+  balance_out(q, b - a, E, k, coef, c, p, red, loss, counts);
 }
 
 struct GateGrad {
@@ -573,12 +671,13 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
   constexpr int PER = GATE_THREADS / G, Q = MAX_TOPK / G;
   __shared__ int32_t sel[PER][MAX_TOPK];
   __shared__ float val[PER][MAX_TOPK];
+  __shared__ float part[PER][G * V];         // what each expert's slots give it
   const int l = threadIdx.x % G, g = threadIdx.x / G, E = a.E, k = a.k;
   for (int64_t t0 = (int64_t)blockIdx.x * PER; t0 < a.T; t0 += (int64_t)gridDim.x * PER) {
     const bool live = t0 + g < a.T;
     const int64_t t = live ? t0 + g : a.T - 1;
     const char* row = at<DT>(a.logits, t * E);
-    float z[V], p[V], d[V], top, total;
+    float z[V], p[V], rest[V], d[V], top, total;
     // everything that hangs on nothing else is asked for first
     load_logits<DT, G, V>(row, E, l, z);
     int32_t id[Q];
@@ -592,7 +691,7 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
     int64_t lo = 0;
     if (a.counts != nullptr && a.seq_off != nullptr) lo = sequence_of<G>(a.seq_off, a.S, t, l);
     lo = min(lo, a.S - 1);          // (behind the last sequence: it does not reach t)
-    shares<G, V>(z, a.sigmoid, p, top, total);
+    shares<G, V>(z, a.sigmoid, p, rest, top, total);
 #pragma unroll
     for (int i = 0; i < V; ++i) d[i] = 0.0f;
     if (a.counts != nullptr) {
@@ -638,25 +737,34 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
         sum += x;
         if (j < k) val[g][j] = x;
       }
+#pragma unroll
+      for (int i = 0; i < V; ++i) part[g][i * G + l] = 0.0f;
       wave_lds();
       if (!a.sigmoid && !a.renorm) {
         sum = group_add<G>(sum);
 #pragma unroll
         for (int i = 0; i < V; ++i) d[i] = fmaf(-p[i], sum, d[i]);
       }
-      for (int j = 0; j < k; ++j) {
-        const int e = sel[g][j];
-        const float x = val[g][j];
+      // a slot adds up all that name its expert, in their order: those of one expert write the same
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] += i * G + l == e ? x : 0.0f;
+      for (int q = 0; q < Q; ++q) {
+        const int j = q * G + l;
+        if (j < k && (unsigned)id[q] < (unsigned)E) {
+          float x = 0.0f;
+          for (int o = 0; o < k; ++o) x += sel[g][o] == id[q] ? val[g][o] : 0.0f;
+          part[g][id[q]] = x;
+        }
       }
+      wave_lds();
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[i] += part[g][i * G + l];
       wave_lds();
     }
     char* out = at<DT>(a.d_logits, t * E);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = i * G + l;
-      if (a.sigmoid) d[i] *= sigmoid_f32(-z[i]);
+      d[i] *= rest[i];
       Raw<DT, 1> o;
       o.set(&d[i]);
       if (live && e < E) o.store(out, (uint32_t)e);
@@ -698,34 +806,35 @@ hipError_t launch_gate(const void* logits, DType dt, int64_t T, int E, bool sigm
   return hipGetLastError();
 }
 
-int balance_splits(int64_t T, int64_t S) {
-  // parts of a sequence: of 32 tokens or more on average, at most 80, about 512 workgroups in all
-  return (int)std::max<int64_t>(1, std::min({(int64_t)80, T / S / 32, (512 + S - 1) / S}));
+// Tokens of a chunk: one turn of a workgroup's groups or more, so that there are at most 128 chunks; 0: a workgroup to each
+// sequence, where they are shorter than two turns on average.
+static int balance_chunk(int64_t T, int64_t S) {
+  if (T / S < 64) return 0;
+  return (int)(32 * ((T + 32 * 128 - 1) / (32 * 128)));
+}
+int64_t balance_parts(int64_t T, int64_t S) {
+  const int chunk = balance_chunk(T, S);
+  return chunk == 0 ? 0 : (T + chunk - 1) / chunk + S;
 }
 
 hipError_t launch_balance(const void* logits, DType dt, int64_t T, int E, bool sigmoid, const int32_t* ids, int k,
                           const int32_t* seq_off, int64_t S, float coef, float* part, float* loss, int32_t* counts,
                           hipStream_t s) {
-  const int splits = balance_splits(T, S);
-  float* pp = splits > 1 ? part : nullptr;
-  int32_t* pc = splits > 1 ? (int32_t*)(part + S * splits * E) : nullptr;
-  // (a grid's y is at most 65535)
-  for (int64_t q0 = 0; q0 < S; q0 += 32768) {
-    const unsigned n = (unsigned)std::min<int64_t>(S - q0, 32768);
-    dispatch_dt(dt, [&](auto d) {
-      dispatch_experts(E, [&](auto lanes, auto values) {
-        constexpr int D = decltype(d)::value, G = decltype(lanes)::value, V = decltype(values)::value;
-        k_balance<D, G, V><<<dim3((unsigned)splits, n), BAL_THREADS, 0, s>>>(
-            logits, T, E, sigmoid, ids, k, seq_off == nullptr ? nullptr : seq_off + q0, coef,
-            pp == nullptr ? nullptr : pp + q0 * splits * E, pc == nullptr ? nullptr : pc + q0 * splits * E, loss + q0,
-            counts + q0 * E);
-      });
+  const int chunk = balance_chunk(T, S);
+  float* pp = part;
+  int32_t* pc = (int32_t*)(part + balance_parts(T, S) * E);
+  dispatch_dt(dt, [&](auto d) {
+    dispatch_experts(E, [&](auto lanes, auto values) {
+      constexpr int D = decltype(d)::value, G = decltype(lanes)::value, V = decltype(values)::value;
+      if (chunk == 0)
+        k_balance<D, G, V><<<(unsigned)S, BAL_THREADS, 0, s>>>(logits, T, E, sigmoid, ids, k, seq_off, coef, loss, counts);
+      else
+        k_balance_chunk<D, G, V><<<(unsigned)((T + chunk - 1) / chunk), BAL_THREADS, 0, s>>>(logits, T, E, sigmoid, ids, k,
+                                                                                           seq_off, S, chunk, pp, pc);
     });
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (splits > 1)
-    k_balance_sum<<<(unsigned)S, BAL_THREADS, 0, s>>>(pp, pc, splits, T, E, k, seq_off, coef, loss, counts);
+  });
+  if (chunk != 0)
+    k_balance_sum<<<(unsigned)S, BAL_THREADS, 0, s>>>(pp, pc, chunk, T, E, k, seq_off, coef, loss, counts);
   return hipGetLastError();
 }
 
