@@ -52,6 +52,8 @@ __device__ __forceinline__ void encode(const float (&v)[8], float up, uint32_t (
   }
 }
 
+constexpr int WRITE_AHEAD = 2;     // pieces of a lane that are in flight together
+
 template <int DT, bool FP8>
 __global__ __launch_bounds__(CACHE_THREADS) void k_cache_write(const void* __restrict__ x, int64_t ldx,
                                                                const int32_t* __restrict__ slots, uint32_t units,
@@ -60,37 +62,47 @@ __global__ __launch_bounds__(CACHE_THREADS) void k_cache_write(const void* __res
                                                                uint8_t* __restrict__ scales) {
   constexpr int EMAX = FP8 ? 8 : 2, BYTES = FP8 ? 8 : 4;
   // whole blocks of 32 columns: per_row and units are multiples of four, so a block's four lanes go together
-  for (int64_t u0 = (int64_t)blockIdx.x * CACHE_THREADS + threadIdx.x; u0 < units;
-       u0 += (int64_t)gridDim.x * CACHE_THREADS) {
-    const uint32_t u = (uint32_t)u0, t = u / per_row, c = u - t * per_row;
-    const uint32_t slot = (uint32_t)slots[t];
-    if (slot >= n_slots) continue;
-    Raw<DT, 8> r;
-    r.load(at<DT>(x, (int64_t)t * ldx), c * 8);
-    float v[8];
-    uint32_t am = 0;
+  for (int64_t u0 = (int64_t)blockIdx.x * (CACHE_THREADS * WRITE_AHEAD) + threadIdx.x; u0 < units;
+       u0 += (int64_t)gridDim.x * (CACHE_THREADS * WRITE_AHEAD)) {
+    Raw<DT, 8> r[WRITE_AHEAD];
+    uint32_t slot[WRITE_AHEAD], col[WRITE_AHEAD];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = r.get(i);
-      am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    for (int j = 0; j < WRITE_AHEAD; ++j) {
+      const int64_t want = u0 + j * CACHE_THREADS;
+      const uint32_t u = (uint32_t)(want < units ? want : u0), t = u / per_row;
+      col[j] = u - t * per_row;
+      slot[j] = want < units ? (uint32_t)slots[t] : n_slots;
+      r[j].load(at<DT>(x, (int64_t)t * ldx), col[j] * 8);
     }
-    am = quad_max<0xB1>(am);   // quad_perm 1 0 3 2
-    am = quad_max<0x4E>(am);   // quad_perm 2 3 0 1
-    const int ef = (int)(am >> 23);
-    uint32_t sb = (uint32_t)max(ef - EMAX, 0);
-    float up = __uint_as_float((254u - sb) << 23);
-    if (ef == 0xFF) {
-      sb = 0xFFu;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-      up = 0.0f;
+    for (int j = 0; j < WRITE_AHEAD; ++j) {
+      if (slot[j] >= n_slots) continue;
+      const uint32_t c = col[j];
+      float v[8];
+      uint32_t am = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = r[j].get(i);
+        am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      }
+      am = quad_max<0xB1>(am);   // quad_perm 1 0 3 2
+      am = quad_max<0x4E>(am);   // quad_perm 2 3 0 1
+      const int ef = (int)(am >> 23);
+      uint32_t sb = (uint32_t)max(ef - EMAX, 0);
+      float up = __uint_as_float((254u - sb) << 23);
+      if (ef == 0xFF) {
+        sb = 0xFFu;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        up = 0.0f;
+      }
+      uint32_t q[FP8 ? 2 : 1];
+      encode<FP8>(v, up, q);
+      uint8_t* dst = codes + ((int64_t)slot[j] * per_row + c) * BYTES;
+      if constexpr (FP8) *(uint2*)dst = make_uint2(q[0], q[1]);
+      else *(uint32_t*)dst = q[0];
+      if ((c & 3) == 0) scales[(int64_t)slot[j] * (per_row >> 2) + (c >> 2)] = (uint8_t)sb;
     }
-    uint32_t q[FP8 ? 2 : 1];
-    encode<FP8>(v, up, q);
-    uint8_t* dst = codes + ((int64_t)slot * per_row + c) * BYTES;
-    if constexpr (FP8) *(uint2*)dst = make_uint2(q[0], q[1]);
-    else *(uint32_t*)dst = q[0];
-    if ((c & 3) == 0) scales[(int64_t)slot * (per_row >> 2) + (c >> 2)] = (uint8_t)sb;
   }
 }
 
@@ -118,51 +130,96 @@ __device__ __forceinline__ void decode(const uint32_t (&q)[FP8 ? 2 : 1], uint32_
   o.set(v);
 }
 
-constexpr int READ_ROWS = 32;      // rows of a workgroup
+constexpr int READ_ROWS = 32;      // rows of a workgroup at most
 constexpr int READ_AHEAD = 4;      // pieces of a lane whose codes are in flight together
 
+// The sequences that a workgroup's rows are of: offsets 64 at a time narrow down to the last one that starts at or before its
+// first row, and those from there on are looked up in LDS, not by a search of dependent loads for each row.
+struct Window {
+  int64_t first;
+  int32_t off[64];
+};
+__device__ __forceinline__ void find_window(const int32_t* seq_off, int64_t B, int64_t r0, int l, Window& w) {
+  int64_t lo = 0, n = B;
+  while (n > 64) {
+    const int64_t step = (n + 63) / 64;
+    const bool before = step * l < n && seq_off[lo + step * l] <= r0;
+    const int64_t skip = step * (int64_t)max((int)__popcll(__ballot(before)) - 1, 0);
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  const int64_t skip = max((int)__popcll(__ballot(l < n && seq_off[lo + min((int64_t)l, n - 1)] <= r0)) - 1, 0);
+  lo += skip;
+  w.off[l] = seq_off[min(lo + l, B)];
+  if (l == 0) w.first = lo;
+}
+
+// `rows_each` rows to a workgroup, a piece of 8 columns to a lane and step: consecutive lanes have consecutive pieces, those
+// of the rows behind one another.
 template <int DT, bool FP8>
 __global__ __launch_bounds__(CACHE_THREADS) void k_cache_read(const uint8_t* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales, uint32_t pages,
-                                                              uint32_t page_size, uint32_t per_row,
+                                                              uint32_t page_size, uint32_t per_row, int rows_each,
+                                                              uint32_t step_row, uint32_t step_col,
                                                               const int32_t* __restrict__ page_table, int64_t table_width,
                                                               const int32_t* __restrict__ seq_off, int64_t B, int64_t rows,
                                                               void* __restrict__ out) {
   constexpr int BYTES = FP8 ? 8 : 4;
   __shared__ int64_t where[READ_ROWS];      // the cache's row of each row; -1: nothing to read, -2: not a sequence's
-  for (int64_t r0 = (int64_t)blockIdx.x * READ_ROWS; r0 < rows; r0 += (int64_t)gridDim.x * READ_ROWS) {
-    if (threadIdx.x < READ_ROWS) {
-      const int64_t r = r0 + threadIdx.x;
+  __shared__ Window win;
+  const uint32_t row0 = threadIdx.x / per_row, col0 = threadIdx.x - row0 * per_row;
+  for (int64_t r0 = (int64_t)blockIdx.x * rows_each; r0 < rows; r0 += (int64_t)gridDim.x * rows_each) {
+    if (threadIdx.x < 64) {
+      const int64_t first = seq_off[0], last = seq_off[B], r = r0 + threadIdx.x;
+      find_window(seq_off, B, r0, threadIdx.x, win);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
       int64_t at = -2;
-      if (r < rows && r >= seq_off[0] && r < seq_off[B]) {
-        int64_t lo = 0, n = B;               // the last sequence that starts at or before r
+      if ((int)threadIdx.x < rows_each && r < rows && r >= first && r < last) {
+        int64_t lo = 0, n = min(B - win.first, (int64_t)64);      // the last sequence that starts at or before r
         while (n > 1) {
           const int64_t half = n >> 1;
-          if (seq_off[lo + half] <= r) { lo += half; n -= half; }
+          if (win.off[lo + half] <= r) { lo += half; n -= half; }
           else n = half;
         }
-        const uint32_t pos = (uint32_t)(r - seq_off[lo]), col = pos / page_size;
+        int32_t begin = win.off[lo];
+        lo += win.first;
+        if (lo == win.first + 63) {                               // or one behind the window
+          n = B - lo;
+          while (n > 1) {
+            const int64_t half = n >> 1;
+            if (seq_off[lo + half] <= r) { lo += half; n -= half; }
+            else n = half;
+          }
+          begin = seq_off[lo];
+        }
+        const uint32_t pos = (uint32_t)(r - begin), col = pos / page_size;
         at = -1;
         if ((int64_t)col < table_width) {
           const uint32_t page = (uint32_t)page_table[lo * table_width + col];
           if (page < pages) at = (int64_t)page * page_size + (pos - col * page_size);
         }
       }
-      where[threadIdx.x] = at;
+      if ((int)threadIdx.x < rows_each) where[threadIdx.x] = at;
     }
     __syncthreads();
-    const uint32_t units = READ_ROWS * per_row;
-    for (uint32_t u0 = threadIdx.x; u0 < units; u0 += CACHE_THREADS * READ_AHEAD) {
-      uint32_t q[READ_AHEAD][FP8 ? 2 : 1], sb[READ_AHEAD];
+    uint32_t row = row0, c = col0;
+    while (row < (uint32_t)rows_each) {
+      uint32_t q[READ_AHEAD][FP8 ? 2 : 1], sb[READ_AHEAD], cs[READ_AHEAD], rs[READ_AHEAD];
+      int64_t w[READ_AHEAD];
 #pragma unroll
       for (int j = 0; j < READ_AHEAD; ++j) {
-        const uint32_t u = min(u0 + j * CACHE_THREADS, units - 1), row = u / per_row, c = u - row * per_row;
-        const int64_t w = where[row];
+        rs[j] = row;
+        cs[j] = c;
+        w[j] = row < (uint32_t)rows_each ? where[row] : -2;
+        row += step_row;
+        c += step_col;
+        if (c >= per_row) { c -= per_row; ++row; }
         q[j][0] = 0;
         if constexpr (FP8) q[j][1] = 0;
         sb[j] = 0;
-        if (w >= 0) {
-          const uint8_t* p = codes + (w * per_row + c) * BYTES;
+        if (w[j] >= 0) {
+          const uint8_t* p = codes + (w[j] * per_row + cs[j]) * BYTES;
           if constexpr (FP8) {
             const uint2 v = *(const uint2*)p;
             q[j][0] = v.x;
@@ -170,18 +227,15 @@ __global__ __launch_bounds__(CACHE_THREADS) void k_cache_read(const uint8_t* __r
           } else {
             q[j][0] = *(const uint32_t*)p;
           }
-          sb[j] = scales[w * (per_row >> 2) + (c >> 2)];
+          sb[j] = scales[w[j] * (per_row >> 2) + (cs[j] >> 2)];
         }
       }
 #pragma unroll
       for (int j = 0; j < READ_AHEAD; ++j) {
-        const uint32_t u = u0 + j * CACHE_THREADS;
-        if (u >= units) break;
-        const uint32_t row = u / per_row, c = u - row * per_row;
-        if (where[row] == -2) continue;
+        if (w[j] == -2) continue;
         Raw<DT, 8> o;
         decode<DT, FP8>(q[j], sb[j], o);
-        o.template store<true>(at<DT>(out, (r0 + row) * (int64_t)per_row * 8), c * 8);
+        o.template store<true>(at<DT>(out, (r0 + rs[j]) * (int64_t)per_row * 8), cs[j] * 8);
       }
     }
     __syncthreads();
@@ -193,7 +247,8 @@ __global__ __launch_bounds__(CACHE_THREADS) void k_cache_read(const uint8_t* __r
 hipError_t launch_cache_write(const void* x, DType dt, int64_t ldx, int64_t T, int64_t width, bool fp8,
                               const int32_t* slots, int64_t n_slots, uint8_t* codes, uint8_t* scales, hipStream_t s) {
   const uint32_t units = (uint32_t)(T * (width / 8));
-  const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)units + CACHE_THREADS - 1) / CACHE_THREADS, 1 << 20);
+  const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)units + CACHE_THREADS * WRITE_AHEAD - 1) /
+                                                        (CACHE_THREADS * WRITE_AHEAD), 1 << 20);
   dispatch_dt(dt, [&](auto d) {
     constexpr int D = decltype(d)::value;
     auto* k = fp8 ? k_cache_write<D, true> : k_cache_write<D, false>;
@@ -205,11 +260,14 @@ hipError_t launch_cache_write(const void* x, DType dt, int64_t ldx, int64_t T, i
 hipError_t launch_cache_read(const uint8_t* codes, const uint8_t* scales, int64_t pages, int64_t page_size,
                              int64_t width, bool fp8, const int32_t* page_table, int64_t table_width,
                              const int32_t* seq_off, int64_t B, int64_t rows, void* out, DType dt, hipStream_t s) {
-  const unsigned grid = (unsigned)std::min<int64_t>((rows + READ_ROWS - 1) / READ_ROWS, 1 << 20);
+  const int64_t per_row = width / 8;
+  const int each = (int)std::clamp<int64_t>(CACHE_THREADS * READ_AHEAD / per_row, 1, READ_ROWS);
+  const unsigned grid = (unsigned)std::min<int64_t>((rows + each - 1) / each, 1 << 20);
   dispatch_dt(dt, [&](auto d) {
     constexpr int D = decltype(d)::value;
     auto* k = fp8 ? k_cache_read<D, true> : k_cache_read<D, false>;
-    k<<<grid, CACHE_THREADS, 0, s>>>(codes, scales, (uint32_t)pages, (uint32_t)page_size, (uint32_t)(width / 8),
+    k<<<grid, CACHE_THREADS, 0, s>>>(codes, scales, (uint32_t)pages, (uint32_t)page_size, (uint32_t)per_row, each,
+                                     (uint32_t)(CACHE_THREADS / per_row), (uint32_t)(CACHE_THREADS % per_row),
                                      page_table, table_width, seq_off, B, rows, out);
   });
   return hipGetLastError();
