@@ -121,6 +121,21 @@ def test_w4_pointers(L):
         assert c(**kw) == VALUE and "overlaps" in L.mx_last_error().decode(), kw
 
 
+def test_w4_workspace(L):
+    """None up to 16 tokens; for parts of K, and for the scales of tiles of 256, so many bytes, aligned, apart."""
+    size = L.mx_w4_linear_workspace_size
+    assert size(16, 1 << 20, 1 << 20) == 0 and size(1, 7168, 7168) == 0 and size(0, 64, 64) == 0
+    parts, tables = size(64, 7168, 512), size(4096, 256, 4096)
+    assert parts >= 2 * 64 * 512 * 4 and tables >= 2 * 8 * 4096 * 4
+    for M, K, N, need in ((64, 7168, 512, parts), (4096, 256, 4096, tables)):
+        # operands 2^40 apart
+        c = lambda **kw: _call(L, "mx_w4_linear", W4, **(dict(M=M, K=K, N=N, ldx=K, ldy=N, x=1 << 40, w=2 << 40, scales=3 << 40,
+                                                              zeros=4 << 40, y=5 << 40, ws=6 << 40) | kw))
+        assert c(ws=None) == NULL and c(ws=(6 << 40) + 64) == ALIGN and c(n=need - 1) == WORKSPACE
+        for p in (1, 2, 3, 4, 5):
+            assert c(ws=p << 40) == VALUE and "overlaps" in L.mx_last_error().decode(), p
+
+
 WRITE = dict(fmt=3, dt=0, x=at(0), ldx=64, T=4, W=64, slots=at(1), pages=8, page=16, codes=at(2), scales=at(3), s=None)
 READ = dict(fmt=0, codes=at(0), scales=at(1), pages=8, page=16, W=64, table=at(2), wide=4, off=at(3), B=2, rows=40, dt=0,
             out=at(4), s=None)

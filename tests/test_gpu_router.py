@@ -220,3 +220,78 @@ def test_many_tokens_run_to_run(mx):
     ids = a[0].cpu().numpy()
     ref = np.stack([np.bincount(ids[p].reshape(-1), minlength=E) for p in (slice(0, 9000), slice(9000, T))])
     assert np.array_equal(s[1].cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [1, 8, 16, 17, 32, 33, 64])
+def test_scores_close_to_each_other(mx, score, k):
+    """Logits a few steps of fp32 apart, with a bias and without: the order of the whole row is decided by 64 bits."""
+    rng = np.random.default_rng(k)
+    T, E = 21, 384
+    z = np.stack([1 + rng.permutation(E) * 2.0 ** -20 for _ in range(T)])
+    z[3] = 0.25                                        # all the same: the lower index first
+    z[4, 5:] = -np.inf                                 # fewer than k are on
+    t, zr = pair(z, "fp32")
+    for bias in (None, np.full(E, 0.5), np.full(E, -3.0)):
+        b, br = (None, None) if bias is None else pair(bias, "fp32")
+        ids, _ = mx.moe_gate(t, k, score, b)
+        ri, _ = o.moe_gate(zr, k, score, br)
+        # scores 2^-20 s (1 - s) apart (softmax: 2^-20 / 384) are 2^-31 or more, sums of 3 in 64 bits off by 2^-50
+        assert np.array_equal(ids.cpu().numpy(), ri), bias is None
+
+
+def test_infinities_and_the_largest_values_of_a_bias(mx):
+    """A bias that swamps the scores: the order is the bias's, equal ones' the lower index."""
+    T, E, k = 5, 100, 7
+    t, zr = pair(np.random.default_rng(3).standard_normal((T, E)), "fp32")
+    bias = np.zeros(E)
+    bias[::3], bias[10], bias[90], bias[20:30] = 1e30, 3e38, -3e38, -np.inf
+    b, br = pair(bias, "fp32")
+    for score in ("softmax", "sigmoid"):
+        ids, w = mx.moe_gate(t, k, score, b)
+        order = sorted(range(E), key=lambda e: (-br[e], e))[:k]
+        assert ids.cpu().tolist() == [order] * T and torch.isfinite(w).all()
+
+
+LONG = [(9000, 40, 3, [0, 5, 5, 4000, 4001, 8999]), (9000, 100, 8, None), (4100, 257, 2, [0] + list(range(30, 4100, 100)) + [4100]),
+        (6000, 33, 4, [10, 10, 90, 5990]), (4096, 60, 6, [0] + [64 * i for i in range(1, 64)] + [4096])]
+
+
+@pytest.mark.parametrize("T,E,k,off", LONG)
+def test_balance_of_long_and_ragged_sequences(mx, T, E, k, off):
+    """Sequences that end inside a chunk of tokens, several in one, tokens of none."""
+    rng = np.random.default_rng(T + E)
+    z, zr = logits(rng, T, E, "fp32", 0.1)
+    ids = rng.integers(-1, E + 1, size=(T, k)).astype(np.int32)
+    for score in ("softmax", "sigmoid"):
+        loss, counts = mx.moe_balance(z, dev(ids, torch.int32), None if off is None else dev(np.array(off), torch.int32),
+                                      score, coef=2.0)
+        rl, rc = o.moe_balance(zr, ids, off, score, 2.0)
+        assert np.array_equal(counts.cpu().numpy(), rc)
+        within(loss, rl, (score_error(zr, E).max() + (T + 40) * U) * rl + 2.0 ** -126, score)
+
+
+def test_grad_of_many_sequences(mx):
+    """More sequences than lanes look at once, empty ones among them."""
+    T, E, k = 3000, 24, 2
+    rng = np.random.default_rng(0)
+    off = np.concatenate([[0, 0, 0], np.sort(rng.integers(0, T - 5, size=1500)), [T - 5]])
+    z, zr = logits(rng, T, E, "fp32")
+    ids, _ = mx.moe_gate(z, k)
+    do = dev(off, torch.int32)
+    loss, counts = mx.moe_balance(z, ids, do)
+    dl, dlr = pair(1 + rng.random(len(off) - 1), "fp32")
+    got = mx.moe_gate_grad(z, ids, None, counts, dl, do)
+    pick = np.r_[0:40, 1500:1540, T - 30:T]
+    seq = np.searchsorted(off, pick, side="right") - 1
+    rc = counts.cpu().numpy()
+    for i, tok in enumerate(pick):
+        q = int(seq[i])
+        if tok >= off[-1]:
+            assert not got[tok].any()
+            continue
+        n = off[q + 1] - off[q]
+        # the token alone, with its sequence's counts; the mean over n tokens goes into the coefficient
+        ref, size = o.moe_gate_grad(zr[tok:tok + 1], ids[tok:tok + 1].cpu().numpy(), None, rc[q:q + 1], dlr[q:q + 1],
+                                    [0, 1], coef=1.0 / n ** 2)
+        within(got[tok:tok + 1], ref, (3 * score_error(zr[tok:tok + 1], E) + 40 * U) * size + rounded(ref, "fp32") + 2.0 ** -120)

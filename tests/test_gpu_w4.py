@@ -205,3 +205,48 @@ def test_past_2_to_the_31(mx):
     y = mx.w4_linear(big[:, 512:512 + K], w, s, out=big[:, :N])
     ref = xr @ v.T
     within(y.contiguous(), ref, bound(xr, m, ref, "bf16"))
+
+
+@pytest.mark.parametrize("M", [3, 11, 20, 70, 140])
+@pytest.mark.parametrize("K", [40032, 33024])
+def test_long_rows(mx, M, K):
+    """More columns than a workgroup has the scales of at a time; rows of scales at odd addresses (K 40032) and not."""
+    rng = np.random.default_rng(M)
+    N = 37
+    x, xr = pair(rng.standard_normal((M, K)), "bf16")
+    for fmt, group, zeros in (("mxfp4", 32, False), ("int4", 32, True), ("int4", 64, False), ("int4", 128, True)):
+        if K % group:
+            continue
+        (w, s, z), v, m = weights(rng, N, K, fmt, group, "bf16", zeros)
+        y = mx.w4_linear(x, w, s, z)
+        ref = xr @ v.T
+        within(y, ref, bound(xr, m, ref, "bf16"), (fmt, group))
+
+
+@pytest.mark.parametrize("M", [4, 30, 90])
+def test_scales_and_zeros_at_odd_addresses(mx, M):
+    """Scales that start one element, zero points and E8M0 bytes that start one byte behind a multiple of 4."""
+    rng = np.random.default_rng(M)
+    K, N = 1024, 50
+    x, xr = pair(rng.standard_normal((M, K)), "fp16")
+    for fmt, group, zeros in (("mxfp4", 32, False), ("int4", 32, True), ("int4", 128, True)):
+        (w, s, z), v, m = weights(rng, N, K, fmt, group, "fp16", zeros)
+        def odd(a):
+            r = torch.empty(a.numel() + 1, dtype=a.dtype, device="cuda")[1:].view(a.shape)
+            return r.copy_(a)
+        y = mx.w4_linear(x, w, odd(s), None if z is None else odd(z))
+        ref = xr @ v.T
+        within(y, ref, bound(xr, m, ref, "fp16"), (fmt, group))
+
+
+def test_tokens_far_apart(mx):
+    """More than 2^24 elements from token to token, more than 16 tokens."""
+    rng = np.random.default_rng(6)
+    M, K, N = 18, 512, 64
+    big = torch.empty((M, (1 << 24) + 8), dtype=torch.bfloat16, device="cuda")
+    x, xr = pair(rng.standard_normal((M, K)), "bf16")
+    big[:, 64:64 + K] = x
+    (w, s, z), v, m = weights(rng, N, K, "int4", 64, "bf16", True)
+    y = mx.w4_linear(big[:, 64:64 + K], w, s, z)
+    ref = xr @ v.T
+    within(y, ref, bound(xr, m, ref, "bf16"))
