@@ -25,6 +25,7 @@
 // DPP rotations of a row of 16 lanes and one row swap. All of it is bound by
 // latency and launches: a training batch of 4096 x 384 fp32 logits is 6.3 MB.
 #include <algorithm>
+#include <utility>
 
 #include "rows.h"
 
@@ -285,6 +286,26 @@ struct Candidates {
   uint16_t e[G];
 };
 
+// How many of a row's 15 other lanes have an o that is at least v.
+template <int... I>
+__device__ __forceinline__ int others_at_least(uint32_t v, uint32_t o, std::integer_sequence<int, I...>) {
+  int n = 0;
+  ((n += (uint32_t)__builtin_amdgcn_update_dpp(0u, o, 0x121 + I, 0xF, 0xF, false) >= v ? 1 : 0), ...);
+  return n;
+}
+// How many of a group's lanes have a value that is at least this lane's.
+template <int G>
+__device__ __forceinline__ int at_least(uint32_t v, int l) {
+  constexpr std::make_integer_sequence<int, 15> turns;
+  int n = 1 + others_at_least(v, v, turns);
+  if constexpr (G == 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    const uint32_t o = l >= 16 ? r[0] : r[1];
+    n += (o >= v ? 1 : 0) + others_at_least(v, o, turns);
+  }
+  return n;
+}
+
 // The choice for k <= G. The k-th largest of the lanes' largest keys is at most the k-th largest of all: the few keys from
 // there on (less, with a bias, what its 32 bits may be off) are all that can be chosen, and are ranked against each other,
 // one a lane. A round over all keys for each of the k instead took 7.5 us for 4096 tokens of 384 experts, and with the
@@ -321,14 +342,7 @@ __device__ __forceinline__ int choose(const float (&z)[V], bool sigmoid, const f
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) most = max(most, key[i]);
-  uint32_t kth = 0;
-  for (int got = 0;;) {             // of the wave's groups the slowest sets the pace
-    const uint32_t top = group_max<G>(most);
-    if (got < k) kth = top;
-    got += (int)group_all<G>(most == top ? 1u : 0u, [](uint32_t p, uint32_t q) { return p + q; });
-    if (most == top) most = 0;
-    if (__all(got >= k || top == 0)) break;
-  }
+  const uint32_t kth = group_max<G>(at_least<G>(most, l) >= k ? most : 0u);
   uint32_t least = max(kth, 1u);
   if constexpr (BIAS) {
     // kth 0 or 1: fewer than k lanes have a number, and all keys are candidates
@@ -393,7 +407,7 @@ __device__ __forceinline__ int choose(const float (&z)[V], bool sigmoid, const f
   if (BIAS) wave_lds();
   int rank = l < n ? 0 : G;
   // (list positions are not in the order of experts)
-#pragma unroll 4
+#pragma unroll 8
   for (int j = 0; j < n; ++j) {
     const uint64_t o = c.key[j];
     rank += o > own || (o == own && (int)c.e[j] < ce);
@@ -630,10 +644,21 @@ __global__ __launch_bounds__(BAL_THREADS) void k_balance_sum(const float* __rest
   if (run < runs) {
     const int64_t at = (c0 + q) * E + e;
     const int i1 = (int)(parts * (run + 1) / runs);
-#pragma unroll 16
-    for (int i = (int)(parts * run / runs); i < i1; ++i) {
-      p += part_p[at + (int64_t)i * E];
-      c += part_c[at + (int64_t)i * E];
+    // a batch of loads at a time, those behind the last of the last again (a loop's own remainder goes one by one)
+    constexpr int AHEAD = 16;
+    for (int i = (int)(parts * run / runs); i < i1; i += AHEAD) {
+      float vp[AHEAD];
+      int32_t vc[AHEAD];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        vp[j] = part_p[at + (int64_t)min(i + j, i1 - 1) * E];
+        vc[j] = part_c[at + (int64_t)min(i + j, i1 - 1) * E];
+      }
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        p += i + j < i1 ? vp[j] : 0.0f;
+        c += i + j < i1 ? vc[j] : 0;
+      }
     }
   }
   sum_p[threadIdx.x] = p;
