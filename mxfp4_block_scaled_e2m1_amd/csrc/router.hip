@@ -406,11 +406,17 @@ __device__ __forceinline__ int choose(const float (&z)[V], bool sigmoid, const f
   }
   if (BIAS) wave_lds();
   int rank = l < n ? 0 : G;
-  // (list positions are not in the order of experts)
-#pragma unroll 8
-  for (int j = 0; j < n; ++j) {
-    const uint64_t o = c.key[j];
-    rank += o > own || (o == own && (int)c.e[j] < ce);
+  // eight at a time, the last again behind the last; list positions are not in the order of experts
+  for (int j = 0; j < n; j += 8) {
+    uint64_t o[8];
+    int e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[i] = c.key[min(j + i, n - 1)];
+      e[i] = c.e[min(j + i, n - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rank += j + i < n && (o[i] > own || (o[i] == own && e[i] < ce));
   }
   wave_lds();
   return rank;
@@ -776,7 +782,17 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
         const int j = q * G + l;
         if (j < k && (unsigned)id[q] < (unsigned)E) {
           float x = 0.0f;
-          for (int o = 0; o < k; ++o) x += sel[g][o] == id[q] ? val[g][o] : 0.0f;
+          for (int o = 0; o < k; o += 8) {
+            int32_t e[8];
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              e[i] = sel[g][min(o + i, k - 1)];
+              v[i] = val[g][min(o + i, k - 1)];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x += o + i < k && e[i] == id[q] ? v[i] : 0.0f;
+          }
           part[g][id[q]] = x;
         }
       }
