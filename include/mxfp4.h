@@ -689,7 +689,7 @@ MX_API size_t mx_lora_add_workspace_size(int64_t M, int64_t K, int64_t R, int32_
  *   topk_ids [T, k] int32; ids outside [0, E) are not counted.
  * 1 <= S <= 2^20, S * E <= 2^28, k >= 1, T * k <= 2^30, coef finite. The sums run in a
  * fixed order for given sizes. workspace: mx_moe_balance_workspace_size(T, E, S)
- * bytes, 256-byte aligned (0 bytes for few tokens a sequence: workspace may then be NULL).
+ * bytes, 256-byte aligned (0 bytes for up to 64 tokens a sequence: it may then be NULL).
  *
  * mx_moe_gate_grad -- the gradient of both for the logits:
  *   d_logits [T, E] of type dt, given
@@ -720,13 +720,15 @@ MX_API mx_status mx_moe_gate_grad(mx_dtype dt, const void* logits, int64_t T, in
  *   w [N, K/2]: two codes a byte, column 2j in the low nibble
  *   MX_FMT_MXFP4: E2M1 codes, scales [N, K/32] E8M0; group is 32, zeros NULL
  *   MX_FMT_INT4:  codes 0 .. 15, scales [N, K/group] of type dt, zeros [N, K/group]
- *                 bytes, or NULL for 8; group 32, 64 or 128
+ *                 bytes 0 .. 15 (y is unspecified with others), or NULL for 8; group 32,
+ *                 64 or 128
  * Codes enter the products exactly, a group's scale multiplies an fp32 sum, and y is
  * rounded once. A token with an infinite or NaN activation has no finite y.
  * K a multiple of group up to 2^20, 1 <= N <= 2^20, 0 <= M <= 2^20, ldx a multiple of 8 of at least K,
  * ldy >= N, both at most 2^30. workspace: mx_w4_linear_workspace_size(M, K, N) bytes,
- * 256-byte aligned (0 bytes for most sizes: it may then be NULL). Alignment: x and w 16
- * bytes, y and an INT4 scale one element. y overlaps no input.
+ * 256-byte aligned (0 bytes up to 16 tokens: it may then be NULL). Alignment: x and w 16
+ * bytes, y and an INT4 scale one element. y overlaps no input (x and y may be column
+ * ranges of one matrix that have none in common).
  */
 MX_API mx_status mx_w4_linear(mx_dtype dt, const void* x, int64_t ldx, int64_t M, int64_t K, mx_format fmt,
                               const uint8_t* w, const void* scales, const uint8_t* zeros, int32_t group, int64_t N,

@@ -12,7 +12,9 @@
 // Both stream rows with next to no arithmetic, so HBM bandwidth bounds them. A lane
 // has 8 columns (16 bytes of a 16-bit type, 8 or 4 of codes), four lanes a block of 32:
 // a wave's loads and stores are whole contiguous runs, and a block's largest magnitude
-// is two DPP exchanges within its four lanes.
+// is two DPP exchanges within its four lanes. Measured, in a graph: 128000 rows of 576
+// columns read from MXFP8 to bf16 in 47 us (224 MB, 4.7 TB/s; a copy of 512 MB reaches
+// 5.2), 8400 rows of 2048 fp16 columns written as MXFP4 in 10.3 and read in 10.2 (44 MB each).
 #include <algorithm>
 
 #include "rows.h"
@@ -154,8 +156,9 @@ __device__ __forceinline__ void find_window(const int32_t* seq_off, int64_t B, i
   if (l == 0) w.first = lo;
 }
 
-// `rows_each` rows to a workgroup, a piece of 8 columns to a lane and step: consecutive lanes have consecutive pieces, those
-// of the rows behind one another.
+// `rows_each` rows to a workgroup, as many as READ_AHEAD pieces a lane are (32 whatever the width left 8400 rows of 2048
+// columns 262 workgroups: 19 us instead of 10.2; 2 or 8 pieces: 128000 rows of 576 in 53 or 52 us instead of 50). A piece is
+// 8 columns: consecutive lanes have consecutive pieces, those of the rows behind one another.
 template <int DT, bool FP8>
 __global__ __launch_bounds__(CACHE_THREADS) void k_cache_read(const uint8_t* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales, uint32_t pages,

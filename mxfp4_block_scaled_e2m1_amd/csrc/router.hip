@@ -18,12 +18,14 @@
 //
 // An expert whose logit is -inf is off: it is never chosen and its share is 0.
 //
-// A token's logits are a few hundred values: a group of 16 or 32 lanes holds them
-// in registers, 4 to 16 a lane (expert i * G + lane), so that a wave has two to four
-// tokens in flight and what is done lane by lane (exponentials, the search for a
-// lane's largest) is shared by all of them; sums and maxima over the group are four
-// DPP rotations of a row of 16 lanes and one row swap. All of it is bound by
-// latency and launches: a training batch of 4096 x 384 fp32 logits is 6.3 MB.
+// A token's logits are a few hundred values: a group of 32 lanes holds them in
+// registers, 2 to 16 a lane (expert 32 i + lane); sums and maxima over the group are
+// four DPP rotations of a row of 16 lanes and one row swap. (16 lanes with twice the
+// values and half the steps: of 60 experts 0.4 us more for the choice of 512 tokens, 0.8
+// for their gradient, as much for 4096.) All of it is bound by latency and launches: a
+// training batch of 4096 x 384 fp32 logits is 6.3 MB, 1.2 us of HBM. Measured, in a graph:
+// its choice with a bias 7.8 us (without 5.4), the balance 9.6 + 5.2, the gradient 10.4;
+// 8 tokens of 48 experts 3.3.
 #include <algorithm>
 #include <utility>
 
@@ -34,41 +36,38 @@ namespace mx {
 namespace {
 
 constexpr int GATE_THREADS = 256;
+constexpr int G = 32;             // lanes of a token: two DPP rows
 
-// op over a group of G lanes (16: a DPP row, 32: two rows), the result in all of them.
-template <int G, class Op>
-__device__ __forceinline__ uint32_t group_all(uint32_t v, Op op) {
+// op over a row of 16 lanes, and over a group; the result in all of them.
+template <class Op>
+__device__ __forceinline__ uint32_t row_all(uint32_t v, Op op) {
   v = op(v, __builtin_amdgcn_update_dpp(0u, v, 0x128, 0xF, 0xF, false));   // row_ror 8, 4, 2, 1
   v = op(v, __builtin_amdgcn_update_dpp(0u, v, 0x124, 0xF, 0xF, false));
   v = op(v, __builtin_amdgcn_update_dpp(0u, v, 0x122, 0xF, 0xF, false));
-  v = op(v, __builtin_amdgcn_update_dpp(0u, v, 0x121, 0xF, 0xF, false));
-  if constexpr (G == 32) {
-    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    v = op(r[0], r[1]);
-  }
-  return v;
+  return op(v, __builtin_amdgcn_update_dpp(0u, v, 0x121, 0xF, 0xF, false));
 }
-template <int G>
+template <class Op>
+__device__ __forceinline__ uint32_t group_all(uint32_t v, Op op) {
+  v = row_all(v, op);
+  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return op(r[0], r[1]);
+}
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  return group_all<G>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+  return group_all(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
-template <int G>
 __device__ __forceinline__ uint32_t group_min(uint32_t v) {
-  return group_all<G>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
+  return group_all(v, [](uint32_t a, uint32_t b) { return min(a, b); });
 }
-template <int G>
 __device__ __forceinline__ float group_fmax(float v) {
-  return __uint_as_float(group_all<G>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+  return __uint_as_float(group_all(__float_as_uint(v), [](uint32_t a, uint32_t b) {
     return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
   }));
 }
-template <int G>
 __device__ __forceinline__ float group_add(float v) {
-  return __uint_as_float(group_all<G>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+  return __uint_as_float(group_all(__float_as_uint(v), [](uint32_t a, uint32_t b) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
   }));
 }
-template <int G>
 __device__ __forceinline__ double group_add(double v) {
   auto step = [&](auto move) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
@@ -79,13 +78,11 @@ __device__ __forceinline__ double group_add(double v) {
   step([](uint32_t x) -> uint32_t { return __builtin_amdgcn_update_dpp(0u, x, 0x124, 0xF, 0xF, false); });
   step([](uint32_t x) -> uint32_t { return __builtin_amdgcn_update_dpp(0u, x, 0x122, 0xF, 0xF, false); });
   step([](uint32_t x) -> uint32_t { return __builtin_amdgcn_update_dpp(0u, x, 0x121, 0xF, 0xF, false); });
-  if constexpr (G == 32) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false);
-    const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
-    v = __builtin_bit_cast(double, ((uint64_t)hi[0] << 32) | lo[0]) +
-        __builtin_bit_cast(double, ((uint64_t)hi[1] << 32) | lo[1]);
-  }
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+  v = __builtin_bit_cast(double, ((uint64_t)hi[0] << 32) | lo[0]) +
+      __builtin_bit_cast(double, ((uint64_t)hi[1] << 32) | lo[1]);
   return v;
 }
 
@@ -98,7 +95,7 @@ __device__ __forceinline__ float logit(const char* row, int e) {
 
 // The lane's logits of a token; -inf behind the last expert. Every load is made (of the last expert where there is none), so
 // that they go out one behind the other.
-template <int DT, int G, int V>
+template <int DT, int V>
 __device__ __forceinline__ void load_logits(const char* row, int E, int l, float (&z)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) z[i] = logit<DT>(row, min(i * G + l, E - 1));
@@ -129,7 +126,7 @@ __device__ __forceinline__ float sigmoid_f32(float z) {
 // The shares p of the lane's logits, 0 for all where no expert is on (or, of
 // sigmoids, none is above 0). Also the softmax's largest logit, the sum of the scores, and what the sigmoids leave of 1
 // (of a softmax: 1).
-template <int G, int V>
+template <int V>
 __device__ __forceinline__ void shares(const float (&z)[V], bool sigmoid, float (&p)[V], float (&rest)[V], float& top,
                                        float& total) {
   top = 0.0f;
@@ -137,7 +134,7 @@ __device__ __forceinline__ void shares(const float (&z)[V], bool sigmoid, float 
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) m = fmaxf(m, z[i]);
-    top = group_fmax<G>(m);
+    top = group_fmax(m);
     if (top == -INFINITY) top = 0.0f;
   }
   float sum = 0.0f;
@@ -147,7 +144,7 @@ __device__ __forceinline__ void shares(const float (&z)[V], bool sigmoid, float 
     p[i] = sigmoid ? sigmoid_f32(z[i], rest[i]) : exp_down(z[i] - top);
     sum += p[i];
   }
-  total = group_add<G>(sum);
+  total = group_add(sum);
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
   for (int i = 0; i < V; ++i) p[i] *= inv;
@@ -170,10 +167,10 @@ __device__ __forceinline__ uint64_t place(double z) {
 // Scores as they are chosen by. Without a bias the logits themselves: their order is
 // the scores'. With one the sum is formed in 64 bits: of 4096 tokens' neighbours in
 // order some lie closer than 32 bits of a score tell apart.
-template <int G, int V, bool BIAS>
+template <int V, bool BIAS>
 struct Keys;
-template <int G, int V>
-struct Keys<G, V, false> {
+template <int V>
+struct Keys<V, false> {
   uint32_t key[V];
   __device__ __forceinline__ void make(const float (&z)[V], bool, const float*, int, int) {
 #pragma unroll
@@ -186,16 +183,16 @@ struct Keys<G, V, false> {
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (key[i] > b) { b = key[i]; at = i * G + l; }
-    const uint32_t top = group_max<G>(b);
-    const int e = (int)group_min<G>(b == top ? (uint32_t)at : 0xFFFFu);
+    const uint32_t top = group_max(b);
+    const int e = (int)group_min(b == top ? (uint32_t)at : 0xFFFFu);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (i * G + l == e) key[i] = 0;
     return top == 0 ? -1 : e;
   }
 };
-template <int G, int V>
-struct Keys<G, V, true> {
+template <int V>
+struct Keys<V, true> {
   uint64_t key[V];
   __device__ __forceinline__ void make(const float (&z)[V], bool sigmoid, const float* bias, int E, int l) {
     double s[V], sum = 0.0;
@@ -203,7 +200,7 @@ struct Keys<G, V, true> {
     if (!sigmoid) {
 #pragma unroll
       for (int i = 0; i < V; ++i) m = fmaxf(m, z[i]);
-      m = group_fmax<G>(m);
+      m = group_fmax(m);
       if (m == -INFINITY) m = 0.0f;
     }
 #pragma unroll
@@ -212,7 +209,7 @@ struct Keys<G, V, true> {
       sum += s[i];
     }
     double inv = 1.0;
-    if (!sigmoid) inv = 1.0 / group_add<G>(sum);
+    if (!sigmoid) inv = 1.0 / group_add(sum);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = i * G + l;
@@ -225,9 +222,9 @@ struct Keys<G, V, true> {
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (key[i] > b) { b = key[i]; at = i * G + l; }
-    const uint32_t hi = group_max<G>((uint32_t)(b >> 32));
-    const uint32_t lo = group_max<G>((uint32_t)(b >> 32) == hi ? (uint32_t)b : 0u);
-    const int e = (int)group_min<G>(b == (((uint64_t)hi << 32) | lo) ? (uint32_t)at : 0xFFFFu);
+    const uint32_t hi = group_max((uint32_t)(b >> 32));
+    const uint32_t lo = group_max((uint32_t)(b >> 32) == hi ? (uint32_t)b : 0u);
+    const int e = (int)group_min(b == (((uint64_t)hi << 32) | lo) ? (uint32_t)at : 0xFFFFu);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (i * G + l == e) key[i] = 0;
@@ -244,7 +241,7 @@ __device__ __forceinline__ void wave_lds() {
 // The scores of the chosen experts, in the lane's slots l, l + G, .. (0 for a slot
 // without an expert): over their sum when `renorm`. The softmax's renormalised ones
 // are a softmax over the chosen logits, which no underflow of the others' spoils.
-template <int DT, int G>
+template <int DT>
 __device__ __forceinline__ void slot_scores(const char* row, const int32_t* sel, int k, int E, int l, bool sigmoid,
                                             bool renorm, float top, float total, float (&s)[MAX_TOPK / G]) {
   float z[MAX_TOPK / G], m = -INFINITY;
@@ -256,7 +253,7 @@ __device__ __forceinline__ void slot_scores(const char* row, const int32_t* sel,
     m = fmaxf(m, z[q]);
   }
   if (!sigmoid && renorm) {
-    top = group_fmax<G>(m);
+    top = group_fmax(m);
     if (top == -INFINITY) top = 0.0f;
   }
   float sum = 0.0f;
@@ -265,7 +262,7 @@ __device__ __forceinline__ void slot_scores(const char* row, const int32_t* sel,
     s[q] = sigmoid ? sigmoid_f32(z[q]) : exp_down(z[q] - top);
     sum += s[q];
   }
-  if (renorm) total = group_add<G>(sum);
+  if (renorm) total = group_add(sum);
   else if (sigmoid) total = 1.0f;
 #pragma unroll
   for (int q = 0; q < MAX_TOPK / G; ++q) s[q] = total == 0.0f ? 0.0f : s[q] / total;
@@ -279,7 +276,6 @@ __device__ __forceinline__ float key_error(bool sigmoid, float key) {
 }
 
 // A token's candidates: a group's lanes each have one.
-template <int G>
 struct Candidates {
   uint64_t key[G];
   float z[G];
@@ -294,15 +290,12 @@ __device__ __forceinline__ int others_at_least(uint32_t v, uint32_t o, std::inte
   return n;
 }
 // How many of a group's lanes have a value that is at least this lane's.
-template <int G>
 __device__ __forceinline__ int at_least(uint32_t v, int l) {
   constexpr std::make_integer_sequence<int, 15> turns;
   int n = 1 + others_at_least(v, v, turns);
-  if constexpr (G == 32) {
-    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    const uint32_t o = l >= 16 ? r[0] : r[1];
-    n += (o >= v ? 1 : 0) + others_at_least(v, o, turns);
-  }
+  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  const uint32_t o = l >= 16 ? r[0] : r[1];
+  n += (o >= v ? 1 : 0) + others_at_least(v, o, turns);
   return n;
 }
 
@@ -311,9 +304,9 @@ __device__ __forceinline__ int at_least(uint32_t v, int l) {
 // one a lane. A round over all keys for each of the k instead took 7.5 us for 4096 tokens of 384 experts, and with the
 // bias, all sums in 64 bits, 14.7. Returns the lane's rank (k or more: not chosen; its logit and expert are then of no
 // use), or -1 for all where there are more candidates than lanes.
-template <int G, int V, bool BIAS>
+template <int V, bool BIAS>
 __device__ __forceinline__ int choose(const float (&z)[V], bool sigmoid, const float (&b)[V], const float* bias, int k,
-                                      int l, Candidates<G>& c, int& n, float& cz, int& ce) {
+                                      int l, Candidates& c, int& n, float& cz, int& ce) {
   float m = 0.0f, a[V];
   uint32_t key[V], most = 0;
   if constexpr (BIAS) {
@@ -322,7 +315,7 @@ __device__ __forceinline__ int choose(const float (&z)[V], bool sigmoid, const f
       m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < V; ++i) m = fmaxf(m, z[i]);
-      m = group_fmax<G>(m);
+      m = group_fmax(m);
       if (m == -INFINITY) m = 0.0f;
     }
 #pragma unroll
@@ -330,7 +323,7 @@ __device__ __forceinline__ int choose(const float (&z)[V], bool sigmoid, const f
       a[i] = sigmoid ? sigmoid_f32(z[i]) : exp_down(z[i] - m);
       sum += a[i];
     }
-    if (!sigmoid) inv = __builtin_amdgcn_rcpf(group_add<G>(sum));
+    if (!sigmoid) inv = __builtin_amdgcn_rcpf(group_add(sum));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       a[i] = fmaf(a[i], inv, b[i]);
@@ -342,7 +335,7 @@ __device__ __forceinline__ int choose(const float (&z)[V], bool sigmoid, const f
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) most = max(most, key[i]);
-  const uint32_t kth = group_max<G>(at_least<G>(most, l) >= k ? most : 0u);
+  const uint32_t kth = group_max(at_least(most, l) >= k ? most : 0u);
   uint32_t least = max(kth, 1u);
   if constexpr (BIAS) {
     // kth 0 or 1: fewer than k lanes have a number, and all keys are candidates
@@ -363,13 +356,11 @@ __device__ __forceinline__ int choose(const float (&z)[V], bool sigmoid, const f
   at += __builtin_amdgcn_update_dpp(0u, at, 0x112, 0xF, 0xF, false);
   at += __builtin_amdgcn_update_dpp(0u, at, 0x114, 0xF, 0xF, false);
   at += __builtin_amdgcn_update_dpp(0u, at, 0x118, 0xF, 0xF, false);
-  uint32_t all = group_all<16>(mine, add);
+  uint32_t all = row_all(mine, add);
   at -= mine;
-  if constexpr (G == 32) {
-    const auto r = __builtin_amdgcn_permlane16_swap(all, all, false, false);
-    if (l >= 16) at += r[0];
-    all = r[0] + r[1];
-  }
+  const auto r = __builtin_amdgcn_permlane16_swap(all, all, false, false);
+  if (l >= 16) at += r[0];
+  all = r[0] + r[1];
   n = (int)all;
   if (!__all(n <= G)) return -1;
 #pragma unroll
@@ -386,7 +377,7 @@ __device__ __forceinline__ int choose(const float (&z)[V], bool sigmoid, const f
       double part = 0.0;
 #pragma unroll
       for (int i = 0; i < V; ++i) part += exp((double)z[i] - (double)m);
-      total = group_add<G>(part);
+      total = group_add(part);
     }
   }
   wave_lds();
@@ -422,35 +413,35 @@ __device__ __forceinline__ int choose(const float (&z)[V], bool sigmoid, const f
   return rank;
 }
 
-template <int DT, int G, int V, bool BIAS>
+template <int DT, int V, bool BIAS>
 __global__ __launch_bounds__(GATE_THREADS) void k_gate(const void* __restrict__ logits, int64_t T, int E, bool sigmoid,
                                                        const float* __restrict__ bias, int k, bool renorm, float scale,
                                                        int32_t* __restrict__ ids, float* __restrict__ w) {
   constexpr int PER = GATE_THREADS / G;
   __shared__ int32_t sel[PER][MAX_TOPK];
-  __shared__ Candidates<G> cand[PER];
+  __shared__ Candidates cand[PER];
   const int l = threadIdx.x % G, g = threadIdx.x / G;
   for (int64_t t0 = (int64_t)blockIdx.x * PER; t0 < T; t0 += (int64_t)gridDim.x * PER) {
     const bool live = t0 + g < T;
     const int64_t t = live ? t0 + g : T - 1;        // all lanes go along: DPP reads only active ones
     const char* row = at<DT>(logits, t * E);
     float z[V], b[V], top = 0.0f, total = 1.0f;
-    load_logits<DT, G, V>(row, E, l, z);
+    load_logits<DT, V>(row, E, l, z);
 #pragma unroll
     for (int i = 0; i < V; ++i) b[i] = BIAS ? bias[min(i * G + l, E - 1)] : 0.0f;
     if (!sigmoid && !renorm) {
       float p[V], rest[V];
-      shares<G, V>(z, false, p, rest, top, total);
+      shares<V>(z, false, p, rest, top, total);
     }
     int rank = -1, n = 0, e = 0;
     float ze = 0.0f;
-    if (k <= G) rank = choose<G, V, BIAS>(z, sigmoid, b, bias, k, l, cand[g], n, ze, e);
+    if (k <= G) rank = choose<V, BIAS>(z, sigmoid, b, bias, k, l, cand[g], n, ze, e);
     if (rank >= 0) {
       // a lane has a slot: the chosen expert's score, as slot_scores forms it
       const bool mine = rank < k;
       if (!mine) ze = -INFINITY;
       if (!sigmoid && renorm) {
-        top = group_fmax<G>(ze);
+        top = group_fmax(ze);
         if (top == -INFINITY) top = 0.0f;
       }
       float s = sigmoid ? sigmoid_f32(ze) : exp_down(ze - top);
@@ -458,7 +449,7 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate(const void* __restrict__ 
         // over the slots in their order, whichever lane they are in
         if (mine) cand[g].z[rank] = s;
         wave_lds();
-        total = group_add<G>(l < min(n, k) ? cand[g].z[l] : 0.0f);
+        total = group_add(l < min(n, k) ? cand[g].z[l] : 0.0f);
         wave_lds();
       } else if (sigmoid) {
         total = 1.0f;
@@ -474,7 +465,7 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate(const void* __restrict__ 
       }
       continue;
     }
-    Keys<G, V, BIAS> keys;
+    Keys<V, BIAS> keys;
     keys.make(z, sigmoid, bias, E, l);
     for (int j = 0; j < k; ++j) {
       const int best = keys.take(l);
@@ -482,7 +473,7 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate(const void* __restrict__ 
     }
     wave_lds();
     float s[MAX_TOPK / G];
-    slot_scores<DT, G>(row, sel[g], k, E, l, sigmoid, renorm, top, total, s);
+    slot_scores<DT>(row, sel[g], k, E, l, sigmoid, renorm, top, total, s);
 #pragma unroll
     for (int q = 0; q < MAX_TOPK / G; ++q) {
       const int j = q * G + l;
@@ -502,12 +493,11 @@ __device__ __forceinline__ void tokens_of(const int32_t* seq_off, int64_t q, int
 }
 
 // The last of the S + 1 offsets that is at or before t, G of them at a time; -1 where t is before all of them.
-template <int G>
 __device__ __forceinline__ int64_t sequence_of(const int32_t* seq_off, int64_t S, int64_t t, int l) {
   int64_t lo = 0, n = S + 1;        // the last offset at or before t is one of lo .. lo + n - 1, or none
   while (n > G) {
     const int64_t step = (n + G - 1) / G, at = lo + step * l;
-    const uint32_t before = group_all<G>(step * l < n && seq_off[min(at, S)] <= t ? 1u : 0u,
+    const uint32_t before = group_all(step * l < n && seq_off[min(at, S)] <= t ? 1u : 0u,
                                          [](uint32_t p, uint32_t q) { return p + q; });
     if (before > 0) {
       const int64_t skip = step * (int64_t)(before - 1);
@@ -517,7 +507,7 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* seq_off, int64_t S
       n = 1;
     }
   }
-  const uint32_t here = group_all<G>(l < n && seq_off[min(lo + l, S)] <= t ? 1u : 0u,
+  const uint32_t here = group_all(l < n && seq_off[min(lo + l, S)] <= t ? 1u : 0u,
                                      [](uint32_t p, uint32_t q) { return p + q; });
   return here == 0 ? -1 : lo + here - 1;
 }
@@ -538,7 +528,7 @@ __device__ __forceinline__ void balance_out(int64_t q, int64_t n, int E, int k, 
 }
 
 // The sums of p and the counts of tokens lo .. hi - 1, by one workgroup: those of expert threadIdx.x come back to a thread.
-template <int DT, int G, int V>
+template <int DT, int V>
 __device__ __forceinline__ void balance_part(const void* logits, int E, bool sigmoid, const int32_t* ids, int k, int64_t lo,
                                              int64_t hi, float (*sums)[G * V], int32_t* hist, float& p_sum, int32_t& c) {
   constexpr int PER = BAL_THREADS / G;
@@ -553,7 +543,7 @@ __device__ __forceinline__ void balance_part(const void* logits, int E, bool sig
   __syncthreads();
   for (int64_t t0 = lo; t0 < hi; t0 += PER) {
     float z[V], p[V], rest[V], top, total;
-    load_logits<DT, G, V>(at<DT>(logits, min(t0 + g, hi - 1) * E), E, l, z);
+    load_logits<DT, V>(at<DT>(logits, min(t0 + g, hi - 1) * E), E, l, z);
     if (t0 == lo) {
       if (first < (uint32_t)E) atomicAdd(&hist[first], 1);
       for (int64_t i = threadIdx.x + BAL_THREADS; i < slots; i += BAL_THREADS) {
@@ -561,17 +551,13 @@ __device__ __forceinline__ void balance_part(const void* logits, int E, bool sig
         if (e < (uint32_t)E) atomicAdd(&hist[e], 1);
       }
     }
-    shares<G, V>(z, sigmoid, p, rest, top, total);
+    shares<V>(z, sigmoid, p, rest, top, total);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] += t0 + g < hi ? p[i] : 0.0f;
   }
   // over the wave's groups, then the waves
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    if constexpr (G == 16) {
-      const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i]), __float_as_uint(acc[i]), false, false);
-      acc[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    }
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i]), __float_as_uint(acc[i]), false, false);
     acc[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
     if ((threadIdx.x & 63) < G) sums[threadIdx.x >> 6][i * G + l] = acc[i];
@@ -586,7 +572,7 @@ __device__ __forceinline__ void balance_part(const void* logits, int E, bool sig
 }
 
 // A workgroup to a sequence, for short ones.
-template <int DT, int G, int V>
+template <int DT, int V>
 __global__ __launch_bounds__(BAL_THREADS) void k_balance(const void* __restrict__ logits, int64_t T, int E, bool sigmoid,
                                                          const int32_t* __restrict__ ids, int k,
                                                          const int32_t* __restrict__ seq_off, float coef,
@@ -598,14 +584,14 @@ __global__ __launch_bounds__(BAL_THREADS) void k_balance(const void* __restrict_
   tokens_of(seq_off, blockIdx.x, T, a, b);
   float p;
   int32_t c;
-  balance_part<DT, G, V>(logits, E, sigmoid, ids, k, a, b, sums, hist, p, c);
+  balance_part<DT, V>(logits, E, sigmoid, ids, k, a, b, sums, hist, p, c);
   balance_out(blockIdx.x, b - a, E, k, coef, c, p, red, loss, counts);
 }
 
 // A workgroup to `chunk` tokens, for long ones: what they give each sequence that they are of. From chunk to chunk and
 // sequence to sequence one of the two moves on, so the part of (chunk, sequence) is row chunk + sequence of the parts, and
 // a sequence's parts are rows that follow one another.
-template <int DT, int G, int V>
+template <int DT, int V>
 __global__ __launch_bounds__(BAL_THREADS) void k_balance_chunk(const void* __restrict__ logits, int64_t T, int E,
                                                                bool sigmoid, const int32_t* __restrict__ ids, int k,
                                                                const int32_t* __restrict__ seq_off, int64_t S, int chunk,
@@ -613,7 +599,7 @@ __global__ __launch_bounds__(BAL_THREADS) void k_balance_chunk(const void* __res
   __shared__ float sums[BAL_WAVES][G * V];
   __shared__ int32_t hist[512];
   const int64_t lo = (int64_t)blockIdx.x * chunk, hi = min(lo + chunk, T);
-  int q = seq_off == nullptr ? 0 : max((int)sequence_of<G>(seq_off, S, lo, threadIdx.x % G), 0);
+  int q = seq_off == nullptr ? 0 : max((int)sequence_of(seq_off, S, lo, threadIdx.x % G), 0);
   for (q = __builtin_amdgcn_readfirstlane(q); q < (int)S; ++q) {
     int64_t a, b;
     tokens_of(seq_off, q, T, a, b);
@@ -623,7 +609,7 @@ __global__ __launch_bounds__(BAL_THREADS) void k_balance_chunk(const void* __res
     if (a >= b) continue;
     float p;
     int32_t c;
-    balance_part<DT, G, V>(logits, E, sigmoid, ids, k, a, b, sums, hist, p, c);
+    balance_part<DT, V>(logits, E, sigmoid, ids, k, a, b, sums, hist, p, c);
     if ((int)threadIdx.x < E) {
       const int64_t at = (blockIdx.x + q) * E + threadIdx.x;
       part_p[at] = p;
@@ -697,7 +683,7 @@ struct GateGrad {
   void* d_logits;
 };
 
-template <int DT, int G, int V>
+template <int DT, int V>
 __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
   constexpr int PER = GATE_THREADS / G, Q = MAX_TOPK / G;
   __shared__ int32_t sel[PER][MAX_TOPK];
@@ -710,7 +696,7 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
     const char* row = at<DT>(a.logits, t * E);
     float z[V], p[V], rest[V], d[V], top, total;
     // everything that hangs on nothing else is asked for first
-    load_logits<DT, G, V>(row, E, l, z);
+    load_logits<DT, V>(row, E, l, z);
     int32_t id[Q];
     float dw[Q];
 #pragma unroll
@@ -720,9 +706,9 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
       dw[q] = a.d_w != nullptr ? a.d_w[j] : 0.0f;
     }
     int64_t lo = 0;
-    if (a.counts != nullptr && a.seq_off != nullptr) lo = sequence_of<G>(a.seq_off, a.S, t, l);
+    if (a.counts != nullptr && a.seq_off != nullptr) lo = sequence_of(a.seq_off, a.S, t, l);
     lo = min(lo, a.S - 1);          // (behind the last sequence: it does not reach t)
-    shares<G, V>(z, a.sigmoid, p, rest, top, total);
+    shares<V>(z, a.sigmoid, p, rest, top, total);
 #pragma unroll
     for (int i = 0; i < V; ++i) d[i] = 0.0f;
     if (a.counts != nullptr) {
@@ -740,7 +726,7 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
         d[i] = e < E && lo >= 0 ? f * (float)a.counts[lo * E + e] : 0.0f;
         dot = fmaf(p[i], d[i], dot);
       }
-      dot = group_add<G>(dot);
+      dot = group_add(dot);
 #pragma unroll
       for (int i = 0; i < V; ++i) d[i] = p[i] * (d[i] - dot);
     }
@@ -752,14 +738,14 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
       }
       wave_lds();
       float s[Q], mean = 0.0f;
-      slot_scores<DT, G>(row, sel[g], k, E, l, a.sigmoid, a.renorm, top, total, s);
+      slot_scores<DT>(row, sel[g], k, E, l, a.sigmoid, a.renorm, top, total, s);
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const int j = q * G + l;
         if (!(j < k && (unsigned)id[q] < (unsigned)E)) dw[q] = 0.0f;
         mean = fmaf(s[q], dw[q], mean);
       }
-      mean = a.renorm ? group_add<G>(mean) : 0.0f;
+      mean = a.renorm ? group_add(mean) : 0.0f;
       float sum = 0.0f;
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
@@ -772,7 +758,7 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
       for (int i = 0; i < V; ++i) part[g][i * G + l] = 0.0f;
       wave_lds();
       if (!a.sigmoid && !a.renorm) {
-        sum = group_add<G>(sum);
+        sum = group_add(sum);
 #pragma unroll
         for (int i = 0; i < V; ++i) d[i] = fmaf(-p[i], sum, d[i]);
       }
@@ -813,19 +799,17 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_grad(GateGrad a) {
   }
 }
 
-// f(lanes of a token, values of a lane). 16 lanes while a lane's values are few.
+// f(values of a lane)
 template <class F>
 void dispatch_experts(int E, F&& f) {
   using std::integral_constant;
-  const integral_constant<int, 16> g16;
-  const integral_constant<int, 32> g32;
-  if (E <= 64) f(g16, integral_constant<int, 4>());
-  else if (E <= 128) f(g16, integral_constant<int, 8>());
-  else if (E <= 192) f(g32, integral_constant<int, 6>());
-  else if (E <= 256) f(g32, integral_constant<int, 8>());
-  else if (E <= 320) f(g32, integral_constant<int, 10>());
-  else if (E <= 384) f(g32, integral_constant<int, 12>());
-  else f(g32, integral_constant<int, 16>());
+  if (E <= 64) f(integral_constant<int, 2>());
+  else if (E <= 128) f(integral_constant<int, 4>());
+  else if (E <= 192) f(integral_constant<int, 6>());
+  else if (E <= 256) f(integral_constant<int, 8>());
+  else if (E <= 320) f(integral_constant<int, 10>());
+  else if (E <= 384) f(integral_constant<int, 12>());
+  else f(integral_constant<int, 16>());
 }
 
 unsigned token_grid(int64_t T, int per) { return (unsigned)std::min<int64_t>((T + per - 1) / per, (int64_t)1 << 20); }
@@ -835,23 +819,27 @@ unsigned token_grid(int64_t T, int per) { return (unsigned)std::min<int64_t>((T 
 hipError_t launch_gate(const void* logits, DType dt, int64_t T, int E, bool sigmoid, const float* bias, int k,
                        bool renorm, float scale, int32_t* ids, float* w, hipStream_t s) {
   dispatch_dt(dt, [&](auto d) {
-    dispatch_experts(E, [&](auto lanes, auto values) {
-      constexpr int D = decltype(d)::value, G = decltype(lanes)::value, V = decltype(values)::value;
+    dispatch_experts(E, [&](auto values) {
+      constexpr int D = decltype(d)::value, V = decltype(values)::value;
       const unsigned grid = token_grid(T, GATE_THREADS / G);
       if (bias != nullptr)
-        k_gate<D, G, V, true><<<grid, GATE_THREADS, 0, s>>>(logits, T, E, sigmoid, bias, k, renorm, scale, ids, w);
+        k_gate<D, V, true><<<grid, GATE_THREADS, 0, s>>>(logits, T, E, sigmoid, bias, k, renorm, scale, ids, w);
       else
-        k_gate<D, G, V, false><<<grid, GATE_THREADS, 0, s>>>(logits, T, E, sigmoid, bias, k, renorm, scale, ids, w);
+        k_gate<D, V, false><<<grid, GATE_THREADS, 0, s>>>(logits, T, E, sigmoid, bias, k, renorm, scale, ids, w);
     });
   });
   return hipGetLastError();
 }
 
-// Tokens of a chunk: one turn of a workgroup's groups or more, so that there are at most 128 chunks; 0: a workgroup to each
-// sequence, where they are shorter than two turns on average.
+// Tokens of a chunk: one turn of a workgroup's groups or more, so that there are 128 chunks at most, and from 8 turns on 256 (a
+// workgroup to a compute unit). 0: a workgroup to each sequence, where they are no longer than two turns on average (a
+// longer one among them then takes its time: an average says little of the longest). us, 384 experts: 4096 tokens in
+// sequences of 32 5.1 and in chunks 9.4, of 64 6.7 and 9.8, of 128 10.0 and 9.6.
 static int balance_chunk(int64_t T, int64_t S) {
-  if (T / S < 64) return 0;
-  return (int)(32 * ((T + 32 * 128 - 1) / (32 * 128)));
+  constexpr int64_t TURN = BAL_THREADS / G;
+  if (T / S <= 2 * TURN) return 0;
+  const int64_t turns = (T + TURN * 128 - 1) / (TURN * 128);
+  return (int)(TURN * (turns <= 8 ? turns : std::max<int64_t>(8, (T + TURN * 256 - 1) / (TURN * 256))));
 }
 int64_t balance_parts(int64_t T, int64_t S) {
   const int chunk = balance_chunk(T, S);
@@ -865,12 +853,12 @@ hipError_t launch_balance(const void* logits, DType dt, int64_t T, int E, bool s
   float* pp = part;
   int32_t* pc = (int32_t*)(part + balance_parts(T, S) * E);
   dispatch_dt(dt, [&](auto d) {
-    dispatch_experts(E, [&](auto lanes, auto values) {
-      constexpr int D = decltype(d)::value, G = decltype(lanes)::value, V = decltype(values)::value;
+    dispatch_experts(E, [&](auto values) {
+      constexpr int D = decltype(d)::value, V = decltype(values)::value;
       if (chunk == 0)
-        k_balance<D, G, V><<<(unsigned)S, BAL_THREADS, 0, s>>>(logits, T, E, sigmoid, ids, k, seq_off, coef, loss, counts);
+        k_balance<D, V><<<(unsigned)S, BAL_THREADS, 0, s>>>(logits, T, E, sigmoid, ids, k, seq_off, coef, loss, counts);
       else
-        k_balance_chunk<D, G, V><<<(unsigned)((T + chunk - 1) / chunk), BAL_THREADS, 0, s>>>(logits, T, E, sigmoid, ids, k,
+        k_balance_chunk<D, V><<<(unsigned)((T + chunk - 1) / chunk), BAL_THREADS, 0, s>>>(logits, T, E, sigmoid, ids, k,
                                                                                            seq_off, S, chunk, pp, pc);
     });
   });
@@ -884,9 +872,9 @@ hipError_t launch_gate_grad(const void* logits, DType dt, int64_t T, int E, bool
                             int64_t S, float coef, const float* d_loss, void* d_logits, hipStream_t s) {
   const GateGrad a{logits, T, E, sigmoid, ids, k, renorm, scale, d_w, counts, seq_off, S, coef, d_loss, d_logits};
   dispatch_dt(dt, [&](auto d) {
-    dispatch_experts(E, [&](auto lanes, auto values) {
-      constexpr int D = decltype(d)::value, G = decltype(lanes)::value, V = decltype(values)::value;
-      k_gate_grad<D, G, V><<<token_grid(T, GATE_THREADS / G), GATE_THREADS, 0, s>>>(a);
+    dispatch_experts(E, [&](auto values) {
+      constexpr int D = decltype(d)::value, V = decltype(values)::value;
+      k_gate_grad<D, V><<<token_grid(T, GATE_THREADS / G), GATE_THREADS, 0, s>>>(a);
     });
   });
   return hipGetLastError();

@@ -37,7 +37,6 @@ struct Tile {
   static constexpr int Y_PITCH = TN * 2 + 8;
   static constexpr int SMEM = SLOTS * SLOT > TM * Y_PITCH ? SLOTS * SLOT : TM * Y_PITCH;
   static constexpr int X_COPIES = X_BYTES / (16 * THREADS);
-  static constexpr int Y_BYTES = TM * Y_PITCH;
 };
 
 // 16-byte chunk c (of 8) of activation row r: 16 rows at one chunk fall in 16 bank groups.
@@ -55,7 +54,7 @@ __device__ __forceinline__ f32x16 mfma32(u32v4 a, u32v4 b, const f32x16& c) {
 }
 
 // Which rows of its tile a wave multiplies.
-template <class T, int DT>
+template <class T>
 struct Place {
   int r32, h, wn, wm;
   __device__ __forceinline__ explicit Place(int wave) {
@@ -71,7 +70,7 @@ struct Place {
 // of the tile's weight row `row` are, scale_zero(b, row, scale, zero) gives that block's. Lane (row, h)
 // has columns 16 h .. 16 h + 15 of a block: step 2 b + m takes 8 m .. 8 m + 7 of them.
 template <class T, int DT, bool INT, int GROUPS, class C, class F>
-__device__ __forceinline__ void stage_products(const Place<T, DT>& me, const uint8_t* sx, bool whole, C&& codes,
+__device__ __forceinline__ void stage_products(const Place<T>& me, const uint8_t* sx, bool whole, C&& codes,
                                                F&& scale_zero, f32x16 (&acc)[T::IB][T::JB]) {
   constexpr int IB = T::IB, JB = T::JB;
   u32v4 w[JB][4];
@@ -136,7 +135,7 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[T::IB][T::JB]) {
 // The finished tile: lane (r32, h) has weight row r32 of a block and tokens 8 (v / 4) + 4 h + v % 4. Through LDS, and
 // out in whole rows.
 template <class T, int DT>
-__device__ __forceinline__ void store_tile(const W4Args& a, const Place<T, DT>& me, uint8_t* smem, int64_t t0, int64_t n0,
+__device__ __forceinline__ void store_tile(const W4Args& a, const Place<T>& me, uint8_t* smem, int64_t t0, int64_t n0,
                                            const f32x16 (&acc)[T::IB][T::JB]) {
   constexpr int Y_PITCH = T::Y_PITCH;
   __syncthreads();
@@ -176,7 +175,7 @@ template <class T, int DT, bool INT, int GROUPS>
 __device__ __forceinline__ void w4_tile(const W4Args& a, uint8_t* smem, int64_t t0, int64_t n0) {
   constexpr int TN = T::TN, SCALES = T::X_BYTES + T::W_BYTES, ZEROS = SCALES + T::S_BYTES, C = T::X_COPIES + 2 + INT;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Place<T, DT> me(wave);
+  const Place<T> me(wave);
   const int blocks = (int)(a.K / 32), stages = (blocks + 1) / 2;
   static_assert(T::W_BYTES == 16 * T::THREADS && 2 * TN == T::THREADS, "one copy of codes and one table entry a thread");
   // this thread's chunks of the activations and the codes, and its entry of each table
@@ -386,7 +385,7 @@ struct Part {
     else wait_copies<0>();
   }
   template <int GROUPS>
-  __device__ __forceinline__ void run(const Place<T, DT>& me, f32x16 (&acc)[T::IB][T::JB]) const {
+  __device__ __forceinline__ void run(const Place<T>& me, f32x16 (&acc)[T::IB][T::JB]) const {
     constexpr int NT = T::TN / 16;
     // of row r: where dword e is from where dword 0 is
     const auto dword = [](const uint8_t* s, int e, int r) {
@@ -434,7 +433,7 @@ __global__ __launch_bounds__(T::THREADS* KG) void k_w4_part(W4Args a, int tiles_
   const int nt = L % tiles_n, mt = L / tiles_n % tiles_m, sp = L / tiles_n / tiles_m;
   const int64_t t0 = (int64_t)mt * T::TM, n0 = (int64_t)nt * T::TN;
   P p(a, smem, t0, n0);
-  const Place<T, DT> me(p.wave % (T::THREADS / 64));
+  const Place<T> me(p.wave % (T::THREADS / 64));
   const int blocks = (int)(a.K / 32), units = (blocks + UNIT - 1) / UNIT;
   const int u0 = units * sp / splits, u1 = units * (sp + 1) / splits;     // (units and splits are small)
   const int64_t groups = a.K >> GL;
@@ -528,10 +527,12 @@ __global__ __launch_bounds__(256) void k_w4_sum(W4Args a, int splits) {
 }  // namespace
 
 // Measured, us, MXFP4 with bf16, K 7168 (a compute unit does a 256 x 256 tile in about 180 us, alone in 165): 1024 tokens to
-// 7168 rows 151 in parts, 183 in tiles of 256; 2048 tokens 340 and 217; 2048 tokens to 1536 rows 90 and 175.
+// 7168 rows 146 in parts, 183 in tiles of 256; 2048 tokens 340 and 217; 2048 tokens to 1536 rows 90 and 175. Up to 16 tokens
+// w4.hip takes 13.0 where 20 tokens in parts take 16.6.
 W4Plan w4_plan(int64_t M, int64_t K, int64_t N) {
   if (M <= W4_FEW) return {16, 1, false};
   if (((M + 255) / 256) * ((N + 255) / 256) >= 160) return {256, 1, true};
+  // the next larger tile takes 32 tokens of 7168 -> 7168 23.4 us instead of 16.9, 64 31.1 instead of 24.7
   const int tokens = M <= 32 ? 32 : M <= 64 ? 64 : 128;
   const int64_t tiles = ((M + tokens - 1) / tokens) * ((N + 127) / 128), units = (K + 255) / 256;
   // one workgroup is on a compute unit at a time: as many parts as leave none without work for long
