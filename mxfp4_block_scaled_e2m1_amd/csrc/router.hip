@@ -433,6 +433,11 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate(const void* __restrict__ 
       float p[V], rest[V];
       shares<V>(z, false, p, rest, top, total);
     }
+    // a NaN logit makes all of a softmax's scores NaN; renormalised ones are formed of the chosen logits, which may lack it
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) nan |= z[i] != z[i];
+    nan = !sigmoid && renorm && (uint32_t)(__ballot(nan) >> (threadIdx.x & 32)) != 0;
     int rank = -1, n = 0, e = 0;
     float ze = 0.0f;
     if (k <= G) rank = choose<V, BIAS>(z, sigmoid, b, bias, k, l, cand[g], n, ze, e);
@@ -457,7 +462,7 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate(const void* __restrict__ 
       s = total == 0.0f ? 0.0f : s / total;
       if (live && mine) {
         ids[t * k + rank] = e;
-        w[t * k + rank] = scale * s;
+        w[t * k + rank] = nan ? NAN : scale * s;
       }
       if (live && l >= n && l < k) {                 // fewer than k are on
         ids[t * k + l] = -1;
@@ -479,7 +484,7 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate(const void* __restrict__ 
       const int j = q * G + l;
       if (live && j < k) {
         ids[t * k + j] = sel[g][j];
-        w[t * k + j] = scale * s[q];
+        w[t * k + j] = sel[g][j] < 0 ? 0.0f : nan ? NAN : scale * s[q];
       }
     }
     wave_lds();

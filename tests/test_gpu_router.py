@@ -295,3 +295,21 @@ def test_grad_of_many_sequences(mx):
         ref, size = o.moe_gate_grad(zr[tok:tok + 1], ids[tok:tok + 1].cpu().numpy(), None, rc[q:q + 1], dlr[q:q + 1],
                                     [0, 1], coef=1.0 / n ** 2)
         within(got[tok:tok + 1], ref, (3 * score_error(zr[tok:tok + 1], E) + 40 * U) * size + rounded(ref, "fp32") + 2.0 ** -120)
+
+
+@pytest.mark.parametrize("k", [4, 40])
+def test_nan_reaches_renormalised_weights(mx, k):
+    """A softmax with a NaN logit has no score, chosen or not; a sigmoid's other scores do not know of it."""
+    z = np.random.default_rng(0).standard_normal((4, 50))
+    z[0, 3] = np.nan
+    z[2, 7:] = -np.inf
+    z[2, 2] = np.nan
+    t = pair(z, "fp32")[0]
+    for bias in (None, pair(np.zeros(50), "fp32")[0]):
+        ids, w = (v.cpu().numpy() for v in mx.moe_gate(t, k, bias=bias))
+        on = ids >= 0
+        assert np.isnan(w[0]).all() and np.isnan(w[2][on[2]]).all() and (w[2][~on[2]] == 0).all()
+        assert on[2].sum() == min(k, 7) and np.isfinite(w[[1, 3]]).all()
+        ids, w = (v.cpu().numpy() for v in mx.moe_gate(t, k, "sigmoid", bias=bias))
+        assert 3 not in ids[0] and np.isfinite(w[[0, 1, 3]]).all()
+        assert np.isfinite(w[2]).all() == (k == 4)
